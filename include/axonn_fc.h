@@ -263,6 +263,144 @@ axonn_status_t axonn_goldfish_ce(const void* logits, int64_t ld_logits, const in
                                  cudaStream_t stream);
 
 /*
+ * Epilogues of an FC layer: bias, activation, dropout and residual.
+ *
+ *   forward    Z = X . W + b;   Y = R + D(act(Z))
+ *   backward   d = act'(Z) D(G);  dZ = d + R;  db = column sums of d
+ *
+ * where G is the gradient of Y, either a matrix (axonn_epi_bwd) or the data
+ * gradient dY . W^T of the layer after it (axonn_fc_dgrad_epi, in whose
+ * epilogue it is then never written out).  dW and dX of the layer itself are
+ * the products above on dZ.  Every part is optional.  All arithmetic is fp32,
+ * and Y, Z and dZ are rounded once.
+ *
+ * Activations: relu (slope 0 at 0; NaN stays), gelu z (1 + erf(z/sqrt 2))/2,
+ * gelu_tanh z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))/2, silu z/(1+e^-z).
+ *
+ * Dropout D drops an element with probability p and scales the others.  Its
+ * mask is computed where it is needed, forward and backward, and never
+ * stored: 16 random bits for each element from Philox4x32-10 (Salmon,
+ * Moraes, Dror and Shaw, SC'11), the key the seed's two 32-bit halves (low
+ * first), the counter (col >> 3, row, offset low, offset high), and the bits
+ * word col & 7 of the output's eight 16-bit words, lowest first.  With
+ * thr = floor(65536 p + 1/2) an element is dropped (set to 0, whatever it
+ * is) where its bits are below thr and is multiplied by the fp32 number
+ * nearest 65536/(65536 - thr) elsewhere; thr = 65536 drops all.  (seed, offset) are two 64-bit words on
+ * the DEVICE, so that a captured graph draws a new mask when they are
+ * changed between replays; the library only reads them.  Calls that must
+ * draw alike, as a forward and its backward, get the same words and rows.
+ */
+#define AXONN_BIAS_F32 0x200u     /* axonn_fc_fwd_epi: the bias is fp32 (else bf16) */
+#define AXONN_IN_F32 0x400u       /* axonn_epi_bwd: dY is fp32 (else bf16); axonn_dropout: X,
+                                     residual and Y are fp32 (else bf16) */
+typedef enum {
+  AXONN_ACT_NONE = 0,
+  AXONN_ACT_RELU = 1,
+  AXONN_ACT_GELU = 2,
+  AXONN_ACT_GELU_TANH = 3,
+  AXONN_ACT_SILU = 4
+} axonn_act_t;
+
+typedef struct {
+  const void* bias;      /* forward: [N] or NULL; bf16, or fp32 with AXONN_BIAS_F32 */
+  void* pre;             /* bf16 Z: written by the forward where not NULL, read by the
+                            backward (NULL only with AXONN_ACT_NONE) */
+  int64_t ld_pre;
+  const void* residual;  /* R or NULL, of the output's type; may be the output itself */
+  int64_t ld_residual;
+  float* dbias;          /* backward: db, fp32 [columns], overwritten; or NULL */
+  const uint64_t* rng;   /* seed and offset (device); may be NULL with p = 0 */
+  int32_t act;           /* axonn_act_t */
+  float p;               /* dropout probability, 0 <= p <= 1 */
+} axonn_epilogue_t;
+
+/* Y = R + D(act(X . W + b)) of the whole layer (grid 1x1x1, else
+ * AXONN_ERR_UNSUPPORTED) in one launch.  X, W, Y and their leading
+ * dimensions as for axonn_fc_fwd; flags AXONN_A_T, AXONN_B_T, AXONN_OUT_F32
+ * (Y and R fp32) and AXONN_BIAS_F32.  bias is 16-byte aligned like every
+ * matrix.  No workspace. */
+axonn_status_t axonn_fc_fwd_epi(const void* X, const void* W, void* Y, int64_t ldx, int64_t ldw,
+                                int64_t ldy, const axonn_fc_shape_t* shape, uint32_t flags,
+                                const axonn_epilogue_t* epi, cudaStream_t stream);
+
+/* dZ = act'(Z) D(dY . W^T) + R, [T x K], and db [K]: the data gradient of
+ * the layer `shape`, turned into the gradient of the pre-activation Z of the
+ * layer before it.  dY, W, dX (here dZ) as for axonn_fc_dgrad; flags
+ * AXONN_A_T, AXONN_B_T and AXONN_OUT_F32 (dZ and R fp32).  dX may be pre
+ * itself (bf16) or R.  db is summed in a fixed order from fp32 values; it
+ * needs a workspace of axonn_epi_workspace_size(T, K) bytes and a second
+ * launch. */
+axonn_status_t axonn_fc_dgrad_epi(const void* dY, const void* W, void* dX, int64_t lddy, int64_t ldw,
+                                  int64_t lddx, const axonn_fc_shape_t* shape, uint32_t flags,
+                                  const axonn_epilogue_t* epi, void* ws, size_t ws_bytes,
+                                  cudaStream_t stream);
+
+/* dZ = act'(Z) D(dY), bf16 [rows x cols], and db [cols], from a gradient
+ * that is already there (bf16, or fp32 with AXONN_IN_F32).  dZ may be dY
+ * (bf16) or pre.  db as for axonn_fc_dgrad_epi.  bias and residual of the
+ * epilogue must be NULL. */
+axonn_status_t axonn_epi_bwd(const void* dY, int64_t lddy, void* dZ, int64_t lddz, int64_t rows,
+                             int64_t cols, uint32_t flags, const axonn_epilogue_t* epi, void* ws,
+                             size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace bytes of the bias gradient over a [rows x cols] matrix:
+ * ceil(rows / 32) * ceil8(cols) * 4.  Host-only. */
+axonn_status_t axonn_epi_workspace_size(int64_t rows, int64_t cols, size_t* bytes);
+
+/* Y = R + D(X) over [rows x cols] (residual NULL: no R), bf16, or fp32 with
+ * AXONN_IN_F32; Y may be X or R.  The backward is the same call on the
+ * gradient.  One launch. */
+axonn_status_t axonn_dropout(const void* X, int64_t ldx, const void* residual, int64_t ld_residual,
+                             void* Y, int64_t ldy, int64_t rows, int64_t cols, float p,
+                             const uint64_t* rng, uint32_t flags, cudaStream_t stream);
+
+/*
+ * Softmax cross-entropy of the logits X . W over a vocabulary, with its
+ * gradients, without the logits ever being written out.
+ *   z_t = X_t . W (fp32);  CE_t = ln sum_v e^(z_tv) - z_t[y_t]
+ *   loss = sum over counted t of CE_t / n, n = number counted (0 when n = 0)
+ *   P_tv = softmax(z_t)_v - [v = y_t] for counted t, g = grad_scale / n
+ *   dX = g P . W^T (rows that do not count: zeros);  dW = g X^T . P
+ * A position counts when its label is in [0, V) and keep (uint8 [T], may be
+ * NULL) is not 0 there; the mask of axonn_goldfish_ce fits.  The others cost
+ * no products and their rows of X are not read: the counted rows are packed
+ * first, and their number stays on the device.
+ *   X        bf16 [T x K];  W bf16 [K x V], or [V x K] with AXONN_B_T (an
+ *            embedding tied to the head)
+ *   token_loss  out, fp32 [T]: CE_t where counted, 0 elsewhere
+ *   lse      out, fp32 [T]: the logsumexp, 0 elsewhere; or NULL
+ *   loss, kept  out, fp32 [1] and int32 [1] (n)
+ *   dX       out, bf16 [T x K], or NULL
+ *   dW       out, in W's layout, or NULL; bf16, fp32 with AXONN_OUT_F32, or
+ *            added into fp32 with AXONN_ACCUM_F32
+ * With dX and dW NULL it is the loss alone.  dX must not overlap X.
+ * The vocabulary is taken in pieces.  The softmax's statistics come from
+ * each piece's product, in fp32, in its epilogue; P is held for one piece at
+ * a time, in bf16 (each entry rounded once), and the products dX and dW read
+ * it from there.  The last piece of the forward sweep stays, each logit as
+ * its distance below a maximum of its row in 16 bits (which changes an entry
+ * of P by at most 2^-12 of itself, and by 2^-32 of that maximum's), and
+ * opens the backward one; the others are computed again.  The piece is as large as the workspace allows: with one
+ * that holds the whole vocabulary nothing is computed twice.
+ *   ws       256-byte aligned; axonn_linear_ce_workspace_size gives its
+ *            bytes for pieces of `piece` columns (rounded up to 256; 0: at
+ *            most 2 GiB of P at a time).  Anything from the size for
+ *            piece = 1 up will do (AXONN_ERR_WORKSPACE below).
+ * All sums are in a fixed order: results are the same on every run.
+ */
+axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_t ldw,
+                               const int32_t* labels, const uint8_t* keep, int64_t T, int64_t K,
+                               int64_t V, float grad_scale, uint32_t flags, float* token_loss,
+                               float* lse, float* loss, int32_t* kept, void* dX, int64_t lddx,
+                               void* dW, int64_t lddw, void* ws, size_t ws_bytes,
+                               cudaStream_t stream);
+
+/* Workspace bytes of axonn_linear_ce; grad != 0 when dX or dW is asked for.
+ * Host-only. */
+axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, uint32_t flags,
+                                              int grad, int64_t piece, size_t* bytes);
+
+/*
  * Per-shape tuning -- the GB300 counterpart of the automatic tuning of BLAS
  * kernels that the pages credit (TL;DR of the sciencestack.ai page; "The
  * reading", review of arXiv 2502.08145).  Runs this call once per candidate -- kernel
@@ -388,7 +526,10 @@ void axonn_debug_set_inject(int mode);
  * the reduction split inside a cluster)
  * axonn_set_kernel_config(c) forces configuration c for all later calls in
  * the process (-1 restores automatic choice); AXONN_ERR_INVALID_ARG if c is
- * out of range.  axonn_last_kernel_config() is the configuration the last
+ * out of range.  The products with an epilogue and those of the linear
+ * cross-entropy have the tiles 0, 2 and 7 (always with a double-buffered
+ * accumulator) and choose among them when another is forced.
+ * axonn_last_kernel_config() is the configuration the last
  * GEMM launch on this thread used (-1 before any). */
 axonn_status_t axonn_set_kernel_config(int config);
 /* SM count of the current device and how many CTA pairs (clusters of 2

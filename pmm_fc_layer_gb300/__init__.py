@@ -25,12 +25,18 @@ OUT_F32 = 0x20
 ZSHARDED = 0x40
 REDUCE_ADD = 0x80
 VGRID_PARTIALS = 0x100
+BIAS_F32 = 0x200
+IN_F32 = 0x400
+
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 OK, ERR_INVALID_ARG, ERR_ALIGNMENT, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT = range(7)
 STATUS_NAMES = ["OK", "INVALID_ARG", "ALIGNMENT", "UNSUPPORTED", "WORKSPACE", "CUDA", "TIMEOUT"]
 
 EXPORTS = ("axonn_fc_fwd", "axonn_fc_dgrad", "axonn_fc_wgrad", "axonn_fc_vgrid_static",
            "axonn_shards_gather", "axonn_fc_wgrad_zsharded", "axonn_goldfish_ce",
+           "axonn_fc_fwd_epi", "axonn_fc_dgrad_epi", "axonn_epi_bwd", "axonn_epi_workspace_size",
+           "axonn_dropout", "axonn_linear_ce", "axonn_linear_ce_workspace_size",
            "axonn_fc_workspace_size", "axonn_fc_tune", "axonn_tune_cache_save",
            "axonn_tune_cache_load", "axonn_tune_cache_clear", "axonn_tune_cache_size",
            "axonn_tune_lookup",
@@ -59,6 +65,14 @@ class Shape(ctypes.Structure):
 
     def __init__(self, T, K, N, grid=(1, 1, 1), coords=(0, 0, 0)):
         super().__init__(T, K, N, *grid, *coords)
+
+
+class Epilogue(ctypes.Structure):
+    """axonn_epilogue_t: bias, activation, dropout and residual of a layer."""
+    _fields_ = [("bias", ctypes.c_void_p), ("pre", ctypes.c_void_p), ("ld_pre", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("ld_residual", ctypes.c_int64),
+                ("dbias", ctypes.c_void_p), ("rng", ctypes.c_void_p), ("act", ctypes.c_int32),
+                ("p", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -94,6 +108,23 @@ def load(path: str | None = None):
         lib.axonn_goldfish_ce.argtypes = [vp, i64, vp, vp, i64, i64, i64, i32, i32, vp, vp, vp, vp,
                                           vp, i64, vp]
         lib.axonn_goldfish_ce.restype = ctypes.c_int
+        epi = ctypes.POINTER(Epilogue)
+        lib.axonn_fc_fwd_epi.argtypes = [vp, vp, vp, i64, i64, i64, ctypes.POINTER(Shape), u32, epi, vp]
+        lib.axonn_fc_fwd_epi.restype = ctypes.c_int
+        lib.axonn_fc_dgrad_epi.argtypes = [vp, vp, vp, i64, i64, i64, ctypes.POINTER(Shape), u32, epi,
+                                           vp, sz, vp]
+        lib.axonn_fc_dgrad_epi.restype = ctypes.c_int
+        lib.axonn_epi_bwd.argtypes = [vp, i64, vp, i64, i64, i64, u32, epi, vp, sz, vp]
+        lib.axonn_epi_bwd.restype = ctypes.c_int
+        lib.axonn_epi_workspace_size.argtypes = [i64, i64, ctypes.POINTER(sz)]
+        lib.axonn_epi_workspace_size.restype = ctypes.c_int
+        lib.axonn_dropout.argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, ctypes.c_float, vp, u32, vp]
+        lib.axonn_dropout.restype = ctypes.c_int
+        lib.axonn_linear_ce.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, ctypes.c_float, u32,
+                                        vp, vp, vp, vp, vp, i64, vp, i64, vp, sz, vp]
+        lib.axonn_linear_ce.restype = ctypes.c_int
+        lib.axonn_linear_ce_workspace_size.argtypes = [i64, i64, i64, u32, i32, i64, ctypes.POINTER(sz)]
+        lib.axonn_linear_ce_workspace_size.restype = ctypes.c_int
         lib.axonn_fc_vgrid_static.argtypes = [ctypes.c_int, vp, vp, vp, i64, i64, i64,
                                               ctypes.POINTER(Shape), u32, vp]
         lib.axonn_fc_vgrid_static.restype = ctypes.c_int
@@ -271,6 +302,146 @@ def axonn_goldfish_ce(logits, input_ids, labels, keep, token_loss, loss, kept, k
                                     _ptr(token_loss), _ptr(loss), _ptr(kept), _ptr(dlogits),
                                     _ld(dlogits, ld_dlogits) if dlogits is not None else 0,
                                     _stream(stream)))
+
+
+def _ws(ws):
+    return (_ptr(ws), ws.numel() * ws.element_size()) if ws is not None else (0, 0)
+
+
+def _typed(name, t, dtype, shape=None):
+    """Checks that a tensor has the type (and shape) the call's flags say."""
+    if t is None or isinstance(t, int):
+        return
+    if str(t.dtype) != "torch." + dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+
+
+def _vector(name, t, dtype, n):
+    _typed(name, t, dtype, (n,))
+    if t is not None and not isinstance(t, int) and n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _epilogue(act, rows, cols, bias=None, pre=None, residual=None, dbias=None, p=0.0, rng=None,
+              out_f32=False, bias_f32=False):
+    if act not in ACTS:
+        raise ValueError(f"activation {act!r} not in {sorted(ACTS)}")
+    _vector("bias", bias, "float32" if bias_f32 else "bfloat16", cols)
+    _vector("dbias", dbias, "float32", cols)
+    _typed("pre", pre, "bfloat16", (rows, cols))
+    _typed("residual", residual, "float32" if out_f32 else "bfloat16", (rows, cols))
+    _rng(rng)
+    return Epilogue(_ptr(bias) or None, _ptr(pre) or None, _ld(pre, None), _ptr(residual) or None,
+                    _ld(residual, None), _ptr(dbias) or None, _ptr(rng) or None, ACTS[act], p)
+
+
+def _rng(rng):
+    if rng is None or isinstance(rng, int):
+        return
+    if str(rng.dtype) not in ("torch.int64", "torch.uint64") or rng.numel() != 2 or not rng.is_contiguous():
+        raise ValueError("rng must be two contiguous 64-bit integers on the device: seed and offset")
+
+
+def axonn_fc_fwd_epi(X, W, Y, shape: Shape, flags: int = 0, bias=None, act="none", pre=None,
+                     residual=None, p=0.0, rng=None, stream=None):
+    """Y = residual + D(act(X . W + bias)) of the whole layer; ``pre`` (bf16)
+    receives X . W + bias where given.  bias is bf16, or fp32 (the tensor's
+    type sets BIAS_F32); residual has Y's type.  D is dropout with probability
+    p and ``rng``, two 64-bit words on the device (seed, offset)."""
+    if bias is not None and not isinstance(bias, int) and str(bias.dtype) == "torch.float32":
+        flags |= BIAS_F32
+    f32 = bool(flags & OUT_F32)
+    _typed("X", X, "bfloat16")
+    _typed("W", W, "bfloat16")
+    _typed("Y", Y, "float32" if f32 else "bfloat16", (shape.T, shape.N))
+    e = _epilogue(act, shape.T, shape.N, bias=bias, pre=pre, residual=residual, p=p, rng=rng,
+                  out_f32=f32, bias_f32=bool(flags & BIAS_F32))
+    _check(load().axonn_fc_fwd_epi(_ptr(X), _ptr(W), _ptr(Y), _ld(X, None), _ld(W, None), _ld(Y, None),
+                                   ctypes.byref(shape), flags, ctypes.byref(e), _stream(stream)))
+
+
+def axonn_fc_dgrad_epi(dY, W, dX, shape: Shape, flags: int = 0, pre=None, act="none", residual=None,
+                       dbias=None, p=0.0, rng=None, ws=None, stream=None):
+    """dX = act'(pre) D(dY . W^T) + residual, and dbias (fp32) = the column
+    sums of act'(pre) D(dY . W^T): the data gradient of this layer as the
+    gradient of the pre-activation before it.  dbias needs ``ws``
+    (axonn_epi_workspace_size(T, K) bytes)."""
+    f32 = bool(flags & OUT_F32)
+    _typed("dY", dY, "bfloat16")
+    _typed("W", W, "bfloat16")
+    _typed("dX", dX, "float32" if f32 else "bfloat16", (shape.T, shape.K))
+    e = _epilogue(act, shape.T, shape.K, pre=pre, residual=residual, dbias=dbias, p=p, rng=rng, out_f32=f32)
+    _check(load().axonn_fc_dgrad_epi(_ptr(dY), _ptr(W), _ptr(dX), _ld(dY, None), _ld(W, None),
+                                     _ld(dX, None), ctypes.byref(shape), flags, ctypes.byref(e),
+                                     *_ws(ws), _stream(stream)))
+
+
+def axonn_epi_bwd(dY, dZ, pre=None, act="none", dbias=None, p=0.0, rng=None, ws=None, stream=None):
+    """dZ (bf16) = act'(pre) D(dY) and dbias (fp32) = its column sums, for
+    dY [rows x cols] in bf16 or fp32 (the tensor's type sets IN_F32)."""
+    rows, cols = dY.shape
+    flags = IN_F32 if str(dY.dtype) == "torch.float32" else 0
+    _typed("dY", dY, "float32" if flags else "bfloat16")
+    _typed("dZ", dZ, "bfloat16", (rows, cols))
+    e = _epilogue(act, rows, cols, pre=pre, dbias=dbias, p=p, rng=rng)
+    _check(load().axonn_epi_bwd(_ptr(dY), _ld(dY, None), _ptr(dZ), _ld(dZ, None), rows, cols, flags,
+                                ctypes.byref(e), *_ws(ws), _stream(stream)))
+
+
+def axonn_epi_workspace_size(rows: int, cols: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load().axonn_epi_workspace_size(rows, cols, ctypes.byref(n)))
+    return n.value
+
+
+def axonn_dropout(X, Y, p, rng, residual=None, stream=None):
+    """Y = residual + D(X), bf16 or fp32 (X's type); its backward is the same
+    call on the gradient."""
+    rows, cols = X.shape
+    kind = "float32" if str(X.dtype) == "torch.float32" else "bfloat16"
+    _typed("X", X, kind)
+    _typed("Y", Y, kind, (rows, cols))
+    _typed("residual", residual, kind, (rows, cols))
+    _rng(rng)
+    _check(load().axonn_dropout(_ptr(X), _ld(X, None), _ptr(residual), _ld(residual, None), _ptr(Y),
+                                _ld(Y, None), rows, cols, p, _ptr(rng),
+                                IN_F32 if kind == "float32" else 0, _stream(stream)))
+
+
+def axonn_linear_ce(X, W, labels, token_loss, loss, kept, ws, keep=None, lse=None, dX=None, dW=None,
+                    grad_scale=1.0, flags: int = 0, stream=None):
+    """Softmax cross-entropy of the logits X . W (W [K x V], or [V x K] with
+    B_T) for int32 labels [T], and its gradients dX (bf16) and dW (bf16;
+    fp32 with OUT_F32, added into with ACCUM_F32) where given; the logits are
+    never written out.  ``ws``: axonn_linear_ce_workspace_size bytes, or less
+    (smaller pieces of the vocabulary)."""
+    T, K = X.shape
+    V = W.shape[0 if flags & B_T else 1]
+    _typed("X", X, "bfloat16")
+    _typed("W", W, "bfloat16", (V, K) if flags & B_T else (K, V))
+    _vector("labels", labels, "int32", T)
+    _vector("keep", keep, "uint8", T)
+    _vector("token_loss", token_loss, "float32", T)
+    _vector("lse", lse, "float32", T)
+    _vector("loss", loss, "float32", 1)
+    _vector("kept", kept, "int32", 1)
+    _typed("dX", dX, "bfloat16", (T, K))
+    _typed("dW", dW, "float32" if flags & (OUT_F32 | ACCUM_F32) else "bfloat16", tuple(W.shape))
+    _check(load().axonn_linear_ce(_ptr(X), _ld(X, None), _ptr(W), _ld(W, None), _ptr(labels), _ptr(keep),
+                                  T, K, V, grad_scale, flags, _ptr(token_loss), _ptr(lse), _ptr(loss),
+                                  _ptr(kept), _ptr(dX), _ld(dX, None), _ptr(dW), _ld(dW, None),
+                                  *_ws(ws), _stream(stream)))
+
+
+def axonn_linear_ce_workspace_size(T: int, K: int, V: int, flags: int = 0, grad: bool = True,
+                                   piece: int = 0) -> int:
+    """Workspace bytes for pieces of ``piece`` vocabulary columns (0: pieces
+    of at most 2 GiB)."""
+    n = ctypes.c_size_t(0)
+    _check(load().axonn_linear_ce_workspace_size(T, K, V, flags, int(grad), piece, ctypes.byref(n)))
+    return n.value
 
 
 def axonn_fc_tune(op, P, Q, C, shape: Shape, flags: int = 0, ws=None, ldp=None, ldq=None,

@@ -20,9 +20,12 @@
 #include <vector>
 
 #include "axonn_fc.h"
+#include "elementwise.h"
+#include "epilogue.h"
 #include "gemm_kernel.cuh"
 #include "goldfish.h"
 #include "kernel_launch.h"
+#include "linear_ce.h"
 
 namespace {
 
@@ -122,6 +125,9 @@ axonn_status_t device_state(DeviceState** out) {
     for (cudaError_t x : es)
       if (x != cudaSuccess)
         return fail(AXONN_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(x));
+    for (cudaError_t x : {axonn::fused_init(), axonn::ce_init()})
+      if (x != cudaSuccess)
+        return fail(AXONN_ERR_CUDA, "fused kernel attributes: %s", cudaGetErrorString(x));
     if (!split_ok)
       return fail(AXONN_ERR_UNSUPPORTED,
                   "a 12-warp GEMM kernel was not built with %d registers per thread",
@@ -1025,6 +1031,349 @@ axonn_status_t static_scratch_addr(void** out) {
   return AXONN_OK;
 }
 
+// ------------------------------------------------------------------ fused
+// Products with a fused epilogue, the elementwise kernels beside them, and
+// the linear cross entropy.
+
+axonn_status_t check_p(float p) {
+  if (!(p >= 0.0f && p <= 1.0f)) return fail(AXONN_ERR_INVALID_ARG, "dropout probability not in [0, 1]");
+  return AXONN_OK;
+}
+
+// D(x)'s threshold and scale (see axonn_dropout in the header).
+axonn_status_t dropout_args(float p, const uint64_t* rng, axonn::DropoutArgs* d) {
+  const axonn_status_t st = check_p(p);
+  if (st != AXONN_OK) return st;
+  d->rng = rng;
+  d->thr = static_cast<uint32_t>(static_cast<double>(p) * 65536.0 + 0.5);
+  d->scale = d->thr < 65536 ? static_cast<float>(65536.0 / (65536.0 - d->thr)) : 0.0f;
+  if (d->thr == 0) return AXONN_OK;
+  if (!rng) return fail(AXONN_ERR_INVALID_ARG, "dropout needs rng (seed and offset on the device)");
+  if ((reinterpret_cast<uintptr_t>(rng) & 7u) != 0)
+    return fail(AXONN_ERR_ALIGNMENT, "rng is not 8-byte aligned");
+  return AXONN_OK;
+}
+
+// A [rows x cols] matrix of bf16 or fp32 in the library's alignment.
+axonn_status_t check_matrix(const char* name, const void* p, int64_t ld, int64_t rows, int64_t cols, bool f32) {
+  if (rows == 0 || cols == 0) return AXONN_OK;
+  if (!p) return fail(AXONN_ERR_INVALID_ARG, "%s is NULL", name);
+  if (ld < cols)
+    return fail(AXONN_ERR_INVALID_ARG, "%s: leading dimension %lld < row length %lld", name, (long long)ld,
+                (long long)cols);
+  if (!aligned16(p)) return fail(AXONN_ERR_ALIGNMENT, "%s is not 16-byte aligned", name);
+  if (ld % (f32 ? 4 : 8) != 0)
+    return fail(AXONN_ERR_ALIGNMENT, "%s: leading dimension %lld misaligned", name, (long long)ld);
+  if (ld * 4 >= (int64_t{1} << 40)) return fail(AXONN_ERR_UNSUPPORTED, "%s: stride too large", name);
+  return AXONN_OK;
+}
+
+axonn_status_t check_rows_cols(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0) return fail(AXONN_ERR_INVALID_ARG, "negative extent");
+  const int64_t lim = (int64_t{1} << 31) - 256;
+  if (rows > lim || cols > lim) return fail(AXONN_ERR_UNSUPPORTED, "extent above 2^31");
+  return AXONN_OK;
+}
+
+axonn_status_t check_act(int32_t act) {
+  if (act < AXONN_ACT_NONE || act > AXONN_ACT_SILU)
+    return fail(AXONN_ERR_INVALID_ARG, "activation %d not in [0, %d]", act, AXONN_ACT_SILU);
+  return AXONN_OK;
+}
+
+// Partial column sums: one row of them per 32 rows of the matrix.
+size_t epi_ws_bytes(int64_t rows, int64_t cols) {
+  return static_cast<size_t>((rows + 31) / 32) * static_cast<size_t>((cols + 7) / 8 * 8) * 4u;
+}
+
+axonn_status_t check_colsum_ws(const void* ws, size_t ws_bytes, int64_t rows, int64_t cols) {
+  const size_t need = epi_ws_bytes(rows, cols);
+  if (need == 0) return AXONN_OK;
+  if (!ws || ws_bytes < need)
+    return fail(AXONN_ERR_WORKSPACE, "the bias gradient needs %zu workspace bytes, got %zu", need,
+                ws ? ws_bytes : size_t{0});
+  if (!aligned16(ws)) return fail(AXONN_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+  return AXONN_OK;
+}
+
+// The tile of a fused product: the one whose waves over the GPU cost least,
+// area over throughput relative to the pair's 256 x 256.
+constexpr double kFusedSpeed[axonn::kFusedConfigs] = {1.0, 0.70, 0.40};
+constexpr int kFusedPlain[axonn::kFusedConfigs] = {2, 0, 7};  // the plain products' configuration of that tile
+int choose_fused(int64_t M, int64_t N, const DeviceState& dev) {
+  const int forced = g_forced_config.load();
+  for (int i = 0; i < axonn::kFusedConfigs; ++i)
+    if (forced == kFusedPlain[i]) return i;
+  int best = 0;
+  double cost = 0;
+  for (int i = 0; i < axonn::kFusedConfigs; ++i) {
+    const axonn::FusedConfig& c = axonn::kFusedConfig[i];
+    const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+    const int64_t slots = c.pair ? dev.max_pairs : dev.sms;
+    const double x = static_cast<double>((tiles + slots - 1) / slots) * c.bm * c.bn /
+                     (kFusedSpeed[i] * (c.pair ? 2 : 1));
+    if (i == 0 || x < cost) {
+      best = i;
+      cost = x;
+    }
+  }
+  return best;
+}
+
+// Everything of a fused product but its epilogue's arguments: tensor maps,
+// extents, tile counts.  *units: persistent CTAs (or CTA pairs) to launch.
+template <class Args>
+axonn_status_t fused_fill(axonn::FusedParams<Args>& P, const OpView& v, int config, int group_m,
+                          const DeviceState& dev, int* units) {
+  memset(&P, 0, sizeof(P));
+  const axonn::FusedConfig& c = axonn::kFusedConfig[config];
+  P.M = static_cast<int32_t>(v.M);
+  P.N = static_cast<int32_t>(v.N);
+  const int64_t tm = (v.M + c.bm - 1) / c.bm, tn = (v.N + c.bn - 1) / c.bn;
+  if (tm * tn > (int64_t{1} << 30)) return fail(AXONN_ERR_UNSUPPORTED, "more than 2^30 output tiles");
+  P.tiles_m = static_cast<int32_t>(tm);
+  P.tiles_n = static_cast<int32_t>(tn);
+  P.num_k = static_cast<int32_t>((v.R + axonn::kBK - 1) / axonn::kBK);
+  P.a_mn = v.a_mn;
+  P.b_mn = v.b_mn;
+  P.a_3d = v.a_mn && v.M % 64 == 0;
+  P.b_3d = v.b_mn && v.N % 64 == 0;
+  P.idesc = make_idesc(c.mma_m, c.bn, v.a_mn, v.b_mn);
+  const uint32_t b_cols = static_cast<uint32_t>(c.pair ? c.bn / 2 : c.bn);
+  if (P.num_k > 0) {
+    axonn_status_t s;
+    if (P.a_3d) s = encode_mn_3d(&P.ta, v.A, v.M, v.R, v.lda, axonn::kBK, 2);
+    else if (v.a_mn) s = encode_2d(&P.ta, v.A, v.M, v.R, v.lda, 64, axonn::kBK);
+    else s = encode_2d(&P.ta, v.A, v.R, v.M, v.lda, axonn::kBK, 128);
+    if (s != AXONN_OK) return s;
+    if (P.b_3d) s = encode_mn_3d(&P.tb, v.B, v.N, v.R, v.ldb, axonn::kBK, b_cols / 64);
+    else if (v.b_mn) s = encode_2d(&P.tb, v.B, v.N, v.R, v.ldb, 64, axonn::kBK);
+    else s = encode_2d(&P.tb, v.B, v.R, v.N, v.ldb, axonn::kBK, b_cols);
+    if (s != AXONN_OK) return s;
+  }
+  P.group_m = group_m;
+  const int64_t budget = g_l2_budget.load();
+  if (budget > 0) {
+    const bool rows = group_m > 0;
+    const int64_t g = std::min<int64_t>(rows ? group_m : -group_m, rows ? tm : tn);
+    const int64_t panel = g * (rows ? c.bm : c.bn) * std::max<int64_t>(v.R, 1) * 2;
+    P.l2_keep = rows ? 1 : 2;
+    P.l2_keep_frac =
+        panel <= budget ? 1.0f : std::max(1.0f / 64.0f, static_cast<float>(budget) / panel);
+  }
+  P.inject = g_inject.load();
+  P.timeout_ns = g_timeout_ns.load();
+  *units = static_cast<int>(std::min<int64_t>(tm * tn, c.pair ? dev.max_pairs : dev.sms));
+  t_last_config = kFusedPlain[config];
+  return AXONN_OK;
+}
+
+// Operand view of a whole-layer product (see fc_op).
+OpView layer_view(int op, const void* P, int64_t ldp, const void* Q, int64_t ldq,
+                  const axonn_fc_shape_t& s, uint32_t flags) {
+  OpView v{};
+  v.A = static_cast<const char*>(P);
+  v.lda = ldp;
+  v.B = static_cast<const char*>(Q);
+  v.ldb = ldq;
+  full_dims(op, s, &v.M, &v.N, &v.R);
+  const bool a_t = (flags & AXONN_A_T) != 0, b_t = (flags & AXONN_B_T) != 0;
+  v.a_mn = op == AXONN_OP_WGRAD ? !a_t : a_t;
+  v.b_mn = op == AXONN_OP_DGRAD ? b_t : !b_t;
+  return v;
+}
+
+axonn_status_t check_operands(const OpView& v, const char* an, const char* bn) {
+  axonn_status_t st = v.a_mn ? check_operand(an, v.A, v.lda, v.R, v.M) : check_operand(an, v.A, v.lda, v.M, v.R);
+  if (st != AXONN_OK) return st;
+  return v.b_mn ? check_operand(bn, v.B, v.ldb, v.R, v.N) : check_operand(bn, v.B, v.ldb, v.N, v.R);
+}
+
+// Shared body of the two products with an epilogue.
+axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t ldp, int64_t ldq, int64_t ldc,
+                        const axonn_fc_shape_t* shape, uint32_t flags, const axonn_epilogue_t* epi,
+                        void* ws, size_t ws_bytes, cudaStream_t stream) {
+  const bool fwd = op == AXONN_OP_FWD;
+  const uint32_t known = AXONN_A_T | AXONN_B_T | AXONN_OUT_F32 | (fwd ? AXONN_BIAS_F32 : 0u);
+  if (flags & ~known) return fail(AXONN_ERR_INVALID_ARG, "flag bits 0x%x do not apply here", flags & ~known);
+  axonn_status_t st = check_shape(op, shape, flags & ~AXONN_BIAS_F32);
+  if (st != AXONN_OK) return st;
+  if (shape->gx * shape->gy * shape->gz != 1)
+    return fail(AXONN_ERR_UNSUPPORTED, "an epilogue needs the whole product: grid 1x1x1, not %dx%dx%d",
+                shape->gx, shape->gy, shape->gz);
+  if (!epi) return fail(AXONN_ERR_INVALID_ARG, "epilogue is NULL");
+  st = check_act(epi->act);
+  if (st != AXONN_OK) return st;
+  if (fwd && epi->dbias) return fail(AXONN_ERR_INVALID_ARG, "dbias belongs to the backward");
+  if (!fwd && epi->bias) return fail(AXONN_ERR_INVALID_ARG, "bias belongs to the forward");
+  const OpView v = layer_view(op, P, ldp, Q, ldq, *shape, flags);
+  st = check_operands(v, fwd ? "X" : "dY", "W");
+  if (st != AXONN_OK) return st;
+  const bool f32 = (flags & AXONN_OUT_F32) != 0;
+  st = check_matrix("output", C, ldc, v.M, v.N, f32);
+  if (st != AXONN_OK) return st;
+  axonn::EpilogueArgs e{};
+  e.out = C;
+  e.ld_out = ldc;
+  e.out_f32 = f32;
+  e.act = epi->act;
+  st = dropout_args(epi->p, epi->rng, &e.drop);
+  if (st != AXONN_OK) return st;
+  if (epi->bias) {
+    if (!aligned16(epi->bias)) return fail(AXONN_ERR_ALIGNMENT, "bias is not 16-byte aligned");
+    e.bias = epi->bias;
+    e.bias_f32 = (flags & AXONN_BIAS_F32) != 0;
+  }
+  const bool needs_pre = !fwd && epi->act != AXONN_ACT_NONE;
+  if (epi->pre || needs_pre) {
+    st = check_matrix("pre", epi->pre, epi->ld_pre, v.M, v.N, false);
+    if (st != AXONN_OK) return st;
+  }
+  if (fwd) e.pre_out = static_cast<uint16_t*>(epi->pre);
+  else e.pre_in = static_cast<const uint16_t*>(epi->pre);
+  e.ld_pre = epi->ld_pre;
+  if (epi->residual) {
+    st = check_matrix("residual", epi->residual, epi->ld_residual, v.M, v.N, f32);
+    if (st != AXONN_OK) return st;
+    e.residual = epi->residual;
+    e.ld_res = epi->ld_residual;
+  }
+  if (epi->dbias) {
+    if (!aligned16(epi->dbias)) return fail(AXONN_ERR_ALIGNMENT, "dbias is not 16-byte aligned");
+    st = check_colsum_ws(ws, ws_bytes, v.M, v.N);
+    if (st != AXONN_OK) return st;
+    e.colsum = static_cast<float*>(ws);
+    e.ld_colsum = (v.N + 7) / 8 * 8;
+  }
+  if (v.N == 0 || (v.M == 0 && !epi->dbias)) return ok();
+  DeviceState* dev = nullptr;
+  st = device_state(&dev);
+  if (st != AXONN_OK) return st;
+  if (v.M > 0) {
+    axonn::FusedParams<axonn::EpilogueArgs> fp;
+    int units = 0;
+    const int config = choose_fused(v.M, v.N, *dev);
+    st = fused_fill(fp, v, config, 16, *dev, &units);
+    if (st != AXONN_OK) return st;
+    fp.epi = e;
+    const cudaError_t ce = axonn::fused_launch(fwd ? axonn::kFusedFwd : axonn::kFusedBwd, config, fp, units,
+                                               g_pdl.load() != 0, stream);
+    if (ce != cudaSuccess) return fail(AXONN_ERR_CUDA, "fused product: %s", cudaGetErrorString(ce));
+  }
+  if (epi->dbias) {
+    const cudaError_t ce =
+        axonn::colsum_launch(e.colsum, e.ld_colsum, (v.M + 31) / 32, v.N, epi->dbias, stream);
+    if (ce != cudaSuccess) return fail(AXONN_ERR_CUDA, "bias gradient: %s", cudaGetErrorString(ce));
+  }
+  return ok();
+}
+
+// ------------------------------------------------------------------ linear CE
+// The workspace, carved in order.  The statistics hold a group of 64 columns
+// at most (the narrowest epilogue warp), so that their size does not depend
+// on the tile chosen.
+constexpr int64_t kCePieceStep = 256;               // columns: whole tiles of every configuration
+constexpr size_t kCePieceDefault = size_t{2} << 30;  // bytes of one piece of the vocabulary
+struct CeLayout {
+  size_t index, labels, coef, label_logit, lse2, stats, x, dx32, piece;
+  int64_t ld_x, ld_dx;
+};
+size_t up256(size_t n) { return (n + 255) & ~size_t{255}; }
+
+CeLayout ce_layout(int64_t T, int64_t K, int64_t V) {
+  CeLayout l{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at += up256(bytes);
+    return r;
+  };
+  const size_t t = static_cast<size_t>(T);
+  l.index = take(4 * t);
+  l.labels = take(4 * t);
+  l.coef = take(4);
+  l.label_logit = take(4 * t);
+  l.lse2 = take(4 * t);
+  l.stats = take(8 * t * static_cast<size_t>((V + 63) / 64));
+  l.ld_x = (K + 7) / 8 * 8;
+  l.x = take(2 * t * static_cast<size_t>(l.ld_x));
+  l.ld_dx = l.ld_x;
+  l.dx32 = l.piece = at;
+  return l;
+}
+
+// Bytes beyond the fixed part for pieces of `cols` columns: the piece, and
+// where there are several of them dX's fp32 sum.
+size_t ce_piece_bytes(int64_t T, int64_t K, int64_t V, int64_t cols) {
+  const int64_t c = std::min(cols, (V + 7) / 8 * 8);
+  size_t b = up256(2 * static_cast<size_t>(T) * static_cast<size_t>(c));
+  if (cols < V) b += up256(4 * static_cast<size_t>(T) * static_cast<size_t>((K + 7) / 8 * 8));
+  return b;
+}
+
+// Columns of one piece that fit `bytes`: the whole vocabulary, else the most
+// whole tiles (0: not even one).
+int64_t ce_piece_cols(int64_t T, int64_t K, int64_t V, size_t bytes) {
+  if (ce_piece_bytes(T, K, V, V) <= bytes) return V;
+  int64_t lo = 0, hi = V / kCePieceStep;  // in steps; lo fits
+  while (lo < hi) {
+    const int64_t mid = (lo + hi + 1) / 2;
+    if (ce_piece_bytes(T, K, V, mid * kCePieceStep) <= bytes) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo * kCePieceStep;
+}
+
+int64_t ce_default_cols(int64_t T, int64_t V) {
+  const size_t row = 2 * static_cast<size_t>(std::max<int64_t>(T, 1));
+  if (row * static_cast<size_t>((V + 7) / 8 * 8) <= kCePieceDefault) return V;
+  // equal pieces, each within the default
+  const int64_t most = std::max<int64_t>(kCePieceStep, static_cast<int64_t>(kCePieceDefault / row) / kCePieceStep * kCePieceStep);
+  const int64_t n = (V + most - 1) / most;
+  return std::min(most, ((V + n - 1) / n + kCePieceStep - 1) / kCePieceStep * kCePieceStep);
+}
+
+axonn_status_t check_ce(int64_t T, int64_t K, int64_t V, uint32_t flags) {
+  if (flags & ~(AXONN_B_T | AXONN_OUT_F32 | AXONN_ACCUM_F32))
+    return fail(AXONN_ERR_INVALID_ARG, "flag bits 0x%x do not apply here",
+                flags & ~(AXONN_B_T | AXONN_OUT_F32 | AXONN_ACCUM_F32));
+  if ((flags & AXONN_ACCUM_F32) && (flags & AXONN_OUT_F32))
+    return fail(AXONN_ERR_INVALID_ARG, "AXONN_ACCUM_F32 and AXONN_OUT_F32 are exclusive");
+  axonn_status_t st = check_rows_cols(T, K);
+  if (st == AXONN_OK) st = check_rows_cols(T, V);
+  if (st != AXONN_OK) return st;
+  if (V < 1) return fail(AXONN_ERR_INVALID_ARG, "vocabulary size %lld", (long long)V);
+  return AXONN_OK;
+}
+
+#define AXONN_CE_RUN(call, what)                                                        \
+  do {                                                                                  \
+    const cudaError_t ce_ = (call);                                                     \
+    if (ce_ != cudaSuccess) return fail(AXONN_ERR_CUDA, what ": %s", cudaGetErrorString(ce_)); \
+  } while (0)
+
+// A product whose tiles are stored as they are, on the fused kernels (whose
+// extent may be the device's count).
+axonn_status_t store_product(const OpView& v, void* out, int64_t ld_out, int mode, const float* scale,
+                             const int32_t* row_map, const int32_t* count, int count_of, int group_m, const DeviceState& dev,
+                             cudaStream_t stream) {
+  if (v.M == 0 || v.N == 0) return AXONN_OK;
+  axonn::FusedParams<axonn::StoreArgs> p;
+  int units = 0;
+  const int config = choose_fused(v.M, v.N, dev);
+  const axonn_status_t st = fused_fill(p, v, config, group_m, dev, &units);
+  if (st != AXONN_OK) return st;
+  p.count = count;
+  p.count_of = count_of;
+  p.epi.out = out;
+  p.epi.ld_out = ld_out;
+  p.epi.row_map = row_map;
+  p.epi.scale = scale;
+  p.epi.mode = mode;
+  AXONN_CE_RUN(axonn::store_launch(config, p, units, g_pdl.load() != 0, stream), "product");
+  return AXONN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1652,6 +2001,284 @@ axonn_status_t axonn_goldfish_ce(const void* logits, int64_t ld_logits, const in
   return ok();
 }
 
+axonn_status_t axonn_fc_fwd_epi(const void* X, const void* W, void* Y, int64_t ldx, int64_t ldw, int64_t ldy,
+                                const axonn_fc_shape_t* shape, uint32_t flags, const axonn_epilogue_t* epi,
+                                cudaStream_t stream) {
+  return fused_op(AXONN_OP_FWD, X, W, Y, ldx, ldw, ldy, shape, flags, epi, nullptr, 0, stream);
+}
+
+axonn_status_t axonn_fc_dgrad_epi(const void* dY, const void* W, void* dX, int64_t lddy, int64_t ldw,
+                                  int64_t lddx, const axonn_fc_shape_t* shape, uint32_t flags,
+                                  const axonn_epilogue_t* epi, void* ws, size_t ws_bytes,
+                                  cudaStream_t stream) {
+  return fused_op(AXONN_OP_DGRAD, dY, W, dX, lddy, ldw, lddx, shape, flags, epi, ws, ws_bytes, stream);
+}
+
+axonn_status_t axonn_epi_workspace_size(int64_t rows, int64_t cols, size_t* bytes) {
+  if (!bytes) return fail(AXONN_ERR_INVALID_ARG, "bytes is NULL");
+  const axonn_status_t st = check_rows_cols(rows, cols);
+  if (st != AXONN_OK) return st;
+  *bytes = epi_ws_bytes(rows, cols);
+  return ok();
+}
+
+axonn_status_t axonn_epi_bwd(const void* dY, int64_t lddy, void* dZ, int64_t lddz, int64_t rows, int64_t cols,
+                             uint32_t flags, const axonn_epilogue_t* epi, void* ws, size_t ws_bytes,
+                             cudaStream_t stream) {
+  if (flags & ~AXONN_IN_F32)
+    return fail(AXONN_ERR_INVALID_ARG, "flag bits 0x%x do not apply here", flags & ~AXONN_IN_F32);
+  axonn_status_t st = check_rows_cols(rows, cols);
+  if (st != AXONN_OK) return st;
+  if (!epi) return fail(AXONN_ERR_INVALID_ARG, "epilogue is NULL");
+  st = check_act(epi->act);
+  if (st != AXONN_OK) return st;
+  if (epi->bias || epi->residual)
+    return fail(AXONN_ERR_INVALID_ARG, "bias and residual do not enter the elementwise backward");
+  const bool f32 = (flags & AXONN_IN_F32) != 0;
+  st = check_matrix("dY", dY, lddy, rows, cols, f32);
+  if (st == AXONN_OK) st = check_matrix("dZ", dZ, lddz, rows, cols, false);
+  if (st == AXONN_OK && epi->act != AXONN_ACT_NONE)
+    st = check_matrix("pre", epi->pre, epi->ld_pre, rows, cols, false);
+  if (st != AXONN_OK) return st;
+  axonn::BwdKernelArgs a{};
+  a.dy = dY;
+  a.ld_dy = lddy;
+  a.dz = static_cast<uint16_t*>(dZ);
+  a.ld_dz = lddz;
+  a.pre = static_cast<const uint16_t*>(epi->pre);
+  a.ld_pre = epi->ld_pre;
+  a.rows = rows;
+  a.cols = cols;
+  a.act = epi->act;
+  st = dropout_args(epi->p, epi->rng, &a.drop);
+  if (st != AXONN_OK) return st;
+  if (epi->dbias) {
+    if (!aligned16(epi->dbias)) return fail(AXONN_ERR_ALIGNMENT, "dbias is not 16-byte aligned");
+    st = check_colsum_ws(ws, ws_bytes, rows, cols);
+    if (st != AXONN_OK) return st;
+    a.colsum = static_cast<float*>(ws);
+    a.ld_colsum = (cols + 7) / 8 * 8;
+  }
+  if (cols == 0 || (rows == 0 && !epi->dbias)) return ok();
+  DeviceState* dev = nullptr;
+  st = device_state(&dev);
+  if (st != AXONN_OK) return st;
+  cudaError_t e = axonn::act_bwd_launch(a, f32, stream);
+  if (e == cudaSuccess && epi->dbias)
+    e = axonn::colsum_launch(a.colsum, a.ld_colsum, axonn::act_bwd_groups(rows), cols, epi->dbias, stream);
+  if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "elementwise backward: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+axonn_status_t axonn_dropout(const void* X, int64_t ldx, const void* residual, int64_t ld_residual, void* Y,
+                             int64_t ldy, int64_t rows, int64_t cols, float p, const uint64_t* rng,
+                             uint32_t flags, cudaStream_t stream) {
+  if (flags & ~AXONN_IN_F32)
+    return fail(AXONN_ERR_INVALID_ARG, "flag bits 0x%x do not apply here", flags & ~AXONN_IN_F32);
+  axonn_status_t st = check_rows_cols(rows, cols);
+  if (st != AXONN_OK) return st;
+  const bool f32 = (flags & AXONN_IN_F32) != 0;
+  axonn::DropoutKernelArgs a{};
+  st = dropout_args(p, rng, &a.drop);
+  if (st == AXONN_OK) st = check_matrix("X", X, ldx, rows, cols, f32);
+  if (st == AXONN_OK) st = check_matrix("Y", Y, ldy, rows, cols, f32);
+  if (st == AXONN_OK && residual) st = check_matrix("residual", residual, ld_residual, rows, cols, f32);
+  if (st != AXONN_OK) return st;
+  if (rows == 0 || cols == 0) return ok();
+  DeviceState* dev = nullptr;
+  st = device_state(&dev);
+  if (st != AXONN_OK) return st;
+  a.x = X;
+  a.residual = residual;
+  a.y = Y;
+  a.ld_x = ldx;
+  a.ld_res = ld_residual;
+  a.ld_y = ldy;
+  a.rows = rows;
+  a.cols = cols;
+  const cudaError_t e = axonn::dropout_launch(a, f32, dev->sms, stream);
+  if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "dropout: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, uint32_t flags, int grad,
+                                              int64_t piece, size_t* bytes) {
+  if (!bytes) return fail(AXONN_ERR_INVALID_ARG, "bytes is NULL");
+  const axonn_status_t st = check_ce(T, K, V, flags);
+  if (st != AXONN_OK) return st;
+  if (piece < 0) return fail(AXONN_ERR_INVALID_ARG, "piece of %lld columns", (long long)piece);
+  size_t b = ce_layout(T, K, V).piece;
+  if (grad) {
+    int64_t cols = piece == 0 ? ce_default_cols(T, V) : piece;
+    if (cols < V) cols = (cols + kCePieceStep - 1) / kCePieceStep * kCePieceStep;
+    b += ce_piece_bytes(T, K, V, std::min(cols, V));
+  }
+  *bytes = b;
+  return ok();
+}
+
+axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_t ldw, const int32_t* labels,
+                               const uint8_t* keep, int64_t T, int64_t K, int64_t V, float grad_scale,
+                               uint32_t flags, float* token_loss, float* lse, float* loss, int32_t* kept,
+                               void* dX, int64_t lddx, void* dW, int64_t lddw, void* ws, size_t ws_bytes,
+                               cudaStream_t stream) {
+  axonn_status_t st = check_ce(T, K, V, flags);
+  if (st != AXONN_OK) return st;
+  const bool w_t = (flags & AXONN_B_T) != 0;
+  const bool w_f32 = (flags & (AXONN_OUT_F32 | AXONN_ACCUM_F32)) != 0;
+  const bool grad = dX != nullptr || dW != nullptr;
+  if (!loss || !kept) return fail(AXONN_ERR_INVALID_ARG, "loss or kept is NULL");
+  if (T > 0 && (!labels || !token_loss)) return fail(AXONN_ERR_INVALID_ARG, "labels or token_loss is NULL");
+  st = check_operand("X", X, ldx, T, K);
+  if (st == AXONN_OK) st = w_t ? check_operand("W", W, ldw, V, K) : check_operand("W", W, ldw, K, V);
+  if (st == AXONN_OK && dX) st = check_matrix("dX", dX, lddx, T, K, false);
+  if (st == AXONN_OK && dW) st = check_matrix("dW", dW, lddw, w_t ? V : K, w_t ? K : V, w_f32);
+  if (st != AXONN_OK) return st;
+  CeLayout l = ce_layout(T, K, V);
+  const size_t least = l.piece + (grad ? std::min(ce_piece_bytes(T, K, V, V),
+                                                  ce_piece_bytes(T, K, V, std::min(kCePieceStep, V)))
+                                       : 0);
+  if (!ws || ws_bytes < least)
+    return fail(AXONN_ERR_WORKSPACE, "linear cross entropy needs at least %zu workspace bytes, got %zu", least,
+                ws ? ws_bytes : size_t{0});
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(AXONN_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
+  // Loss alone: one product over the whole vocabulary, nothing kept.
+  const int64_t cols = grad ? ce_piece_cols(T, K, V, ws_bytes - l.piece) : V;
+  const int64_t pieces = (V + cols - 1) / cols;
+  if (pieces > 1) l.piece += up256(4 * static_cast<size_t>(T) * static_cast<size_t>(l.ld_dx));
+  DeviceState* dev = nullptr;
+  st = device_state(&dev);
+  if (st != AXONN_OK) return st;
+  char* base = static_cast<char*>(ws);
+  const int64_t ld_piece = (std::min(cols, V) + 7) / 8 * 8;
+  uint16_t* piece = reinterpret_cast<uint16_t*>(base + l.piece);
+  float* dx32 = reinterpret_cast<float*>(base + l.dx32);
+  const int config = choose_fused(T, std::min(cols, V), *dev);
+  const bool pdl = g_pdl.load() != 0;
+
+  axonn::CeRowArgs a{};
+  a.x = static_cast<const uint16_t*>(X);
+  a.ld_x = ldx;
+  a.labels = labels;
+  a.keep = keep;
+  a.rows = T;
+  a.cols = K;
+  a.vocab = V;
+  a.grad_scale = grad_scale;
+  a.index = reinterpret_cast<int32_t*>(base + l.index);
+  a.packed_labels = reinterpret_cast<int32_t*>(base + l.labels);
+  a.packed_x = reinterpret_cast<uint16_t*>(base + l.x);
+  a.ld_packed = l.ld_x;
+  a.coef = reinterpret_cast<float*>(base + l.coef);
+  a.stats = reinterpret_cast<const float2*>(base + l.stats);
+  a.group_cols = axonn::kFusedConfig[config].warp_cols;
+  a.groups = (V + a.group_cols - 1) / a.group_cols;
+  a.label_logit = reinterpret_cast<const float*>(base + l.label_logit);
+  a.lse2 = reinterpret_cast<float*>(base + l.lse2);
+  a.token_loss = token_loss;
+  a.lse = lse;
+  a.loss = loss;
+  a.kept = kept;
+  a.dx = static_cast<uint16_t*>(dX);
+  a.ld_dx = lddx;
+
+  AXONN_CE_RUN(axonn::ce_index_launch(a, stream), "packing");
+  AXONN_CE_RUN(axonn::ce_gather_launch(a, dev->sms, stream), "packing");
+
+  // X . W over columns [c0, c0 + n): the packed rows against a piece of W.
+  const char* Wb = static_cast<const char*>(W);
+  auto logits_view = [&](int64_t c0, int64_t n) {
+    OpView v{};
+    v.A = reinterpret_cast<const char*>(a.packed_x);
+    v.lda = l.ld_x;
+    v.a_mn = false;
+    v.B = Wb + 2 * (w_t ? c0 * ldw : c0);
+    v.ldb = ldw;
+    v.b_mn = !w_t;
+    v.M = T;
+    v.N = n;
+    v.R = K;
+    return v;
+  };
+  auto logits = [&](axonn::CeKind kind, int64_t c0, int64_t n, bool keep_piece) -> axonn_status_t {
+    if (T == 0) return AXONN_OK;
+    axonn::FusedParams<axonn::CeArgs> p;
+    int units = 0;
+    const axonn_status_t s = fused_fill(p, logits_view(c0, n), config, 16, *dev, &units);
+    if (s != AXONN_OK) return s;
+    p.count = kept;
+    p.count_of = 1;
+    p.epi.labels = a.packed_labels;
+    p.epi.rows = T;
+    p.epi.col0 = c0;
+    p.epi.stats = reinterpret_cast<float2*>(base + l.stats);
+    p.epi.ld_stats = T;
+    p.epi.label_logit = reinterpret_cast<float*>(base + l.label_logit);
+    p.epi.piece = keep_piece ? piece : nullptr;
+    p.epi.ld_piece = ld_piece;
+    p.epi.lse2 = a.lse2;
+    AXONN_CE_RUN(axonn::ce_launch(kind, config, p, units, pdl, stream), "logits product");
+    return AXONN_OK;
+  };
+  // Forward over the pieces; the last one stays.
+  for (int64_t i = 0; i < pieces; ++i) {
+    const int64_t c0 = i * cols, n = std::min(cols, V - c0);
+    st = logits(axonn::kCeStats, c0, n, grad && i == pieces - 1);
+    if (st != AXONN_OK) return st;
+  }
+  AXONN_CE_RUN(axonn::ce_combine_launch(a, stream), "logsumexp");
+  AXONN_CE_RUN(axonn::ce_mean_launch(a, stream), "mean");
+  if (!grad) return ok();
+
+  // Backward: the piece that is there first, then the others, recomputed.
+  for (int64_t j = 0; j < pieces; ++j) {
+    const int64_t i = j == 0 ? pieces - 1 : j - 1;
+    const int64_t c0 = i * cols, n = std::min(cols, V - c0);
+    if (j == 0) {
+      AXONN_CE_RUN(axonn::ce_scale_launch(a, piece, ld_piece, c0, n, stream), "probabilities");
+    } else {
+      st = logits(axonn::kCeProb, c0, n, true);
+      if (st != AXONN_OK) return st;
+    }
+    if (dX) {  // dX = P . W^T, rows scattered to their places
+      OpView v = logits_view(c0, n);
+      v.A = reinterpret_cast<const char*>(piece);
+      v.lda = ld_piece;
+      v.b_mn = w_t;
+      v.N = K;
+      v.R = n;
+      const bool one = pieces == 1;
+      st = store_product(v, one ? dX : static_cast<void*>(dx32), one ? lddx : l.ld_dx,
+                         one ? axonn::kOutBF16 : (j == 0 ? axonn::kOutF32 : axonn::kOutF32Accum),
+                         a.coef, one ? a.index : nullptr, kept, 1, 16, *dev, stream);
+      if (st != AXONN_OK) return st;
+    }
+    if (dW) {  // dW = X^T . P ([K x V]) or P^T . X ([V x K])
+      OpView x{};
+      x.R = T;
+      x.a_mn = x.b_mn = true;
+      const char* xp = reinterpret_cast<const char*>(a.packed_x);
+      const char* pp = reinterpret_cast<const char*>(piece);
+      x.A = w_t ? pp : xp;
+      x.lda = w_t ? ld_piece : l.ld_x;
+      x.M = w_t ? n : K;
+      x.B = w_t ? xp : pp;
+      x.ldb = w_t ? l.ld_x : ld_piece;
+      x.N = w_t ? K : n;
+      const int64_t off = w_t ? c0 * lddw : c0;
+      const int mode = (flags & AXONN_ACCUM_F32) ? axonn::kOutF32Accum
+                       : (flags & AXONN_OUT_F32) ? axonn::kOutF32
+                                                 : axonn::kOutBF16;
+      st = store_product(x, static_cast<char*>(dW) + off * (w_f32 ? 4 : 2), lddw, mode, a.coef, nullptr, kept, 2,
+                         16, *dev, stream);
+      if (st != AXONN_OK) return st;
+    }
+  }
+  if (dX && pieces > 1) AXONN_CE_RUN(axonn::ce_scatter_launch(a, dx32, l.ld_dx, dev->sms, stream), "dX");
+  return ok();
+}
+
 axonn_status_t axonn_fc_block_extents(int op, const axonn_fc_shape_t* shape, int64_t* rows,
                                       int64_t* red, int64_t* cols) {
   if (!rows || !red || !cols) return fail(AXONN_ERR_INVALID_ARG, "NULL output");
@@ -1671,13 +2298,16 @@ axonn_status_t axonn_sync_status(cudaStream_t stream, uint64_t* detail) {
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "stream: %s", cudaGetErrorString(e));
   // One error word per kernel translation unit; report the first set.
   unsigned long long word = 0, w1 = 0, w8 = 0, w64 = 0;
-  unsigned long long wg = 0;
+  unsigned long long wg = 0, we = 0, wc = 0;
   e = axonn::kernels_take_status<1>(&w1, stream);
   if (e == cudaSuccess) e = axonn::kernels_take_status<kFewProblems>(&w8, stream);
   if (e == cudaSuccess) e = axonn::kernels_take_status<kMaxProblems>(&w64, stream);
   if (e == cudaSuccess) e = axonn::goldfish_take_status(&wg, stream);
+  if (e == cudaSuccess) e = axonn::fused_take_status(&we, stream);
+  if (e == cudaSuccess) e = axonn::ce_take_status(&wc, stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
-  word = w1 ? w1 : (w8 ? w8 : (w64 ? w64 : wg));
+  for (unsigned long long w : {w1, w8, w64, wg, we, wc})
+    if (word == 0) word = w;
   if (word == 0) return ok();
   if (detail) *detail = word;
   return fail(AXONN_ERR_TIMEOUT, "device wait expired: CTA %llu, site %llu", (word >> 8) & 0xFFFFFFull,

@@ -1,0 +1,50 @@
+// Host interface of the linear cross entropy's row kernels (linear_ce.cu).
+#pragma once
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace axonn {
+
+// Only the rows whose label counts take part: they are packed, in order,
+// into the first n of `rows` places, and n stays on the device.
+struct CeRowArgs {
+  const uint16_t* x;      // bf16 [rows x cols], as the caller has it
+  int64_t ld_x;
+  const int32_t* labels;  // [rows]
+  const uint8_t* keep;    // or null: every label in range counts
+  int64_t rows, cols, vocab;
+  float grad_scale;
+  int32_t* index;         // [rows] packed place -> row
+  int32_t* packed_labels; // [rows]
+  uint16_t* packed_x;     // bf16 [rows x ld_packed]
+  int64_t ld_packed;
+  float* coef;            // [1] grad_scale / n
+  const float2* stats;    // [groups x rows]
+  int64_t groups;
+  int32_t group_cols;
+  const float* label_logit;  // [rows], packed
+  float* lse2;               // [rows], packed
+  float* token_loss;         // [rows]
+  float* lse;                // [rows] natural logsumexp of the counted rows (0 elsewhere), or null
+  float* loss;
+  int32_t* kept;
+  uint16_t* dx;              // rows that do not count are zeroed here, or null
+  int64_t ld_dx;
+};
+
+// n, the packing, and the zeros of the rows that do not count.
+cudaError_t ce_index_launch(const CeRowArgs& a, cudaStream_t stream);
+cudaError_t ce_gather_launch(const CeRowArgs& a, int sms, cudaStream_t stream);
+// Each packed row's logsumexp from its groups' statistics, and its loss.
+cudaError_t ce_combine_launch(const CeRowArgs& a, cudaStream_t stream);
+// The mean of the counted losses, in a fixed order.
+cudaError_t ce_mean_launch(const CeRowArgs& a, cudaStream_t stream);
+// The kept distances of columns [col0, col0 + cols) to P = softmax - onehot,
+// in place.
+cudaError_t ce_scale_launch(const CeRowArgs& a, uint16_t* piece, int64_t ld_piece, int64_t col0,
+                            int64_t cols, cudaStream_t stream);
+// Packed fp32 rows rounded to bf16 at their places in dx.
+cudaError_t ce_scatter_launch(const CeRowArgs& a, const float* packed, int64_t ld, int sms,
+                              cudaStream_t stream);
+
+}  // namespace axonn

@@ -1,0 +1,372 @@
+"""The products with an epilogue, the elementwise backward and dropout
+against their 64-bit forms.
+
+Bounds (derived, not fitted).  A product of bf16 operands accumulates in fp32
+over ceil(K/16) steps, each off by at most 2^-23 of the running sum, which
+never exceeds S = |A|.|B| (+ |b|): (K/16 + 2) 2^-23 S.  An activation or its
+slope changes by at most 1.13 times its argument's error and is itself
+computed to 2^-20 of its value plus 2^-21 (two SFU steps, or erfc); dropout
+scales both.  The output is rounded once: half an ulp, 2^-8 of its value in
+bf16 (8 significant bits) and 2^-24 in fp32, where one more bit is allowed for
+the sum with the residual.
+A column sum over T rows adds T 2^-24 of the sum of magnitudes.
+"""
+import numpy as np
+import pytest
+
+from oracle import epilogue as ep
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def free_choice(cuda_lib):
+    cuda_lib.axonn_set_kernel_config(-1)
+    yield
+    cuda_lib.axonn_set_kernel_config(-1)
+
+
+def dev(a, dtype, pad=8):
+    """fp64 values (already representable) -> a CUDA view with a row stride
+    that is a multiple of 8 and larger than the row."""
+    import torch
+    rows, cols = a.shape
+    ld = (cols + 7) // 8 * 8 + pad
+    full = torch.full((rows, ld), float("nan"), dtype=dtype, device="cuda")
+    full[:, :cols] = torch.from_numpy(a).to("cuda").to(dtype)
+    return full[:, :cols]
+
+
+def bf16(a):
+    """Rounded to the nearest bf16 value, as fp64."""
+    import torch
+    return torch.from_numpy(np.asarray(a, dtype=np.float32)).to(torch.bfloat16).to(torch.float64).numpy()
+
+
+def host(t):
+    import torch
+    return t.to(torch.float64).cpu().numpy()
+
+
+def words(seed=0x123456789ABCDEF0, offset=(7 << 32) + 11):
+    import torch
+    as_signed = [w - 2**64 if w >= 2**63 else w for w in (seed, offset)]
+    return torch.tensor(as_signed, dtype=torch.int64, device="cuda"), seed, offset
+
+
+def untouched(t):
+    """The row padding still holds what it held."""
+    import torch
+    full = t._base
+    return bool(torch.isnan(full[:, t.shape[1]:].float()).all())
+
+
+def inside(got, ref, bound, what):
+    assert np.isfinite(got).all(), what
+    worst = float((np.abs(got - ref) / bound).max()) if got.size else 0.0
+    assert worst <= 1.0, f"{what}: {worst:.3f} of the bound"
+
+
+def product_error(K, S):
+    return (K / 16 + 2) * 2.0**-23 * S
+
+
+SIZES = [(1, 64, 128), (1, 520, 72), (3, 8, 1), (31, 65, 33), (130, 200, 264), (257, 130, 521), (300, 72, 1000)]
+
+
+@pytest.mark.parametrize("config", [2, 0, 7])
+@pytest.mark.parametrize("n,size", list(enumerate(SIZES)))
+def test_forward(cuda_lib, n, size, config):
+    fc = cuda_lib
+    import torch
+    T, K, N = size
+    rng = np.random.default_rng(100 + n)
+    for k, act in enumerate(ep.ACTS):
+        f32, a_t, b_t = (n + k) % 3 == 0, (n + k) % 2 == 1, (n + k) % 4 >= 2
+        bias_kind = ("", "bf16", "f32")[(n + k + config) % 3]
+        p = (0.0, 0.3)[(n + k) % 2]
+        res, pre = (n + k) % 3 != 1, (n + k) % 2 == 0
+        X, W = bf16(rng.normal(size=(T, K))), bf16(rng.normal(size=(K, N)) * 0.2)
+        b = rng.normal(size=N).astype(np.float32).astype(np.float64)
+        b = bf16(b) if bias_kind == "bf16" else (b if bias_kind else np.zeros(N))
+        out = torch.float32 if f32 else torch.bfloat16
+        R = rng.normal(size=(T, N)).astype(np.float32).astype(np.float64)
+        R = R if f32 else bf16(R)
+        words_d, seed, offset = words()
+        fc.axonn_set_kernel_config(config)
+        Y = dev(np.zeros((T, N)), out)
+        Z = dev(np.zeros((T, N)), torch.bfloat16) if pre else None
+        bias = None
+        if bias_kind:
+            bias = torch.from_numpy(b).to("cuda").to(torch.bfloat16 if bias_kind == "bf16" else torch.float32)
+        flags = (fc.OUT_F32 if f32 else 0) | (fc.A_T if a_t else 0) | (fc.B_T if b_t else 0)
+        fc.axonn_fc_fwd_epi(dev(X.T if a_t else X, torch.bfloat16), dev(W.T if b_t else W, torch.bfloat16), Y,
+                            fc.Shape(T, K, N), flags, bias=bias, act=act, pre=Z,
+                            residual=dev(R, out) if res else None, p=p, rng=words_d if p else None)
+        fc.axonn_sync_status()
+        assert fc.axonn_last_kernel_config() == config
+        z = X @ W + b
+        S = np.abs(X) @ np.abs(W) + np.abs(b)
+        a = ep.act(z, act)
+        err = 1.13 * product_error(K, S) + 2.0**-20 * np.abs(a) + 2.0**-21
+        keep, scale = ep.keep_mask(T, N, p, seed, offset) if p else (np.ones((T, N), bool), 1.0)
+        ref = np.where(keep, a * scale, 0.0) + (R if res else 0.0)
+        bound = scale * err + (2.0**-23 if f32 else 2.0**-8) * np.abs(ref) + 1e-30
+        inside(host(Y), ref, bound, f"{act} {size} out")
+        assert untouched(Y)
+        if pre:
+            inside(host(Z), z, product_error(K, S) + 2.0**-8 * np.abs(z) + 1e-30, f"{act} {size} pre")
+            assert untouched(Z)
+
+
+@pytest.mark.parametrize("config", [2, 0, 7])
+@pytest.mark.parametrize("n,size", list(enumerate(SIZES)))
+def test_data_gradient(cuda_lib, n, size, config):
+    """dZ [T x N] of a following layer W [N x K]."""
+    fc = cuda_lib
+    import torch
+    T, K, N = size
+    rng = np.random.default_rng(200 + n)
+    for k, act in enumerate(ep.ACTS):
+        f32, a_t, b_t = (n + k) % 3 == 1, (n + k) % 2 == 0, (n + k) % 4 >= 2
+        p, res, db = (0.0, 0.4)[(n + k) % 2], (n + k) % 3 == 0, (n + k) % 4 != 3
+        G, W = bf16(rng.normal(size=(T, K))), bf16(rng.normal(size=(N, K)) * 0.2)
+        Z = bf16(rng.normal(size=(T, N)) * 2)
+        R = rng.normal(size=(T, N)).astype(np.float32).astype(np.float64)
+        R = R if f32 else bf16(R)
+        out = torch.float32 if f32 else torch.bfloat16
+        words_d, seed, offset = words()
+        fc.axonn_set_kernel_config(config)
+        dZ = dev(np.zeros((T, N)), out)
+        dbias = torch.full((N,), float("nan"), device="cuda") if db else None
+        ws = torch.full((fc.axonn_epi_workspace_size(T, N),), 255, dtype=torch.uint8, device="cuda")
+        flags = (fc.OUT_F32 if f32 else 0) | (fc.A_T if a_t else 0) | (fc.B_T if b_t else 0)
+        fc.axonn_fc_dgrad_epi(dev(G.T if a_t else G, torch.bfloat16), dev(W.T if b_t else W, torch.bfloat16),
+                              dZ, fc.Shape(T, N, K), flags, pre=dev(Z, torch.bfloat16), act=act,
+                              residual=dev(R, out) if res else None, dbias=dbias, p=p,
+                              rng=words_d if p else None, ws=ws)
+        fc.axonn_sync_status()
+        keep, scale = ep.keep_mask(T, N, p, seed, offset) if p else (np.ones((T, N), bool), 1.0)
+        g = np.where(keep, (G @ W.T) * scale, 0.0)
+        d = g * ep.slope(Z, act)
+        err = scale * 1.13 * product_error(K, np.abs(G) @ np.abs(W).T) + np.abs(g) * 2.0**-20 + 1e-30
+        ref = d + (R if res else 0.0)
+        inside(host(dZ), ref, err + (2.0**-23 if f32 else 2.0**-8) * np.abs(ref), f"{act} {size} dZ")
+        assert untouched(dZ)
+        if db:
+            inside(host(dbias), d.sum(0), err.sum(0) + T * 2.0**-24 * np.abs(d).sum(0), f"{act} {size} db")
+
+
+@pytest.mark.parametrize("size", [(1, 8), (3, 1), (64, 256), (65, 257), (200, 1003), (130, 2048)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_elementwise_backward(cuda_lib, size, f32):
+    fc = cuda_lib
+    import torch
+    T, N = size
+    rng = np.random.default_rng(7)
+    for k, act in enumerate(ep.ACTS):
+        p, db = (0.0, 0.25)[k % 2], k != 3
+        dY = rng.normal(size=(T, N)).astype(np.float32).astype(np.float64)
+        dY = dY if f32 else bf16(dY)
+        Z = bf16(rng.normal(size=(T, N)) * 2)
+        words_d, seed, offset = words()
+        dZ = dev(np.zeros((T, N)), torch.bfloat16)
+        dbias = torch.full((N,), float("nan"), device="cuda") if db else None
+        ws = torch.full((fc.axonn_epi_workspace_size(T, N),), 255, dtype=torch.uint8, device="cuda")
+        fc.axonn_epi_bwd(dev(dY, torch.float32 if f32 else torch.bfloat16), dZ,
+                         pre=None if act == "none" else dev(Z, torch.bfloat16), act=act, dbias=dbias, p=p,
+                         rng=words_d if p else None, ws=ws)
+        fc.axonn_sync_status()
+        g = ep.drop(dY, p, seed, offset)
+        d = g * ep.slope(Z, act)
+        err = np.abs(g) * 2.0**-20 + 1e-30
+        inside(host(dZ), d, err + 2.0**-8 * np.abs(d), f"{act} dZ")
+        assert untouched(dZ)
+        if db:
+            inside(host(dbias), d.sum(0), err.sum(0) + T * 2.0**-24 * np.abs(d).sum(0), f"{act} db")
+
+
+@pytest.mark.parametrize("size", [(1, 1), (1, 8), (5, 7), (64, 768), (33, 1003), (700, 520)])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("p", [0.0, 1e-6, 0.1, 0.5, 1.0])
+def test_dropout(cuda_lib, size, f32, p):
+    """The mask bit for bit, the values to one rounding."""
+    fc = cuda_lib
+    import torch
+    T, N = size
+    rng = np.random.default_rng(9)
+    kind = torch.float32 if f32 else torch.bfloat16
+    X, R = (rng.normal(size=(T, N)).astype(np.float32).astype(np.float64) for _ in range(2))
+    X, R = (X, R) if f32 else (bf16(X), bf16(R))
+    words_d, seed, offset = words()
+    for res in (False, True):
+        Y = dev(np.zeros((T, N)), kind)
+        fc.axonn_dropout(dev(X, kind), Y, p, words_d, residual=dev(R, kind) if res else None)
+        fc.axonn_sync_status()
+        ref = ep.drop(X, p, seed, offset) + (R if res else 0.0)
+        inside(host(Y), ref, (2.0**-22 if f32 else 2.0**-8) * (np.abs(ref) + np.abs(R) * f32) + 1e-30, "Y")
+        assert untouched(Y)
+        if not res:
+            keep, _ = ep.keep_mask(T, N, p, seed, offset)
+            assert np.array_equal(host(Y) != 0, keep & (X != 0))
+
+
+def test_dropout_in_an_epilogue_is_the_same_mask(cuda_lib):
+    """D alone, in the forward's and in the backward's epilogue."""
+    fc = cuda_lib
+    import torch
+    T, N = 200, 328
+    words_d, _, _ = words(seed=2**64 - 5, offset=2**63 + 3)
+    one = torch.ones((T, N), device="cuda", dtype=torch.bfloat16)
+    eye = torch.eye(N, device="cuda", dtype=torch.bfloat16)
+    outs = [torch.empty_like(one) for _ in range(4)]
+    fc.axonn_dropout(one, outs[0], 0.3, words_d)
+    fc.axonn_fc_fwd_epi(one, eye, outs[1], fc.Shape(T, N, N), p=0.3, rng=words_d)
+    fc.axonn_fc_dgrad_epi(one, eye, outs[2], fc.Shape(T, N, N), p=0.3, rng=words_d)
+    fc.axonn_epi_bwd(one, outs[3], p=0.3, rng=words_d)
+    fc.axonn_sync_status()
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+    assert 0.6 < float((outs[0] != 0).float().mean()) < 0.8
+
+
+def test_dropped_infinities_and_nan_vanish(cuda_lib):
+    fc = cuda_lib
+    import torch
+    T, N = 40, 72
+    words_d, seed, offset = words()
+    keep = torch.from_numpy(ep.keep_mask(T, N, 0.5, seed, offset)[0]).cuda()
+    X = torch.where(keep, 1.0, float("nan")).to(torch.bfloat16)
+    X[0] = torch.where(keep[0], 1.0, float("-inf")).to(torch.bfloat16)
+    Y = torch.empty_like(X)
+    fc.axonn_dropout(X, Y, 0.5, words_d)
+    dZ = torch.empty_like(X)
+    fc.axonn_epi_bwd(X, dZ, p=0.5, rng=words_d)
+    fc.axonn_sync_status()
+    want = torch.where(keep, 2.0, 0.0).to(torch.bfloat16)
+    assert torch.equal(Y, want) and torch.equal(dZ, want)
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_extreme_pre_activations(cuda_lib, act):
+    """Large, tiny and zero pre-activations: values and slopes are the limits
+    of the formulas; NaN stays NaN."""
+    fc = cuda_lib
+    import torch
+    z = np.array([0.0, -0.0, 1e-30, -1e-30, 30.0, -30.0, 1e4, -1e4, 3e38, -3e38])
+    Z = dev(bf16(z)[None, :], torch.bfloat16)
+    one = dev(np.ones((1, z.size)), torch.bfloat16)
+    dZ = dev(np.zeros((1, z.size)), torch.bfloat16)
+    fc.axonn_epi_bwd(one, dZ, pre=Z, act=act)
+    # K = 1: Z times one is Z itself
+    X, Y = dev(np.ones((1, 1)), torch.bfloat16), dev(np.zeros((1, z.size)), torch.float32)
+    fc.axonn_fc_fwd_epi(X, Z, Y, fc.Shape(1, 1, z.size), fc.OUT_F32, act=act)
+    fc.axonn_sync_status()
+    at0 = {"relu": 0.0}.get(act, 0.5)
+    want = np.array([at0, at0, 1.0 if act == "relu" else 0.5, at0, 1, 0, 1, 0, 1, 0])
+    assert np.abs(host(dZ)[0] - want).max() < 1e-6
+    big = np.where(z > 1, bf16(z), 0.0)
+    y = host(Y)[0]
+    assert np.all(np.abs(y[4:] - big[4:]) <= 1e-6 * np.abs(big[4:]) + 1e-6) and np.all(np.abs(y[:4]) < 1e-29)
+    N = dev(np.full((1, 8), np.nan), torch.bfloat16)
+    Yn = dev(np.zeros((1, 8)), torch.float32)
+    fc.axonn_fc_fwd_epi(X, N, Yn, fc.Shape(1, 1, 8), fc.OUT_F32, act=act)
+    fc.axonn_epi_bwd(one[:, :8], dZ[:, :8], pre=N, act=act)
+    fc.axonn_sync_status()
+    assert bool(torch.isnan(Yn).all()) and bool(torch.isnan(dZ[:, :8].float()).all())
+
+
+def test_in_place(cuda_lib):
+    """Y over R, dZ over Z, dropout over its input: as into other memory."""
+    fc = cuda_lib
+    import torch
+    T, K, N = 300, 136, 520
+    rng = np.random.default_rng(5)
+    X, W, R, Z = (bf16(rng.normal(size=s)) for s in ((T, K), (K, N), (T, N), (T, N)))
+    Xd, Wd = dev(X, torch.bfloat16), dev(W, torch.bfloat16)
+    words_d, _, _ = words()
+    other, same = dev(R, torch.bfloat16), dev(R, torch.bfloat16)
+    Y = dev(R * 0, torch.bfloat16)
+    kw = dict(act="silu", p=0.2, rng=words_d)
+    fc.axonn_fc_fwd_epi(Xd, Wd, Y, fc.Shape(T, K, N), residual=other, **kw)
+    fc.axonn_fc_fwd_epi(Xd, Wd, same, fc.Shape(T, K, N), residual=same, **kw)
+    Zd, D = dev(Z, torch.bfloat16), dev(R * 0, torch.bfloat16)
+    Wt = dev(W.T.copy(), torch.bfloat16)   # the next layer's weight [N x K]
+    fc.axonn_fc_dgrad_epi(Xd, Wt, D, fc.Shape(T, N, K), pre=Zd, **kw)
+    fc.axonn_fc_dgrad_epi(Xd, Wt, Zd, fc.Shape(T, N, K), pre=Zd, **kw)
+    A, B = dev(R, torch.bfloat16), dev(R * 0, torch.bfloat16)
+    fc.axonn_dropout(A, B, 0.2, words_d)
+    fc.axonn_dropout(A, A, 0.2, words_d)
+    fc.axonn_sync_status()
+    assert torch.equal(Y, same) and torch.equal(D, Zd) and torch.equal(A, B)
+
+
+def test_empty_and_zero_length(cuda_lib):
+    fc = cuda_lib
+    import torch
+    e = lambda r, c, t=torch.bfloat16: torch.full((r, c), 7.0, device="cuda", dtype=t)  # noqa: E731
+    # no rows: the bias gradient is the empty sum
+    db = torch.full((16,), float("nan"), device="cuda")
+    ws = torch.empty(16, dtype=torch.uint8, device="cuda")
+    fc.axonn_fc_dgrad_epi(e(0, 8), e(16, 8), e(0, 16), fc.Shape(0, 16, 8), dbias=db, ws=ws)
+    assert bool((db == 0).all())
+    db.fill_(float("nan"))
+    fc.axonn_epi_bwd(e(0, 16), e(0, 16), dbias=db, ws=ws)
+    assert bool((db == 0).all())
+    # an empty reduction: act(b), dropped and joined as ever
+    Y, R = e(5, 16), e(5, 16)
+    b = torch.linspace(-2, 2, 16, device="cuda")
+    fc.axonn_fc_fwd_epi(e(5, 0), e(0, 16), Y, fc.Shape(5, 0, 16), bias=b, act="relu", residual=R)
+    fc.axonn_sync_status()
+    want = (torch.relu(b) + 7.0).to(torch.bfloat16).expand(5, 16)
+    assert torch.equal(Y, want)
+    # no columns, no rows: nothing happens
+    fc.axonn_fc_fwd_epi(e(5, 8), e(8, 0), e(5, 0), fc.Shape(5, 8, 0))
+    fc.axonn_dropout(e(0, 8), e(0, 8), 0.5, words()[0])
+    fc.axonn_sync_status()
+
+
+def test_other_stream_and_graph(cuda_lib):
+    """On a side stream, and captured: a replay draws with the words that are
+    on the device then."""
+    fc = cuda_lib
+    import torch
+    T, N = 96, 264
+    X = torch.ones((T, N), device="cuda", dtype=torch.bfloat16)
+    eye = torch.eye(N, device="cuda", dtype=torch.bfloat16)
+    words_d, seed, offset = words()
+    Y = torch.empty_like(X)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        fc.axonn_fc_fwd_epi(X, eye, Y, fc.Shape(T, N, N), p=0.5, rng=words_d)  # first use outside the capture
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            fc.axonn_fc_fwd_epi(X, eye, Y, fc.Shape(T, N, N), p=0.5, rng=words_d)
+    torch.cuda.synchronize()
+    for step in range(3):
+        words_d[1] = step
+        g.replay()
+        torch.cuda.synchronize()
+        keep, _ = ep.keep_mask(T, N, 0.5, seed, step)
+        assert np.array_equal(host(Y) != 0, keep)
+
+
+def test_repeatable(cuda_lib):
+    """The bias gradient's sum has one order."""
+    fc = cuda_lib
+    import torch
+    T, N, K = 1500, 1000, 520
+    g = torch.Generator(device="cuda").manual_seed(3)
+    G = torch.randn((T, K), device="cuda", generator=g).to(torch.bfloat16)
+    W = torch.randn((N, K), device="cuda", generator=g).to(torch.bfloat16)
+    Z = torch.randn((T, N), device="cuda", generator=g).to(torch.bfloat16)
+    ws = torch.empty(fc.axonn_epi_workspace_size(T, N), dtype=torch.uint8, device="cuda")
+    got = []
+    for _ in range(3):
+        D, db = torch.empty((T, N), device="cuda", dtype=torch.bfloat16), torch.empty(N, device="cuda")
+        fc.axonn_fc_dgrad_epi(G, W, D, fc.Shape(T, N, K), pre=Z, act="gelu", dbias=db, ws=ws)
+        got.append((D, db))
+    fc.axonn_sync_status()
+    for D, db in got[1:]:
+        assert torch.equal(D, got[0][0]) and torch.equal(db, got[0][1])

@@ -1,0 +1,238 @@
+"""The linear cross-entropy against its 64-bit form.
+
+Bounds (derived).  A logit is a bf16 product accumulated in fp32: off by at
+most e_z = (K/16 + 2) 2^-23 |X|.|W|.  The logsumexp and the label's logit are
+each off by at most the row's largest e_z, plus 2^-21 of the logsumexp's
+magnitude and 2^-20 for the exponentials' and the logarithm's own error; the
+mean's bound is the mean of the rows'.  An entry of P is then relatively off
+by twice that, by 2^-12 for a logit kept in 16 bits (half a step of 2^-11 in
+the exponent, times ln 2; entries under 2^-32 of a group's maximum are 0) and
+by its rounding to bf16 (half an ulp: 2^-8 of 8 significant bits), the label's
+by the same of max(p, 1 - p) <= 1; dX and dW sum |P||W| and |X||P| of it,
+accumulate in fp32 and round once.
+"""
+import numpy as np
+import pytest
+
+from oracle import epilogue as ep
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def free_choice(cuda_lib):
+    cuda_lib.axonn_set_kernel_config(-1)
+    yield
+    cuda_lib.axonn_set_kernel_config(-1)
+
+
+def bf16(a):
+    import torch
+    return torch.from_numpy(np.asarray(a, dtype=np.float32)).to(torch.bfloat16).to(torch.float64).numpy()
+
+
+def dev(a, dtype, pad=8):
+    import torch
+    rows, cols = a.shape
+    full = torch.full((rows, (cols + 7) // 8 * 8 + pad), float("nan"), dtype=dtype, device="cuda")
+    full[:, :cols] = torch.from_numpy(a).to("cuda").to(dtype)
+    return full[:, :cols]
+
+
+def host(t):
+    import torch
+    return t.to(torch.float64).cpu().numpy()
+
+
+def run(fc, X, W, labels, keep=None, tied=False, grad=True, dw="bf16", piece=0, scale=1.0, old=None):
+    import torch
+    T, K = X.shape
+    V = W.shape[1]
+    flags = (fc.B_T if tied else 0) | {"bf16": 0, "f32": fc.OUT_F32, "add": fc.ACCUM_F32}[dw]
+    Wd = dev(W.T.copy() if tied else W, torch.bfloat16)
+    o = {"token_loss": torch.full((T,), float("nan"), device="cuda"),
+         "lse": torch.full((T,), float("nan"), device="cuda"),
+         "loss": torch.full((1,), float("nan"), device="cuda"),
+         "kept": torch.full((1,), -7, device="cuda", dtype=torch.int32)}
+    if grad:
+        o["dX"] = dev(np.full((T, K), 7.0), torch.bfloat16)
+        kind = torch.bfloat16 if dw == "bf16" else torch.float32
+        start = old if old is not None else np.full((K, V), 7.0)
+        o["dW"] = dev(start.T.copy() if tied else start, kind)
+    n = fc.axonn_linear_ce_workspace_size(T, K, V, flags, grad, piece)
+    ws = torch.full((max(n, 16),), 255, dtype=torch.uint8, device="cuda")  # NaN in every format
+    fc.axonn_linear_ce(dev(X, torch.bfloat16), Wd, torch.from_numpy(labels.astype(np.int32)).cuda(),
+                       o["token_loss"], o["loss"], o["kept"], ws,
+                       keep=None if keep is None else torch.from_numpy(keep.astype(np.uint8)).cuda(),
+                       lse=o["lse"], dX=o.get("dX"), dW=o.get("dW"), grad_scale=scale, flags=flags)
+    fc.axonn_sync_status()
+    if grad:
+        for t in (o["dX"], o["dW"]):
+            assert bool(torch.isnan(t._base[:, t.shape[1]:].float()).all())  # the padding is untouched
+    got = {k: host(v) for k, v in o.items()}
+    if grad and tied:
+        got["dW"] = got["dW"].T
+    return got
+
+
+def check(got, X, W, labels, keep=None, scale=1.0, dw="bf16", old=0.0):
+    K = X.shape[1]
+    r = ep.linear_ce(X, W, labels, keep, scale)
+    c = r["counted"]
+    assert got["kept"][0] == r["n"]
+    assert (got["token_loss"][~c] == 0).all() and (got["lse"][~c] == 0).all()
+    Xc = X[c]
+    ez = (K / 16 + 2) * 2.0**-23 * (np.abs(Xc) @ np.abs(W))
+    row = 2 * ez.max(axis=1, initial=0.0) + 2.0**-21 * np.abs(r["lse"][c]) + 2.0**-20
+    assert (np.abs(got["lse"] - r["lse"])[c] <= row).all()
+    assert (np.abs(got["token_loss"] - r["token_loss"])[c] <= row).all()
+    n = max(r["n"], 1)
+    assert abs(got["loss"][0] - r["loss"]) <= row.sum() / n + 2.0**-20 * abs(r["loss"])
+    if "dX" not in got:
+        return
+    P = np.abs(r["P"])
+    eP = P * (2.0**-8 + 2.0**-12 + 2 * row[:, None]) + 2.0**-32 * abs(scale) / n
+    y = labels[c]
+    at = (np.arange(len(y)), y)
+    eP[at] += 2 * row * abs(scale) / n  # the label's entry: p - 1 has p's absolute error
+    bX = np.zeros_like(X)
+    bX[c] = eP @ np.abs(W).T + (W.shape[1] / 16 + 2) * 2.0**-23 * (P @ np.abs(W).T)
+    bW = np.abs(Xc).T @ eP + (len(y) / 16 + 2) * 2.0**-23 * (np.abs(Xc).T @ P)
+    assert (got["dX"][~c] == 0).all()
+    assert (np.abs(got["dX"] - r["dX"]) <= bX + 2.0**-8 * np.abs(r["dX"]) + 1e-30).all()
+    want = r["dW"] + old
+    unit = 2.0**-8 if dw == "bf16" else 2.0**-22
+    assert (np.abs(got["dW"] - want) <= bW + unit * (np.abs(want) + np.abs(old)) + 1e-30).all()
+
+
+def case(T, K, V, seed=1, spread=1.0):
+    rng = np.random.default_rng(seed)
+    X = bf16(rng.normal(size=(T, K)))
+    W = bf16(rng.normal(size=(K, V)) * spread / np.sqrt(K))
+    return X, W, rng.integers(0, V, size=T), rng
+
+
+SIZES = [(1, 8, 1), (1, 64, 1000), (2, 72, 257), (33, 130, 300), (130, 64, 1003), (300, 200, 2000), (257, 40, 4097)]
+
+
+@pytest.mark.parametrize("config", [2, 0, 7])
+@pytest.mark.parametrize("tied", [False, True])
+@pytest.mark.parametrize("size", SIZES)
+def test_against_64_bits(cuda_lib, size, tied, config):
+    X, W, labels, rng = case(*size)
+    cuda_lib.axonn_set_kernel_config(config)
+    check(run(cuda_lib, X, W, labels, tied=tied), X, W, labels)
+
+
+@pytest.mark.parametrize("piece", [1, 512, 1024])
+@pytest.mark.parametrize("tied", [False, True])
+def test_in_pieces(cuda_lib, piece, tied):
+    """Pieces of 256, 512 and 1024 columns of a 1990-token vocabulary: the
+    last one short, and all but one computed again."""
+    X, W, labels, rng = case(200, 72, 1990, seed=4)
+    labels[::7] = -1
+    got = run(cuda_lib, X, W, labels, tied=tied, piece=piece)
+    check(got, X, W, labels)
+    loss = run(cuda_lib, X, W, labels, tied=tied, grad=False)
+    check(loss, X, W, labels)
+
+
+@pytest.mark.parametrize("dw", ["f32", "add"])
+@pytest.mark.parametrize("piece", [0, 256])
+def test_fp32_weight_gradient(cuda_lib, dw, piece):
+    X, W, labels, rng = case(150, 64, 700, seed=6)
+    old = rng.normal(size=W.shape).astype(np.float32).astype(np.float64)
+    got = run(cuda_lib, X, W, labels, dw=dw, piece=piece, scale=64.0, old=old)
+    check(got, X, W, labels, scale=64.0, dw=dw, old=old if dw == "add" else 0.0)
+
+
+@pytest.mark.parametrize("which", ["none", "all", "one", "half", "keep"])
+@pytest.mark.parametrize("piece", [0, 256])
+def test_masks(cuda_lib, which, piece):
+    """Rows that do not count hold NaN and infinities; nothing of them is
+    seen, and a mask may leave nothing at all."""
+    X, W, labels, rng = case(130, 72, 600, seed=8)
+    keep = None
+    if which == "none":
+        labels[:] = 600
+    elif which == "one":
+        labels[np.arange(130) != 77] = -100
+    elif which == "half":
+        labels[rng.random(130) < 0.5] = -1
+    elif which == "keep":
+        keep = (rng.random(130) < 0.5).astype(np.uint8) * 3
+    counted = (labels >= 0) & (labels < 600) & (keep != 0 if keep is not None else True)
+    dirty = X.copy()
+    dirty[~counted] = np.where(rng.random((int((~counted).sum()), 72)) < 0.5, np.nan, np.inf)
+    got = run(cuda_lib, dirty, W, labels, keep, piece=piece)
+    check(got, X, W, labels, keep)
+
+
+def test_confident_rows(cuda_lib):
+    """Logits of +-60: a label with probability near 1 has a small gradient
+    of its own, the others underflow to 0, and a label far below the maximum
+    has a large loss."""
+    T, K, V = 64, 32, 900
+    rng = np.random.default_rng(2)
+    X, W = bf16(np.eye(T, K) * 60 + np.eye(T, K, -32) * 60), bf16(rng.choice([-1.0, 1.0], size=(K, V)) * 0.5)
+    labels = rng.integers(0, V, size=T)
+    for t in range(32):
+        W[t % K, labels[t]] = 1.0   # the only largest logit of rows t and t + 32
+    check(run(cuda_lib, X, W, labels), X, W, labels)
+    check(run(cuda_lib, X, W, labels, piece=256), X, W, labels)
+
+
+def test_infinite_and_nan_logits(cuda_lib):
+    """A column of -inf logits has probability 0; a row with a NaN has a NaN
+    loss, and no other row does."""
+    import torch
+    X, W, labels, rng = case(40, 16, 300, seed=12)
+    X = np.abs(X) + 0.5
+    X = bf16(X)
+    Wi = W.copy()
+    Wi[0, 5] = -np.inf
+    labels[labels == 5] = 6
+    got = run(cuda_lib, X, Wi, labels)
+    Wf = W.copy()
+    Wf[:, 5] = bf16(np.full(16, -1e30))   # as good as -inf in 64 bits
+    r = ep.linear_ce(X, Wf, labels)
+    assert np.abs(got["token_loss"] - r["token_loss"]).max() < 1e-4
+    X[7, 3] = np.nan
+    got = run(cuda_lib, X, W, labels, grad=False)
+    assert np.isnan(got["token_loss"][7]) and np.isfinite(np.delete(got["token_loss"], 7)).all()
+
+
+def test_empty(cuda_lib):
+    """No positions: loss 0, nothing counted, a zero weight gradient (an
+    unchanged one where it accumulates)."""
+    X, W, labels, _ = case(0, 16, 50)
+    got = run(cuda_lib, X, W, labels)
+    assert got["loss"][0] == 0 and got["kept"][0] == 0 and (got["dW"] == 0).all()
+    got = run(cuda_lib, X, W, labels, dw="add")
+    assert (got["dW"] == 7).all()
+
+
+def test_loss_does_not_depend_on_the_workspace(cuda_lib):
+    """Same statistics whatever is kept: the loss is the same number, and it
+    is the same on every run."""
+    X, W, labels, _ = case(300, 128, 3000 // 2, seed=5)
+    a, b, c = (run(cuda_lib, X, W, labels, grad=g, piece=p) for g, p in ((True, 0), (True, 0), (False, 0)))
+    assert np.array_equal(a["token_loss"], b["token_loss"]) and np.array_equal(a["token_loss"], c["token_loss"])
+    assert np.array_equal(a["dX"], b["dX"]) and np.array_equal(a["dW"], b["dW"])
+
+
+def test_expired_wait_is_reported(cuda_lib):
+    """Operand loads withheld: the bounded waits expire, the status says so,
+    and the next call is right."""
+    fc = cuda_lib
+    X, W, labels, _ = case(40, 64, 300)
+    fc.axonn_set_wait_timeout_ns(2_000_000)
+    fc.axonn_debug_set_inject(1)
+    try:
+        with pytest.raises(fc.AxonnError) as e:
+            run(fc, X, W, labels, grad=False)
+        assert e.value.status == fc.ERR_TIMEOUT
+    finally:
+        fc.axonn_debug_set_inject(0)
+        fc.axonn_set_wait_timeout_ns(4_000_000_000)
+    check(run(fc, X, W, labels), X, W, labels)
