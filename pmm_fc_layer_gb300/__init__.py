@@ -210,10 +210,27 @@ def _ld(t, ld):
     return t.stride(0)
 
 
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """The current stream's handle, without building a Stream object for each
+    call (a third of a small call's host time) where torch offers that."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.init()
+        get, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        if get is not None and device is not None:
+            _raw_stream = lambda: get(device())  # noqa: E731
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
+
+
 def _stream(stream) -> int:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -305,43 +322,68 @@ def axonn_goldfish_ce(logits, input_ids, labels, keep, token_loss, loss, kept, k
 
 
 def _ws(ws):
-    return (_ptr(ws), ws.numel() * ws.element_size()) if ws is not None else (0, 0)
+    return (ws.data_ptr(), ws.numel() * ws.element_size()) if ws is not None else (None, 0)
 
 
-def _typed(name, t, dtype, shape=None):
-    """Checks that a tensor has the type (and shape) the call's flags say."""
-    if t is None or isinstance(t, int):
-        return
-    if str(t.dtype) != "torch." + dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {shape}, got {tuple(t.shape)}")
+_dtypes = {}
+
+
+def _dtype(name):
+    """torch's dtype of that name (torch is imported at the first call)."""
+    if not _dtypes:
+        import torch
+        _dtypes.update(bf16=torch.bfloat16, f32=torch.float32, i32=torch.int32, u8=torch.uint8,
+                       words=(torch.int64, torch.uint64))
+    return _dtypes[name]
+
+
+def _matrix(name, t, dtype, rows, cols):
+    """(pointer, leading dimension) of a [rows x cols] matrix of that type, or
+    (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dtype is not _dtype(dtype):
+        raise ValueError(f"{name} must be {_dtype(dtype)}, got {t.dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(t.shape)}")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), ld
 
 
 def _vector(name, t, dtype, n):
-    _typed(name, t, dtype, (n,))
-    if t is not None and not isinstance(t, int) and n > 1 and t.stride(0) != 1:
-        raise ValueError(f"{name} must be contiguous")
-
-
-def _epilogue(act, rows, cols, bias=None, pre=None, residual=None, dbias=None, p=0.0, rng=None,
-              out_f32=False, bias_f32=False):
-    if act not in ACTS:
-        raise ValueError(f"activation {act!r} not in {sorted(ACTS)}")
-    _vector("bias", bias, "float32" if bias_f32 else "bfloat16", cols)
-    _vector("dbias", dbias, "float32", cols)
-    _typed("pre", pre, "bfloat16", (rows, cols))
-    _typed("residual", residual, "float32" if out_f32 else "bfloat16", (rows, cols))
-    _rng(rng)
-    return Epilogue(_ptr(bias) or None, _ptr(pre) or None, _ld(pre, None), _ptr(residual) or None,
-                    _ld(residual, None), _ptr(dbias) or None, _ptr(rng) or None, ACTS[act], p)
+    """Pointer of a contiguous vector of n elements of that type, or None."""
+    if t is None:
+        return None
+    if t.dtype is not _dtype(dtype):
+        raise ValueError(f"{name} must be {_dtype(dtype)}, got {t.dtype}")
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous of {n} elements")
+    return t.data_ptr()
 
 
 def _rng(rng):
-    if rng is None or isinstance(rng, int):
-        return
-    if str(rng.dtype) not in ("torch.int64", "torch.uint64") or rng.numel() != 2 or not rng.is_contiguous():
+    if rng is None:
+        return None
+    if rng.dtype not in _dtype("words") or rng.shape != (2,) or rng.stride(0) != 1:
         raise ValueError("rng must be two contiguous 64-bit integers on the device: seed and offset")
+    return rng.data_ptr()
+
+
+def _act(act):
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError(f"activation {act!r} not in {sorted(ACTS)}")
+    return code
+
+
+def _layer(shape, flags, rows_name, A, rows, red, W):
+    """(pointer, ld) of a product's operands: A [rows x red] (stored the other
+    way round with A_T) and W [shape.K x shape.N] (with B_T likewise)."""
+    a = _matrix(rows_name, A, "bf16", *((red, rows) if flags & A_T else (rows, red)))
+    w = _matrix("W", W, "bf16", *((shape.N, shape.K) if flags & B_T else (shape.K, shape.N)))
+    return a, w
 
 
 def axonn_fc_fwd_epi(X, W, Y, shape: Shape, flags: int = 0, bias=None, act="none", pre=None,
@@ -350,16 +392,17 @@ def axonn_fc_fwd_epi(X, W, Y, shape: Shape, flags: int = 0, bias=None, act="none
     receives X . W + bias where given.  bias is bf16, or fp32 (the tensor's
     type sets BIAS_F32); residual has Y's type.  D is dropout with probability
     p and ``rng``, two 64-bit words on the device (seed, offset)."""
-    if bias is not None and not isinstance(bias, int) and str(bias.dtype) == "torch.float32":
+    T, N = shape.T, shape.N
+    if bias is not None and bias.dtype is _dtype("f32"):
         flags |= BIAS_F32
-    f32 = bool(flags & OUT_F32)
-    _typed("X", X, "bfloat16")
-    _typed("W", W, "bfloat16")
-    _typed("Y", Y, "float32" if f32 else "bfloat16", (shape.T, shape.N))
-    e = _epilogue(act, shape.T, shape.N, bias=bias, pre=pre, residual=residual, p=p, rng=rng,
-                  out_f32=f32, bias_f32=bool(flags & BIAS_F32))
-    _check(load().axonn_fc_fwd_epi(_ptr(X), _ptr(W), _ptr(Y), _ld(X, None), _ld(W, None), _ld(Y, None),
-                                   ctypes.byref(shape), flags, ctypes.byref(e), _stream(stream)))
+    out = "f32" if flags & OUT_F32 else "bf16"
+    x, w = _layer(shape, flags, "X", X, T, shape.K, W)
+    y = _matrix("Y", Y, out, T, N)
+    e = Epilogue(_vector("bias", bias, "f32" if flags & BIAS_F32 else "bf16", N),
+                 *_matrix("pre", pre, "bf16", T, N), *_matrix("residual", residual, out, T, N),
+                 None, _rng(rng), _act(act), p)
+    _check(load().axonn_fc_fwd_epi(x[0], w[0], y[0], x[1], w[1], y[1], ctypes.byref(shape), flags,
+                                   ctypes.byref(e), _stream(stream)))
 
 
 def axonn_fc_dgrad_epi(dY, W, dX, shape: Shape, flags: int = 0, pre=None, act="none", residual=None,
@@ -368,26 +411,26 @@ def axonn_fc_dgrad_epi(dY, W, dX, shape: Shape, flags: int = 0, pre=None, act="n
     sums of act'(pre) D(dY . W^T): the data gradient of this layer as the
     gradient of the pre-activation before it.  dbias needs ``ws``
     (axonn_epi_workspace_size(T, K) bytes)."""
-    f32 = bool(flags & OUT_F32)
-    _typed("dY", dY, "bfloat16")
-    _typed("W", W, "bfloat16")
-    _typed("dX", dX, "float32" if f32 else "bfloat16", (shape.T, shape.K))
-    e = _epilogue(act, shape.T, shape.K, pre=pre, residual=residual, dbias=dbias, p=p, rng=rng, out_f32=f32)
-    _check(load().axonn_fc_dgrad_epi(_ptr(dY), _ptr(W), _ptr(dX), _ld(dY, None), _ld(W, None),
-                                     _ld(dX, None), ctypes.byref(shape), flags, ctypes.byref(e),
-                                     *_ws(ws), _stream(stream)))
+    T, K = shape.T, shape.K
+    out = "f32" if flags & OUT_F32 else "bf16"
+    g, w = _layer(shape, flags, "dY", dY, T, shape.N, W)
+    y = _matrix("dX", dX, out, T, K)
+    e = Epilogue(None, *_matrix("pre", pre, "bf16", T, K), *_matrix("residual", residual, out, T, K),
+                 _vector("dbias", dbias, "f32", K), _rng(rng), _act(act), p)
+    _check(load().axonn_fc_dgrad_epi(g[0], w[0], y[0], g[1], w[1], y[1], ctypes.byref(shape), flags,
+                                     ctypes.byref(e), *_ws(ws), _stream(stream)))
 
 
 def axonn_epi_bwd(dY, dZ, pre=None, act="none", dbias=None, p=0.0, rng=None, ws=None, stream=None):
     """dZ (bf16) = act'(pre) D(dY) and dbias (fp32) = its column sums, for
     dY [rows x cols] in bf16 or fp32 (the tensor's type sets IN_F32)."""
     rows, cols = dY.shape
-    flags = IN_F32 if str(dY.dtype) == "torch.float32" else 0
-    _typed("dY", dY, "float32" if flags else "bfloat16")
-    _typed("dZ", dZ, "bfloat16", (rows, cols))
-    e = _epilogue(act, rows, cols, pre=pre, dbias=dbias, p=p, rng=rng)
-    _check(load().axonn_epi_bwd(_ptr(dY), _ld(dY, None), _ptr(dZ), _ld(dZ, None), rows, cols, flags,
-                                ctypes.byref(e), *_ws(ws), _stream(stream)))
+    f32 = dY.dtype is _dtype("f32")
+    e = Epilogue(None, *_matrix("pre", pre, "bf16", rows, cols), None, 0,
+                 _vector("dbias", dbias, "f32", cols), _rng(rng), _act(act), p)
+    _check(load().axonn_epi_bwd(*_matrix("dY", dY, "f32" if f32 else "bf16", rows, cols),
+                                *_matrix("dZ", dZ, "bf16", rows, cols), rows, cols,
+                                IN_F32 if f32 else 0, ctypes.byref(e), *_ws(ws), _stream(stream)))
 
 
 def axonn_epi_workspace_size(rows: int, cols: int) -> int:
@@ -400,14 +443,12 @@ def axonn_dropout(X, Y, p, rng, residual=None, stream=None):
     """Y = residual + D(X), bf16 or fp32 (X's type); its backward is the same
     call on the gradient."""
     rows, cols = X.shape
-    kind = "float32" if str(X.dtype) == "torch.float32" else "bfloat16"
-    _typed("X", X, kind)
-    _typed("Y", Y, kind, (rows, cols))
-    _typed("residual", residual, kind, (rows, cols))
-    _rng(rng)
-    _check(load().axonn_dropout(_ptr(X), _ld(X, None), _ptr(residual), _ld(residual, None), _ptr(Y),
-                                _ld(Y, None), rows, cols, p, _ptr(rng),
-                                IN_F32 if kind == "float32" else 0, _stream(stream)))
+    f32 = X.dtype is _dtype("f32")
+    kind = "f32" if f32 else "bf16"
+    _check(load().axonn_dropout(*_matrix("X", X, kind, rows, cols),
+                                *_matrix("residual", residual, kind, rows, cols),
+                                *_matrix("Y", Y, kind, rows, cols), rows, cols, p, _rng(rng),
+                                IN_F32 if f32 else 0, _stream(stream)))
 
 
 def axonn_linear_ce(X, W, labels, token_loss, loss, kept, ws, keep=None, lse=None, dX=None, dW=None,
@@ -419,20 +460,14 @@ def axonn_linear_ce(X, W, labels, token_loss, loss, kept, ws, keep=None, lse=Non
     (smaller pieces of the vocabulary)."""
     T, K = X.shape
     V = W.shape[0 if flags & B_T else 1]
-    _typed("X", X, "bfloat16")
-    _typed("W", W, "bfloat16", (V, K) if flags & B_T else (K, V))
-    _vector("labels", labels, "int32", T)
-    _vector("keep", keep, "uint8", T)
-    _vector("token_loss", token_loss, "float32", T)
-    _vector("lse", lse, "float32", T)
-    _vector("loss", loss, "float32", 1)
-    _vector("kept", kept, "int32", 1)
-    _typed("dX", dX, "bfloat16", (T, K))
-    _typed("dW", dW, "float32" if flags & (OUT_F32 | ACCUM_F32) else "bfloat16", tuple(W.shape))
-    _check(load().axonn_linear_ce(_ptr(X), _ld(X, None), _ptr(W), _ld(W, None), _ptr(labels), _ptr(keep),
-                                  T, K, V, grad_scale, flags, _ptr(token_loss), _ptr(lse), _ptr(loss),
-                                  _ptr(kept), _ptr(dX), _ld(dX, None), _ptr(dW), _ld(dW, None),
-                                  *_ws(ws), _stream(stream)))
+    wshape = (V, K) if flags & B_T else (K, V)
+    _check(load().axonn_linear_ce(
+        *_matrix("X", X, "bf16", T, K), *_matrix("W", W, "bf16", *wshape),
+        _vector("labels", labels, "i32", T), _vector("keep", keep, "u8", T), T, K, V, grad_scale, flags,
+        _vector("token_loss", token_loss, "f32", T), _vector("lse", lse, "f32", T),
+        _vector("loss", loss, "f32", 1), _vector("kept", kept, "i32", 1), *_matrix("dX", dX, "bf16", T, K),
+        *_matrix("dW", dW, "f32" if flags & (OUT_F32 | ACCUM_F32) else "bf16", *wshape),
+        *_ws(ws), _stream(stream)))
 
 
 def axonn_linear_ce_workspace_size(T: int, K: int, V: int, flags: int = 0, grad: bool = True,

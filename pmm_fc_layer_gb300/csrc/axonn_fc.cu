@@ -1046,6 +1046,7 @@ axonn_status_t dropout_args(float p, const uint64_t* rng, axonn::DropoutArgs* d)
   if (st != AXONN_OK) return st;
   d->rng = rng;
   d->thr = static_cast<uint32_t>(static_cast<double>(p) * 65536.0 + 0.5);
+  d->above = static_cast<uint32_t>((static_cast<uint64_t>(d->thr) << 16) - 1);
   d->scale = d->thr < 65536 ? static_cast<float>(65536.0 / (65536.0 - d->thr)) : 0.0f;
   if (d->thr == 0) return AXONN_OK;
   if (!rng) return fail(AXONN_ERR_INVALID_ARG, "dropout needs rng (seed and offset on the device)");

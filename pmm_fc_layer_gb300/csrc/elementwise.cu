@@ -13,38 +13,58 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Eight elements of a row, n of them existing (the others are neither read
-// nor written).  Full vectors are 16-byte aligned: base pointers and leading
-// dimensions are checked by the host and columns are multiples of 8.
-__device__ __forceinline__ void load8(const uint16_t* p, int n, float (&x)[8]) {
-  if (n >= 8) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// Eight consecutive elements of a row, kept as loaded: 4 words of bf16 or 8
+// of fp32.  n of them exist (the others are neither read nor written).  Full
+// vectors are 16-byte aligned: base pointers and leading dimensions are
+// checked by the host and columns are multiples of 8.  Every element is
+// touched once, so loads and stores are marked streaming (not kept in the
+// caches at the expense of others).
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<uint16_t> {
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const uint16_t* p, int n) {
+    if (n >= 8) {
+      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = (2 * j < n ? p[2 * j] : 0u) | ((2 * j + 1 < n ? p[2 * j + 1] : 0u) << 16);
+    }
+  }
+  __device__ __forceinline__ void values(float (&x)[8]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       x[2 * j] = __uint_as_float(w[j] << 16);
       x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = j < n ? bf16_bits_f32(p[j]) : 0.0f;
   }
-}
-__device__ __forceinline__ void load8(const float* p, int n, float (&x)[8]) {
-  if (n >= 8) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-  } else {
+};
+template <>
+struct Vec8<float> {
+  float w[8];
+  __device__ __forceinline__ void load(const float* p, int n) {
+    if (n >= 8) {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = j < n ? p[j] : 0.0f;
+      for (int j = 0; j < 8; ++j) w[j] = j < n ? p[j] : 0.0f;
+    }
   }
-}
+  __device__ __forceinline__ void values(float (&x)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = w[j];
+  }
+};
 __device__ __forceinline__ void store8(uint16_t* p, int n, const float (&x)[8]) {
   const uint32_t w[4] = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                          pack_bf16(x[6], x[7])};
   if (n >= 8) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -53,8 +73,8 @@ __device__ __forceinline__ void store8(uint16_t* p, int n, const float (&x)[8]) 
 }
 __device__ __forceinline__ void store8(float* p, int n, const float (&x)[8]) {
   if (n >= 8) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -62,81 +82,133 @@ __device__ __forceinline__ void store8(float* p, int n, const float (&x)[8]) {
   }
 }
 
-// The vectors of the matrix in row order, dealt out to the grid's threads.
-// The row and column of a thread's next vector follow from the last by one
-// addition and one wrap.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(DropoutKernelArgs a) {
+// The vectors of the matrix in row order, dealt out to the grid's threads
+// kDropUnroll at a time: all their loads are issued before the first is
+// used, which is what keeps enough bytes in flight.  The row and column of a
+// thread's next vector follow from the last by one addition and one wrap.
+constexpr int kDropUnroll = 4;
+template <typename T, bool kRes>
+constexpr int kDropBlocks = sizeof(T) == 2 ? (kRes ? 4 : 5) : (kRes ? 2 : 3);  // resident on an SM
+template <typename T, bool kRes>
+__global__ void __launch_bounds__(kThreads, kDropBlocks<T, kRes>) dropout_kernel(DropoutKernelArgs a) {
   const T* X = static_cast<const T*>(a.x);
   const T* R = static_cast<const T*>(a.residual);
   T* Y = static_cast<T*>(a.y);
-  const int64_t n8 = (a.cols + 7) / 8;
+  const int n8 = static_cast<int>((a.cols + 7) / 8);
+  const int tail = static_cast<int>(a.cols - 8 * static_cast<int64_t>(n8 - 1));  // of a row's last vector
   const int64_t total = a.rows * n8;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
   int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   if (i >= total) return;
   const DropRng g = load_rng(a.drop);
-  const int64_t dr = stride / n8, dc = stride - dr * n8;
-  int64_t row = i / n8, c8 = i - row * n8;
-  for (; i < total; i += stride) {
-    const int n = static_cast<int>(min(static_cast<int64_t>(8), a.cols - 8 * c8));
-    float x[8], r[8];
-    load8(X + row * a.ld_x + 8 * c8, n, x);
-    if (R) load8(R + row * a.ld_res + 8 * c8, n, r);
-    const uint32_t bits =
-        a.drop.thr != 0 ? keep8(a.drop, g, static_cast<uint32_t>(row), static_cast<uint32_t>(c8)) : 0xFFu;
+  const int dr = static_cast<int>(stride / n8), dc = static_cast<int>(stride - static_cast<int64_t>(dr) * n8);
+  int row = static_cast<int>(i / n8), c8 = static_cast<int>(i - static_cast<int64_t>(row) * n8);
+  while (i < total) {
+    Vec8<T> x[kDropUnroll], r[kDropUnroll];
+    int rows[kDropUnroll], cols[kDropUnroll];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      // R + scale x in one rounding
-      const float base = R ? r[j] : 0.0f;
-      x[j] = (bits >> j) & 1u ? fmaf(x[j], a.drop.scale, base) : base;
+    for (int u = 0; u < kDropUnroll; ++u) {
+      rows[u] = row;
+      cols[u] = c8;
+      if (i + u * stride < total) {
+        const int n = c8 + 1 < n8 ? 8 : tail;
+        x[u].load(X + row * a.ld_x + 8 * static_cast<int64_t>(c8), n);
+        if (kRes) r[u].load(R + row * a.ld_res + 8 * static_cast<int64_t>(c8), n);
+      }
+      row += dr;
+      c8 += dc;
+      if (c8 >= n8) {
+        c8 -= n8;
+        ++row;
+      }
     }
-    store8(Y + row * a.ld_y + 8 * c8, n, x);
-    row += dr;
-    c8 += dc;
-    if (c8 >= n8) {
-      c8 -= n8;
-      ++row;
+#pragma unroll
+    for (int u = 0; u < kDropUnroll; ++u) {
+      if (i + u * stride >= total) break;
+      float v[8], b[8] = {};
+      x[u].values(v);
+      if (kRes) r[u].values(b);
+      if (a.drop.thr != 0) {
+        drop8_add(a.drop, drop_words(g, static_cast<uint32_t>(rows[u]), static_cast<uint32_t>(cols[u])), v, b);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += b[j];
+      }
+      store8(Y + rows[u] * a.ld_y + 8 * static_cast<int64_t>(cols[u]), cols[u] + 1 < n8 ? 8 : tail, v);
     }
+    i += kDropUnroll * stride;
   }
 }
 
 // A block covers kBwdRows rows x 256 columns: each of its eight warps takes
-// every eighth row, a lane eight columns.  A lane adds its rows' columns in
-// order, the block its warps' sums in order: partial sums of kBwdRows rows.
+// every eighth row, a lane eight columns, kBwdUnroll rows' loads at a time.
+// A lane adds its rows' columns in order, the block its warps' sums in
+// order: partial sums of kBwdRows rows.  The activation and whether there is
+// dropout are compiled in: at 6 bytes an element the arithmetic has about 40
+// instructions an element to spend, and the general form took more.
 constexpr int kBwdRows = 64;
+constexpr int kBwdUnroll = 4;
 static_assert(kBwdRows >= 32, "the partial sums' workspace holds one row of them per 32 rows");
+static_assert(kBwdRows % (8 * kBwdUnroll) == 0, "whole batches of rows");
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) act_bwd_kernel(BwdKernelArgs a) {
+// One lane's eight columns over rows r0, r0 + 8, ... below r1; kFull: all
+// eight exist.
+template <typename T, int ACT, bool kDrop, bool kFull>
+__device__ __forceinline__ void act_bwd_rows(const BwdKernelArgs& a, const DropRng& g, int64_t r0, int64_t r1,
+                                             int64_t col, int n, float (&sum)[8]) {
+  constexpr int U = kFull ? kBwdUnroll * 2 / static_cast<int>(sizeof(T)) : 1;  // the same bytes in flight for fp32
+  if (kFull) n = 8;
+  const T* dy = static_cast<const T*>(a.dy) + r0 * a.ld_dy + col;
+  const uint16_t* pre = a.pre + r0 * a.ld_pre + col;
+  uint16_t* dz = a.dz + r0 * a.ld_dz + col;
+#pragma unroll 1
+  for (int64_t base = r0; base < r1; base += 8 * U) {
+    Vec8<T> x[U];
+    Vec8<uint16_t> z[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (base + 8 * u < r1) {
+        x[u].load(dy, n);
+        if (ACT != kActNone) z[u].load(pre, n);
+      }
+      dy += 8 * a.ld_dy;
+      if (ACT != kActNone) pre += 8 * a.ld_pre;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (base + 8 * u < r1) {
+        float v[8];
+        x[u].values(v);
+        if (kDrop) drop8(a.drop, g, static_cast<uint32_t>(base + 8 * u), static_cast<uint32_t>(col / 8), v);
+        if (ACT != kActNone) {
+          float s[8];
+          z[u].values(s);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] *= act_slope<ACT>(s[j]);
+        }
+        store8(dz, n, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      }
+      dz += 8 * a.ld_dz;
+    }
+  }
+}
+
+template <typename T, int ACT, bool kDrop>
+__global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(BwdKernelArgs a) {
   __shared__ float part[8][32][9];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const T* dY = static_cast<const T*>(a.dy);
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + 8 * lane;
   const int n = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(8), a.cols - col)));
-  const DropRng g = load_rng(a.drop);
+  DropRng g{0, 0};
+  if (kDrop) g = load_rng(a.drop);
   for (int64_t group = blockIdx.y; group * kBwdRows < a.rows; group += gridDim.y) {
-    const int64_t r0 = group * kBwdRows;
-    const int64_t r1 = min(a.rows, r0 + kBwdRows);
+    const int64_t r0 = group * kBwdRows + warp;
+    const int64_t r1 = min(a.rows, group * kBwdRows + kBwdRows);
     float sum[8] = {};
-    if (n > 0) {
-#pragma unroll 4
-      for (int64_t row = r0 + warp; row < r1; row += 8) {
-        float x[8];
-        load8(dY + row * a.ld_dy + col, n, x);
-        if (a.act != kActNone) {
-          float z[8];
-          load8(a.pre + row * a.ld_pre + col, n, z);
-          if (a.drop.thr != 0) drop8(a.drop, g, static_cast<uint32_t>(row), static_cast<uint32_t>(col / 8), x);
-          apply_slope(a.act, x, z);
-        } else if (a.drop.thr != 0) {
-          drop8(a.drop, g, static_cast<uint32_t>(row), static_cast<uint32_t>(col / 8), x);
-        }
-        store8(a.dz + row * a.ld_dz + col, n, x);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum[j] += x[j];
-      }
-    }
+    if (n == 8) act_bwd_rows<T, ACT, kDrop, true>(a, g, r0, r1, col, 8, sum);
+    else if (n > 0) act_bwd_rows<T, ACT, kDrop, false>(a, g, r0, r1, col, n, sum);
     if (a.colsum) {
       __syncthreads();
 #pragma unroll
@@ -151,6 +223,17 @@ __global__ void __launch_bounds__(kThreads) act_bwd_kernel(BwdKernelArgs a) {
         a.colsum[group * a.ld_colsum + at] = s;
       }
     }
+  }
+}
+
+template <typename T, bool kDrop>
+void act_bwd_start(const BwdKernelArgs& a, dim3 grid, cudaStream_t stream) {
+  switch (a.act) {
+    case kActRelu: act_bwd_kernel<T, kActRelu, kDrop><<<grid, kThreads, 0, stream>>>(a); break;
+    case kActGelu: act_bwd_kernel<T, kActGelu, kDrop><<<grid, kThreads, 0, stream>>>(a); break;
+    case kActGeluTanh: act_bwd_kernel<T, kActGeluTanh, kDrop><<<grid, kThreads, 0, stream>>>(a); break;
+    case kActSilu: act_bwd_kernel<T, kActSilu, kDrop><<<grid, kThreads, 0, stream>>>(a); break;
+    default: act_bwd_kernel<T, kActNone, kDrop><<<grid, kThreads, 0, stream>>>(a); break;
   }
 }
 
@@ -179,13 +262,20 @@ __global__ void __launch_bounds__(kThreads) colsum_kernel(const float* part, int
 
 }  // namespace
 
-cudaError_t dropout_launch(const DropoutKernelArgs& a, bool f32, int sms, cudaStream_t stream) {
+namespace {
+template <typename T, bool kRes>
+cudaError_t dropout_start(const DropoutKernelArgs& a, int sms, cudaStream_t stream) {
   const int64_t vectors = a.rows * ((a.cols + 7) / 8);
-  const int64_t blocks = std::min<int64_t>((vectors + kThreads - 1) / kThreads, int64_t{8} * sms);
-  if (blocks == 0) return cudaSuccess;
-  if (f32) dropout_kernel<float><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
-  else dropout_kernel<uint16_t><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
+  const int64_t blocks =
+      std::min<int64_t>((vectors + kThreads - 1) / kThreads, int64_t{kDropBlocks<T, kRes>} * sms);
+  if (blocks > 0) dropout_kernel<T, kRes><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t dropout_launch(const DropoutKernelArgs& a, bool f32, int sms, cudaStream_t stream) {
+  if (f32) return a.residual ? dropout_start<float, true>(a, sms, stream) : dropout_start<float, false>(a, sms, stream);
+  return a.residual ? dropout_start<uint16_t, true>(a, sms, stream) : dropout_start<uint16_t, false>(a, sms, stream);
 }
 
 cudaError_t act_bwd_launch(const BwdKernelArgs& a, bool dy_f32, cudaStream_t stream) {
@@ -193,8 +283,9 @@ cudaError_t act_bwd_launch(const BwdKernelArgs& a, bool dy_f32, cudaStream_t str
   const int64_t groups = (a.rows + kBwdRows - 1) / kBwdRows;
   const dim3 grid(static_cast<unsigned>((a.cols + 255) / 256),
                   static_cast<unsigned>(std::min<int64_t>(groups, 65535)));
-  if (dy_f32) act_bwd_kernel<float><<<grid, kThreads, 0, stream>>>(a);
-  else act_bwd_kernel<uint16_t><<<grid, kThreads, 0, stream>>>(a);
+  const bool drop = a.drop.thr != 0;
+  if (dy_f32) drop ? act_bwd_start<float, true>(a, grid, stream) : act_bwd_start<float, false>(a, grid, stream);
+  else drop ? act_bwd_start<uint16_t, true>(a, grid, stream) : act_bwd_start<uint16_t, false>(a, grid, stream);
   return cudaGetLastError();
 }
 

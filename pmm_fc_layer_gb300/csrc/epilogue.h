@@ -16,6 +16,7 @@ enum Activation : int32_t { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTa
 struct DropoutArgs {
   const uint64_t* rng;  // device: seed, offset
   uint32_t thr;         // floor(65536 p + 1/2), 0 .. 65536
+  uint32_t above;       // thr 2^16 - 1
   float scale;          // 65536 / (65536 - thr), 0 where thr = 65536
 };
 

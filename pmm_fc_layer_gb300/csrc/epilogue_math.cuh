@@ -41,10 +41,30 @@ __device__ __forceinline__ float gelu_tanh_gate(float z) {
   return sigmoid(2.0f * kGeluC0 * z * fmaf(kGeluC1 * z, z, 1.0f));
 }
 
+// The normal distribution's tail beyond |z| and its density at z.  The tail
+// is half of erfc(|z| / sqrt 2) by formula 7.1.26 of Abramowitz and Stegun
+// (C. Hastings' rational approximation): t (a1 + .. + a5 t^4) e^(-z^2 / 2),
+// t = 1 / (1 + p |z| / sqrt 2), within 1.5e-7 of erfc, which leaves 1e-7 of z
+// in GELU.  It costs two SFU steps, half of what erfcf costs, and the slope
+// uses the exponential again.
+__device__ __forceinline__ float normal_tail(float z, float& e) {
+  e = ex2_approx(-0.5f * kEpiLog2e * z * z);
+  const float t = rcp_approx(fmaf(0.3275911f * kRsqrt2, fabsf(z), 1.0f));
+  float h = fmaf(t, 1.061405429f, -1.453152027f);
+  h = fmaf(t, h, 1.421413741f);
+  h = fmaf(t, h, -0.284496736f);
+  h = fmaf(t, h, 0.254829592f);
+  return 0.5f * h * t * e;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float z) {
   if constexpr (ACT == kActRelu) return z < 0.0f ? 0.0f : z;  // NaN stays
-  if constexpr (ACT == kActGelu) return 0.5f * z * erfcf(-kRsqrt2 * z);
+  if constexpr (ACT == kActGelu) {
+    float e;
+    const float h = normal_tail(z, e);
+    return z * (z >= 0.0f ? 1.0f - h : h);
+  }
   if constexpr (ACT == kActGeluTanh) return z * gelu_tanh_gate(z);
   if constexpr (ACT == kActSilu) return z * sigmoid(z);
   return z;
@@ -53,8 +73,11 @@ __device__ __forceinline__ float act_value(float z) {
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if constexpr (ACT == kActRelu) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-  if constexpr (ACT == kActGelu)
-    return fmaf(z * kRsqrt2Pi, ex2_approx(-0.5f * kEpiLog2e * z * z), 0.5f * erfcf(-kRsqrt2 * z));
+  if constexpr (ACT == kActGelu) {
+    float e;
+    const float h = normal_tail(z, e);
+    return fmaf(z * kRsqrt2Pi, e, z >= 0.0f ? 1.0f - h : h);
+  }
   if constexpr (ACT == kActGeluTanh) {
     // with s = sigmoid(2u): s + z s (1 - s) 2 u'(z).  z is clamped where the
     // gate has long saturated, so that its square cannot overflow.
@@ -132,29 +155,37 @@ __device__ __forceinline__ DropRng load_rng(const DropoutArgs& d) {
   return r;
 }
 
-// The eight consecutive columns 8 * col8 .. of one row: bit j of the result
-// is set where D keeps column j.  One generator call gives all eight.
-__device__ __forceinline__ uint32_t keep8(const DropoutArgs& d, const DropRng& g, uint32_t row, uint32_t col8) {
-  const uint4 r = philox4x32_10(make_uint4(col8, row, static_cast<uint32_t>(g.offset),
-                                           static_cast<uint32_t>(g.offset >> 32)),
-                                static_cast<uint32_t>(g.seed), static_cast<uint32_t>(g.seed >> 32));
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-  uint32_t bits = 0;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    bits |= ((w[j] & 0xFFFFu) >= d.thr ? 1u : 0u) << (2 * j);
-    bits |= ((w[j] >> 16) >= d.thr ? 2u : 0u) << (2 * j);
-  }
-  return bits;
+// The generator's four words for the eight consecutive columns 8 * col8 ..
+// of one row.
+__device__ __forceinline__ uint4 drop_words(const DropRng& g, uint32_t row, uint32_t col8) {
+  return philox4x32_10(make_uint4(col8, row, static_cast<uint32_t>(g.offset),
+                                  static_cast<uint32_t>(g.offset >> 32)),
+                       static_cast<uint32_t>(g.seed), static_cast<uint32_t>(g.seed >> 32));
 }
 
-// D over those columns.  A dropped element becomes 0 whatever it was (an
-// infinity or NaN there does not survive), hence a select.
+// v[j] = base[j] + D(v[j]) over those columns, in one rounding.  A half word
+// u is at least thr exactly when u 2^16 is above `above` = thr 2^16 - 1, the
+// upper half whatever lies below it.  A dropped element becomes 0 whatever it
+// was (an infinity or NaN there does not survive), hence a select.
+__device__ __forceinline__ void drop8_add(const DropoutArgs& d, const uint4& r, float* v, const float* base) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float lo = fmaf(v[2 * j], d.scale, base[2 * j]);
+    const float hi = fmaf(v[2 * j + 1], d.scale, base[2 * j + 1]);
+    v[2 * j] = (w[j] << 16) > d.above ? lo : base[2 * j];
+    v[2 * j + 1] = w[j] > d.above ? hi : base[2 * j + 1];
+  }
+}
 __device__ __forceinline__ void drop8(const DropoutArgs& d, const DropRng& g, uint32_t row, uint32_t col8,
                                       float* v) {
-  const uint32_t bits = keep8(d, g, row, col8);
+  const uint4 r = drop_words(g, row, col8);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = (bits >> j) & 1u ? v[j] * d.scale : 0.0f;
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = (w[j] << 16) > d.above ? v[2 * j] * d.scale : 0.0f;
+    v[2 * j + 1] = w[j] > d.above ? v[2 * j + 1] * d.scale : 0.0f;
+  }
 }
 
 // ------------------------------------------------------------------ rows
