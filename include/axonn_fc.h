@@ -527,8 +527,7 @@ void axonn_debug_set_inject(int mode);
  * axonn_set_kernel_config(c) forces configuration c for all later calls in
  * the process (-1 restores automatic choice); AXONN_ERR_INVALID_ARG if c is
  * out of range.  The products with an epilogue and those of the linear
- * cross-entropy have the tiles 0, 2 and 7 (always with a double-buffered
- * accumulator) and choose among them when another is forced.
+ * cross-entropy have the tiles 0, 2, 6 and 7 and choose among them when another is forced.
  * axonn_last_kernel_config() is the configuration the last
  * GEMM launch on this thread used (-1 before any). */
 axonn_status_t axonn_set_kernel_config(int config);

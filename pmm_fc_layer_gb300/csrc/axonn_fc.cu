@@ -125,13 +125,12 @@ axonn_status_t device_state(DeviceState** out) {
     for (cudaError_t x : es)
       if (x != cudaSuccess)
         return fail(AXONN_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(x));
-    for (cudaError_t x : {axonn::fused_init(), axonn::ce_init()})
+    for (cudaError_t x : {axonn::fused_init(&split_ok), axonn::ce_init(&split_ok)})
       if (x != cudaSuccess)
         return fail(AXONN_ERR_CUDA, "fused kernel attributes: %s", cudaGetErrorString(x));
     if (!split_ok)
       return fail(AXONN_ERR_UNSUPPORTED,
-                  "a 12-warp GEMM kernel was not built with %d registers per thread",
-                  axonn::kRegsAtLaunch);
+                  "a GEMM kernel was not built with the registers per thread its split assumes");
     int clusters = 0;
     if (axonn::pair_clusters_resident(d.sms, &clusters) != cudaSuccess || clusters <= 0) {
       (void)cudaGetLastError();
@@ -1099,8 +1098,8 @@ axonn_status_t check_colsum_ws(const void* ws, size_t ws_bytes, int64_t rows, in
 
 // The tile of a fused product: the one whose waves over the GPU cost least,
 // area over throughput relative to the pair's 256 x 256.
-constexpr double kFusedSpeed[axonn::kFusedConfigs] = {1.0, 0.70, 0.40};
-constexpr int kFusedPlain[axonn::kFusedConfigs] = {2, 0, 7};  // the plain products' configuration of that tile
+constexpr double kFusedSpeed[axonn::kFusedConfigs] = {1.0, 0.70, 0.40, 1.12};
+constexpr int kFusedPlain[axonn::kFusedConfigs] = {2, 0, 7, 6};  // the plain products' configuration of that tile
 int choose_fused(int64_t M, int64_t N, const DeviceState& dev) {
   const int forced = g_forced_config.load();
   for (int i = 0; i < axonn::kFusedConfigs; ++i)
@@ -1119,6 +1118,27 @@ int choose_fused(int64_t M, int64_t N, const DeviceState& dev) {
     }
   }
   return best;
+}
+
+// The map by which epilogues write a [rows x cols] matrix of bf16, fp32 or
+// 16-bit words: boxes of 64-byte row segments x 32 rows.
+axonn_status_t encode_out(axonn::OutMatrix* m, void* base, int64_t rows, int64_t cols, int64_t ld, bool f32) {
+  m->base = base;
+  m->ld = ld;
+  auto fn = encode_fn();
+  if (!fn) return fail(AXONN_ERR_CUDA, "cuTensorMapEncodeTiled unavailable from the driver");
+  const cuuint64_t size = f32 ? 4 : 2;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * size};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / size), 32};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = fn(&m->map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2,
+                        base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(AXONN_ERR_CUDA, "cuTensorMapEncodeTiled (output) failed (%d)", static_cast<int>(r));
+  return AXONN_OK;
 }
 
 // Everything of a fused product but its epilogue's arguments: tensor maps,
@@ -1143,9 +1163,17 @@ axonn_status_t fused_fill(axonn::FusedParams<Args>& P, const OpView& v, int conf
   const uint32_t b_cols = static_cast<uint32_t>(c.pair ? c.bn / 2 : c.bn);
   if (P.num_k > 0) {
     axonn_status_t s;
-    if (P.a_3d) s = encode_mn_3d(&P.ta, v.A, v.M, v.R, v.lda, axonn::kBK, 2);
+    // Rows of A that a CTA loads.  A product with fewer rows than the tile
+    // loads those alone (in eights, the swizzle's atom): the rest of the
+    // stage holds whatever it held, and so do accumulator rows that no
+    // epilogue looks at.  Zero-filled boxes of 128 rows bounded the one-token
+    // product, at 3.4 of 6.8 TB/s of weights.
+    uint32_t a_rows = static_cast<uint32_t>(c.pair ? c.bm / 2 : c.bm), a_box = 128;
+    if (!c.pair && !v.a_mn && v.M < 128) a_rows = a_box = static_cast<uint32_t>((v.M + 7) / 8 * 8);
+    P.load_bytes = (c.pair ? 2 : 1) * (a_rows + b_cols) * axonn::kBK * 2;
+    if (P.a_3d) s = encode_mn_3d(&P.ta, v.A, v.M, v.R, v.lda, axonn::kBK, a_rows / 64);
     else if (v.a_mn) s = encode_2d(&P.ta, v.A, v.M, v.R, v.lda, 64, axonn::kBK);
-    else s = encode_2d(&P.ta, v.A, v.R, v.M, v.lda, axonn::kBK, 128);
+    else s = encode_2d(&P.ta, v.A, v.R, v.M, v.lda, axonn::kBK, a_box);
     if (s != AXONN_OK) return s;
     if (P.b_3d) s = encode_mn_3d(&P.tb, v.B, v.N, v.R, v.ldb, axonn::kBK, b_cols / 64);
     else if (v.b_mn) s = encode_2d(&P.tb, v.B, v.N, v.R, v.ldb, 64, axonn::kBK);
@@ -1214,8 +1242,6 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
   st = check_matrix("output", C, ldc, v.M, v.N, f32);
   if (st != AXONN_OK) return st;
   axonn::EpilogueArgs e{};
-  e.out = C;
-  e.ld_out = ldc;
   e.out_f32 = f32;
   e.act = epi->act;
   st = dropout_args(epi->p, epi->rng, &e.drop);
@@ -1230,7 +1256,7 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
     st = check_matrix("pre", epi->pre, epi->ld_pre, v.M, v.N, false);
     if (st != AXONN_OK) return st;
   }
-  if (fwd) e.pre_out = static_cast<uint16_t*>(epi->pre);
+  if (fwd) e.pre_out = epi->pre != nullptr;
   else e.pre_in = static_cast<const uint16_t*>(epi->pre);
   e.ld_pre = epi->ld_pre;
   if (epi->residual) {
@@ -1255,6 +1281,8 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
     int units = 0;
     const int config = choose_fused(v.M, v.N, *dev);
     st = fused_fill(fp, v, config, 16, *dev, &units);
+    if (st == AXONN_OK) st = encode_out(&fp.out, C, v.M, v.N, ldc, f32);
+    if (st == AXONN_OK && e.pre_out) st = encode_out(&fp.out2, epi->pre, v.M, v.N, epi->ld_pre, false);
     if (st != AXONN_OK) return st;
     fp.epi = e;
     const cudaError_t ce = axonn::fused_launch(fwd ? axonn::kFusedFwd : axonn::kFusedBwd, config, fp, units,
@@ -1270,13 +1298,11 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
 }
 
 // ------------------------------------------------------------------ linear CE
-// The workspace, carved in order.  The statistics hold a group of 64 columns
-// at most (the narrowest epilogue warp), so that their size does not depend
-// on the tile chosen.
+// The workspace, carved in order.
 constexpr int64_t kCePieceStep = 256;               // columns: whole tiles of every configuration
 constexpr size_t kCePieceDefault = size_t{2} << 30;  // bytes of one piece of the vocabulary
 struct CeLayout {
-  size_t index, labels, coef, label_logit, lse2, stats, x, dx32, piece;
+  size_t index, place, labels, coef, label_logit, lse2, stats, x, dx32, piece;
   int64_t ld_x, ld_dx;
 };
 size_t up256(size_t n) { return (n + 255) & ~size_t{255}; }
@@ -1291,11 +1317,12 @@ CeLayout ce_layout(int64_t T, int64_t K, int64_t V) {
   };
   const size_t t = static_cast<size_t>(T);
   l.index = take(4 * t);
+  l.place = take(4 * t);
   l.labels = take(4 * t);
   l.coef = take(4);
   l.label_logit = take(4 * t);
   l.lse2 = take(4 * t);
-  l.stats = take(8 * t * static_cast<size_t>((V + 63) / 64));
+  l.stats = take(8 * t * static_cast<size_t>((V + axonn::kEpilogueCols - 1) / axonn::kEpilogueCols));
   l.ld_x = (K + 7) / 8 * 8;
   l.x = take(2 * t * static_cast<size_t>(l.ld_x));
   l.ld_dx = l.ld_x;
@@ -1356,19 +1383,17 @@ axonn_status_t check_ce(int64_t T, int64_t K, int64_t V, uint32_t flags) {
 // A product whose tiles are stored as they are, on the fused kernels (whose
 // extent may be the device's count).
 axonn_status_t store_product(const OpView& v, void* out, int64_t ld_out, int mode, const float* scale,
-                             const int32_t* row_map, const int32_t* count, int count_of, int group_m, const DeviceState& dev,
+                             const int32_t* count, int count_of, int group_m, const DeviceState& dev,
                              cudaStream_t stream) {
   if (v.M == 0 || v.N == 0) return AXONN_OK;
   axonn::FusedParams<axonn::StoreArgs> p;
   int units = 0;
   const int config = choose_fused(v.M, v.N, dev);
-  const axonn_status_t st = fused_fill(p, v, config, group_m, dev, &units);
+  axonn_status_t st = fused_fill(p, v, config, group_m, dev, &units);
+  if (st == AXONN_OK) st = encode_out(&p.out, out, v.M, v.N, ld_out, mode != axonn::kOutBF16);
   if (st != AXONN_OK) return st;
   p.count = count;
   p.count_of = count_of;
-  p.epi.out = out;
-  p.epi.ld_out = ld_out;
-  p.epi.row_map = row_map;
   p.epi.scale = scale;
   p.epi.mode = mode;
   AXONN_CE_RUN(axonn::store_launch(config, p, units, g_pdl.load() != 0, stream), "product");
@@ -2168,12 +2193,13 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
   a.vocab = V;
   a.grad_scale = grad_scale;
   a.index = reinterpret_cast<int32_t*>(base + l.index);
+  a.place = reinterpret_cast<int32_t*>(base + l.place);
   a.packed_labels = reinterpret_cast<int32_t*>(base + l.labels);
   a.packed_x = reinterpret_cast<uint16_t*>(base + l.x);
   a.ld_packed = l.ld_x;
   a.coef = reinterpret_cast<float*>(base + l.coef);
   a.stats = reinterpret_cast<const float2*>(base + l.stats);
-  a.group_cols = axonn::kFusedConfig[config].warp_cols;
+  a.group_cols = axonn::kEpilogueCols;
   a.groups = (V + a.group_cols - 1) / a.group_cols;
   a.label_logit = reinterpret_cast<const float*>(base + l.label_logit);
   a.lse2 = reinterpret_cast<float*>(base + l.lse2);
@@ -2206,7 +2232,8 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
     if (T == 0) return AXONN_OK;
     axonn::FusedParams<axonn::CeArgs> p;
     int units = 0;
-    const axonn_status_t s = fused_fill(p, logits_view(c0, n), config, 16, *dev, &units);
+    axonn_status_t s = fused_fill(p, logits_view(c0, n), config, 16, *dev, &units);
+    if (s == AXONN_OK && keep_piece) s = encode_out(&p.out, piece, T, n, ld_piece, false);
     if (s != AXONN_OK) return s;
     p.count = kept;
     p.count_of = 1;
@@ -2216,8 +2243,7 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
     p.epi.stats = reinterpret_cast<float2*>(base + l.stats);
     p.epi.ld_stats = T;
     p.epi.label_logit = reinterpret_cast<float*>(base + l.label_logit);
-    p.epi.piece = keep_piece ? piece : nullptr;
-    p.epi.ld_piece = ld_piece;
+    p.epi.keep_piece = keep_piece;
     p.epi.lse2 = a.lse2;
     AXONN_CE_RUN(axonn::ce_launch(kind, config, p, units, pdl, stream), "logits product");
     return AXONN_OK;
@@ -2242,19 +2268,6 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
       st = logits(axonn::kCeProb, c0, n, true);
       if (st != AXONN_OK) return st;
     }
-    if (dX) {  // dX = P . W^T, rows scattered to their places
-      OpView v = logits_view(c0, n);
-      v.A = reinterpret_cast<const char*>(piece);
-      v.lda = ld_piece;
-      v.b_mn = w_t;
-      v.N = K;
-      v.R = n;
-      const bool one = pieces == 1;
-      st = store_product(v, one ? dX : static_cast<void*>(dx32), one ? lddx : l.ld_dx,
-                         one ? axonn::kOutBF16 : (j == 0 ? axonn::kOutF32 : axonn::kOutF32Accum),
-                         a.coef, one ? a.index : nullptr, kept, 1, 16, *dev, stream);
-      if (st != AXONN_OK) return st;
-    }
     if (dW) {  // dW = X^T . P ([K x V]) or P^T . X ([V x K])
       OpView x{};
       x.R = T;
@@ -2271,12 +2284,30 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
       const int mode = (flags & AXONN_ACCUM_F32) ? axonn::kOutF32Accum
                        : (flags & AXONN_OUT_F32) ? axonn::kOutF32
                                                  : axonn::kOutBF16;
-      st = store_product(x, static_cast<char*>(dW) + off * (w_f32 ? 4 : 2), lddw, mode, a.coef, nullptr, kept, 2,
+      st = store_product(x, static_cast<char*>(dW) + off * (w_f32 ? 4 : 2), lddw, mode, a.coef, kept, 2, 16,
+                         *dev, stream);
+      if (st != AXONN_OK) return st;
+    }
+    if (dX) {
+      // dX = P . W^T, packed: in bf16 over the packed X, which nothing reads
+      // any more, or summed over the pieces in fp32
+      OpView v = logits_view(c0, n);
+      v.A = reinterpret_cast<const char*>(piece);
+      v.lda = ld_piece;
+      v.b_mn = w_t;
+      v.N = K;
+      v.R = n;
+      const bool one = pieces == 1;
+      st = store_product(v, one ? static_cast<void*>(a.packed_x) : static_cast<void*>(dx32),
+                         one ? l.ld_x : l.ld_dx,
+                         one ? axonn::kOutBF16 : (j == 0 ? axonn::kOutF32 : axonn::kOutF32Accum), a.coef, kept, 1,
                          16, *dev, stream);
       if (st != AXONN_OK) return st;
     }
   }
-  if (dX && pieces > 1) AXONN_CE_RUN(axonn::ce_scatter_launch(a, dx32, l.ld_dx, dev->sms, stream), "dX");
+  if (dX)
+    AXONN_CE_RUN(axonn::ce_unpack_launch(a, pieces == 1 ? static_cast<const void*>(a.packed_x) : dx32,
+                                         pieces == 1 ? l.ld_x : l.ld_dx, pieces > 1, dev->sms, stream), "dX");
   return ok();
 }
 

@@ -23,10 +23,8 @@ struct DropoutArgs {
 // Epilogue of Y = R + D(act(acc + b)), Z = acc + b, and of
 // dZ = act'(Z) D(acc) + R with its column sums.
 struct EpilogueArgs {
-  void* out;
-  int64_t ld_out;
   const void* bias;      // [N] or null
-  uint16_t* pre_out;     // forward: Z in bf16, or null
+  int32_t pre_out;       // forward: Z is written
   const uint16_t* pre_in;  // backward: Z
   int64_t ld_pre;
   const void* residual;  // of the output's type, or null
@@ -47,19 +45,23 @@ struct CeArgs {
   float2* stats;          // [vocabulary groups x ld_stats] (max, sum of exp) of each row and group
   int64_t ld_stats;
   float* label_logit;     // [T]
-  uint16_t* piece;        // [T x N]: distances (16 bits), or probabilities (bf16); may be null
-  int64_t ld_piece;
+  int32_t keep_piece;     // the piece [T x N] is written: distances (16 bits), or probabilities (bf16)
   const float* lse2;      // [T] logsumexp in base 2 (the recomputing product)
 };
 
 // Output of a product times a number on the device (null: 1): bf16, fp32, or
-// added into fp32; row i goes to row row_map[i] where a map is given.
+// added into fp32.
 struct StoreArgs {
-  void* out;
-  int64_t ld_out;
-  const int32_t* row_map;
   const float* scale;
   int32_t mode;  // OutMode: kOutBF16, kOutF32, kOutF32Accum
+};
+
+// A matrix that an epilogue writes: by TMA through the map, or element by
+// element.
+struct OutMatrix {
+  CUtensorMap map;
+  void* base;
+  int64_t ld;
 };
 
 // One product with a fused epilogue: C[M x N] = A . B with the operand
@@ -67,6 +69,8 @@ struct StoreArgs {
 template <class Args>
 struct FusedParams {
   CUtensorMap ta, tb;
+  OutMatrix out;   // the output (the piece, for the linear cross entropy)
+  OutMatrix out2;  // the forward's pre-activation
   Args epi;
   // A count on the device that takes the place of M (count_of = 1) or of the
   // reduction's length (2; rows of both operands from the count to the next
@@ -77,6 +81,7 @@ struct FusedParams {
   int32_t tiles_m, tiles_n;
   uint32_t idesc;
   int32_t a_mn, b_mn, a_3d, b_3d;
+  uint32_t load_bytes;  // of one stage (of both CTAs of a pair)
   int32_t group_m;
   int32_t l2_keep;
   float l2_keep_frac;
@@ -85,26 +90,28 @@ struct FusedParams {
 };
 
 // Tiles of the fused products: 0 a CTA pair's 256 x 256, 1 128 x 128,
-// 2 128 x 64.
+// 2 128 x 64, 3 a CTA pair's 512 x 256.
 struct FusedConfig {
   int bm, bn;
   bool pair;
   int mma_m;
-  int warp_cols;  // columns of one epilogue warp: the groups of CeArgs::stats
 };
-constexpr int kFusedConfigs = 3;
+constexpr int kEpilogueCols = 64;  // columns of one epilogue warp: the groups of CeArgs::stats
+constexpr int kFusedConfigs = 4;
 constexpr FusedConfig kFusedConfig[kFusedConfigs] = {
-    {256, 256, true, 256, 128}, {128, 128, false, 128, 128}, {128, 64, false, 128, 64}};
+    {256, 256, true, 256}, {128, 128, false, 128}, {128, 64, false, 128}, {512, 256, true, 256}};
 
 enum FusedKind : int { kFusedFwd = 0, kFusedBwd = 1 };
 enum CeKind : int { kCeStats = 0, kCeProb = 1 };
 
-cudaError_t fused_init();  // shared-memory limits on the current device
+// Shared-memory limits on the current device; *regs_ok = false if a kernel
+// was not built with the registers that its split assumes.
+cudaError_t fused_init(bool* regs_ok);
 cudaError_t fused_launch(FusedKind kind, int config, const FusedParams<EpilogueArgs>& p, int units,
                          bool pdl, cudaStream_t stream);
 cudaError_t fused_take_status(unsigned long long* word, cudaStream_t stream);
 
-cudaError_t ce_init();
+cudaError_t ce_init(bool* regs_ok);
 cudaError_t ce_launch(CeKind kind, int config, const FusedParams<CeArgs>& p, int units, bool pdl,
                       cudaStream_t stream);
 cudaError_t store_launch(int config, const FusedParams<StoreArgs>& p, int units, bool pdl,

@@ -93,13 +93,12 @@ __device__ __forceinline__ float act_slope(float z) {
   return 1.0f;
 }
 
-// v[j] = act(v[j]) and v[j] *= act'(z[j]) over N values; the switch is
-// outside the loop.
-template <int N>
-__device__ __forceinline__ void apply_act(int act, float (&v)[N]) {
+// v[j] = act(v[j]), and v[j] *= act'(z_j) for z in bf16 pairs, over 16 values;
+// the switch is outside the loop.
+__device__ __forceinline__ void apply_act16(int act, float* v) {
 #define AXONN_EACH(A)                        \
   case A:                                    \
-    _Pragma("unroll") for (int j = 0; j < N; ++j) v[j] = act_value<A>(v[j]); \
+    _Pragma("unroll") for (int j = 0; j < 16; ++j) v[j] = act_value<A>(v[j]); \
     break
   switch (act) {
     AXONN_EACH(kActRelu);
@@ -110,11 +109,11 @@ __device__ __forceinline__ void apply_act(int act, float (&v)[N]) {
   }
 #undef AXONN_EACH
 }
-template <int N>
-__device__ __forceinline__ void apply_slope(int act, float (&v)[N], const float (&z)[N]) {
-#define AXONN_EACH(A)                        \
-  case A:                                    \
-    _Pragma("unroll") for (int j = 0; j < N; ++j) v[j] *= act_slope<A>(z[j]); \
+__device__ __forceinline__ void apply_slope16(int act, float* v, const uint32_t* z) {
+#define AXONN_EACH(A)                                                                     \
+  case A:                                                                                 \
+    _Pragma("unroll") for (int j = 0; j < 16; ++j) v[j] *=                                \
+        act_slope<A>(__uint_as_float((j & 1) ? z[j >> 1] & 0xFFFF0000u : z[j >> 1] << 16)); \
     break
   switch (act) {
     AXONN_EACH(kActRelu);
@@ -196,76 +195,60 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-// 32 consecutive elements of a row, as loaded: bf16 in 16 words or fp32 in
-// 32.  `n` of them exist; a full segment is 16-byte aligned (base pointers
+// 16 consecutive elements of a row, as loaded: bf16 in 8 words or fp32 in
+// 16.  `n` of them exist; a full segment is 16-byte aligned (base pointers
 // and leading dimensions are checked by the host, columns are multiples of
-// 32), a short one is read element by element so that nothing past the row's
+// 16), a short one is read element by element so that nothing past the row's
 // end is touched.
-__device__ __forceinline__ void load_row32_bf16(const uint16_t* p, int n, uint32_t (&w)[16]) {
-  if (n >= 32) {
+template <bool kF32>
+struct Row16 {
+  uint32_t w[kF32 ? 16 : 8];
+  __device__ __forceinline__ void load(const void* base, int64_t at, int n) {
+    if constexpr (kF32) {
+      const float* p = reinterpret_cast<const float*>(base) + at;
+      if (n >= 16) {
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const uint4 a = reinterpret_cast<const uint4*>(p)[v];
-      w[4 * v] = a.x;
-      w[4 * v + 1] = a.y;
-      w[4 * v + 2] = a.z;
-      w[4 * v + 3] = a.w;
-    }
-    return;
-  }
+        for (int v = 0; v < 4; ++v) {
+          const uint4 a = reinterpret_cast<const uint4*>(p)[v];
+          w[4 * v] = a.x;
+          w[4 * v + 1] = a.y;
+          w[4 * v + 2] = a.z;
+          w[4 * v + 3] = a.w;
+        }
+      } else {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint32_t lo = 2 * j < n ? p[2 * j] : 0u;
-    const uint32_t hi = 2 * j + 1 < n ? p[2 * j + 1] : 0u;
-    w[j] = lo | (hi << 16);
-  }
-}
-
-__device__ __forceinline__ void unpack32(const uint32_t (&w)[16], float (&x)[32]) {
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    x[2 * j] = __uint_as_float(w[j] << 16);
-    x[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-  }
-}
-
-// 32 columns of one output row (n of them exist), rounded to nearest even
-// once when bf16.  A thread writes its own row, so 32-byte vectors (whole L2
-// sectors) where the address allows them.
-__device__ __forceinline__ void store_row32_u16(uint16_t* p, int n, const uint32_t (&w)[16]) {
-  if (n >= 32) {
-    if ((reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
-      st_global_v8(p, w);
-      st_global_v8(p + 16, w + 8);
+        for (int j = 0; j < 16; ++j) w[j] = j < n ? __float_as_uint(p[j]) : 0u;
+      }
     } else {
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + at;
+      if (n >= 16) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        reinterpret_cast<uint4*>(p)[v] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+        for (int v = 0; v < 2; ++v) {
+          const uint4 a = reinterpret_cast<const uint4*>(p)[v];
+          w[4 * v] = a.x;
+          w[4 * v + 1] = a.y;
+          w[4 * v + 2] = a.z;
+          w[4 * v + 3] = a.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t lo = 2 * j < n ? p[2 * j] : 0u;
+          const uint32_t hi = 2 * j + 1 < n ? p[2 * j + 1] : 0u;
+          w[j] = lo | (hi << 16);
+        }
+      }
     }
-    return;
   }
-#pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (j < n) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
-}
-
-__device__ __forceinline__ void store_row32_bf16(uint16_t* p, int n, const float (&x)[32]) {
-  uint32_t w[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) w[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-  store_row32_u16(p, n, w);
-}
-
-__device__ __forceinline__ void store_row32_f32(float* p, int n, const float (&x)[32]) {
-  if (n >= 32) {
-#pragma unroll
-    for (int v = 0; v < 8; ++v)
-      reinterpret_cast<float4*>(p)[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
-    return;
+  __device__ __forceinline__ float value(int j) const {  // j known at compile time
+    if constexpr (kF32) return __uint_as_float(w[j]);
+    else return __uint_as_float((j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
   }
-#pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (j < n) p[j] = x[j];
+};
+
+// Asks for a line to be brought into L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }
 
 // The linear cross entropy keeps a logit z of a piece as its distance below

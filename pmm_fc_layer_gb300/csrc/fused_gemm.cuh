@@ -6,18 +6,22 @@
 // operand stages by TMA, warp 1 issues the MMAs, the others are the
 // epilogue.  What differs is the balance.  A fused epilogue costs several
 // times a plain store (an activation, a generator call for every eight
-// elements, one or two operands to read), so
-//  - the accumulator is always double-buffered in TMEM (2 x BN columns):
-//    the epilogue has a whole tile's mainloop to finish in, where the
-//    512 x 256 tile of the plain products would hold up the next tile's MMAs
-//    for as long as the arithmetic takes;
-//  - the 256-column tile has two epilogue warps per 32 rows, 128 columns
-//    each;
-//  - every operand that the epilogue reads is asked for before its use:
-//    the first 32 columns before the accumulator is ready, the next 32
-//    while the present ones are worked on.
-// kPair: a CTA pair shares one 256 x 256 tile (cta_group::2), each CTA
-// loading its 128 rows of A and its half of B (32 KB a stage, 6 stages).
+// elements, one or two operands to read), so it has to run beside the
+// mainloop, in one of two ways:
+//  - kHalves = 1 (tiles of 128 rows a CTA): the accumulator is
+//    double-buffered in TMEM (2 x BN columns), and the epilogue (a warp for
+//    every 32 rows x 64 columns) has a whole tile's mainloop to finish in.
+//  - kHalves = 2 (a CTA pair's 512 x 256 tile): two accumulators of 128 rows
+//    a CTA, which share each B slice (a quarter fewer operand bytes a
+//    multiply-add than 256 x 256, and under the power cap 10 to 20 % faster)
+//    and fill TMEM.  Sixteen epilogue warps take one half at a time: they
+//    move it into registers whole (64 columns a thread), release it, and
+//    then work on it.  The MMAs are issued with the halves out of step by
+//    kSkew stages: at a tile's end half 0 runs ahead and is done first, at
+//    the next one's start it begins first, and the epilogue's work on half 0
+//    fits between the two.
+// kPair: a CTA pair shares one tile (cta_group::2), each CTA loading its own
+// rows of A and its half of B.
 // Waits are bounded, and an expired one is recorded and reported, as in the
 // plain products.
 #pragma once
@@ -27,20 +31,35 @@
 
 namespace axonn {
 
-template <int BN, int STAGES, bool kPair>
+template <int BN, int STAGES, bool kPair, int kHalves>
 struct FusedLayout {
-  static constexpr int kABytes = 128 * kBK * 2;
+  static constexpr int kAHalfBytes = 128 * kBK * 2;
+  static constexpr int kABytes = kHalves * kAHalfBytes;
   static constexpr int kBCols = kPair ? BN / 2 : BN;  // columns of B one CTA loads
   static constexpr int kBBytes = kBCols * kBK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kNumBars = 2 * STAGES + 5;
-  static constexpr int kEpiWarpSets = BN == 256 ? 2 : 1;  // warps per 32 rows
-  static constexpr int kEpi = 4 * kEpiWarpSets;
-  static constexpr int kThreads = 64 + 32 * kEpi;
-  static constexpr int kWarpCols = BN / kEpiWarpSets;
-  // 1024 B of slack to align the ring, the ring, barriers, TMEM slot, abort
-  static constexpr int kBytes = 1024 + STAGES * kStageBytes + kNumBars * 8 + 16;
+  static constexpr int kSlotBytes = 2048;  // an epilogue warp's staging slot: 32 rows of 64 bytes
+  static constexpr int kEpiSets = BN / 64;  // warps per 32 rows, 64 columns each
+  static constexpr int kEpi = 4 * kEpiSets;
+  static constexpr int kEpiFirst = kHalves == 2 ? 4 : 2;
+  static constexpr int kThreads = 32 * (kEpiFirst + kEpi);
+  static constexpr int kWarpCols = 64;
+  // 1024 B of slack to align the ring, the ring, the staging slots, barriers,
+  // TMEM slot, abort flag
+  static constexpr int kBytes = 1024 + STAGES * kStageBytes + kEpi * kSlotBytes + kNumBars * 8 + 16;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
 };
+
+// Registers of a thread of the 20-warp kernels: warpgroup 0 (producer, MMA
+// issuer) gives up what the four epilogue warpgroups, which hold 64
+// accumulator words a thread, take.  The shares add up to the launch's
+// allocation; the host checks that the kernels were built with it.
+constexpr int kFusedRegsAtLaunch = 96;
+constexpr int kFusedRegsControl = 32;
+constexpr int kFusedRegsEpilogue = 112;
+static_assert(128 * kFusedRegsControl + 512 * kFusedRegsEpilogue <= 640 * kFusedRegsAtLaunch,
+              "register split exceeds the launch allocation");
 
 // Tile t of the grouped rasterisation (see decode_tile in gemm_kernel.cuh):
 // group_m > 0 walks that many tile rows before the next tile column,
@@ -65,13 +84,17 @@ struct EpiTile {
   uint32_t t_row;
   int row, col;
   int M, N;
+  int rows;                          // rows that stores write: M, unless an epilogue pads
+  uint32_t slot;                     // shared memory, kSlotBytes
+  const OutMatrix* out;
+  const OutMatrix* out2;
   bool has;  // false: the reduction is empty and the accumulator is zero
 };
 
 __device__ __forceinline__ void load_acc32(const EpiTile& t, int c, float (&x)[32]) {
   uint32_t r[32];
   if (t.has) {
-    __syncwarp();  // the whole warp loads: lanes past the last row come back from skipped stores
+    __syncwarp();  // the whole warp loads: lanes past the last row come back from skipped work
     tmem_ld_32x32b_x32(t.t_row + c * 32, r);
     tmem_ld_wait();
 #pragma unroll
@@ -82,20 +105,175 @@ __device__ __forceinline__ void load_acc32(const EpiTile& t, int c, float (&x)[3
   }
 }
 
-template <class Epi, int BN, int STAGES, bool kPair>
-__global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair>::kThreads, 1)
+// The slot's layout: row r's 16-byte chunk c at c ^ (r / 2 % 4) of its 64
+// bytes, the 64-byte swizzle of TMA.  A warp's row-wise accesses (a lane its
+// own row) and its chunk-wise ones (four lanes a row) both spread over the
+// banks.
+__device__ __forceinline__ uint32_t slot_at(const EpiTile& t, int row, int chunk) {
+  return t.slot + static_cast<uint32_t>(row * 64 + ((chunk ^ ((row >> 1) & 3)) * 16));
+}
+
+// 64 bytes of each of the warp's 32 rows of a matrix that the epilogue reads,
+// at column `col`.  Four lanes read a row's 64 bytes (a load touches 8 lines;
+// a lane reading its own row would touch 32, at 16 bytes a cycle), and the
+// slot hands every lane its own row: start() asks for the words, finish()
+// exchanges them.  Nothing past row M or column N is read (zeros there).
+template <typename T>
+struct RowSegment {
+  uint4 v[4];
+  __device__ __forceinline__ void start(const EpiTile& t, const void* base, int64_t ld, int col) {
+    constexpr int kPer16 = 16 / static_cast<int>(sizeof(T));
+    const int lane = threadIdx.x & 31;
+    const int row0 = t.row - lane, c = col + (lane & 3) * kPer16;
+    const T* p = static_cast<const T*>(base) + static_cast<int64_t>(row0 + (lane >> 2)) * ld + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (row0 + 8 * i + (lane >> 2) < t.M && c < t.N) {
+        const T* q = p + 8 * i * ld;
+        if (c + kPer16 <= t.N) {
+          v[i] = *reinterpret_cast<const uint4*>(q);
+        } else {  // the row's last, partial 16 bytes
+          uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < kPer16; ++j)
+            if (c + j < t.N) {
+              if constexpr (sizeof(T) == 4) w[j] = q[j];
+              else w[j >> 1] |= static_cast<uint32_t>(q[j]) << (16 * (j & 1));
+            }
+          v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+    }
+  }
+  // This lane's row: 16 words.
+  __device__ __forceinline__ void finish(const EpiTile& t, uint32_t (&w)[16]) const {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last store has read it
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      st_shared_v4(slot_at(t, 8 * i + (lane >> 2), lane & 3), v[i].x, v[i].y, v[i].z, v[i].w);
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float4 f = ld_shared_v4(slot_at(t, lane, c));
+      w[4 * c] = __float_as_uint(f.x);
+      w[4 * c + 1] = __float_as_uint(f.y);
+      w[4 * c + 2] = __float_as_uint(f.z);
+      w[4 * c + 3] = __float_as_uint(f.w);
+    }
+    __syncwarp();
+  }
+};
+
+// Writes 64 bytes of each of the warp's 32 rows (16 words a lane, its own
+// row's) at column `col` of a matrix: through the warp's staging slot and one
+// TMA store.  Row-wise stores from registers, 32 bytes a lane, moved about 18
+// bytes a cycle and SM and held up the next tile's MMAs behind the registers
+// they came from.  Rows past t.rows and columns past t.N are not written;
+// where a row's last 16 bytes are only partly the matrix' own (a TMA store
+// writes them whole), that segment goes element by element.
+template <typename T>
+__device__ __forceinline__ void store_segment(const EpiTile& t, const OutMatrix* m, int col, const uint32_t (&w)[16]) {
+  constexpr int kPer16 = 16 / static_cast<int>(sizeof(T)), kCols = 64 / static_cast<int>(sizeof(T));
+  const int lane = threadIdx.x & 31;
+  if (col + kCols > t.N && t.N % kPer16 != 0) {
+    if (t.row < t.rows) {
+      T* p = static_cast<T*>(m->base) + t.row * m->ld + col;
+      const int n = t.N - col;
+#pragma unroll
+      for (int j = 0; j < kCols; ++j)
+        if (j < n) p[j] = static_cast<T>(sizeof(T) == 4 ? w[j % 16] : w[(j >> 1) % 16] >> (16 * (j & 1)));
+    }
+    return;
+  }
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the slot has been read
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    st_shared_v4(slot_at(t, lane, c), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+  fence_proxy_async_shared();
+  __syncwarp();
+  if (lane == 0 && t.row < t.rows) {  // lane 0 has the first row
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(&m->map)),
+                 "r"(t.slot), "r"(col), "r"(t.row)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+
+// 32 columns of the warp's rows, in bf16 (one rounding) or fp32.
+__device__ __forceinline__ void store_bf16(const EpiTile& t, const OutMatrix* m, int col, const float (&x)[32]) {
+  uint32_t w[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) w[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+  store_segment<uint16_t>(t, m, col, w);
+}
+__device__ __forceinline__ void store_f32(const EpiTile& t, const OutMatrix* m, int col, const float (&x)[32]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (col + 16 * h >= t.N) break;
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(x[16 * h + j]);
+    store_segment<uint32_t>(t, m, col + 16 * h, w);
+  }
+}
+
+// The 32-column steps of a tile part, for an epilogue given as
+//   void prefetch(args, tile, cols)        asks for what it will read into L2
+//   void step(args, state, tile, c, x)     works on columns 32 c .. of the part
+// The operands are asked for before the accumulator is ready.  kHold: the
+// whole part goes to registers and TMEM is released before any of the work.
+template <class Epi, int kCols, bool kHold, class Ready, class Release>
+__device__ __forceinline__ bool epilogue_steps(const typename Epi::Args& a, const typename Epi::State& st,
+                                               const EpiTile& t, Ready&& ready, Release&& release) {
+  if (t.col < t.N && t.row < t.M) Epi::prefetch(a, t, min(kCols, t.N - t.col));
+  if (!ready()) return false;
+  if constexpr (kHold) {
+    float x[kCols / 32][32];
+#pragma unroll
+    for (int c = 0; c < kCols / 32; ++c)
+      if (t.col + 32 * c < t.N) load_acc32(t, c, x[c]);
+    release();
+#pragma unroll
+    for (int c = 0; c < kCols / 32; ++c)
+      if (t.col + 32 * c < t.N) Epi::step(a, st, t, c, x[c]);
+  } else {
+#pragma unroll 1
+    for (int c = 0; c < kCols / 32; ++c) {
+      if (t.col + 32 * c >= t.N) break;
+      float x[32];
+      load_acc32(t, c, x);
+      Epi::step(a, st, t, c, x);
+    }
+    release();
+  }
+  return true;
+}
+
+template <class Epi, int BN, int STAGES, bool kPair, int kHalves>
+__global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThreads, 1)
     fused_gemm_kernel(const __grid_constant__ FusedParams<typename Epi::Args> P) {
-  using L = FusedLayout<BN, STAGES, kPair>;
+  using L = FusedLayout<BN, STAGES, kPair, kHalves>;
   constexpr uint32_t kAccCols = BN < 128 ? 128 : BN;  // TMEM columns of one accumulator
   constexpr uint32_t kTmemCols = 2 * kAccCols;
-  constexpr int kTileM = kPair ? 256 : 128;
+  constexpr int kCtaM = 128 * kHalves;
+  constexpr int kTileM = kPair ? 2 * kCtaM : kCtaM;
+  // Stages by which half 0 runs ahead at a tile's two ends: all the ring
+  // holds.
+  constexpr int kSkew = STAGES;
   static_assert(kTmemCols == 256 || kTmemCols == 512, "TMEM columns");
+  static_assert(kHalves == 1 || kPair, "two halves: a CTA pair's tile");
 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t raw = smem_addr(smem_raw);
   const uint32_t ring = (raw + 1023u) & ~1023u;
   uint8_t* ring_ptr = smem_raw + (ring - raw);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(ring_ptr + STAGES * L::kStageBytes);
+  const uint32_t slots = ring + STAGES * L::kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring_ptr + STAGES * L::kStageBytes + L::kEpi * L::kSlotBytes);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -159,6 +337,9 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair>::kThreads, 1)
   }
   const int total = tiles_m * P.tiles_n;
 
+  if constexpr (kHalves == 2) {
+    if (warp < L::kEpiFirst) setmaxnreg_dec<kFusedRegsControl>();
+  }
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0 && P.inject != 1) {
@@ -170,22 +351,28 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair>::kThreads, 1)
       for (int t = unit; ok && t < total; t += units) {
         int mb, nb;
         fused_tile(t, P.group_m, tiles_m, P.tiles_n, mb, nb);
-        const int m0 = mb * kTileM + static_cast<int>(rank) * 128;
+        const int m0 = mb * kTileM + static_cast<int>(rank) * kCtaM;
         const int n0 = nb * BN + static_cast<int>(rank) * L::kBCols;
         for (int k = 0; k < num_k; ++k) {
           ok = wait_bounded(empty_bar(stage), phase ^ 1u, tmo, abort_flag, kSiteProducerEmpty);
           if (!ok) break;
-          if (leader) mbar_arrive_expect_tx(full_bar(stage), (kPair ? 2 : 1) * L::kStageBytes);
+          if (leader) mbar_arrive_expect_tx(full_bar(stage), P.load_bytes);
           const int r0 = k * kBK;
           if constexpr (kPair) {
             const uint32_t fb = mapa_shared(full_bar(stage), 0);
             if (P.a_3d) {
               tma_load_3d_pair(a_tile(stage), &P.ta, fb, 0, r0, m0 / 64, pol_a);
-            } else if (P.a_mn) {
-              tma_load_2d_pair(a_tile(stage), &P.ta, fb, m0, r0, pol_a);
-              tma_load_2d_pair(a_tile(stage) + kBK * 128, &P.ta, fb, m0 + 64, r0, pol_a);
             } else {
-              tma_load_2d_pair(a_tile(stage), &P.ta, fb, r0, m0, pol_a);
+#pragma unroll
+              for (int h = 0; h < kHalves; ++h) {
+                const uint32_t at = a_tile(stage) + h * L::kAHalfBytes;
+                if (P.a_mn) {
+                  tma_load_2d_pair(at, &P.ta, fb, m0 + 128 * h, r0, pol_a);
+                  tma_load_2d_pair(at + kBK * 128, &P.ta, fb, m0 + 128 * h + 64, r0, pol_a);
+                } else {
+                  tma_load_2d_pair(at, &P.ta, fb, r0, m0 + 128 * h, pol_a);
+                }
+              }
             }
             if (P.b_3d) {
               tma_load_3d_pair(b_tile(stage), &P.tb, fb, 0, r0, n0 / 64, pol_b);
@@ -236,79 +423,154 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair>::kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && leader && num_k > 0) {
-      int stage = 0;
-      uint32_t phase = 0, acc = 0;
+      uint32_t acc = 0;
       bool ok = true;
-      for (int t = unit; ok && t < total; t += units, ++acc) {
-        const uint32_t b = acc & 1u;
-        ok = wait_bounded(tempty_bar(b), ((acc >> 1) & 1u) ^ 1u, tmo, abort_flag, kSiteMmaTmemEmpty);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + b * kAccCols;
-        for (int k = 0; k < num_k; ++k) {
-          ok = wait_bounded(full_bar(stage), phase, tmo, abort_flag, kSiteMmaFull);
+      // The MMAs of one stage into one accumulator.
+      auto multiply = [&](int stage, int half, uint32_t d_tmem, bool first) {
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk) {
+          const uint64_t ad = operand_desc<kBK>(a_tile(stage) + half * L::kAHalfBytes, kk, P.a_mn);
+          const uint64_t bd = operand_desc<kBK>(b_tile(stage), kk, P.b_mn);
+          const uint32_t add = (!first || kk != 0) ? 1u : 0u;
+          if constexpr (kPair) umma_bf16_pair(d_tmem, ad, bd, P.idesc, add);
+          else umma_bf16(d_tmem, ad, bd, P.idesc, add);
+        }
+      };
+      auto commit = [&](uint32_t bar) {
+        if constexpr (kPair) umma_commit_pair_mc(bar, 0x3);
+        else umma_commit(bar);
+      };
+      if constexpr (kHalves == 1) {
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int t = unit; ok && t < total; t += units, ++acc) {
+          const uint32_t b = acc & 1u;
+          ok = wait_bounded(tempty_bar(b), ((acc >> 1) & 1u) ^ 1u, tmo, abort_flag, kSiteMmaTmemEmpty);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kBK / 16; ++kk) {
-            const uint64_t ad = operand_desc<kBK>(a_tile(stage), kk, P.a_mn);
-            const uint64_t bd = operand_desc<kBK>(b_tile(stage), kk, P.b_mn);
-            const uint32_t add = (k != 0 || kk != 0) ? 1u : 0u;
-            if constexpr (kPair) umma_bf16_pair(d_tmem, ad, bd, P.idesc, add);
-            else umma_bf16(d_tmem, ad, bd, P.idesc, add);
+          for (int k = 0; k < num_k; ++k) {
+            ok = wait_bounded(full_bar(stage), phase, tmo, abort_flag, kSiteMmaFull);
+            if (!ok) break;
+            tc_fence_after();
+            multiply(stage, 0, tmem_base + b * kAccCols, k == 0);
+            commit(empty_bar(stage));
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          if constexpr (kPair) umma_commit_pair_mc(empty_bar(stage), 0x3);
-          else umma_commit(empty_bar(stage));
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (!ok) break;
+          commit(tfull_bar(b));
         }
-        if (!ok) break;
-        if constexpr (kPair) umma_commit_pair_mc(tfull_bar(b), 0x3);
-        else umma_commit(tfull_bar(b));
+      } else {
+        // Half 0 runs stages [0, a), then both halves alternate, then half 0
+        // runs [e, num_k); half 1 follows at either end.  No stage is held
+        // over more than the ring: kSkew <= STAGES.
+        const int a = min(kSkew, num_k), e = max(a, num_k - kSkew);
+        uint32_t base = 0;  // stages consumed before this tile
+        auto run = [&](int half, int k0, int k1, bool wait_full, bool free_stage) -> bool {
+          for (int k = k0; k < k1; ++k) {
+            const uint32_t i = base + k;
+            const int stage = static_cast<int>(i % STAGES);
+            if (wait_full) {
+              if (!wait_bounded(full_bar(stage), (i / STAGES) & 1u, tmo, abort_flag, kSiteMmaFull)) return false;
+              tc_fence_after();
+            }
+            multiply(stage, half, tmem_base + half * kAccCols, k == 0);
+            if (free_stage) commit(empty_bar(stage));
+          }
+          return true;
+        };
+        for (int t = unit; ok && t < total; t += units, ++acc) {
+          const uint32_t parity = (acc & 1u) ^ 1u;
+          ok = wait_bounded(tempty_bar(0), parity, tmo, abort_flag, kSiteMmaTmemEmpty);
+          if (!ok) break;
+          tc_fence_after();
+          ok = run(0, 0, a, true, false);
+          if (!ok) break;
+          if (a == num_k) commit(tfull_bar(0));
+          ok = wait_bounded(tempty_bar(1), parity, tmo, abort_flag, kSiteMmaTmemEmpty);
+          if (!ok) break;
+          tc_fence_after();
+          ok = run(1, 0, a, false, true);
+          // in step: both halves take a B slice one after the other
+          for (int k = a; ok && k < e; ++k) {
+            const uint32_t i = base + k;
+            const int stage = static_cast<int>(i % STAGES);
+            ok = wait_bounded(full_bar(stage), (i / STAGES) & 1u, tmo, abort_flag, kSiteMmaFull);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < kBK / 16; ++kk) {
+              const uint64_t bd = operand_desc<kBK>(b_tile(stage), kk, P.b_mn);
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                umma_bf16_pair(tmem_base + h * kAccCols,
+                               operand_desc<kBK>(a_tile(stage) + h * L::kAHalfBytes, kk, P.a_mn), bd, P.idesc,
+                               (k != 0 || kk != 0) ? 1u : 0u);
+            }
+            commit(empty_bar(stage));
+          }
+          ok = ok && run(0, e, num_k, true, false);
+          if (!ok) break;
+          if (a < num_k) commit(tfull_bar(0));
+          run(1, e, num_k, false, true);
+          commit(tfull_bar(1));
+          base += static_cast<uint32_t>(num_k);
+        }
       }
       // Every MMA of this thread is done before TMEM is released.
       if constexpr (kPair) umma_commit_pair(mma_done_bar);
       else umma_commit(mma_done_bar);
       wait_bounded(mma_done_bar, 0, tmo, abort_flag, kSiteDrainMma, false);
     }
-  } else {
+  } else if (warp >= L::kEpiFirst) {
+    if constexpr (kHalves == 2) setmaxnreg_inc<kFusedRegsEpilogue>();
     // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;         // the TMEM lane quarter this warp may access
-    const int set = (warp - 2) >> 2;  // which columns of the tile
+    const int q = warp & 3;  // the TMEM lane quarter this warp may access
+    const int set = (warp - L::kEpiFirst) >> 2;  // which columns of the tile
     typename Epi::State st = Epi::begin(P.epi);
     uint32_t acc = 0;
     bool ok = true;
     for (int t = unit; ok && t < total; t += units, ++acc) {
       int mb, nb;
       fused_tile(t, P.group_m, tiles_m, P.tiles_n, mb, nb);
-      const uint32_t b = acc & 1u;
-      EpiTile tile;
-      tile.t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * kAccCols + set * L::kWarpCols;
-      tile.row = mb * kTileM + static_cast<int>(rank) * 128 + q * 32 + lane;
-      tile.col = nb * BN + set * L::kWarpCols;
-      tile.M = M;
-      tile.N = P.N;
-      tile.has = num_k > 0;
-      auto ready = [&]() -> bool {
-        if (!tile.has) return true;
-        int got = 1;
-        if (lane == 0)
-          got = wait_bounded(tfull_bar(b), (acc >> 1) & 1u, tmo, abort_flag, kSiteEpiTmemFull);
-        got = __shfl_sync(0xFFFFFFFFu, got, 0);
-        tc_fence_after();
-        return got != 0;
-      };
-      ok = Epi::template run<L::kWarpCols>(P.epi, st, tile, ready);
-      if (!ok) break;
-      tc_fence_before();
-      __syncwarp();
-      if (tile.has && lane == 0) {
-        if (leader) mbar_arrive(tempty_bar(b));
-        else mbar_arrive_cluster(mapa_shared(tempty_bar(b), 0));
+#pragma unroll 1
+      for (int half = 0; ok && half < kHalves; ++half) {
+        // buffers alternate by tile (one half), or belong to the halves
+        const uint32_t b = kHalves == 1 ? acc & 1u : static_cast<uint32_t>(half);
+        const uint32_t parity = kHalves == 1 ? (acc >> 1) & 1u : acc & 1u;
+        EpiTile tile;
+        tile.t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * kAccCols + set * L::kWarpCols;
+        tile.row = mb * kTileM + static_cast<int>(rank) * kCtaM + half * 128 + q * 32 + lane;
+        tile.col = nb * BN + set * L::kWarpCols;
+        tile.M = tile.rows = M;
+        tile.N = P.N;
+        tile.slot = slots + static_cast<uint32_t>((warp - L::kEpiFirst) * L::kSlotBytes);
+        tile.out = &P.out;
+        tile.out2 = &P.out2;
+        tile.has = num_k > 0;
+        auto ready = [&]() -> bool {
+          if (!tile.has) return true;
+          int got = 1;
+          if (lane == 0) got = wait_bounded(tfull_bar(b), parity, tmo, abort_flag, kSiteEpiTmemFull);
+          got = __shfl_sync(0xFFFFFFFFu, got, 0);
+          tc_fence_after();
+          return got != 0;
+        };
+        auto release = [&]() {  // once, when this warp has read its part
+          tc_fence_before();
+          __syncwarp();
+          if (tile.has && lane == 0) {
+            if (leader) mbar_arrive(tempty_bar(b));
+            else mbar_arrive_cluster(mapa_shared(tempty_bar(b), 0));
+          }
+        };
+        ok = Epi::template run<L::kWarpCols, kHalves == 2>(P.epi, st, tile, ready, release);
       }
     }
+    // this warp's stores are complete before the CTA may exit
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
@@ -324,11 +586,11 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair>::kThreads, 1)
 }
 
 // Shared-memory limit and launch of one instantiation.
-template <class Epi, int BN, int STAGES, bool kPair>
+template <class Epi, int BN, int STAGES, bool kPair, int kHalves>
 struct Fused {
-  using L = FusedLayout<BN, STAGES, kPair>;
+  using L = FusedLayout<BN, STAGES, kPair, kHalves>;
   static cudaError_t init() {
-    return cudaFuncSetAttribute(fused_gemm_kernel<Epi, BN, STAGES, kPair>,
+    return cudaFuncSetAttribute(fused_gemm_kernel<Epi, BN, STAGES, kPair, kHalves>,
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   }
   static cudaError_t launch(const FusedParams<typename Epi::Args>& p, int units, bool pdl,
@@ -352,27 +614,41 @@ struct Fused {
     }
     cfg.attrs = attr;
     cfg.numAttrs = static_cast<unsigned>(n);
-    return cudaLaunchKernelEx(&cfg, fused_gemm_kernel<Epi, BN, STAGES, kPair>, p);
+    return cudaLaunchKernelEx(&cfg, fused_gemm_kernel<Epi, BN, STAGES, kPair, kHalves>, p);
   }
 };
 
-constexpr int kFusedPairStages = 6, kFused128Stages = 6, kFused64Stages = 8;
-
+// The configurations of kFusedConfig, in its order.
 template <class Epi>
-cudaError_t fused_init_all() {
-  cudaError_t e = Fused<Epi, 256, kFusedPairStages, true>::init();
-  if (e == cudaSuccess) e = Fused<Epi, 128, kFused128Stages, false>::init();
-  if (e == cudaSuccess) e = Fused<Epi, 64, kFused64Stages, false>::init();
-  return e;
+using FusedC0 = Fused<Epi, 256, 6, true, 1>;
+template <class Epi>
+using FusedC1 = Fused<Epi, 128, 6, false, 1>;
+template <class Epi>
+using FusedC2 = Fused<Epi, 64, 8, false, 1>;
+template <class Epi>
+using FusedC3 = Fused<Epi, 256, 4, true, 2>;
+
+// *regs_ok becomes false if a register split would not find its registers.
+template <class Epi>
+cudaError_t fused_init_all(bool* regs_ok) {
+  cudaFuncAttributes attr = {};
+  const cudaError_t q =
+      cudaFuncGetAttributes(&attr, reinterpret_cast<const void*>(fused_gemm_kernel<Epi, 256, 4, true, 2>));
+  if (q != cudaSuccess) return q;
+  if (attr.numRegs != kFusedRegsAtLaunch) *regs_ok = false;
+  for (cudaError_t e : {FusedC0<Epi>::init(), FusedC1<Epi>::init(), FusedC2<Epi>::init(), FusedC3<Epi>::init()})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
 }
 
 template <class Epi>
 cudaError_t fused_launch_config(int config, const FusedParams<typename Epi::Args>& p, int units, bool pdl,
                                 cudaStream_t s) {
   switch (config) {
-    case 0: return Fused<Epi, 256, kFusedPairStages, true>::launch(p, units, pdl, s);
-    case 1: return Fused<Epi, 128, kFused128Stages, false>::launch(p, units, pdl, s);
-    case 2: return Fused<Epi, 64, kFused64Stages, false>::launch(p, units, pdl, s);
+    case 0: return FusedC0<Epi>::launch(p, units, pdl, s);
+    case 1: return FusedC1<Epi>::launch(p, units, pdl, s);
+    case 2: return FusedC2<Epi>::launch(p, units, pdl, s);
+    case 3: return FusedC3<Epi>::launch(p, units, pdl, s);
     default: return cudaErrorInvalidValue;
   }
 }

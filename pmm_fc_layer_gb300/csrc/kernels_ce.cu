@@ -15,8 +15,8 @@ namespace {
 
 struct NoState {};
 
-// 32 distances of one row (n exist) in steps of 1 / kCeStep, up to kCeFar.
-__device__ __forceinline__ void store_distance32(uint16_t* p, int n, const float (&x)[32]) {
+// 32 distances of each row in steps of 1 / kCeStep, up to kCeFar.
+__device__ __forceinline__ void store_distances(const EpiTile& t, int col, const float (&x)[32]) {
   uint32_t w[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -24,7 +24,7 @@ __device__ __forceinline__ void store_distance32(uint16_t* p, int n, const float
     const uint32_t hi = __float2uint_rn(fminf(x[2 * j + 1] * kCeStep, static_cast<float>(kCeFar)));
     w[j] = __byte_perm(lo, hi, 0x5410);
   }
-  store_row32_u16(p, n, w);
+  store_segment<uint16_t>(t, t.out, col, w);
 }
 
 struct StatsEpilogue {
@@ -32,30 +32,21 @@ struct StatsEpilogue {
   using State = NoState;
   static __device__ __forceinline__ State begin(const Args&) { return {}; }
 
-  template <int kCols, class Ready>
-  static __device__ __forceinline__ bool run(const Args& a, const State&, const EpiTile& t, Ready&& ready) {
+  template <int kCols, bool kHold, class Ready, class Release>
+  static __device__ __forceinline__ bool run(const Args& a, const State&, const EpiTile& t, Ready&& ready,
+                                             Release&& release) {
     const bool in = t.row < t.M;
     const int width = min(kCols, t.N - t.col);
     // the label's place among this warp's columns (outside: another warp's)
     const int64_t y = in ? a.labels[t.row] - a.col0 - t.col : -1;
     if (!ready()) return false;
-    if (width <= 0) return true;
-    float m = -INFINITY;
-#pragma unroll 1
-    for (int c = 0; c < kCols / 32 && 32 * c < width; ++c) {
-      float x[32];
-      load_acc32(t, c, x);
+    float m = -INFINITY, s = 0.0f, mb = 0.0f;
+    auto take_max = [&](int c, const float(&x)[32]) {
 #pragma unroll
       for (int j = 0; j < 32; ++j)
         if (32 * c + j < width) m = fmaxf(m, x[j]);  // skips NaN, which the sum then shows
-    }
-    // A row whose every logit is -inf sums to 0 (not to e^(-inf + inf)).
-    const float mb = m == -INFINITY ? 0.0f : m * kEpiLog2e;
-    float s = 0.0f;
-#pragma unroll 1
-    for (int c = 0; c < kCols / 32 && 32 * c < width; ++c) {
-      float x[32];
-      load_acc32(t, c, x);
+    };
+    auto take_sum = [&](int c, float(&x)[32]) {
       const int64_t d = y - 32 * c;
       if (d >= 0 && d < 32 && d < width - 32 * c) {
         float zy = 0.0f;
@@ -67,18 +58,45 @@ struct StatsEpilogue {
       // distance below the maximum, in powers of two
 #pragma unroll
       for (int j = 0; j < 32; ++j) x[j] = 32 * c + j < width ? fmaf(x[j], -kEpiLog2e, mb) : INFINITY;
-      if (a.piece && in) store_distance32(a.piece + t.row * a.ld_piece + t.col + 32 * c, width - 32 * c, x);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] = ex2_approx(-x[j]);
+      if (a.keep_piece) store_distances(t, t.col + 32 * c, x);
       float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
       for (int j = 0; j < 32; j += 2) {
-        s0 += x[j];
-        s1 += x[j + 1];
+        s0 += ex2_approx(-x[j]);
+        s1 += ex2_approx(-x[j + 1]);
       }
       s += s0 + s1;
+    };
+    // A row whose every logit is -inf sums to 0 (not to e^(-inf + inf)).
+    auto set_base = [&]() { mb = m == -INFINITY ? 0.0f : m * kEpiLog2e; };
+    if constexpr (kHold) {  // the columns stay in registers
+      float x[kCols / 32][32];
+#pragma unroll
+      for (int c = 0; c < kCols / 32; ++c) {
+        if (32 * c < width) load_acc32(t, c, x[c]);
+        take_max(c, x[c]);
+      }
+      release();
+      set_base();
+#pragma unroll
+      for (int c = 0; c < kCols / 32; ++c)
+        if (32 * c < width) take_sum(c, x[c]);
+    } else {  // they are read twice
+      float x[32];
+#pragma unroll 1
+      for (int c = 0; c < kCols / 32 && 32 * c < width; ++c) {
+        load_acc32(t, c, x);
+        take_max(c, x);
+      }
+      set_base();
+#pragma unroll 1
+      for (int c = 0; c < kCols / 32 && 32 * c < width; ++c) {
+        load_acc32(t, c, x);
+        take_sum(c, x);
+      }
     }
-    if (in) a.stats[((a.col0 + t.col) / kCols) * a.ld_stats + t.row] = make_float2(m, s);
+    if (!kHold) release();
+    if (in && width > 0) a.stats[((a.col0 + t.col) / kCols) * a.ld_stats + t.row] = make_float2(m, s);
     return true;
   }
 };
@@ -87,51 +105,55 @@ struct ProbEpilogue {
   using Args = CeArgs;
   using State = NoState;
   static __device__ __forceinline__ State begin(const Args&) { return {}; }
+  static __device__ __forceinline__ void prefetch(const Args&, const EpiTile&, int) {}
 
-  template <int kCols, class Ready>
-  static __device__ __forceinline__ bool run(const Args& a, const State&, const EpiTile& t, Ready&& ready) {
+  static __device__ __forceinline__ void step(const Args& a, const State&, const EpiTile& t, int c,
+                                              float (&x)[32]) {
     const bool in = t.row < t.M;
-    // Rows up to the next multiple of 64 are zeros: the weight gradient's
-    // reduction runs over them.
-    const bool pad = !in && t.row < ((t.M + 63) & ~63) && t.row < a.rows;
-    const int64_t y = in ? a.labels[t.row] - a.col0 - t.col : -1;
+    const int col = t.col + 32 * c;
+    const int64_t d = in ? a.labels[t.row] - a.col0 - col : -1;
     const float lse2 = in ? a.lse2[t.row] : 0.0f;
-    if (!ready()) return false;
-#pragma unroll 1
-    for (int c = 0; c < kCols / 32; ++c) {
-      const int col = t.col + 32 * c, n = t.N - col;
-      if (n <= 0) break;
-      float x[32];
-      load_acc32(t, c, x);
-      const int64_t d = y - 32 * c;
+    // Rows past the last, up to the next multiple of 64, are zeros: the
+    // weight gradient's reduction runs over them.
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        float p = ex2_approx(fmaf(x[j], kEpiLog2e, -lse2));
-        if (j == d) p -= 1.0f;
-        x[j] = in ? p : 0.0f;
-      }
-      if (in || pad) store_row32_bf16(a.piece + t.row * a.ld_piece + col, n, x);
+    for (int j = 0; j < 32; ++j) {
+      float p = ex2_approx(fmaf(x[j], kEpiLog2e, -lse2));
+      if (j == d) p -= 1.0f;
+      x[j] = in ? p : 0.0f;
     }
-    return true;
+    EpiTile padded = t;
+    padded.rows = (t.M + 63) & ~63;
+    store_bf16(padded, t.out, col, x);
+  }
+
+  template <int kCols, bool kHold, class Ready, class Release>
+  static __device__ __forceinline__ bool run(const Args& a, const State& st, const EpiTile& t, Ready&& ready,
+                                             Release&& release) {
+    return epilogue_steps<ProbEpilogue, kCols, kHold>(a, st, t, ready, release);
   }
 };
 
-// The products that follow: a tile as it is, rows possibly scattered.
+// The products that follow: a tile times a number.
 struct StoreEpilogue {
   using Args = StoreArgs;
-  using State = NoState;
-  static __device__ __forceinline__ State begin(const Args&) { return {}; }
+  using State = float;  // the scale
+  static __device__ __forceinline__ State begin(const Args& a) { return a.scale ? *a.scale : 1.0f; }
 
-  static __device__ __forceinline__ void store(const Args& a, int64_t row, int col, int n, bool has,
-                                               const float (&x)[32]) {
+  static __device__ __forceinline__ void prefetch(const Args&, const EpiTile&, int) {}
+
+  static __device__ __forceinline__ void step(const Args& a, const State& scale, const EpiTile& t, int c,
+                                              float (&x)[32]) {
+    const int col = t.col + 32 * c, n = t.N - col;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x[j] *= scale;
     if (a.mode == kOutBF16) {
-      store_row32_bf16(reinterpret_cast<uint16_t*>(a.out) + row * a.ld_out + col, n, x);
-      return;
-    }
-    float* o = reinterpret_cast<float*>(a.out) + row * a.ld_out + col;
-    if (a.mode == kOutF32) {
-      store_row32_f32(o, n, x);
-    } else if (has) {  // one writer an element: the reduction rounds as a load-add-store would
+      store_bf16(t, t.out, col, x);
+    } else if (a.mode == kOutF32) {
+      store_f32(t, t.out, col, x);
+    } else if (t.has && t.row < t.M) {
+      // added by the L2's reductions: one writer an element, so that they
+      // round as a load-add-store would
+      float* o = static_cast<float*>(t.out->base) + t.row * t.out->ld + col;
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
         if (j + 4 <= n) {
@@ -146,32 +168,19 @@ struct StoreEpilogue {
     }
   }
 
-  template <int kCols, class Ready>
-  static __device__ __forceinline__ bool run(const Args& a, const State&, const EpiTile& t, Ready&& ready) {
-    const bool in = t.row < t.M;
-    const int64_t row = in && a.row_map ? a.row_map[t.row] : t.row;
-    const float scale = a.scale ? *a.scale : 1.0f;
-    if (!ready()) return false;
-#pragma unroll 1
-    for (int c = 0; c < kCols / 32; ++c) {
-      const int col = t.col + 32 * c, n = t.N - col;
-      if (n <= 0) break;
-      float x[32];
-      load_acc32(t, c, x);
-#pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] *= scale;
-      if (in) store(a, row, col, n, t.has, x);
-    }
-    return true;
+  template <int kCols, bool kHold, class Ready, class Release>
+  static __device__ __forceinline__ bool run(const Args& a, const State& st, const EpiTile& t, Ready&& ready,
+                                             Release&& release) {
+    return epilogue_steps<StoreEpilogue, kCols, kHold>(a, st, t, ready, release);
   }
 };
 
 }  // namespace
 
-cudaError_t ce_init() {
-  cudaError_t e = fused_init_all<StatsEpilogue>();
-  if (e == cudaSuccess) e = fused_init_all<ProbEpilogue>();
-  return e == cudaSuccess ? fused_init_all<StoreEpilogue>() : e;
+cudaError_t ce_init(bool* regs_ok) {
+  cudaError_t e = fused_init_all<StatsEpilogue>(regs_ok);
+  if (e == cudaSuccess) e = fused_init_all<ProbEpilogue>(regs_ok);
+  return e == cudaSuccess ? fused_init_all<StoreEpilogue>(regs_ok) : e;
 }
 
 cudaError_t store_launch(int config, const FusedParams<StoreArgs>& p, int units, bool pdl,

@@ -9,206 +9,198 @@
 namespace axonn {
 namespace {
 
-// 32 elements of a row in the output's type, kept as loaded.
-struct RowSegment {
-  uint32_t w[32];
-};
-__device__ __forceinline__ void load_segment(RowSegment& s, const void* base, int64_t ld, bool f32, int row,
-                                             int col, int n) {
-  if (!f32) {
-    uint32_t h[16];
-    load_row32_bf16(reinterpret_cast<const uint16_t*>(base) + row * ld + col, n, h);
+// The bias of 16 columns (n exist): every lane reads the same addresses.
+__device__ __forceinline__ void add_bias16(const EpilogueArgs& a, int col, int n, float* x) {
+  if (a.bias_f32) {
+    Row16<true> b;
+    b.load(a.bias, col, n);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) s.w[j] = h[j];
-    return;
-  }
-  const float* p = reinterpret_cast<const float*>(base) + row * ld + col;
-  if (n >= 32) {
-#pragma unroll
-    for (int v = 0; v < 8; ++v) {
-      const uint4 a = reinterpret_cast<const uint4*>(p)[v];
-      s.w[4 * v] = a.x;
-      s.w[4 * v + 1] = a.y;
-      s.w[4 * v + 2] = a.z;
-      s.w[4 * v + 3] = a.w;
-    }
+    for (int j = 0; j < 16; ++j) x[j] += b.value(j);
   } else {
+    Row16<false> b;
+    b.load(a.bias, col, n);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) s.w[j] = j < n ? __float_as_uint(p[j]) : 0u;
-  }
-}
-__device__ __forceinline__ void add_segment(const RowSegment& s, bool f32, float (&x)[32]) {
-  if (f32) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] += __uint_as_float(s.w[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      x[2 * j] += __uint_as_float(s.w[j] << 16);
-      x[2 * j + 1] += __uint_as_float(s.w[j] & 0xFFFF0000u);
-    }
+    for (int j = 0; j < 16; ++j) x[j] += b.value(j);
   }
 }
 
-// The bias of 32 columns (n exist): every lane reads the same addresses.
-__device__ __forceinline__ void add_bias(const EpilogueArgs& a, int col, int n, float (&x)[32]) {
-  if (a.bias_f32) {
-    const float* b = reinterpret_cast<const float*>(a.bias) + col;
-    if (n >= 32) {
+__device__ __forceinline__ void drop16(const DropoutArgs& d, const DropRng& g, int row, int col, float* x) {
 #pragma unroll
-      for (int v = 0; v < 8; ++v) {
-        const float4 f = reinterpret_cast<const float4*>(b)[v];
-        x[4 * v] += f.x;
-        x[4 * v + 1] += f.y;
-        x[4 * v + 2] += f.z;
-        x[4 * v + 3] += f.w;
+  for (int o = 0; o < 2; ++o) drop8(d, g, static_cast<uint32_t>(row), static_cast<uint32_t>(col) / 8 + o, x + 8 * o);
+}
+
+// L2 lines of `cols` columns of a thread's row.
+__device__ __forceinline__ void prefetch_row(const void* base, int64_t at, int cols, int bytes) {
+  const char* p = static_cast<const char*>(base) + at * bytes;
+  for (int b = 0; b < cols * bytes; b += 128) prefetch_l2(p + b);
+}
+
+// R over 32 columns: bf16 in one segment, fp32 in two.
+template <bool kF32>
+struct Residual {
+  RowSegment<uint16_t> half;
+  __device__ __forceinline__ void start(const EpilogueArgs& a, const EpiTile& t, int col) {
+    if constexpr (!kF32) half.start(t, a.residual, a.ld_res, col);
+  }
+  __device__ __forceinline__ void add(const EpilogueArgs& a, const EpiTile& t, int col, float (&x)[32]) {
+    uint32_t w[16];
+    if constexpr (!kF32) {
+      half.finish(t, w);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        x[2 * j] += __uint_as_float(w[j] << 16);
+        x[2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) x[j] += b[j];
+      for (int h = 0; h < 2; ++h) {
+        if (col + 16 * h >= t.N) break;
+        RowSegment<uint32_t> r;
+        r.start(t, a.residual, a.ld_res, col + 16 * h);
+        r.finish(t, w);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[16 * h + j] += __uint_as_float(w[j]);
+      }
     }
-    return;
   }
-  uint32_t w[16];
-  load_row32_bf16(reinterpret_cast<const uint16_t*>(a.bias) + col, n, w);
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    x[2 * j] += __uint_as_float(w[j] << 16);
-    x[2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
-  }
+};
+
+// kF32: the output and the residual are fp32 (else bf16).
+template <bool kF32>
+__device__ __forceinline__ void store_out(const EpiTile& t, int col, const float (&x)[32]) {
+  if constexpr (kF32) store_f32(t, t.out, col, x);
+  else store_bf16(t, t.out, col, x);
 }
 
-__device__ __forceinline__ void store_out(const EpilogueArgs& a, int row, int col, int n, const float (&x)[32]) {
-  if (a.out_f32) store_row32_f32(reinterpret_cast<float*>(a.out) + row * a.ld_out + col, n, x);
-  else store_row32_bf16(reinterpret_cast<uint16_t*>(a.out) + row * a.ld_out + col, n, x);
-}
-
-__device__ __forceinline__ void drop32(const DropoutArgs& d, const DropRng& g, int row, int col, float (&x)[32]) {
-#pragma unroll
-  for (int o = 0; o < 4; ++o) drop8(d, g, static_cast<uint32_t>(row), static_cast<uint32_t>(col) / 8 + o, x + 8 * o);
-}
-
+template <bool kF32>
 struct FwdEpilogue {
   using Args = EpilogueArgs;
   using State = DropRng;
   static __device__ __forceinline__ State begin(const Args& a) { return load_rng(a.drop); }
 
-  template <int kCols, class Ready>
-  static __device__ __forceinline__ bool run(const Args& a, const State& g, const EpiTile& t, Ready&& ready) {
-    const bool in = t.row < t.M;
-    const bool res = a.residual != nullptr && in;
-    RowSegment r;
-    if (res && t.col < t.N) load_segment(r, a.residual, a.ld_res, a.out_f32, t.row, t.col, t.N - t.col);
-    if (!ready()) return false;
-#pragma unroll 1
-    for (int c = 0; c < kCols / 32; ++c) {
-      const int col = t.col + 32 * c, n = t.N - col;
-      if (n <= 0) break;
-      float x[32];
-      load_acc32(t, c, x);
-      if (a.bias) add_bias(a, col, n, x);
-      if (a.pre_out && in) store_row32_bf16(a.pre_out + t.row * a.ld_pre + col, n, x);
-      apply_act(a.act, x);
-      if (a.drop.thr != 0) drop32(a.drop, g, t.row, col, x);
-      if (res) {
-        add_segment(r, a.out_f32, x);
-        // the next columns' residual, before these are stored
-        if (c + 1 < kCols / 32 && n > 32)
-          load_segment(r, a.residual, a.ld_res, a.out_f32, t.row, col + 32, n - 32);
-      }
-      if (in) store_out(a, t.row, col, n, x);
+  static __device__ __forceinline__ void prefetch(const Args& a, const EpiTile& t, int cols) {
+    if (a.residual) prefetch_row(a.residual, t.row * a.ld_res + t.col, cols, kF32 ? 4 : 2);
+  }
+
+  static __device__ __forceinline__ void step(const Args& a, const State& rng, const EpiTile& t, int c,
+                                              float (&x)[32]) {
+    const int col = t.col + 32 * c;
+    Residual<kF32> r;
+    if (a.residual) r.start(a, t, col);
+    if (a.bias) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (col + 16 * h < t.N) add_bias16(a, col + 16 * h, t.N - col - 16 * h, x + 16 * h);
     }
-    return true;
+    if (a.pre_out) store_bf16(t, t.out2, col, x);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      apply_act16(a.act, x + 16 * h);
+      if (a.drop.thr != 0) drop16(a.drop, rng, t.row, col + 16 * h, x + 16 * h);
+    }
+    if (a.residual) r.add(a, t, col, x);
+    store_out<kF32>(t, col, x);
+  }
+
+  template <int kCols, bool kHold, class Ready, class Release>
+  static __device__ __forceinline__ bool run(const Args& a, const State& g, const EpiTile& t, Ready&& ready,
+                                             Release&& release) {
+    return epilogue_steps<FwdEpilogue, kCols, kHold>(a, g, t, ready, release);
   }
 };
 
 // Column sums over the 32 rows of a warp: at each step a lane keeps half of
 // its columns and hands the other half to the lane across, so that 31
 // shuffles (rather than 32 x 5) leave lane j with the sum of column j.  The
-// order of the additions is fixed.
-__device__ __forceinline__ float column_sum32(const float (&x)[32]) {
+// order of the additions is fixed.  x is used up.
+__device__ __forceinline__ float column_sum32(float (&x)[32]) {
   const int lane = threadIdx.x & 31;
-  float v[16];
-  {
-    const bool up = lane & 16;
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
-      v[j] = (up ? x[j + 16] : x[j]) + __shfl_xor_sync(0xFFFFFFFFu, up ? x[j] : x[j + 16], 16);
-  }
-#pragma unroll
-  for (int w = 8; w >= 1; w >>= 1) {
+  for (int w = 16; w >= 1; w >>= 1) {
     const bool up = lane & w;
 #pragma unroll
-    for (int j = 0; j < w; ++j)
-      v[j] = (up ? v[j + w] : v[j]) + __shfl_xor_sync(0xFFFFFFFFu, up ? v[j] : v[j + w], w);
+    for (int j = 0; j < w; ++j) {
+      const float give = up ? x[j] : x[j + w];
+      x[j] = (up ? x[j + w] : x[j]) + __shfl_xor_sync(0xFFFFFFFFu, give, w);
+    }
   }
-  return v[0];
+  return x[0];
 }
 
+template <bool kF32>
 struct BwdEpilogue {
   using Args = EpilogueArgs;
   using State = DropRng;
   static __device__ __forceinline__ State begin(const Args& a) { return load_rng(a.drop); }
 
-  template <int kCols, class Ready>
-  static __device__ __forceinline__ bool run(const Args& a, const State& g, const EpiTile& t, Ready&& ready) {
+  static __device__ __forceinline__ void prefetch(const Args& a, const EpiTile& t, int cols) {
+    if (a.act != kActNone) prefetch_row(a.pre_in, t.row * a.ld_pre + t.col, cols, 2);
+    if (a.residual) prefetch_row(a.residual, t.row * a.ld_res + t.col, cols, kF32 ? 4 : 2);
+  }
+
+  static __device__ __forceinline__ void step(const Args& a, const State& rng, const EpiTile& t, int c,
+                                              float (&x)[32]) {
+    const int col = t.col + 32 * c;
     const bool in = t.row < t.M;
-    const bool res = a.residual != nullptr && in;
-    const bool slope = a.act != kActNone && in;
-    const int lane = threadIdx.x & 31;
-    RowSegment r;
-    uint32_t zw[16] = {};
-    if (t.col < t.N) {
-      if (slope) load_row32_bf16(a.pre_in + t.row * a.ld_pre + t.col, t.N - t.col, zw);
-      if (res) load_segment(r, a.residual, a.ld_res, a.out_f32, t.row, t.col, t.N - t.col);
-    }
-    if (!ready()) return false;
-#pragma unroll 1
-    for (int c = 0; c < kCols / 32; ++c) {
-      const int col = t.col + 32 * c, n = t.N - col;
-      if (n <= 0) break;
-      const bool more = c + 1 < kCols / 32 && n > 32;
-      float x[32];
-      load_acc32(t, c, x);
-      if (a.drop.thr != 0) drop32(a.drop, g, t.row, col, x);
-      if (slope) {
-        float z[32];
-        unpack32(zw, z);
-        if (more) load_row32_bf16(a.pre_in + t.row * a.ld_pre + col + 32, n - 32, zw);
-        apply_slope(a.act, x, z);
-      }
-      if (a.colsum) {
-        // Rows past the end hold zero-filled operands' products, which are
-        // 0; they are set so here in any case (a NaN weight would not be).
-        float y[32];
+    RowSegment<uint16_t> z;
+    if (a.act != kActNone) z.start(t, a.pre_in, a.ld_pre, col);
+    if (a.drop.thr != 0) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) y[j] = in ? x[j] : 0.0f;
-        const float s = column_sum32(y);
-        const int64_t group = t.row >> 5;  // the same for the warp: rows are 32-aligned
-        if (lane < n && (t.row & ~31) < t.M) a.colsum[group * a.ld_colsum + col + lane] = s;
-      }
-      if (res) {
-        add_segment(r, a.out_f32, x);
-        if (more) load_segment(r, a.residual, a.ld_res, a.out_f32, t.row, col + 32, n - 32);
-      }
-      if (in) store_out(a, t.row, col, n, x);
+      for (int h = 0; h < 2; ++h) drop16(a.drop, rng, t.row, col + 16 * h, x + 16 * h);
     }
-    return true;
+    if (a.act != kActNone) {
+      uint32_t w[16];
+      z.finish(t, w);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) apply_slope16(a.act, x + 16 * h, w + 8 * h);
+    }
+    if (a.residual) {
+      Residual<kF32> r;
+      r.start(a, t, col);
+      float y[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) y[j] = x[j];
+      r.add(a, t, col, y);
+      store_out<kF32>(t, col, y);
+    } else {
+      store_out<kF32>(t, col, x);
+    }
+    if (!a.colsum) return;
+    // d without the residual; nothing from rows past the end.
+    if (!in) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+    }
+    __syncwarp();
+    const float s = column_sum32(x);
+    const int at = col + static_cast<int>(threadIdx.x & 31);
+    const int64_t group = t.row >> 5;  // the same for the warp: its rows are 32-aligned
+    if (at < t.N && (t.row & ~31) < t.M) a.colsum[group * a.ld_colsum + at] = s;
+  }
+
+  template <int kCols, bool kHold, class Ready, class Release>
+  static __device__ __forceinline__ bool run(const Args& a, const State& g, const EpiTile& t, Ready&& ready,
+                                             Release&& release) {
+    return epilogue_steps<BwdEpilogue, kCols, kHold>(a, g, t, ready, release);
   }
 };
 
 }  // namespace
 
-cudaError_t fused_init() {
-  const cudaError_t e = fused_init_all<FwdEpilogue>();
-  return e == cudaSuccess ? fused_init_all<BwdEpilogue>() : e;
+cudaError_t fused_init(bool* regs_ok) {
+  for (cudaError_t e : {fused_init_all<FwdEpilogue<false>>(regs_ok), fused_init_all<FwdEpilogue<true>>(regs_ok),
+                        fused_init_all<BwdEpilogue<false>>(regs_ok), fused_init_all<BwdEpilogue<true>>(regs_ok)})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
 }
 
 cudaError_t fused_launch(FusedKind kind, int config, const FusedParams<EpilogueArgs>& p, int units,
                          bool pdl, cudaStream_t stream) {
-  return kind == kFusedFwd ? fused_launch_config<FwdEpilogue>(config, p, units, pdl, stream)
-                           : fused_launch_config<BwdEpilogue>(config, p, units, pdl, stream);
+  if (kind == kFusedFwd)
+    return p.epi.out_f32 ? fused_launch_config<FwdEpilogue<true>>(config, p, units, pdl, stream)
+                         : fused_launch_config<FwdEpilogue<false>>(config, p, units, pdl, stream);
+  return p.epi.out_f32 ? fused_launch_config<BwdEpilogue<true>>(config, p, units, pdl, stream)
+                       : fused_launch_config<BwdEpilogue<false>>(config, p, units, pdl, stream);
 }
 
 cudaError_t fused_take_status(unsigned long long* word, cudaStream_t stream) {

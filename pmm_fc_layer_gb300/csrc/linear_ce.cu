@@ -50,7 +50,9 @@ __global__ void __launch_bounds__(1024) ce_index_kernel(CeRowArgs a) {
       const int at = before + __popc(ballot & ((1u << lane) - 1u));
       a.index[at] = static_cast<int32_t>(t);
       a.packed_labels[at] = y;
+      a.place[t] = at;
     } else if (t < a.rows) {
+      a.place[t] = -1;
       a.token_loss[t] = 0.0f;
       if (a.lse) a.lse[t] = 0.0f;
     }
@@ -80,20 +82,6 @@ __global__ void __launch_bounds__(256) ce_gather_kernel(CeRowArgs a) {
     for (int64_t v = lane; v < vecs; v += 32)
       reinterpret_cast<uint4*>(dst)[v] = src ? reinterpret_cast<const uint4*>(src)[v] : make_uint4(0, 0, 0, 0);
     for (int64_t c = 8 * vecs + lane; c < a.cols; c += 32) dst[c] = src ? src[c] : 0;
-  }
-}
-
-// Zeroes the rows of dX that do not count.
-__global__ void __launch_bounds__(256) ce_zero_kernel(CeRowArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-  const int64_t vecs = a.cols / 8;
-  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < a.rows; t += warps) {
-    const int32_t y = a.labels[t];
-    if (y >= 0 && y < a.vocab && (!a.keep || a.keep[t] != 0)) continue;
-    uint16_t* dst = a.dx + t * a.ld_dx;
-    for (int64_t v = lane; v < vecs; v += 32) reinterpret_cast<uint4*>(dst)[v] = make_uint4(0, 0, 0, 0);
-    for (int64_t c = 8 * vecs + lane; c < a.cols; c += 32) dst[c] = 0;
   }
 }
 
@@ -209,18 +197,31 @@ __global__ void __launch_bounds__(256) ce_scale_kernel(CeRowArgs a, uint16_t* pi
   }
 }
 
-__global__ void __launch_bounds__(256) ce_scatter_kernel(CeRowArgs a, const float* packed, int64_t ld) {
-  const int64_t n4 = (a.cols + 3) / 4, total = *a.kept * n4;
-  for (int64_t i = blockIdx.x * int64_t{256} + threadIdx.x; i < total; i += gridDim.x * int64_t{256}) {
-    const int64_t r = i / n4, c = 4 * (i - r * n4);
-    const float* s = packed + r * ld + c;
-    uint16_t* d = a.dx + a.index[r] * a.ld_dx + c;
-    if (c + 4 <= a.cols) {
-      const float4 v = *reinterpret_cast<const float4*>(s);
-      *reinterpret_cast<uint2*>(d) = make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
-    } else {
-      for (int64_t j = 0; c + j < a.cols; ++j) d[j] = static_cast<uint16_t>(pack_bf16(s[j], 0.0f));
+// A warp takes a row of dX at a time: its packed row, rounded if fp32, or
+// zeros.
+template <bool kF32>
+__global__ void __launch_bounds__(256) ce_unpack_kernel(CeRowArgs a, const void* packed, int64_t ld) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+  const int64_t vecs = a.cols / 8;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < a.rows; t += warps) {
+    const int64_t at = a.place[t];
+    uint16_t* dst = a.dx + t * a.ld_dx;
+    const uint16_t* s16 = static_cast<const uint16_t*>(packed) + at * ld;
+    const float* s32 = static_cast<const float*>(packed) + at * ld;
+#pragma unroll 4
+    for (int64_t v = lane; v < vecs; v += 32) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (at >= 0 && kF32) {
+        const float4 p = reinterpret_cast<const float4*>(s32)[2 * v], q = reinterpret_cast<const float4*>(s32)[2 * v + 1];
+        w = make_uint4(pack_bf16(p.x, p.y), pack_bf16(p.z, p.w), pack_bf16(q.x, q.y), pack_bf16(q.z, q.w));
+      } else if (at >= 0) {
+        w = reinterpret_cast<const uint4*>(s16)[v];
+      }
+      reinterpret_cast<uint4*>(dst)[v] = w;
     }
+    for (int64_t c = 8 * vecs + lane; c < a.cols; c += 32)
+      dst[c] = at < 0 ? 0 : (kF32 ? static_cast<uint16_t>(pack_bf16(s32[c], 0.0f)) : s16[c]);
   }
 }
 
@@ -238,9 +239,6 @@ cudaError_t ce_index_launch(const CeRowArgs& a, cudaStream_t stream) {
 cudaError_t ce_gather_launch(const CeRowArgs& a, int sms, cudaStream_t stream) {
   if (a.rows == 0 || a.cols == 0) return cudaSuccess;
   ce_gather_kernel<<<row_blocks(a.rows, sms), 256, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !a.dx) return e;
-  ce_zero_kernel<<<row_blocks(a.rows, sms), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -264,12 +262,11 @@ cudaError_t ce_scale_launch(const CeRowArgs& a, uint16_t* piece, int64_t ld_piec
   return cudaGetLastError();
 }
 
-cudaError_t ce_scatter_launch(const CeRowArgs& a, const float* packed, int64_t ld, int sms,
-                              cudaStream_t stream) {
-  const int64_t n4 = a.rows * ((a.cols + 3) / 4);
-  if (n4 == 0) return cudaSuccess;
-  const int64_t blocks = std::min<int64_t>((n4 + 255) / 256, int64_t{8} * sms);
-  ce_scatter_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a, packed, ld);
+cudaError_t ce_unpack_launch(const CeRowArgs& a, const void* packed, int64_t ld, bool f32, int sms,
+                             cudaStream_t stream) {
+  if (a.rows == 0 || a.cols == 0) return cudaSuccess;
+  if (f32) ce_unpack_kernel<true><<<row_blocks(a.rows, sms), 256, 0, stream>>>(a, packed, ld);
+  else ce_unpack_kernel<false><<<row_blocks(a.rows, sms), 256, 0, stream>>>(a, packed, ld);
   return cudaGetLastError();
 }
 

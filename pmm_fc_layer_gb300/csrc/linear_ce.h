@@ -15,6 +15,7 @@ struct CeRowArgs {
   int64_t rows, cols, vocab;
   float grad_scale;
   int32_t* index;         // [rows] packed place -> row
+  int32_t* place;         // [rows] row -> packed place, or -1
   int32_t* packed_labels; // [rows]
   uint16_t* packed_x;     // bf16 [rows x ld_packed]
   int64_t ld_packed;
@@ -28,11 +29,11 @@ struct CeRowArgs {
   float* lse;                // [rows] natural logsumexp of the counted rows (0 elsewhere), or null
   float* loss;
   int32_t* kept;
-  uint16_t* dx;              // rows that do not count are zeroed here, or null
+  uint16_t* dx;              // or null
   int64_t ld_dx;
 };
 
-// n, the packing, and the zeros of the rows that do not count.
+// n, the packing, and the losses (0) of the rows that do not count.
 cudaError_t ce_index_launch(const CeRowArgs& a, cudaStream_t stream);
 cudaError_t ce_gather_launch(const CeRowArgs& a, int sms, cudaStream_t stream);
 // Each packed row's logsumexp from its groups' statistics, and its loss.
@@ -43,8 +44,9 @@ cudaError_t ce_mean_launch(const CeRowArgs& a, cudaStream_t stream);
 // in place.
 cudaError_t ce_scale_launch(const CeRowArgs& a, uint16_t* piece, int64_t ld_piece, int64_t col0,
                             int64_t cols, cudaStream_t stream);
-// Packed fp32 rows rounded to bf16 at their places in dx.
-cudaError_t ce_scatter_launch(const CeRowArgs& a, const float* packed, int64_t ld, int sms,
-                              cudaStream_t stream);
+// dx from its packed rows (bf16, or fp32 to be rounded); zeros where a row
+// does not count.
+cudaError_t ce_unpack_launch(const CeRowArgs& a, const void* packed, int64_t ld, bool f32, int sms,
+                             cudaStream_t stream);
 
 }  // namespace axonn

@@ -74,7 +74,7 @@ def product_error(K, S):
 SIZES = [(1, 64, 128), (1, 520, 72), (3, 8, 1), (31, 65, 33), (130, 200, 264), (257, 130, 521), (300, 72, 1000)]
 
 
-@pytest.mark.parametrize("config", [2, 0, 7])
+@pytest.mark.parametrize("config", [2, 0, 6, 7])
 @pytest.mark.parametrize("n,size", list(enumerate(SIZES)))
 def test_forward(cuda_lib, n, size, config):
     fc = cuda_lib
@@ -119,7 +119,7 @@ def test_forward(cuda_lib, n, size, config):
             assert untouched(Z)
 
 
-@pytest.mark.parametrize("config", [2, 0, 7])
+@pytest.mark.parametrize("config", [2, 0, 6, 7])
 @pytest.mark.parametrize("n,size", list(enumerate(SIZES)))
 def test_data_gradient(cuda_lib, n, size, config):
     """dZ [T x N] of a following layer W [N x K]."""

@@ -115,7 +115,7 @@ def case(T, K, V, seed=1, spread=1.0):
 SIZES = [(1, 8, 1), (1, 64, 1000), (2, 72, 257), (33, 130, 300), (130, 64, 1003), (300, 200, 2000), (257, 40, 4097)]
 
 
-@pytest.mark.parametrize("config", [2, 0, 7])
+@pytest.mark.parametrize("config", [2, 0, 6, 7])
 @pytest.mark.parametrize("tied", [False, True])
 @pytest.mark.parametrize("size", SIZES)
 def test_against_64_bits(cuda_lib, size, tied, config):
@@ -236,3 +236,17 @@ def test_expired_wait_is_reported(cuda_lib):
         fc.axonn_debug_set_inject(0)
         fc.axonn_set_wait_timeout_ns(4_000_000_000)
     check(run(fc, X, W, labels), X, W, labels)
+
+
+@pytest.mark.parametrize("n", [31, 32, 33, 64, 65, 96, 128, 129])
+@pytest.mark.parametrize("piece", [0, 256])
+def test_counted_rows_at_the_edges_of_a_tile(cuda_lib, n, piece):
+    """The weight gradient's reduction runs in steps of 64 packed rows, an
+    epilogue warp owns 32: whatever lies past the last row adds nothing.  The
+    workspace starts as NaN."""
+    X, W, labels, rng = case(200, 72, 700, seed=20 + n)
+    keep = np.zeros(200, dtype=np.uint8)
+    keep[rng.permutation(200)[:n]] = 1
+    for config in (6, 2, 0, 7):
+        cuda_lib.axonn_set_kernel_config(config)
+        check(run(cuda_lib, X, W, labels, keep, piece=piece), X, W, labels, keep)
