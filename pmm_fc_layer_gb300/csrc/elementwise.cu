@@ -181,10 +181,7 @@ __device__ __forceinline__ void act_bwd_rows(const BwdKernelArgs& a, const DropR
         x[u].values(v);
         if (kDrop) drop8(a.drop, g, static_cast<uint32_t>(base + 8 * u), static_cast<uint32_t>(col / 8), v);
         if (ACT != kActNone) {
-          float s[8];
-          z[u].values(s);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] *= act_slope<ACT>(s[j]);
+          act_slopes<ACT, 8>(v, z[u].w);
         }
         store8(dz, n, v);
 #pragma unroll

@@ -27,102 +27,169 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// 1 / (1 + e^-x); NaN stays NaN, and the ends are 0 and 1.
-__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.0f + ex2_approx(-kEpiLog2e * x)); }
-
-// The tanh form of GELU, 0.5 z (1 + tanh(u)) with u = c0 (z + c1 z^3), is
-// z sigmoid(2u).
-constexpr float kGeluC0 = 0.7978845608028654f;  // sqrt(2/pi)
-constexpr float kGeluC1 = 0.044715f;
-constexpr float kRsqrt2 = 0.7071067811865476f;
-constexpr float kRsqrt2Pi = 0.3989422804014327f;
-
-__device__ __forceinline__ float gelu_tanh_gate(float z) {
-  return sigmoid(2.0f * kGeluC0 * z * fmaf(kGeluC1 * z, z, 1.0f));
+// Two fp32 numbers in a register pair: one instruction for both (the f32x2
+// forms of sm_100 and later; each half rounds as its scalar form does).
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void split(F2 a, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 min2(F2 a, float b) {
+  float x, y;
+  split(a, x, y);
+  return f2(fminf(x, b), fminf(y, b));
+}
+__device__ __forceinline__ F2 ex2_2(F2 a) {
+  float x, y;
+  split(a, x, y);
+  return f2(ex2_approx(x), ex2_approx(y));
+}
+__device__ __forceinline__ F2 rcp_2(F2 a) {
+  float x, y;
+  split(a, x, y);
+  return f2(rcp_approx(x), rcp_approx(y));
 }
 
-// The normal distribution's tail beyond |z| and its density at z.  The tail
-// is half of erfc(|z| / sqrt 2) by formula 7.1.26 of Abramowitz and Stegun
-// (C. Hastings' rational approximation): t (a1 + .. + a5 t^4) e^(-z^2 / 2),
+// 1 / (1 + 2^-a): with a = x log2 e the logistic function; NaN stays NaN, and
+// the ends are 0 and 1.  `neg` is -a.
+__device__ __forceinline__ F2 logistic2(F2 neg) { return rcp_2(add2(ex2_2(neg), f2(1.0f))); }
+
+// The tanh form of GELU, 0.5 z (1 + tanh(u)) with u = c0 (z + c1 z^3), is
+// z sigmoid(2u); -2u log2 e = z (kTanhA + kTanhB z^2).  z^2 is clamped where
+// the gate has long saturated, so that nothing overflows.
+constexpr float kGeluC0 = 0.7978845608028654f;  // sqrt(2/pi)
+constexpr float kGeluC1 = 0.044715f;
+constexpr float kTanhA = -2.0f * kGeluC0 * kEpiLog2e;
+constexpr float kTanhB = kTanhA * kGeluC1;
+constexpr float kRsqrt2 = 0.7071067811865476f;
+constexpr float kRsqrt2Pi = 0.3989422804014327f;
+__device__ __forceinline__ F2 gelu_tanh_gate2(F2 z, F2& zz) {
+  zz = min2(mul2(z, z), 4096.0f);
+  return logistic2(mul2(z, fma2(zz, f2(kTanhB), f2(kTanhA))));
+}
+
+// The normal distribution function at z, and e = e^(-z^2 / 2).  Its tail
+// beyond |z| is half of erfc(|z| / sqrt 2) by formula 7.1.26 of Abramowitz
+// and Stegun (C. Hastings' rational approximation): t (a1 + .. + a5 t^4) e,
 // t = 1 / (1 + p |z| / sqrt 2), within 1.5e-7 of erfc, which leaves 1e-7 of z
 // in GELU.  It costs two SFU steps, half of what erfcf costs, and the slope
 // uses the exponential again.
-__device__ __forceinline__ float normal_tail(float z, float& e) {
-  e = ex2_approx(-0.5f * kEpiLog2e * z * z);
-  const float t = rcp_approx(fmaf(0.3275911f * kRsqrt2, fabsf(z), 1.0f));
-  float h = fmaf(t, 1.061405429f, -1.453152027f);
-  h = fmaf(t, h, 1.421413741f);
-  h = fmaf(t, h, -0.284496736f);
-  h = fmaf(t, h, 0.254829592f);
-  return 0.5f * h * t * e;
+__device__ __forceinline__ F2 normal_cdf2(F2 z, F2& e) {
+  float z0, z1;
+  split(z, z0, z1);
+  e = ex2_2(mul2(mul2(z, f2(-0.5f * kEpiLog2e)), z));
+  const F2 t = rcp_2(fma2(f2(fabsf(z0), fabsf(z1)), f2(0.3275911f * kRsqrt2), f2(1.0f)));
+  F2 h = fma2(t, f2(0.5f * 1.061405429f), f2(0.5f * -1.453152027f));
+  h = fma2(t, h, f2(0.5f * 1.421413741f));
+  h = fma2(t, h, f2(0.5f * -0.284496736f));
+  h = fma2(t, h, f2(0.5f * 0.254829592f));
+  h = mul2(mul2(h, t), e);
+  float h0, h1;
+  split(h, h0, h1);
+  return f2(z0 >= 0.0f ? 1.0f - h0 : h0, z1 >= 0.0f ? 1.0f - h1 : h1);
 }
 
+// act and its slope at two points.
 template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (ACT == kActRelu) return z < 0.0f ? 0.0f : z;  // NaN stays
-  if constexpr (ACT == kActGelu) {
-    float e;
-    const float h = normal_tail(z, e);
-    return z * (z >= 0.0f ? 1.0f - h : h);
+__device__ __forceinline__ F2 act_value2(F2 z) {
+  if constexpr (ACT == kActRelu) {
+    float x, y;
+    split(z, x, y);
+    return f2(x < 0.0f ? 0.0f : x, y < 0.0f ? 0.0f : y);  // NaN stays
   }
-  if constexpr (ACT == kActGeluTanh) return z * gelu_tanh_gate(z);
-  if constexpr (ACT == kActSilu) return z * sigmoid(z);
+  if constexpr (ACT == kActGelu) {
+    F2 e;
+    return mul2(z, normal_cdf2(z, e));
+  }
+  if constexpr (ACT == kActGeluTanh) {
+    F2 zz;
+    return mul2(z, gelu_tanh_gate2(z, zz));
+  }
+  if constexpr (ACT == kActSilu) return mul2(z, logistic2(mul2(z, f2(-kEpiLog2e))));
   return z;
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-  if constexpr (ACT == kActRelu) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
+__device__ __forceinline__ F2 act_slope2(F2 z) {
+  if constexpr (ACT == kActRelu) {
+    float x, y;
+    split(z, x, y);
+    return f2(x > 0.0f ? 1.0f : (x <= 0.0f ? 0.0f : x), y > 0.0f ? 1.0f : (y <= 0.0f ? 0.0f : y));
+  }
   if constexpr (ACT == kActGelu) {
-    float e;
-    const float h = normal_tail(z, e);
-    return fmaf(z * kRsqrt2Pi, e, z >= 0.0f ? 1.0f - h : h);
+    F2 e;
+    const F2 cdf = normal_cdf2(z, e);
+    return fma2(mul2(z, f2(kRsqrt2Pi)), e, cdf);
   }
   if constexpr (ACT == kActGeluTanh) {
-    // with s = sigmoid(2u): s + z s (1 - s) 2 u'(z).  z is clamped where the
-    // gate has long saturated, so that its square cannot overflow.
-    const float s = gelu_tanh_gate(z);
-    const float c = fminf(fmaxf(z, -64.0f), 64.0f);
-    return fmaf(c * s * (1.0f - s), 2.0f * kGeluC0 * fmaf(3.0f * kGeluC1 * c, c, 1.0f), s);
+    // with s = sigmoid(2u): s + z s (1 - s) 2 u'(z)
+    F2 zz;
+    const F2 s = gelu_tanh_gate2(z, zz);
+    const F2 w = mul2(z, fma2(mul2(s, f2(-1.0f)), s, s));  // 0 where the gate has saturated
+    return fma2(w, fma2(zz, f2(6.0f * kGeluC0 * kGeluC1), f2(2.0f * kGeluC0)), s);
   }
   if constexpr (ACT == kActSilu) {
-    const float s = sigmoid(z);
-    const float c = fminf(fmaxf(z, -1e4f), 1e4f);
-    return fmaf(c * s, 1.0f - s, s);
+    const F2 s = logistic2(mul2(z, f2(-kEpiLog2e)));
+    return fma2(z, fma2(mul2(s, f2(-1.0f)), s, s), s);
   }
-  return 1.0f;
+  return f2(1.0f);
 }
 
 // v[j] = act(v[j]), and v[j] *= act'(z_j) for z in bf16 pairs, over 16 values;
 // the switch is outside the loop.
+template <int ACT, int N>
+__device__ __forceinline__ void act_values(float* v) {
+#pragma unroll
+  for (int j = 0; j < N; j += 2) split(act_value2<ACT>(f2(v[j], v[j + 1])), v[j], v[j + 1]);
+}
+template <int ACT, int N>
+__device__ __forceinline__ void act_slopes(float* v, const uint32_t* z) {
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    const uint32_t w = z[j >> 1];
+    const F2 s = act_slope2<ACT>(f2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)));
+    split(mul2(f2(v[j], v[j + 1]), s), v[j], v[j + 1]);
+  }
+}
 __device__ __forceinline__ void apply_act16(int act, float* v) {
-#define AXONN_EACH(A)                        \
-  case A:                                    \
-    _Pragma("unroll") for (int j = 0; j < 16; ++j) v[j] = act_value<A>(v[j]); \
-    break
   switch (act) {
-    AXONN_EACH(kActRelu);
-    AXONN_EACH(kActGelu);
-    AXONN_EACH(kActGeluTanh);
-    AXONN_EACH(kActSilu);
+    case kActRelu: act_values<kActRelu, 16>(v); break;
+    case kActGelu: act_values<kActGelu, 16>(v); break;
+    case kActGeluTanh: act_values<kActGeluTanh, 16>(v); break;
+    case kActSilu: act_values<kActSilu, 16>(v); break;
     default: break;
   }
-#undef AXONN_EACH
 }
 __device__ __forceinline__ void apply_slope16(int act, float* v, const uint32_t* z) {
-#define AXONN_EACH(A)                                                                     \
-  case A:                                                                                 \
-    _Pragma("unroll") for (int j = 0; j < 16; ++j) v[j] *=                                \
-        act_slope<A>(__uint_as_float((j & 1) ? z[j >> 1] & 0xFFFF0000u : z[j >> 1] << 16)); \
-    break
   switch (act) {
-    AXONN_EACH(kActRelu);
-    AXONN_EACH(kActGelu);
-    AXONN_EACH(kActGeluTanh);
-    AXONN_EACH(kActSilu);
+    case kActRelu: act_slopes<kActRelu, 16>(v, z); break;
+    case kActGelu: act_slopes<kActGelu, 16>(v, z); break;
+    case kActGeluTanh: act_slopes<kActGeluTanh, 16>(v, z); break;
+    case kActSilu: act_slopes<kActSilu, 16>(v, z); break;
     default: break;
   }
-#undef AXONN_EACH
 }
 
 // ------------------------------------------------------------------ dropout

@@ -254,6 +254,21 @@ __device__ __forceinline__ bool epilogue_steps(const typename Epi::Args& a, cons
   return true;
 }
 
+// Barrier of the epilogue's threads that ORs a predicate over them.
+template <int kThreads>
+__device__ __forceinline__ bool epilogue_any(bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(pred)), "n"(kThreads)
+      : "memory");
+  return r != 0;
+}
+
 template <class Epi, int BN, int STAGES, bool kPair, int kHalves>
 __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThreads, 1)
     fused_gemm_kernel(const __grid_constant__ FusedParams<typename Epi::Args> P) {
@@ -552,11 +567,16 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
         tile.has = num_k > 0;
         auto ready = [&]() -> bool {
           if (!tile.has) return true;
-          int got = 1;
-          if (lane == 0) got = wait_bounded(tfull_bar(b), parity, tmo, abort_flag, kSiteEpiTmemFull);
-          got = __shfl_sync(0xFFFFFFFFu, got, 0);
+          // One warp polls; the others sleep in a hardware barrier, which
+          // also tells them how it ended.
+          bool late = false;
+          if (warp == L::kEpiFirst) {
+            if (lane == 0) late = !wait_bounded(tfull_bar(b), parity, tmo, abort_flag, kSiteEpiTmemFull);
+            late = __shfl_sync(0xFFFFFFFFu, late, 0);
+          }
+          late = epilogue_any<32 * L::kEpi>(late);
           tc_fence_after();
-          return got != 0;
+          return !late;
         };
         auto release = [&]() {  // once, when this warp has read its part
           tc_fence_before();

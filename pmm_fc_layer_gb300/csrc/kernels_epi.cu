@@ -85,14 +85,14 @@ struct FwdEpilogue {
   static __device__ __forceinline__ void step(const Args& a, const State& rng, const EpiTile& t, int c,
                                               float (&x)[32]) {
     const int col = t.col + 32 * c;
-    Residual<kF32> r;
-    if (a.residual) r.start(a, t, col);
     if (a.bias) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         if (col + 16 * h < t.N) add_bias16(a, col + 16 * h, t.N - col - 16 * h, x + 16 * h);
     }
     if (a.pre_out) store_bf16(t, t.out2, col, x);
+    Residual<kF32> r;
+    if (a.residual) r.start(a, t, col);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       apply_act16(a.act, x + 16 * h);
