@@ -1096,25 +1096,46 @@ axonn_status_t check_colsum_ws(const void* ws, size_t ws_bytes, int64_t rows, in
   return AXONN_OK;
 }
 
-// The tile of a fused product: the one whose waves over the GPU cost least,
-// area over throughput relative to the pair's 256 x 256.
-constexpr double kFusedSpeed[axonn::kFusedConfigs] = {1.0, 0.70, 0.40, 1.12};
+// How to run a fused product: its tile, and (where its output can be fp32
+// parts to be summed afterwards) the ranges its reduction is cut into.
+struct FusedChoice {
+  int config = 0;
+  int splits = 1;
+};
+// TFLOP/s of each tile on full waves (GB300, 8192 x 24576 x 6144 and
+// multiples of whole waves), shared by the units that run at once.
+constexpr double kFusedRate[axonn::kFusedConfigs] = {1580, 1100, 630, 1720};
 constexpr int kFusedPlain[axonn::kFusedConfigs] = {2, 0, 7, 6};  // the plain products' configuration of that tile
-int choose_fused(int64_t M, int64_t N, const DeviceState& dev) {
+constexpr double kFusedBytes = 6e6;  // bytes a microsecond that the parts of a split are written and read at
+constexpr int kFusedMostSplits = 16;
+// The choice of least estimated time: rounds of tiles over the units that run
+// at once, each as long as a tile's share of the reduction, and for a split
+// its parts' traffic (8 bytes an element and part).
+FusedChoice choose_fused(int64_t M, int64_t N, int64_t R, bool split, const DeviceState& dev) {
   const int forced = g_forced_config.load();
+  int only = -1;
   for (int i = 0; i < axonn::kFusedConfigs; ++i)
-    if (forced == kFusedPlain[i]) return i;
-  int best = 0;
-  double cost = 0;
+    if (forced == kFusedPlain[i]) only = i;
+  FusedChoice best;
+  double least = 0;
+  bool first = true;
   for (int i = 0; i < axonn::kFusedConfigs; ++i) {
+    if (only >= 0 && i != only) continue;
     const axonn::FusedConfig& c = axonn::kFusedConfig[i];
-    const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
     const int64_t slots = c.pair ? dev.max_pairs : dev.sms;
-    const double x = static_cast<double>((tiles + slots - 1) / slots) * c.bm * c.bn /
-                     (kFusedSpeed[i] * (c.pair ? 2 : 1));
-    if (i == 0 || x < cost) {
-      best = i;
-      cost = x;
+    const int64_t tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn);
+    const double tile_us = 2.0 * c.bm * c.bn * static_cast<double>(std::max<int64_t>(R, 1)) * slots /
+                           (kFusedRate[i] * 1e6);
+    for (int s = 1; s <= (split ? kFusedMostSplits : 1); ++s) {
+      if (s > 1 && R / s < 1024) break;
+      const double us = static_cast<double>((tiles * s + slots - 1) / slots) * tile_us / s +
+                        (s > 1 ? s * 8.0 * M * N / kFusedBytes : 0.0);
+      if (first || us < least) {
+        first = false;
+        least = us;
+        best.config = i;
+        best.splits = s;
+      }
     }
   }
   return best;
@@ -1190,6 +1211,7 @@ axonn_status_t fused_fill(axonn::FusedParams<Args>& P, const OpView& v, int conf
     P.l2_keep_frac =
         panel <= budget ? 1.0f : std::max(1.0f / 64.0f, static_cast<float>(budget) / panel);
   }
+  P.splits = 1;
   P.inject = g_inject.load();
   P.timeout_ns = g_timeout_ns.load();
   *units = static_cast<int>(std::min<int64_t>(tm * tn, c.pair ? dev.max_pairs : dev.sms));
@@ -1279,7 +1301,7 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
   if (v.M > 0) {
     axonn::FusedParams<axonn::EpilogueArgs> fp;
     int units = 0;
-    const int config = choose_fused(v.M, v.N, *dev);
+    const int config = choose_fused(v.M, v.N, v.R, false, *dev).config;
     st = fused_fill(fp, v, config, 16, *dev, &units);
     if (st == AXONN_OK) st = encode_out(&fp.out, C, v.M, v.N, ldc, f32);
     if (st == AXONN_OK && e.pre_out) st = encode_out(&fp.out2, epi->pre, v.M, v.N, epi->ld_pre, false);
@@ -1302,8 +1324,8 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
 constexpr int64_t kCePieceStep = 256;               // columns: whole tiles of every configuration
 constexpr size_t kCePieceDefault = size_t{2} << 30;  // bytes of one piece of the vocabulary
 struct CeLayout {
-  size_t index, place, labels, coef, label_logit, lse2, stats, x, dx32, piece;
-  int64_t ld_x, ld_dx;
+  size_t index, place, labels, coef, label_logit, lse2, stats, x, end;
+  int64_t ld_x;
 };
 size_t up256(size_t n) { return (n + 255) & ~size_t{255}; }
 
@@ -1319,37 +1341,52 @@ CeLayout ce_layout(int64_t T, int64_t K, int64_t V) {
   l.index = take(4 * t);
   l.place = take(4 * t);
   l.labels = take(4 * t);
-  l.coef = take(4);
+  l.coef = take(8);  // and the combining kernel's counter
   l.label_logit = take(4 * t);
   l.lse2 = take(4 * t);
   l.stats = take(8 * t * static_cast<size_t>((V + axonn::kEpilogueCols - 1) / axonn::kEpilogueCols));
   l.ld_x = (K + 7) / 8 * 8;
   l.x = take(2 * t * static_cast<size_t>(l.ld_x));
-  l.ld_dx = l.ld_x;
-  l.dx32 = l.piece = at;
+  l.end = at;
   return l;
 }
 
-// Bytes beyond the fixed part for pieces of `cols` columns: the piece, and
-// where there are several of them dX's fp32 sum.
-size_t ce_piece_bytes(int64_t T, int64_t K, int64_t V, int64_t cols) {
-  const int64_t c = std::min(cols, (V + 7) / 8 * 8);
-  size_t b = up256(2 * static_cast<size_t>(T) * static_cast<size_t>(c));
-  if (cols < V) b += up256(4 * static_cast<size_t>(T) * static_cast<size_t>((K + 7) / 8 * 8));
-  return b;
+// What a call with gradients adds to that: the piece of the vocabulary held
+// at a time, and dX in fp32 where it is a sum over pieces, or over the ranges
+// of a split reduction (parts of ce_part_rows rows each).
+struct CePlan {
+  int64_t cols = 0;  // columns of a piece; V: all of them
+  int splits = 1;    // parts of dX
+  size_t dx_bytes = 0, piece_bytes = 0;
+  size_t bytes() const { return dx_bytes + piece_bytes; }
+};
+int64_t ce_part_rows(int64_t T) { return (T + 31) / 32 * 32; }
+
+CePlan ce_plan(int64_t T, int64_t K, int64_t V, int64_t cols, int splits) {
+  CePlan p;
+  p.cols = std::min(cols, V);
+  p.splits = cols < V ? 1 : splits;
+  p.piece_bytes = up256(2 * static_cast<size_t>(T) * static_cast<size_t>((p.cols + 7) / 8 * 8));
+  if (cols < V || splits > 1)
+    p.dx_bytes = up256(4 * static_cast<size_t>(p.splits) * static_cast<size_t>(ce_part_rows(T)) *
+                       static_cast<size_t>((K + 7) / 8 * 8));
+  return p;
 }
 
-// Columns of one piece that fit `bytes`: the whole vocabulary, else the most
-// whole tiles (0: not even one).
-int64_t ce_piece_cols(int64_t T, int64_t K, int64_t V, size_t bytes) {
-  if (ce_piece_bytes(T, K, V, V) <= bytes) return V;
-  int64_t lo = 0, hi = V / kCePieceStep;  // in steps; lo fits
+// The plan that fits `bytes`: the whole vocabulary (with the split, or else
+// without), else the most whole tiles of it.  cols = 0: not even one.
+CePlan ce_fit(int64_t T, int64_t K, int64_t V, int splits, size_t bytes) {
+  for (int s : {splits, 1}) {
+    const CePlan p = ce_plan(T, K, V, V, s);
+    if (p.bytes() <= bytes) return p;
+  }
+  int64_t lo = 0, hi = (V - 1) / kCePieceStep;  // in steps; lo fits
   while (lo < hi) {
     const int64_t mid = (lo + hi + 1) / 2;
-    if (ce_piece_bytes(T, K, V, mid * kCePieceStep) <= bytes) lo = mid;
+    if (ce_plan(T, K, V, mid * kCePieceStep, 1).bytes() <= bytes) lo = mid;
     else hi = mid - 1;
   }
-  return lo * kCePieceStep;
+  return lo > 0 ? ce_plan(T, K, V, lo * kCePieceStep, 1) : CePlan{};
 }
 
 int64_t ce_default_cols(int64_t T, int64_t V) {
@@ -1380,24 +1417,38 @@ axonn_status_t check_ce(int64_t T, int64_t K, int64_t V, uint32_t flags) {
     if (ce_ != cudaSuccess) return fail(AXONN_ERR_CUDA, what ": %s", cudaGetErrorString(ce_)); \
   } while (0)
 
-// A product whose tiles are stored as they are, on the fused kernels (whose
-// extent may be the device's count).
-axonn_status_t store_product(const OpView& v, void* out, int64_t ld_out, int mode, const float* scale,
-                             const int32_t* count, int count_of, int group_m, const DeviceState& dev,
-                             cudaStream_t stream) {
+// A product whose tiles are stored times a number, on the fused kernels
+// (whose extent may be the device's count).  With splits > 1 the output is
+// that many matrices, split_rows rows apart.
+axonn_status_t store_product(const OpView& v, FusedChoice choice, void* out, int64_t ld_out, int mode,
+                             const float* scale, const int32_t* count, int count_of, int64_t split_rows,
+                             const DeviceState& dev, cudaStream_t stream) {
   if (v.M == 0 || v.N == 0) return AXONN_OK;
   axonn::FusedParams<axonn::StoreArgs> p;
   int units = 0;
-  const int config = choose_fused(v.M, v.N, dev);
-  axonn_status_t st = fused_fill(p, v, config, group_m, dev, &units);
-  if (st == AXONN_OK) st = encode_out(&p.out, out, v.M, v.N, ld_out, mode != axonn::kOutBF16);
+  axonn_status_t st = fused_fill(p, v, choice.config, 16, dev, &units);
+  const int64_t rows = choice.splits > 1 ? choice.splits * split_rows : v.M;
+  if (rows > INT32_MAX) return fail(AXONN_ERR_UNSUPPORTED, "more than 2^31 rows of parts");
+  if (st == AXONN_OK) st = encode_out(&p.out, out, rows, v.N, ld_out, mode != axonn::kOutBF16);
   if (st != AXONN_OK) return st;
+  const axonn::FusedConfig& c = axonn::kFusedConfig[choice.config];
+  p.splits = choice.splits;
+  p.split_rows = static_cast<int32_t>(choice.splits > 1 ? split_rows : 0);
+  units = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.splits,
+                                             c.pair ? dev.max_pairs : dev.sms));
   p.count = count;
   p.count_of = count_of;
   p.epi.scale = scale;
   p.epi.mode = mode;
-  AXONN_CE_RUN(axonn::store_launch(config, p, units, g_pdl.load() != 0, stream), "product");
+  AXONN_CE_RUN(axonn::store_launch(choice.config, p, units, g_pdl.load() != 0, stream), "product");
   return AXONN_OK;
+}
+
+// dX's choice: a product of few tiles with the vocabulary as its reduction.
+FusedChoice choose_dx(int64_t T, int64_t K, int64_t V) {
+  DeviceState* dev = nullptr;
+  if (T == 0 || K == 0 || device_state(&dev) != AXONN_OK) return {};
+  return choose_fused(T, K, V, true, *dev);
 }
 
 }  // namespace
@@ -2133,11 +2184,11 @@ axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, u
   const axonn_status_t st = check_ce(T, K, V, flags);
   if (st != AXONN_OK) return st;
   if (piece < 0) return fail(AXONN_ERR_INVALID_ARG, "piece of %lld columns", (long long)piece);
-  size_t b = ce_layout(T, K, V).piece;
+  size_t b = ce_layout(T, K, V).end;
   if (grad) {
     int64_t cols = piece == 0 ? ce_default_cols(T, V) : piece;
     if (cols < V) cols = (cols + kCePieceStep - 1) / kCePieceStep * kCePieceStep;
-    b += ce_piece_bytes(T, K, V, std::min(cols, V));
+    b += ce_plan(T, K, V, cols, choose_dx(T, K, V).splits).bytes();
   }
   *bytes = b;
   return ok();
@@ -2160,27 +2211,31 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
   if (st == AXONN_OK && dX) st = check_matrix("dX", dX, lddx, T, K, false);
   if (st == AXONN_OK && dW) st = check_matrix("dW", dW, lddw, w_t ? V : K, w_t ? K : V, w_f32);
   if (st != AXONN_OK) return st;
-  CeLayout l = ce_layout(T, K, V);
-  const size_t least = l.piece + (grad ? std::min(ce_piece_bytes(T, K, V, V),
-                                                  ce_piece_bytes(T, K, V, std::min(kCePieceStep, V)))
+  const CeLayout l = ce_layout(T, K, V);
+  FusedChoice dx_choice = dX ? choose_dx(T, K, V) : FusedChoice{};
+  const size_t room = ws_bytes > l.end ? ws_bytes - l.end : 0;
+  // Loss alone: one product over the whole vocabulary, nothing kept.
+  const CePlan plan = grad ? ce_fit(T, K, V, dx_choice.splits, room) : ce_plan(0, 0, V, V, 1);
+  if (!ws || ws_bytes < l.end || plan.cols == 0) {
+    const size_t least = l.end + (grad ? std::min(ce_plan(T, K, V, V, 1).bytes(),
+                                                  ce_plan(T, K, V, kCePieceStep, 1).bytes())
                                        : 0);
-  if (!ws || ws_bytes < least)
     return fail(AXONN_ERR_WORKSPACE, "linear cross entropy needs at least %zu workspace bytes, got %zu", least,
                 ws ? ws_bytes : size_t{0});
+  }
   if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
     return fail(AXONN_ERR_ALIGNMENT, "workspace is not 256-byte aligned");
-  // Loss alone: one product over the whole vocabulary, nothing kept.
-  const int64_t cols = grad ? ce_piece_cols(T, K, V, ws_bytes - l.piece) : V;
+  const int64_t cols = plan.cols;
   const int64_t pieces = (V + cols - 1) / cols;
-  if (pieces > 1) l.piece += up256(4 * static_cast<size_t>(T) * static_cast<size_t>(l.ld_dx));
   DeviceState* dev = nullptr;
   st = device_state(&dev);
   if (st != AXONN_OK) return st;
+  if (plan.splits != dx_choice.splits) dx_choice = choose_fused(T, K, cols, false, *dev);
   char* base = static_cast<char*>(ws);
-  const int64_t ld_piece = (std::min(cols, V) + 7) / 8 * 8;
-  uint16_t* piece = reinterpret_cast<uint16_t*>(base + l.piece);
-  float* dx32 = reinterpret_cast<float*>(base + l.dx32);
-  const int config = choose_fused(T, std::min(cols, V), *dev);
+  const int64_t ld_piece = (cols + 7) / 8 * 8;
+  float* dx32 = reinterpret_cast<float*>(base + l.end);
+  uint16_t* piece = reinterpret_cast<uint16_t*>(base + l.end + plan.dx_bytes);
+  const int config = choose_fused(T, cols, K, false, *dev).config;
   const bool pdl = g_pdl.load() != 0;
 
   axonn::CeRowArgs a{};
@@ -2198,6 +2253,7 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
   a.packed_x = reinterpret_cast<uint16_t*>(base + l.x);
   a.ld_packed = l.ld_x;
   a.coef = reinterpret_cast<float*>(base + l.coef);
+  a.done = reinterpret_cast<uint32_t*>(base + l.coef + 4);
   a.stats = reinterpret_cast<const float2*>(base + l.stats);
   a.group_cols = axonn::kEpilogueCols;
   a.groups = (V + a.group_cols - 1) / a.group_cols;
@@ -2211,7 +2267,7 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
   a.ld_dx = lddx;
 
   AXONN_CE_RUN(axonn::ce_index_launch(a, stream), "packing");
-  AXONN_CE_RUN(axonn::ce_gather_launch(a, dev->sms, stream), "packing");
+  AXONN_CE_RUN(axonn::ce_gather_launch(a, stream), "packing");
 
   // X . W over columns [c0, c0 + n): the packed rows against a piece of W.
   const char* Wb = static_cast<const char*>(W);
@@ -2255,10 +2311,10 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
     if (st != AXONN_OK) return st;
   }
   AXONN_CE_RUN(axonn::ce_combine_launch(a, stream), "logsumexp");
-  AXONN_CE_RUN(axonn::ce_mean_launch(a, stream), "mean");
   if (!grad) return ok();
 
   // Backward: the piece that is there first, then the others, recomputed.
+  const bool in_place = pieces == 1 && dx_choice.splits == 1;
   for (int64_t j = 0; j < pieces; ++j) {
     const int64_t i = j == 0 ? pieces - 1 : j - 1;
     const int64_t c0 = i * cols, n = std::min(cols, V - c0);
@@ -2284,30 +2340,28 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
       const int mode = (flags & AXONN_ACCUM_F32) ? axonn::kOutF32Accum
                        : (flags & AXONN_OUT_F32) ? axonn::kOutF32
                                                  : axonn::kOutBF16;
-      st = store_product(x, static_cast<char*>(dW) + off * (w_f32 ? 4 : 2), lddw, mode, a.coef, kept, 2, 16,
-                         *dev, stream);
+      st = store_product(x, choose_fused(x.M, x.N, x.R, false, *dev), static_cast<char*>(dW) + off * (w_f32 ? 4 : 2),
+                         lddw, mode, a.coef, kept, 2, 0, *dev, stream);
       if (st != AXONN_OK) return st;
     }
     if (dX) {
       // dX = P . W^T, packed: in bf16 over the packed X, which nothing reads
-      // any more, or summed over the pieces in fp32
+      // any more, or in fp32, summed over the pieces or in parts
       OpView v = logits_view(c0, n);
       v.A = reinterpret_cast<const char*>(piece);
       v.lda = ld_piece;
       v.b_mn = w_t;
       v.N = K;
       v.R = n;
-      const bool one = pieces == 1;
-      st = store_product(v, one ? static_cast<void*>(a.packed_x) : static_cast<void*>(dx32),
-                         one ? l.ld_x : l.ld_dx,
-                         one ? axonn::kOutBF16 : (j == 0 ? axonn::kOutF32 : axonn::kOutF32Accum), a.coef, kept, 1,
-                         16, *dev, stream);
+      st = store_product(v, dx_choice, in_place ? static_cast<void*>(a.packed_x) : static_cast<void*>(dx32), l.ld_x,
+                         in_place ? axonn::kOutBF16 : (j == 0 ? axonn::kOutF32 : axonn::kOutF32Accum), a.coef,
+                         kept, 1, ce_part_rows(T), *dev, stream);
       if (st != AXONN_OK) return st;
     }
   }
   if (dX)
-    AXONN_CE_RUN(axonn::ce_unpack_launch(a, pieces == 1 ? static_cast<const void*>(a.packed_x) : dx32,
-                                         pieces == 1 ? l.ld_x : l.ld_dx, pieces > 1, dev->sms, stream), "dX");
+    AXONN_CE_RUN(axonn::ce_unpack_launch(a, in_place ? static_cast<const void*>(a.packed_x) : dx32, l.ld_x,
+                                         in_place ? 0 : dx_choice.splits, ce_part_rows(T), dev->sms, stream), "dX");
   return ok();
 }
 

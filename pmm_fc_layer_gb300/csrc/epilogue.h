@@ -77,6 +77,9 @@ struct FusedParams {
   // multiple of 64 are then zero), read when the product starts.
   const int32_t* count;
   int32_t count_of;
+  // The reduction in `splits` consecutive ranges, each a product of its own:
+  // range s writes the rows from s * split_rows on.
+  int32_t splits, split_rows;
   int32_t M, N, num_k;
   int32_t tiles_m, tiles_n;
   uint32_t idesc;

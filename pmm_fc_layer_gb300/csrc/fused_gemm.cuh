@@ -85,6 +85,7 @@ struct EpiTile {
   int row, col;
   int M, N;
   int rows;                          // rows that stores write: M, unless an epilogue pads
+  int row_off;                       // where row 0 of the output lies (a split reduction's range)
   uint32_t slot;                     // shared memory, kSlotBytes
   const OutMatrix* out;
   const OutMatrix* out2;
@@ -180,7 +181,7 @@ __device__ __forceinline__ void store_segment(const EpiTile& t, const OutMatrix*
   const int lane = threadIdx.x & 31;
   if (col + kCols > t.N && t.N % kPer16 != 0) {
     if (t.row < t.rows) {
-      T* p = static_cast<T*>(m->base) + t.row * m->ld + col;
+      T* p = static_cast<T*>(m->base) + static_cast<int64_t>(t.row + t.row_off) * m->ld + col;
       const int n = t.N - col;
 #pragma unroll
       for (int j = 0; j < kCols; ++j)
@@ -198,7 +199,7 @@ __device__ __forceinline__ void store_segment(const EpiTile& t, const OutMatrix*
   if (lane == 0 && t.row < t.rows) {  // lane 0 has the first row
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                      reinterpret_cast<uint64_t>(&m->map)),
-                 "r"(t.slot), "r"(col), "r"(t.row)
+                 "r"(t.slot), "r"(col), "r"(t.row + t.row_off)
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
@@ -340,17 +341,23 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
   const uint32_t tmem_base = *tmem_slot;
   const uint64_t tmo = P.timeout_ns;
   griddep_wait();  // nothing above touches what the previous kernel writes
-  int M = P.M, tiles_m = P.tiles_m, num_k = P.num_k;
+  int M = P.M, tiles_m = P.tiles_m, all_k = P.num_k;
   if (P.count_of != 0) {
     const int n = *P.count;
     if (P.count_of == 1) {
       M = n;
       tiles_m = (n + kTileM - 1) / kTileM;
     } else {
-      num_k = (n + kBK - 1) / kBK;
+      all_k = (n + kBK - 1) / kBK;
     }
   }
-  const int total = tiles_m * P.tiles_n;
+  const int per_split = tiles_m * P.tiles_n;
+  const int total = per_split * P.splits;
+  // Range s of the reduction: stages [all_k s / splits, all_k (s + 1) / splits).
+  auto range = [&](int split, int& k0) {
+    k0 = static_cast<int>(static_cast<int64_t>(all_k) * split / P.splits);
+    return static_cast<int>(static_cast<int64_t>(all_k) * (split + 1) / P.splits) - k0;
+  };
 
   if constexpr (kHalves == 2) {
     if (warp < L::kEpiFirst) setmaxnreg_dec<kFusedRegsControl>();
@@ -364,15 +371,16 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
       const uint64_t pol_a = l2_policy(P.l2_keep == 1, P.l2_keep_frac);
       const uint64_t pol_b = l2_policy(P.l2_keep == 2, P.l2_keep_frac);
       for (int t = unit; ok && t < total; t += units) {
-        int mb, nb;
-        fused_tile(t, P.group_m, tiles_m, P.tiles_n, mb, nb);
+        int mb, nb, k_first;
+        const int num_k = range(t / per_split, k_first);
+        fused_tile(t % per_split, P.group_m, tiles_m, P.tiles_n, mb, nb);
         const int m0 = mb * kTileM + static_cast<int>(rank) * kCtaM;
         const int n0 = nb * BN + static_cast<int>(rank) * L::kBCols;
         for (int k = 0; k < num_k; ++k) {
           ok = wait_bounded(empty_bar(stage), phase ^ 1u, tmo, abort_flag, kSiteProducerEmpty);
           if (!ok) break;
           if (leader) mbar_arrive_expect_tx(full_bar(stage), P.load_bytes);
-          const int r0 = k * kBK;
+          const int r0 = (k_first + k) * kBK;
           if constexpr (kPair) {
             const uint32_t fb = mapa_shared(full_bar(stage), 0);
             if (P.a_3d) {
@@ -437,7 +445,7 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && leader && num_k > 0) {
+    if (lane == 0 && leader && all_k > 0) {
       uint32_t acc = 0;
       bool ok = true;
       // The MMAs of one stage into one accumulator.
@@ -458,7 +466,10 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
       if constexpr (kHalves == 1) {
         int stage = 0;
         uint32_t phase = 0;
-        for (int t = unit; ok && t < total; t += units, ++acc) {
+        for (int t = unit; ok && t < total; t += units) {
+          int k_first;
+          const int num_k = range(t / per_split, k_first);
+          if (num_k == 0) continue;  // as the epilogue counts
           const uint32_t b = acc & 1u;
           ok = wait_bounded(tempty_bar(b), ((acc >> 1) & 1u) ^ 1u, tmo, abort_flag, kSiteMmaTmemEmpty);
           if (!ok) break;
@@ -476,12 +487,12 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
           }
           if (!ok) break;
           commit(tfull_bar(b));
+          ++acc;
         }
       } else {
         // Half 0 runs stages [0, a), then both halves alternate, then half 0
         // runs [e, num_k); half 1 follows at either end.  No stage is held
         // over more than the ring: kSkew <= STAGES.
-        const int a = min(kSkew, num_k), e = max(a, num_k - kSkew);
         uint32_t base = 0;  // stages consumed before this tile
         auto run = [&](int half, int k0, int k1, bool wait_full, bool free_stage) -> bool {
           for (int k = k0; k < k1; ++k) {
@@ -496,7 +507,11 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
           }
           return true;
         };
-        for (int t = unit; ok && t < total; t += units, ++acc) {
+        for (int t = unit; ok && t < total; t += units) {
+          int k_first;
+          const int num_k = range(t / per_split, k_first);
+          if (num_k == 0) continue;  // as the epilogue counts
+          const int a = min(kSkew, num_k), e = max(a, num_k - kSkew);
           const uint32_t parity = (acc & 1u) ^ 1u;
           ok = wait_bounded(tempty_bar(0), parity, tmo, abort_flag, kSiteMmaTmemEmpty);
           if (!ok) break;
@@ -532,6 +547,7 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
           run(1, e, num_k, false, true);
           commit(tfull_bar(1));
           base += static_cast<uint32_t>(num_k);
+          ++acc;
         }
       }
       // Every MMA of this thread is done before TMEM is released.
@@ -547,9 +563,11 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
     typename Epi::State st = Epi::begin(P.epi);
     uint32_t acc = 0;
     bool ok = true;
-    for (int t = unit; ok && t < total; t += units, ++acc) {
-      int mb, nb;
-      fused_tile(t, P.group_m, tiles_m, P.tiles_n, mb, nb);
+    for (int t = unit; ok && t < total; t += units) {
+      int mb, nb, k_first;
+      const int split = t / per_split;
+      const bool has = range(split, k_first) > 0;
+      fused_tile(t - split * per_split, P.group_m, tiles_m, P.tiles_n, mb, nb);
 #pragma unroll 1
       for (int half = 0; ok && half < kHalves; ++half) {
         // buffers alternate by tile (one half), or belong to the halves
@@ -564,7 +582,8 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
         tile.slot = slots + static_cast<uint32_t>((warp - L::kEpiFirst) * L::kSlotBytes);
         tile.out = &P.out;
         tile.out2 = &P.out2;
-        tile.has = num_k > 0;
+        tile.row_off = split * P.split_rows;
+        tile.has = has;
         auto ready = [&]() -> bool {
           if (!tile.has) return true;
           // One warp polls; the others sleep in a hardware barrier, which
@@ -588,6 +607,7 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
         };
         ok = Epi::template run<L::kWarpCols, kHalves == 2>(P.epi, st, tile, ready, release);
       }
+      if (has) ++acc;
     }
     // this warp's stores are complete before the CTA may exit
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");

@@ -153,7 +153,7 @@ struct StoreEpilogue {
     } else if (t.has && t.row < t.M) {
       // added by the L2's reductions: one writer an element, so that they
       // round as a load-add-store would
-      float* o = static_cast<float*>(t.out->base) + t.row * t.out->ld + col;
+      float* o = static_cast<float*>(t.out->base) + static_cast<int64_t>(t.row + t.row_off) * t.out->ld + col;
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
         if (j + 4 <= n) {

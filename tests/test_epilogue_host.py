@@ -188,7 +188,8 @@ def test_workspace_sizes(fc):
     T, K, V = 4096, 512, 128256
     loss = fc.axonn_linear_ce_workspace_size(T, K, V, grad=False)
     whole = fc.axonn_linear_ce_workspace_size(T, K, V)
-    assert whole - loss == 2 * T * V                  # all of P in one piece
+    # all of P in one piece, and dX as the fp32 parts of a split reduction, if any
+    assert 2 * T * V <= whole - loss <= 2 * T * V + 16 * 4 * T * K
     piece = fc.axonn_linear_ce_workspace_size(T, K, V, piece=8192)
     assert piece - loss == 2 * T * 8192 + 4 * T * K   # a piece, and dX's fp32 sum
     assert fc.axonn_linear_ce_workspace_size(T, K, V, piece=8191) == piece
