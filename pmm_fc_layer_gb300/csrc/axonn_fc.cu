@@ -23,6 +23,7 @@
 #include "elementwise.h"
 #include "epilogue.h"
 #include "gemm_kernel.cuh"
+#include "gemv.h"
 #include "goldfish.h"
 #include "kernel_launch.h"
 #include "linear_ce.h"
@@ -1299,16 +1300,36 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
   st = device_state(&dev);
   if (st != AXONN_OK) return st;
   if (v.M > 0) {
-    axonn::FusedParams<axonn::EpilogueArgs> fp;
-    int units = 0;
-    const int config = choose_fused(v.M, v.N, v.R, false, *dev).config;
-    st = fused_fill(fp, v, config, 16, *dev, &units);
-    if (st == AXONN_OK) st = encode_out(&fp.out, C, v.M, v.N, ldc, f32);
-    if (st == AXONN_OK && e.pre_out) st = encode_out(&fp.out2, epi->pre, v.M, v.N, epi->ld_pre, false);
-    if (st != AXONN_OK) return st;
-    fp.epi = e;
-    const cudaError_t ce = axonn::fused_launch(fwd ? axonn::kFusedFwd : axonn::kFusedBwd, config, fp, units,
-                                               g_pdl.load() != 0, stream);
+    const axonn::FusedKind kind = fwd ? axonn::kFusedFwd : axonn::kFusedBwd;
+    cudaError_t ce;
+    if (g_forced_config.load() < 0 && axonn::gemv_wins(v.M, v.N, v.R, dev->sms)) {
+      axonn::GemvArgs p{};
+      p.A = reinterpret_cast<const uint16_t*>(v.A);
+      p.lda = v.lda;
+      p.a_mn = v.a_mn;
+      p.B = reinterpret_cast<const uint16_t*>(v.B);
+      p.ldb = v.ldb;
+      p.M = static_cast<int32_t>(v.M);
+      p.N = v.N;
+      p.R = v.R;
+      p.out = C;
+      p.ld_out = ldc;
+      p.out2 = fwd ? epi->pre : nullptr;
+      p.ld_out2 = epi->ld_pre;
+      p.epi = e;
+      t_last_config = -1;
+      ce = axonn::gemv_launch(kind, p, v.b_mn, dev->sms, g_pdl.load() != 0, stream);
+    } else {
+      axonn::FusedParams<axonn::EpilogueArgs> p;
+      int units = 0;
+      const int config = choose_fused(v.M, v.N, v.R, false, *dev).config;
+      st = fused_fill(p, v, config, 16, *dev, &units);
+      if (st == AXONN_OK) st = encode_out(&p.out, C, v.M, v.N, ldc, f32);
+      if (st == AXONN_OK && e.pre_out) st = encode_out(&p.out2, epi->pre, v.M, v.N, epi->ld_pre, false);
+      if (st != AXONN_OK) return st;
+      p.epi = e;
+      ce = axonn::fused_launch(kind, config, p, units, g_pdl.load() != 0, stream);
+    }
     if (ce != cudaSuccess) return fail(AXONN_ERR_CUDA, "fused product: %s", cudaGetErrorString(ce));
   }
   if (epi->dbias) {
