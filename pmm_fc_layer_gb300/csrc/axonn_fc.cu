@@ -1334,7 +1334,7 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
   }
   if (epi->dbias) {
     const cudaError_t ce =
-        axonn::colsum_launch(e.colsum, e.ld_colsum, (v.M + 31) / 32, v.N, epi->dbias, stream);
+        axonn::colsum_launch(e.colsum, e.ld_colsum, (v.M + 31) / 32, v.N, epi->dbias, g_pdl.load() != 0, stream);
     if (ce != cudaSuccess) return fail(AXONN_ERR_CUDA, "bias gradient: %s", cudaGetErrorString(ce));
   }
   return ok();
@@ -2161,9 +2161,10 @@ axonn_status_t axonn_epi_bwd(const void* dY, int64_t lddy, void* dZ, int64_t ldd
   DeviceState* dev = nullptr;
   st = device_state(&dev);
   if (st != AXONN_OK) return st;
-  cudaError_t e = axonn::act_bwd_launch(a, f32, stream);
+  cudaError_t e = axonn::act_bwd_launch(a, f32, g_pdl.load() != 0, stream);
   if (e == cudaSuccess && epi->dbias)
-    e = axonn::colsum_launch(a.colsum, a.ld_colsum, axonn::act_bwd_groups(rows), cols, epi->dbias, stream);
+    e = axonn::colsum_launch(a.colsum, a.ld_colsum, axonn::act_bwd_groups(rows), cols, epi->dbias,
+                             g_pdl.load() != 0, stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "elementwise backward: %s", cudaGetErrorString(e));
   return ok();
 }
@@ -2194,7 +2195,7 @@ axonn_status_t axonn_dropout(const void* X, int64_t ldx, const void* residual, i
   a.ld_y = ldy;
   a.rows = rows;
   a.cols = cols;
-  const cudaError_t e = axonn::dropout_launch(a, f32, dev->sms, stream);
+  const cudaError_t e = axonn::dropout_launch(a, f32, dev->sms, g_pdl.load() != 0, stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "dropout: %s", cudaGetErrorString(e));
   return ok();
 }
@@ -2287,8 +2288,8 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
   a.dx = static_cast<uint16_t*>(dX);
   a.ld_dx = lddx;
 
-  AXONN_CE_RUN(axonn::ce_index_launch(a, stream), "packing");
-  AXONN_CE_RUN(axonn::ce_gather_launch(a, stream), "packing");
+  AXONN_CE_RUN(axonn::ce_index_launch(a, pdl, stream), "packing");
+  AXONN_CE_RUN(axonn::ce_gather_launch(a, pdl, stream), "packing");
 
   // X . W over columns [c0, c0 + n): the packed rows against a piece of W.
   const char* Wb = static_cast<const char*>(W);
@@ -2331,7 +2332,7 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
     st = logits(axonn::kCeStats, c0, n, grad && i == pieces - 1);
     if (st != AXONN_OK) return st;
   }
-  AXONN_CE_RUN(axonn::ce_combine_launch(a, stream), "logsumexp");
+  AXONN_CE_RUN(axonn::ce_combine_launch(a, pdl, stream), "logsumexp");
   if (!grad) return ok();
 
   // Backward: the piece that is there first, then the others, recomputed.
@@ -2340,7 +2341,7 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
     const int64_t i = j == 0 ? pieces - 1 : j - 1;
     const int64_t c0 = i * cols, n = std::min(cols, V - c0);
     if (j == 0) {
-      AXONN_CE_RUN(axonn::ce_scale_launch(a, piece, ld_piece, c0, n, stream), "probabilities");
+      AXONN_CE_RUN(axonn::ce_scale_launch(a, piece, ld_piece, c0, n, pdl, stream), "probabilities");
     } else {
       st = logits(axonn::kCeProb, c0, n, true);
       if (st != AXONN_OK) return st;
@@ -2382,7 +2383,7 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
   }
   if (dX)
     AXONN_CE_RUN(axonn::ce_unpack_launch(a, in_place ? static_cast<const void*>(a.packed_x) : dx32, l.ld_x,
-                                         in_place ? 0 : dx_choice.splits, ce_part_rows(T), dev->sms, stream), "dX");
+                                         in_place ? 0 : dx_choice.splits, ce_part_rows(T), dev->sms, pdl, stream), "dX");
   return ok();
 }
 

@@ -6,6 +6,7 @@
 #include <algorithm>
 
 #include "elementwise.h"
+#include "launch.h"
 #include "vec8.cuh"
 
 namespace axonn {
@@ -22,6 +23,8 @@ template <typename T, bool kRes>
 constexpr int kDropBlocks = sizeof(T) == 2 ? (kRes ? 4 : 5) : (kRes ? 2 : 3);  // resident on an SM
 template <typename T, bool kRes>
 __global__ void __launch_bounds__(kThreads, kDropBlocks<T, kRes>) dropout_kernel(DropoutKernelArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
   const T* X = static_cast<const T*>(a.x);
   const T* R = static_cast<const T*>(a.residual);
   T* Y = static_cast<T*>(a.y);
@@ -125,6 +128,8 @@ __device__ __forceinline__ void act_bwd_rows(const BwdKernelArgs& a, const DropR
 
 template <typename T, int ACT, bool kDrop>
 __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(BwdKernelArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
   __shared__ float part[8][32][9];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 256 + 8 * lane;
@@ -155,13 +160,13 @@ __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(BwdKernelArgs a) {
 }
 
 template <typename T, bool kDrop>
-void act_bwd_start(const BwdKernelArgs& a, dim3 grid, cudaStream_t stream) {
+cudaError_t act_bwd_start(const BwdKernelArgs& a, dim3 grid, bool pdl, cudaStream_t stream) {
   switch (a.act) {
-    case kActRelu: act_bwd_kernel<T, kActRelu, kDrop><<<grid, kThreads, 0, stream>>>(a); break;
-    case kActGelu: act_bwd_kernel<T, kActGelu, kDrop><<<grid, kThreads, 0, stream>>>(a); break;
-    case kActGeluTanh: act_bwd_kernel<T, kActGeluTanh, kDrop><<<grid, kThreads, 0, stream>>>(a); break;
-    case kActSilu: act_bwd_kernel<T, kActSilu, kDrop><<<grid, kThreads, 0, stream>>>(a); break;
-    default: act_bwd_kernel<T, kActNone, kDrop><<<grid, kThreads, 0, stream>>>(a); break;
+    case kActRelu: return launch_after(act_bwd_kernel<T, kActRelu, kDrop>, grid, kThreads, pdl, stream, a);
+    case kActGelu: return launch_after(act_bwd_kernel<T, kActGelu, kDrop>, grid, kThreads, pdl, stream, a);
+    case kActGeluTanh: return launch_after(act_bwd_kernel<T, kActGeluTanh, kDrop>, grid, kThreads, pdl, stream, a);
+    case kActSilu: return launch_after(act_bwd_kernel<T, kActSilu, kDrop>, grid, kThreads, pdl, stream, a);
+    default: return launch_after(act_bwd_kernel<T, kActNone, kDrop>, grid, kThreads, pdl, stream, a);
   }
 }
 
@@ -170,6 +175,8 @@ void act_bwd_start(const BwdKernelArgs& a, dim3 grid, cudaStream_t stream) {
 // sums in order.
 __global__ void __launch_bounds__(kThreads) colsum_kernel(const float* part, int64_t ld, int64_t groups,
                                                           int64_t cols, float* out) {
+  griddep_launch_dependents();
+  griddep_wait();
   __shared__ float sums[8][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + lane;
@@ -192,38 +199,42 @@ __global__ void __launch_bounds__(kThreads) colsum_kernel(const float* part, int
 
 namespace {
 template <typename T, bool kRes>
-cudaError_t dropout_start(const DropoutKernelArgs& a, int sms, cudaStream_t stream) {
+cudaError_t dropout_start(const DropoutKernelArgs& a, int sms, bool pdl, cudaStream_t stream) {
   const int64_t vectors = a.rows * ((a.cols + 7) / 8);
   const int64_t blocks =
       std::min<int64_t>((vectors + kThreads - 1) / kThreads, int64_t{kDropBlocks<T, kRes>} * sms);
-  if (blocks > 0) dropout_kernel<T, kRes><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  if (blocks == 0) return cudaSuccess;
+  return launch_after(dropout_kernel<T, kRes>, dim3(static_cast<unsigned>(blocks)), kThreads, pdl, stream, a);
 }
 }  // namespace
 
-cudaError_t dropout_launch(const DropoutKernelArgs& a, bool f32, int sms, cudaStream_t stream) {
-  if (f32) return a.residual ? dropout_start<float, true>(a, sms, stream) : dropout_start<float, false>(a, sms, stream);
-  return a.residual ? dropout_start<uint16_t, true>(a, sms, stream) : dropout_start<uint16_t, false>(a, sms, stream);
+cudaError_t dropout_launch(const DropoutKernelArgs& a, bool f32, int sms, bool pdl, cudaStream_t stream) {
+  if (f32)
+    return a.residual ? dropout_start<float, true>(a, sms, pdl, stream)
+                      : dropout_start<float, false>(a, sms, pdl, stream);
+  return a.residual ? dropout_start<uint16_t, true>(a, sms, pdl, stream)
+                    : dropout_start<uint16_t, false>(a, sms, pdl, stream);
 }
 
-cudaError_t act_bwd_launch(const BwdKernelArgs& a, bool dy_f32, cudaStream_t stream) {
+cudaError_t act_bwd_launch(const BwdKernelArgs& a, bool dy_f32, bool pdl, cudaStream_t stream) {
   if (a.rows == 0 || a.cols == 0) return cudaSuccess;
   const int64_t groups = (a.rows + kBwdRows - 1) / kBwdRows;
   const dim3 grid(static_cast<unsigned>((a.cols + 255) / 256),
                   static_cast<unsigned>(std::min<int64_t>(groups, 65535)));
   const bool drop = a.drop.thr != 0;
-  if (dy_f32) drop ? act_bwd_start<float, true>(a, grid, stream) : act_bwd_start<float, false>(a, grid, stream);
-  else drop ? act_bwd_start<uint16_t, true>(a, grid, stream) : act_bwd_start<uint16_t, false>(a, grid, stream);
-  return cudaGetLastError();
+  if (dy_f32)
+    return drop ? act_bwd_start<float, true>(a, grid, pdl, stream) : act_bwd_start<float, false>(a, grid, pdl, stream);
+  return drop ? act_bwd_start<uint16_t, true>(a, grid, pdl, stream)
+              : act_bwd_start<uint16_t, false>(a, grid, pdl, stream);
 }
 
 int64_t act_bwd_groups(int64_t rows) { return (rows + kBwdRows - 1) / kBwdRows; }
 
-cudaError_t colsum_launch(const float* part, int64_t ld, int64_t groups, int64_t cols, float* out,
+cudaError_t colsum_launch(const float* part, int64_t ld, int64_t groups, int64_t cols, float* out, bool pdl,
                           cudaStream_t stream) {
   if (cols == 0) return cudaSuccess;
-  colsum_kernel<<<static_cast<unsigned>((cols + 31) / 32), kThreads, 0, stream>>>(part, ld, groups, cols, out);
-  return cudaGetLastError();
+  return launch_after(colsum_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)), kThreads, pdl, stream, part, ld,
+                      groups, cols, out);
 }
 
 }  // namespace axonn

@@ -24,10 +24,10 @@ struct BwdKernelArgs {
   DropoutArgs drop;
 };
 
-cudaError_t dropout_launch(const DropoutKernelArgs& a, bool f32, int sms, cudaStream_t stream);
-cudaError_t act_bwd_launch(const BwdKernelArgs& a, bool dy_f32, cudaStream_t stream);
+cudaError_t dropout_launch(const DropoutKernelArgs& a, bool f32, int sms, bool pdl, cudaStream_t stream);
+cudaError_t act_bwd_launch(const BwdKernelArgs& a, bool dy_f32, bool pdl, cudaStream_t stream);
 int64_t act_bwd_groups(int64_t rows);
 cudaError_t colsum_launch(const float* part, int64_t ld, int64_t groups, int64_t cols, float* out,
-                          cudaStream_t stream);
+                          bool pdl, cudaStream_t stream);
 
 }  // namespace axonn

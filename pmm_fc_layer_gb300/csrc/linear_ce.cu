@@ -17,6 +17,7 @@
 #include <algorithm>
 
 #include "epilogue_math.cuh"
+#include "launch.h"
 #include "linear_ce.h"
 
 namespace axonn {
@@ -28,6 +29,8 @@ constexpr float kCeLn2 = 0.6931471805599453f;
 // a place is the counted labels before it, by a scan of the threads' counts
 // within a warp and the warps' totals across them.
 __global__ void __launch_bounds__(1024) ce_index_kernel(CeRowArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
   __shared__ int totals[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int n = 0;
@@ -82,6 +85,8 @@ __global__ void __launch_bounds__(1024) ce_index_kernel(CeRowArgs a) {
 // multiple of 64 rows, which the weight gradient's reduction reads): blocks
 // over rows and 2048 columns, a thread eight of them.
 __global__ void __launch_bounds__(256) ce_gather_kernel(CeRowArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t n = *a.kept;
   const int64_t pad = min(a.rows, (n + 63) / 64 * 64);
   const int64_t c = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
@@ -115,6 +120,8 @@ __device__ __forceinline__ void ce_join(float& m, float& s, float m2, float s2) 
 // finishes last adds up the losses, in row order.
 template <int kRows>
 __global__ void __launch_bounds__(1024) ce_combine_kernel(CeRowArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
   __shared__ float pm[32][kRows], ps[32][kRows];
   __shared__ float part[32];
   __shared__ bool last;
@@ -173,6 +180,8 @@ __global__ void __launch_bounds__(1024) ce_combine_kernel(CeRowArgs a) {
 // bytes an element.
 __global__ void __launch_bounds__(256) ce_scale_kernel(CeRowArgs a, uint16_t* piece, int64_t ld,
                                                        int64_t col0, int64_t cols) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t c = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
   if (c >= cols) return;
   const int n = static_cast<int>(min(static_cast<int64_t>(8), cols - c));
@@ -229,6 +238,8 @@ __global__ void __launch_bounds__(256) ce_scale_kernel(CeRowArgs a, uint16_t* pi
 template <bool kF32>
 __global__ void __launch_bounds__(256) ce_unpack_kernel(CeRowArgs a, const void* packed, int64_t ld, int splits,
                                                         int64_t split_rows) {
+  griddep_launch_dependents();
+  griddep_wait();
   const int64_t vecs = (a.cols + 7) / 8;
   for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
     const int64_t at = a.place[t];
@@ -264,46 +275,40 @@ __global__ void __launch_bounds__(256) ce_unpack_kernel(CeRowArgs a, const void*
 
 }  // namespace
 
-cudaError_t ce_index_launch(const CeRowArgs& a, cudaStream_t stream) {
-  ce_index_kernel<<<1, 1024, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t ce_index_launch(const CeRowArgs& a, bool pdl, cudaStream_t stream) {
+  return launch_after(ce_index_kernel, dim3(1), 1024, pdl, stream, a);
 }
 
-cudaError_t ce_gather_launch(const CeRowArgs& a, cudaStream_t stream) {
+cudaError_t ce_gather_launch(const CeRowArgs& a, bool pdl, cudaStream_t stream) {
   if (a.rows == 0 || a.cols == 0) return cudaSuccess;
   const dim3 grid(static_cast<unsigned>((a.cols + 2047) / 2048),
                   static_cast<unsigned>(std::min<int64_t>(a.rows, 65535)));
-  ce_gather_kernel<<<grid, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(ce_gather_kernel, grid, 256, pdl, stream, a);
 }
 
-cudaError_t ce_combine_launch(const CeRowArgs& a, cudaStream_t stream) {
+cudaError_t ce_combine_launch(const CeRowArgs& a, bool pdl, cudaStream_t stream) {
   // Eight rows read a group's statistics as whole 64 bytes; fewer rows a
   // block where there are not enough of them to fill the GPU (16 rows x 2004
-  // groups: 28 us by 32 rows a block, 7 by 2).
+  // groups: 28 us by 32 rows a block, 10 by 2).
   const int rows = a.rows >= 1024 ? 8 : 2;
-  const unsigned blocks = static_cast<unsigned>(std::max<int64_t>(1, (a.rows + rows - 1) / rows));
-  if (rows == 8) ce_combine_kernel<8><<<blocks, 1024, 0, stream>>>(a);
-  else ce_combine_kernel<2><<<blocks, 1024, 0, stream>>>(a);
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(std::max<int64_t>(1, (a.rows + rows - 1) / rows)));
+  return launch_after(rows == 8 ? ce_combine_kernel<8> : ce_combine_kernel<2>, grid, 1024, pdl, stream, a);
 }
 
 cudaError_t ce_scale_launch(const CeRowArgs& a, uint16_t* piece, int64_t ld_piece, int64_t col0,
-                            int64_t cols, cudaStream_t stream) {
+                            int64_t cols, bool pdl, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
   const dim3 grid(static_cast<unsigned>((cols + 2047) / 2048),
                   static_cast<unsigned>(std::min<int64_t>(a.rows, 65535)));
-  ce_scale_kernel<<<grid, 256, 0, stream>>>(a, piece, ld_piece, col0, cols);
-  return cudaGetLastError();
+  return launch_after(ce_scale_kernel, grid, 256, pdl, stream, a, piece, ld_piece, col0, cols);
 }
 
 cudaError_t ce_unpack_launch(const CeRowArgs& a, const void* packed, int64_t ld, int splits,
-                             int64_t split_rows, int sms, cudaStream_t stream) {
+                             int64_t split_rows, int sms, bool pdl, cudaStream_t stream) {
   if (a.rows == 0 || a.cols == 0) return cudaSuccess;
-  const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{8} * sms));
-  if (splits > 0) ce_unpack_kernel<true><<<blocks, 256, 0, stream>>>(a, packed, ld, splits, split_rows);
-  else ce_unpack_kernel<false><<<blocks, 256, 0, stream>>>(a, packed, ld, 0, 0);
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{8} * sms)));
+  return launch_after(splits > 0 ? ce_unpack_kernel<true> : ce_unpack_kernel<false>, grid, 256, pdl, stream, a,
+                      packed, ld, splits, split_rows);
 }
 
 }  // namespace axonn

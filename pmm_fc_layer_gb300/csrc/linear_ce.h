@@ -35,18 +35,18 @@ struct CeRowArgs {
 };
 
 // n, the packing, and the losses (0) of the rows that do not count.
-cudaError_t ce_index_launch(const CeRowArgs& a, cudaStream_t stream);
-cudaError_t ce_gather_launch(const CeRowArgs& a, cudaStream_t stream);
+cudaError_t ce_index_launch(const CeRowArgs& a, bool pdl, cudaStream_t stream);
+cudaError_t ce_gather_launch(const CeRowArgs& a, bool pdl, cudaStream_t stream);
 // Each packed row's logsumexp from its groups' statistics, its loss, and the
 // mean of the counted losses.
-cudaError_t ce_combine_launch(const CeRowArgs& a, cudaStream_t stream);
+cudaError_t ce_combine_launch(const CeRowArgs& a, bool pdl, cudaStream_t stream);
 // The kept distances of columns [col0, col0 + cols) to P = softmax - onehot,
 // in place.
 cudaError_t ce_scale_launch(const CeRowArgs& a, uint16_t* piece, int64_t ld_piece, int64_t col0,
-                            int64_t cols, cudaStream_t stream);
+                            int64_t cols, bool pdl, cudaStream_t stream);
 // dx from its packed rows: bf16 (splits = 0), or the sum of `splits` fp32
 // matrices split_rows rows apart, in order; zeros where a row does not count.
 cudaError_t ce_unpack_launch(const CeRowArgs& a, const void* packed, int64_t ld, int splits,
-                             int64_t split_rows, int sms, cudaStream_t stream);
+                             int64_t split_rows, int sms, bool pdl, cudaStream_t stream);
 
 }  // namespace axonn
