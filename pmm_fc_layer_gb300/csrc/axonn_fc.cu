@@ -1129,7 +1129,12 @@ FusedChoice choose_fused(int64_t M, int64_t N, int64_t R, bool split, const Devi
                            (kFusedRate[i] * 1e6);
     for (int s = 1; s <= (split ? kFusedMostSplits : 1); ++s) {
       if (s > 1 && R / s < 1024) break;
-      const double us = static_cast<double>((tiles * s + slots - 1) / slots) * tile_us / s +
+      // a last round of the 512-row tiles that fills at most half the units
+      // runs their halves side by side
+      const int64_t over = tiles * s % slots;
+      const double rounds = static_cast<double>(tiles * s / slots) +
+                            (over == 0 ? 0.0 : (c.bm == 512 && 2 * over <= slots ? 0.6 : 1.0));
+      const double us = rounds * tile_us / s +
                         (s > 1 ? s * 8.0 * M * N / kFusedBytes : 0.0);
       if (first || us < least) {
         first = false;
@@ -1193,7 +1198,7 @@ axonn_status_t fused_fill(axonn::FusedParams<Args>& P, const OpView& v, int conf
     uint32_t a_rows = static_cast<uint32_t>(c.pair ? c.bm / 2 : c.bm), a_box = 128;
     if (!c.pair && !v.a_mn && v.M < 128) a_rows = a_box = static_cast<uint32_t>((v.M + 7) / 8 * 8);
     P.load_bytes = (c.pair ? 2 : 1) * (a_rows + b_cols) * axonn::kBK * 2;
-    if (P.a_3d) s = encode_mn_3d(&P.ta, v.A, v.M, v.R, v.lda, axonn::kBK, a_rows / 64);
+    if (P.a_3d) s = encode_mn_3d(&P.ta, v.A, v.M, v.R, v.lda, axonn::kBK, 2);
     else if (v.a_mn) s = encode_2d(&P.ta, v.A, v.M, v.R, v.lda, 64, axonn::kBK);
     else s = encode_2d(&P.ta, v.A, v.R, v.M, v.lda, axonn::kBK, a_box);
     if (s != AXONN_OK) return s;

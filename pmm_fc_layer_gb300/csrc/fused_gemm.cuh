@@ -19,7 +19,8 @@
 //    then work on it.  The MMAs are issued with the halves out of step by
 //    kSkew stages: at a tile's end half 0 runs ahead and is done first, at
 //    the next one's start it begins first, and the epilogue's work on half 0
-//    fits between the two.
+//    fits between the two.  Tiles of a last round that fills at most half of
+//    the units go to twice as many of them, a half each.
 // kPair: a CTA pair shares one tile (cta_group::2), each CTA loading its own
 // rows of A and its half of B.
 // Waits are bounded, and an expired one is recorded and reported, as in the
@@ -353,6 +354,15 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
   }
   const int per_split = tiles_m * P.tiles_n;
   const int total = per_split * P.splits;
+  // A unit's items: the tiles unit, unit + units, ...; where the last round
+  // would leave half the units idle, its tiles' halves are items instead.
+  const int over = total % units;
+  const int whole = kHalves == 2 && 2 * over <= units ? total - over : total;
+  const int items = whole + 2 * (total - whole);
+  auto item_tile = [&](int i, int& half) {  // half: -1 for all of the tile
+    half = i < whole ? -1 : (i - whole) & 1;
+    return i < whole ? i : whole + (i - whole) / 2;
+  };
   // Range s of the reduction: stages [all_k s / splits, all_k (s + 1) / splits).
   auto range = [&](int split, int& k0) {
     k0 = static_cast<int>(static_cast<int64_t>(all_k) * split / P.splits);
@@ -370,26 +380,28 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
       bool ok = true;
       const uint64_t pol_a = l2_policy(P.l2_keep == 1, P.l2_keep_frac);
       const uint64_t pol_b = l2_policy(P.l2_keep == 2, P.l2_keep_frac);
-      for (int t = unit; ok && t < total; t += units) {
-        int mb, nb, k_first;
+      for (int i = unit; ok && i < items; i += units) {
+        int mb, nb, k_first, only;
+        const int t = item_tile(i, only);
         const int num_k = range(t / per_split, k_first);
         fused_tile(t % per_split, P.group_m, tiles_m, P.tiles_n, mb, nb);
+        const uint32_t bytes = P.load_bytes - (only >= 0 ? (kPair ? 2 : 1) * L::kAHalfBytes : 0);
         const int m0 = mb * kTileM + static_cast<int>(rank) * kCtaM;
         const int n0 = nb * BN + static_cast<int>(rank) * L::kBCols;
         for (int k = 0; k < num_k; ++k) {
           ok = wait_bounded(empty_bar(stage), phase ^ 1u, tmo, abort_flag, kSiteProducerEmpty);
           if (!ok) break;
-          if (leader) mbar_arrive_expect_tx(full_bar(stage), P.load_bytes);
+          if (leader) mbar_arrive_expect_tx(full_bar(stage), bytes);
           const int r0 = (k_first + k) * kBK;
           if constexpr (kPair) {
             const uint32_t fb = mapa_shared(full_bar(stage), 0);
-            if (P.a_3d) {
-              tma_load_3d_pair(a_tile(stage), &P.ta, fb, 0, r0, m0 / 64, pol_a);
-            } else {
 #pragma unroll
-              for (int h = 0; h < kHalves; ++h) {
-                const uint32_t at = a_tile(stage) + h * L::kAHalfBytes;
-                if (P.a_mn) {
+            for (int h = 0; h < kHalves; ++h) {
+              const uint32_t at = a_tile(stage) + h * L::kAHalfBytes;
+              if (kHalves == 1 || only < 0 || only == h) {
+                if (P.a_3d) {
+                  tma_load_3d_pair(at, &P.ta, fb, 0, r0, (m0 + 128 * h) / 64, pol_a);
+                } else if (P.a_mn) {
                   tma_load_2d_pair(at, &P.ta, fb, m0 + 128 * h, r0, pol_a);
                   tma_load_2d_pair(at + kBK * 128, &P.ta, fb, m0 + 128 * h + 64, r0, pol_a);
                 } else {
@@ -466,7 +478,7 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
       if constexpr (kHalves == 1) {
         int stage = 0;
         uint32_t phase = 0;
-        for (int t = unit; ok && t < total; t += units) {
+        for (int t = unit; ok && t < items; t += units) {
           int k_first;
           const int num_k = range(t / per_split, k_first);
           if (num_k == 0) continue;  // as the epilogue counts
@@ -507,19 +519,30 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
           }
           return true;
         };
-        for (int t = unit; ok && t < total; t += units) {
-          int k_first;
-          const int num_k = range(t / per_split, k_first);
+        uint32_t uses[2] = {0, 0};  // of each half's accumulator
+        for (int i = unit; ok && i < items; i += units) {
+          int k_first, only;
+          const int num_k = range(item_tile(i, only) / per_split, k_first);
           if (num_k == 0) continue;  // as the epilogue counts
+          if (only >= 0) {
+            ok = wait_bounded(tempty_bar(only), (uses[only] & 1u) ^ 1u, tmo, abort_flag, kSiteMmaTmemEmpty);
+            if (!ok) break;
+            tc_fence_after();
+            ok = run(only, 0, num_k, true, true);
+            if (!ok) break;
+            commit(tfull_bar(only));
+            ++uses[only];
+            base += static_cast<uint32_t>(num_k);
+            continue;
+          }
           const int a = min(kSkew, num_k), e = max(a, num_k - kSkew);
-          const uint32_t parity = (acc & 1u) ^ 1u;
-          ok = wait_bounded(tempty_bar(0), parity, tmo, abort_flag, kSiteMmaTmemEmpty);
+          ok = wait_bounded(tempty_bar(0), (uses[0] & 1u) ^ 1u, tmo, abort_flag, kSiteMmaTmemEmpty);
           if (!ok) break;
           tc_fence_after();
           ok = run(0, 0, a, true, false);
           if (!ok) break;
           if (a == num_k) commit(tfull_bar(0));
-          ok = wait_bounded(tempty_bar(1), parity, tmo, abort_flag, kSiteMmaTmemEmpty);
+          ok = wait_bounded(tempty_bar(1), (uses[1] & 1u) ^ 1u, tmo, abort_flag, kSiteMmaTmemEmpty);
           if (!ok) break;
           tc_fence_after();
           ok = run(1, 0, a, false, true);
@@ -547,7 +570,8 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
           run(1, e, num_k, false, true);
           commit(tfull_bar(1));
           base += static_cast<uint32_t>(num_k);
-          ++acc;
+          ++uses[0];
+          ++uses[1];
         }
       }
       // Every MMA of this thread is done before TMEM is released.
@@ -561,18 +585,20 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
     const int q = warp & 3;  // the TMEM lane quarter this warp may access
     const int set = (warp - L::kEpiFirst) >> 2;  // which columns of the tile
     typename Epi::State st = Epi::begin(P.epi);
-    uint32_t acc = 0;
+    uint32_t uses[2] = {0, 0};  // tiles (one half: uses[0] alone), or of each half's accumulator
     bool ok = true;
-    for (int t = unit; ok && t < total; t += units) {
-      int mb, nb, k_first;
+    for (int i = unit; ok && i < items; i += units) {
+      int mb, nb, k_first, only;
+      const int t = item_tile(i, only);
       const int split = t / per_split;
       const bool has = range(split, k_first) > 0;
       fused_tile(t - split * per_split, P.group_m, tiles_m, P.tiles_n, mb, nb);
 #pragma unroll 1
       for (int half = 0; ok && half < kHalves; ++half) {
+        if (kHalves == 2 && only >= 0 && only != half) continue;
         // buffers alternate by tile (one half), or belong to the halves
-        const uint32_t b = kHalves == 1 ? acc & 1u : static_cast<uint32_t>(half);
-        const uint32_t parity = kHalves == 1 ? (acc >> 1) & 1u : acc & 1u;
+        const uint32_t b = kHalves == 1 ? uses[0] & 1u : static_cast<uint32_t>(half);
+        const uint32_t parity = kHalves == 1 ? (uses[0] >> 1) & 1u : uses[half] & 1u;
         EpiTile tile;
         tile.t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + b * kAccCols + set * L::kWarpCols;
         tile.row = mb * kTileM + static_cast<int>(rank) * kCtaM + half * 128 + q * 32 + lane;
@@ -606,8 +632,8 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
           }
         };
         ok = Epi::template run<L::kWarpCols, kHalves == 2>(P.epi, st, tile, ready, release);
+        if (has) ++uses[kHalves == 1 ? 0 : half];
       }
-      if (has) ++acc;
     }
     // this warp's stores are complete before the CTA may exit
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
