@@ -72,14 +72,16 @@ __device__ __forceinline__ void store_out(const EpiTile& t, int col, const float
   else store_bf16(t, t.out, col, x);
 }
 
-template <bool kF32>
+// kJoin: there is dropout or a residual.  The 20-warp kernels hold 64 words a
+// thread and spill with either compiled in, which costs the plain form 3 %.
+template <bool kF32, bool kJoin>
 struct FwdEpilogue {
   using Args = EpilogueArgs;
   using State = DropRng;
   static __device__ __forceinline__ State begin(const Args& a) { return load_rng(a.drop); }
 
   static __device__ __forceinline__ void prefetch(const Args& a, const EpiTile& t, int cols) {
-    if (a.residual) prefetch_row(a.residual, t.row * a.ld_res + t.col, cols, kF32 ? 4 : 2);
+    if (kJoin && a.residual) prefetch_row(a.residual, t.row * a.ld_res + t.col, cols, kF32 ? 4 : 2);
   }
 
   static __device__ __forceinline__ void step(const Args& a, const State& rng, const EpiTile& t, int c,
@@ -92,13 +94,13 @@ struct FwdEpilogue {
     }
     if (a.pre_out) store_bf16(t, t.out2, col, x);
     Residual<kF32> r;
-    if (a.residual) r.start(a, t, col);
+    if (kJoin && a.residual) r.start(a, t, col);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       apply_act16(a.act, x + 16 * h);
-      if (a.drop.thr != 0) drop16(a.drop, rng, t.row, col + 16 * h, x + 16 * h);
+      if (kJoin && a.drop.thr != 0) drop16(a.drop, rng, t.row, col + 16 * h, x + 16 * h);
     }
-    if (a.residual) r.add(a, t, col, x);
+    if (kJoin && a.residual) r.add(a, t, col, x);
     store_out<kF32>(t, col, x);
   }
 
@@ -127,7 +129,7 @@ __device__ __forceinline__ float column_sum32(float (&x)[32]) {
   return x[0];
 }
 
-template <bool kF32>
+template <bool kF32, bool kJoin>
 struct BwdEpilogue {
   using Args = EpilogueArgs;
   using State = DropRng;
@@ -135,7 +137,7 @@ struct BwdEpilogue {
 
   static __device__ __forceinline__ void prefetch(const Args& a, const EpiTile& t, int cols) {
     if (a.act != kActNone) prefetch_row(a.pre_in, t.row * a.ld_pre + t.col, cols, 2);
-    if (a.residual) prefetch_row(a.residual, t.row * a.ld_res + t.col, cols, kF32 ? 4 : 2);
+    if (kJoin && a.residual) prefetch_row(a.residual, t.row * a.ld_res + t.col, cols, kF32 ? 4 : 2);
   }
 
   static __device__ __forceinline__ void step(const Args& a, const State& rng, const EpiTile& t, int c,
@@ -144,7 +146,7 @@ struct BwdEpilogue {
     const bool in = t.row < t.M;
     RowSegment<uint16_t> z;
     if (a.act != kActNone) z.start(t, a.pre_in, a.ld_pre, col);
-    if (a.drop.thr != 0) {
+    if (kJoin && a.drop.thr != 0) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) drop16(a.drop, rng, t.row, col + 16 * h, x + 16 * h);
     }
@@ -154,7 +156,7 @@ struct BwdEpilogue {
 #pragma unroll
       for (int h = 0; h < 2; ++h) apply_slope16(a.act, x + 16 * h, w + 8 * h);
     }
-    if (a.residual) {
+    if (kJoin && a.residual) {
       Residual<kF32> r;
       r.start(a, t, col);
       float y[32];
@@ -188,19 +190,31 @@ struct BwdEpilogue {
 }  // namespace
 
 cudaError_t fused_init(bool* regs_ok) {
-  for (cudaError_t e : {fused_init_all<FwdEpilogue<false>>(regs_ok), fused_init_all<FwdEpilogue<true>>(regs_ok),
-                        fused_init_all<BwdEpilogue<false>>(regs_ok), fused_init_all<BwdEpilogue<true>>(regs_ok)})
+  for (cudaError_t e :
+       {fused_init_all<FwdEpilogue<false, false>>(regs_ok), fused_init_all<FwdEpilogue<false, true>>(regs_ok),
+        fused_init_all<FwdEpilogue<true, false>>(regs_ok), fused_init_all<FwdEpilogue<true, true>>(regs_ok),
+        fused_init_all<BwdEpilogue<false, false>>(regs_ok), fused_init_all<BwdEpilogue<false, true>>(regs_ok),
+        fused_init_all<BwdEpilogue<true, false>>(regs_ok), fused_init_all<BwdEpilogue<true, true>>(regs_ok)})
     if (e != cudaSuccess) return e;
   return cudaSuccess;
 }
 
+namespace {
+template <template <bool, bool> class Epi>
+cudaError_t launch_kind(int config, const FusedParams<EpilogueArgs>& p, int units, bool pdl, cudaStream_t s) {
+  const bool join = p.epi.residual != nullptr || p.epi.drop.thr != 0;
+  if (p.epi.out_f32)
+    return join ? fused_launch_config<Epi<true, true>>(config, p, units, pdl, s)
+                : fused_launch_config<Epi<true, false>>(config, p, units, pdl, s);
+  return join ? fused_launch_config<Epi<false, true>>(config, p, units, pdl, s)
+              : fused_launch_config<Epi<false, false>>(config, p, units, pdl, s);
+}
+}  // namespace
+
 cudaError_t fused_launch(FusedKind kind, int config, const FusedParams<EpilogueArgs>& p, int units,
                          bool pdl, cudaStream_t stream) {
-  if (kind == kFusedFwd)
-    return p.epi.out_f32 ? fused_launch_config<FwdEpilogue<true>>(config, p, units, pdl, stream)
-                         : fused_launch_config<FwdEpilogue<false>>(config, p, units, pdl, stream);
-  return p.epi.out_f32 ? fused_launch_config<BwdEpilogue<true>>(config, p, units, pdl, stream)
-                       : fused_launch_config<BwdEpilogue<false>>(config, p, units, pdl, stream);
+  return kind == kFusedFwd ? launch_kind<FwdEpilogue>(config, p, units, pdl, stream)
+                           : launch_kind<BwdEpilogue>(config, p, units, pdl, stream);
 }
 
 cudaError_t fused_take_status(unsigned long long* word, cudaStream_t stream) {
