@@ -93,14 +93,16 @@ struct FwdEpilogue {
         if (col + 16 * h < t.N) add_bias16(a, col + 16 * h, t.N - col - 16 * h, x + 16 * h);
     }
     if (a.pre_out) store_bf16(t, t.out2, col, x);
-    Residual<kF32> r;
-    if (kJoin && a.residual) r.start(a, t, col);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       apply_act16(a.act, x + 16 * h);
       if (kJoin && a.drop.thr != 0) drop16(a.drop, rng, t.row, col + 16 * h, x + 16 * h);
     }
-    if (kJoin && a.residual) r.add(a, t, col, x);
+    if (kJoin && a.residual) {
+      Residual<kF32> r;
+      r.start(a, t, col);
+      r.add(a, t, col, x);
+    }
     store_out<kF32>(t, col, x);
   }
 
@@ -144,13 +146,13 @@ struct BwdEpilogue {
                                               float (&x)[32]) {
     const int col = t.col + 32 * c;
     const bool in = t.row < t.M;
-    RowSegment<uint16_t> z;
-    if (a.act != kActNone) z.start(t, a.pre_in, a.ld_pre, col);
     if (kJoin && a.drop.thr != 0) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) drop16(a.drop, rng, t.row, col + 16 * h, x + 16 * h);
     }
     if (a.act != kActNone) {
+      RowSegment<uint16_t> z;
+      z.start(t, a.pre_in, a.ld_pre, col);
       uint32_t w[16];
       z.finish(t, w);
 #pragma unroll
@@ -159,6 +161,11 @@ struct BwdEpilogue {
     if (kJoin && a.residual) {
       Residual<kF32> r;
       r.start(a, t, col);
+      if (!a.colsum) {
+        r.add(a, t, col, x);
+        store_out<kF32>(t, col, x);
+        return;
+      }
       float y[32];
 #pragma unroll
       for (int j = 0; j < 32; ++j) y[j] = x[j];
