@@ -1107,12 +1107,20 @@ struct FusedChoice {
 // multiples of whole waves), shared by the units that run at once.
 constexpr double kFusedRate[axonn::kFusedConfigs] = {1580, 1100, 630, 1720};
 constexpr int kFusedPlain[axonn::kFusedConfigs] = {2, 0, 7, 6};  // the plain products' configuration of that tile
+// What a tile takes at least, however short its reduction: its epilogue, a
+// light one (stores; an activation) and a heavy one (the cross entropy's
+// statistics, dropout or a residual).  512 x 256 tiles also wait for part of
+// it at every tile's end.  us, GB300: 7877 x 728 x 8292 with 512 x 256 tiles
+// takes 17 a tile, the statistics of 490 x 768 x 50257 28 and with 256 x 256
+// tiles 9.8.
+constexpr double kFusedFloor[2][axonn::kFusedConfigs] = {{6.5, 4, 2.5, 13}, {10, 6, 4, 26}};
+constexpr double kFusedExposed = 3;
 constexpr double kFusedBytes = 6e6;  // bytes a microsecond that the parts of a split are written and read at
 constexpr int kFusedMostSplits = 16;
 // The choice of least estimated time: rounds of tiles over the units that run
 // at once, each as long as a tile's share of the reduction, and for a split
 // its parts' traffic (8 bytes an element and part).
-FusedChoice choose_fused(int64_t M, int64_t N, int64_t R, bool split, const DeviceState& dev) {
+FusedChoice choose_fused(int64_t M, int64_t N, int64_t R, bool heavy, bool split, const DeviceState& dev) {
   const int forced = g_forced_config.load();
   int only = -1;
   for (int i = 0; i < axonn::kFusedConfigs; ++i)
@@ -1134,7 +1142,8 @@ FusedChoice choose_fused(int64_t M, int64_t N, int64_t R, bool split, const Devi
       const int64_t over = tiles * s % slots;
       const double rounds = static_cast<double>(tiles * s / slots) +
                             (over == 0 ? 0.0 : (c.bm == 512 && 2 * over <= slots ? 0.6 : 1.0));
-      const double us = rounds * tile_us / s +
+      const double each = std::max(tile_us / s, kFusedFloor[heavy ? 1 : 0][i]) + (c.bm == 512 ? kFusedExposed : 0.0);
+      const double us = rounds * each +
                         (s > 1 ? s * 8.0 * M * N / kFusedBytes : 0.0);
       if (first || us < least) {
         first = false;
@@ -1327,7 +1336,7 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
     } else {
       axonn::FusedParams<axonn::EpilogueArgs> p;
       int units = 0;
-      const int config = choose_fused(v.M, v.N, v.R, false, *dev).config;
+      const int config = choose_fused(v.M, v.N, v.R, e.residual || e.drop.thr != 0, false, *dev).config;
       st = fused_fill(p, v, config, 16, *dev, &units);
       if (st == AXONN_OK) st = encode_out(&p.out, C, v.M, v.N, ldc, f32);
       if (st == AXONN_OK && e.pre_out) st = encode_out(&p.out2, epi->pre, v.M, v.N, epi->ld_pre, false);
@@ -1474,7 +1483,7 @@ axonn_status_t store_product(const OpView& v, FusedChoice choice, void* out, int
 FusedChoice choose_dx(int64_t T, int64_t K, int64_t V) {
   DeviceState* dev = nullptr;
   if (T == 0 || K == 0 || device_state(&dev) != AXONN_OK) return {};
-  return choose_fused(T, K, V, true, *dev);
+  return choose_fused(T, K, V, false, true, *dev);
 }
 
 }  // namespace
@@ -2257,12 +2266,12 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
   DeviceState* dev = nullptr;
   st = device_state(&dev);
   if (st != AXONN_OK) return st;
-  if (plan.splits != dx_choice.splits) dx_choice = choose_fused(T, K, cols, false, *dev);
+  if (plan.splits != dx_choice.splits) dx_choice = choose_fused(T, K, cols, false, false, *dev);
   char* base = static_cast<char*>(ws);
   const int64_t ld_piece = (cols + 7) / 8 * 8;
   float* dx32 = reinterpret_cast<float*>(base + l.end);
   uint16_t* piece = reinterpret_cast<uint16_t*>(base + l.end + plan.dx_bytes);
-  const int config = choose_fused(T, cols, K, false, *dev).config;
+  const int config = choose_fused(T, cols, K, true, false, *dev).config;
   const bool pdl = g_pdl.load() != 0;
 
   axonn::CeRowArgs a{};
@@ -2367,7 +2376,7 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
       const int mode = (flags & AXONN_ACCUM_F32) ? axonn::kOutF32Accum
                        : (flags & AXONN_OUT_F32) ? axonn::kOutF32
                                                  : axonn::kOutBF16;
-      st = store_product(x, choose_fused(x.M, x.N, x.R, false, *dev), static_cast<char*>(dW) + off * (w_f32 ? 4 : 2),
+      st = store_product(x, choose_fused(x.M, x.N, x.R, false, false, *dev), static_cast<char*>(dW) + off * (w_f32 ? 4 : 2),
                          lddw, mode, a.coef, kept, 2, 0, *dev, stream);
       if (st != AXONN_OK) return st;
     }
