@@ -84,6 +84,8 @@ struct DeviceState {
   // Clusters of the reduction-split kernels resident at once, by tile
   // ([0] 128 x 128, [1] 128 x 64) and pieces ([1] 2, [2] 4, [3] 8).
   int split_clusters[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  // Clusters of 2..8 CTAs of fused_cluster_kernel resident at once.
+  int fused_clusters[9] = {};
   bool attrs_set = false;
 };
 
@@ -150,6 +152,11 @@ axonn_status_t device_state(DeviceState** out) {
           n = 0;  // this split is not offered on the device
         }
         d.split_clusters[t][lg] = n;
+      }
+    for (int pieces = 2; pieces <= 8; ++pieces)
+      if (axonn::fused_clusters_resident(d.sms, pieces, &d.fused_clusters[pieces]) != cudaSuccess) {
+        (void)cudaGetLastError();
+        d.fused_clusters[pieces] = 0;
       }
     d.attrs_set = true;
   }
@@ -1102,6 +1109,7 @@ axonn_status_t check_colsum_ws(const void* ws, size_t ws_bytes, int64_t rows, in
 struct FusedChoice {
   int config = 0;
   int splits = 1;
+  double us = 0;  // the estimate
 };
 // TFLOP/s of each tile on full waves (GB300, 8192 x 24576 x 6144 and
 // multiples of whole waves), shared by the units that run at once.
@@ -1150,10 +1158,26 @@ FusedChoice choose_fused(int64_t M, int64_t N, int64_t R, bool heavy, bool split
         least = us;
         best.config = i;
         best.splits = s;
+        best.us = us;
       }
     }
   }
   return best;
+}
+
+// Pieces of the reduction for a product whose 128 x 128 tiles leave most SMs
+// idle, each tile's CTAs a cluster (fused_cluster_kernel): as many as leave
+// all clusters resident at once, of at least eight stages, where the estimate (kFusedExchange
+// for the parts' way through shared memory) is below that of `whole`; else 1.
+constexpr double kFusedExchange = 4;
+int cluster_pieces(int64_t M, int64_t N, int64_t R, const FusedChoice& whole, const DeviceState& dev) {
+  if (g_forced_config.load() >= 0) return 1;
+  const int64_t tiles = ((M + 127) / 128) * ((N + 127) / 128);
+  int64_t most = std::min<int64_t>(8, (R + 63) / 64 / 8);
+  while (most > 1 && tiles > dev.fused_clusters[most]) --most;
+  if (most < 2) return 1;
+  const double tile_us = 2.0 * 128 * 128 * static_cast<double>(R) * dev.sms / (kFusedRate[1] * 1e6);
+  return tile_us / most + kFusedFloor[0][1] + kFusedExchange < whole.us ? static_cast<int>(most) : 1;
 }
 
 // The map by which epilogues write a [rows x cols] matrix of bf16, fp32 or
@@ -1336,13 +1360,16 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
     } else {
       axonn::FusedParams<axonn::EpilogueArgs> p;
       int units = 0;
-      const int config = choose_fused(v.M, v.N, v.R, e.residual || e.drop.thr != 0, false, *dev).config;
+      const FusedChoice choice = choose_fused(v.M, v.N, v.R, e.residual || e.drop.thr != 0, false, *dev);
+      const int pieces = cluster_pieces(v.M, v.N, v.R, choice, *dev);
+      const int config = pieces > 1 ? 1 : choice.config;
       st = fused_fill(p, v, config, 16, *dev, &units);
       if (st == AXONN_OK) st = encode_out(&p.out, C, v.M, v.N, ldc, f32);
       if (st == AXONN_OK && e.pre_out) st = encode_out(&p.out2, epi->pre, v.M, v.N, epi->ld_pre, false);
       if (st != AXONN_OK) return st;
       p.epi = e;
-      ce = axonn::fused_launch(kind, config, p, units, g_pdl.load() != 0, stream);
+      ce = pieces > 1 ? axonn::fused_cluster(kind, p, p.tiles_m * p.tiles_n, pieces, g_pdl.load() != 0, stream)
+                      : axonn::fused_launch(kind, config, p, units, g_pdl.load() != 0, stream);
     }
     if (ce != cudaSuccess) return fail(AXONN_ERR_CUDA, "fused product: %s", cudaGetErrorString(ce));
   }

@@ -112,6 +112,12 @@ enum CeKind : int { kCeStats = 0, kCeProb = 1 };
 cudaError_t fused_init(bool* regs_ok);
 cudaError_t fused_launch(FusedKind kind, int config, const FusedParams<EpilogueArgs>& p, int units,
                          bool pdl, cudaStream_t stream);
+// How many such clusters the GPU holds at once.
+cudaError_t fused_clusters_resident(int sms, int pieces, int* clusters);
+// One 128 x 128 tile for every cluster of `pieces` CTAs, the reduction cut
+// over them (p as filled for configuration 1).
+cudaError_t fused_cluster(FusedKind kind, const FusedParams<EpilogueArgs>& p, int tiles, int pieces, bool pdl,
+                          cudaStream_t stream);
 cudaError_t fused_take_status(unsigned long long* word, cudaStream_t stream);
 
 cudaError_t ce_init(bool* regs_ok);

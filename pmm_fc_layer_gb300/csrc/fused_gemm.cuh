@@ -651,6 +651,225 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
   }
 }
 
+// Products of few tiles over a long reduction (a layer answering some tens of
+// tokens): a cluster of S CTAs takes one 128 x 128 tile, each CTA a range of
+// the reduction.  When its range is done, a CTA leaves its fp32 accumulator
+// in the shared memory that held its operands.  The tile's sixteen blocks of
+// 32 x 32 are then dealt out to the cluster's warps; a warp adds up the S
+// parts of its block in the order of the ranges and runs the epilogue on it.
+// One tile a cluster, nothing persistent: it is launched where all CTAs fit
+// the GPU at once.
+constexpr int kClusterStages = 6;
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
+}
+
+template <class Epi>
+__global__ void __launch_bounds__(FusedLayout<128, kClusterStages, false, 1>::kThreads, 1)
+    fused_cluster_kernel(const __grid_constant__ FusedParams<typename Epi::Args> P) {
+  using L = FusedLayout<128, kClusterStages, false, 1>;
+  constexpr int STAGES = kClusterStages;
+  static_assert(16 * 4096 <= STAGES * L::kStageBytes, "the accumulator fits the ring");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw);
+  const uint32_t ring = (raw + 1023u) & ~1023u;
+  uint8_t* ring_ptr = smem_raw + (ring - raw);
+  const uint32_t slots = ring + STAGES * L::kStageBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring_ptr + STAGES * L::kStageBytes + L::kEpi * L::kSlotBytes);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + L::kNumBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  auto full_bar = [&](int s) { return smem_addr(bars + s); };
+  auto empty_bar = [&](int s) { return smem_addr(bars + STAGES + s); };
+  const uint32_t tfull_bar = smem_addr(bars + 2 * STAGES);
+  auto a_tile = [&](int s) { return ring + s * L::kStageBytes; };
+  auto b_tile = [&](int s) { return ring + s * L::kStageBytes + L::kABytes; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = static_cast<int>(cluster_nctarank()), rank = static_cast<int>(cluster_ctarank());
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(tfull_bar, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0 && P.num_k > 0) {
+    prefetch_tmap(&P.ta);
+    prefetch_tmap(&P.tb);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_addr(tmem_slot), 128);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint64_t tmo = P.timeout_ns;
+  int mb, nb;
+  fused_tile(static_cast<int>(cluster_id_x()), P.group_m, P.tiles_m, P.tiles_n, mb, nb);
+  const int m0 = mb * 128, n0 = nb * 128;
+  const int k0 = static_cast<int>(static_cast<int64_t>(P.num_k) * rank / S);
+  const int k1 = static_cast<int>(static_cast<int64_t>(P.num_k) * (rank + 1) / S);
+  griddep_wait();
+
+  bool late = false;
+  if (warp == 0) {
+    if (lane == 0 && P.inject != 1) {
+      const uint64_t pol = l2_policy(false, 1.0f);
+      int loads = 0;
+      for (int k = k0; k < k1; ++k, ++loads) {
+        const int stage = loads % STAGES;
+        if (!wait_bounded(empty_bar(stage), ((loads / STAGES) & 1) ^ 1u, tmo, abort_flag, kSiteProducerEmpty)) break;
+        mbar_arrive_expect_tx(full_bar(stage), P.load_bytes);
+        const uint32_t fb = full_bar(stage);
+        const int r0 = k * kBK;
+        if (P.a_3d) {
+          tma_load_3d(a_tile(stage), &P.ta, fb, 0, r0, m0 / 64, pol);
+        } else if (P.a_mn) {
+          tma_load_2d(a_tile(stage), &P.ta, fb, m0, r0, pol);
+          tma_load_2d(a_tile(stage) + kBK * 128, &P.ta, fb, m0 + 64, r0, pol);
+        } else {
+          tma_load_2d(a_tile(stage), &P.ta, fb, r0, m0, pol);
+        }
+        if (P.b_3d) {
+          tma_load_3d(b_tile(stage), &P.tb, fb, 0, r0, n0 / 64, pol);
+        } else if (P.b_mn) {
+          tma_load_2d(b_tile(stage), &P.tb, fb, n0, r0, pol);
+          tma_load_2d(b_tile(stage) + kBK * 128, &P.tb, fb, n0 + 64, r0, pol);
+        } else {
+          tma_load_2d(b_tile(stage), &P.tb, fb, r0, n0, pol);
+        }
+      }
+      griddep_launch_dependents();
+      for (int s = 0; s < STAGES; ++s)  // the last load of each stage has landed
+        if (loads > s)
+          wait_bounded(full_bar(s), ((loads - s + STAGES - 1) / STAGES - 1) & 1u, tmo, abort_flag, kSiteDrainLoads,
+                       false);
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && k1 > k0) {
+      bool ok = true;
+      for (int k = k0; k < k1; ++k) {
+        const int i = k - k0, stage = i % STAGES;
+        ok = wait_bounded(full_bar(stage), (i / STAGES) & 1u, tmo, abort_flag, kSiteMmaFull);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kBK / 16; ++kk)
+          umma_bf16(tmem_base, operand_desc<kBK>(a_tile(stage), kk, P.a_mn),
+                    operand_desc<kBK>(b_tile(stage), kk, P.b_mn), P.idesc, (i != 0 || kk != 0) ? 1u : 0u);
+        umma_commit(empty_bar(stage));
+      }
+      umma_commit(tfull_bar);  // also where a wait expired: what was issued is drained
+      wait_bounded(tfull_bar, 0, tmo, abort_flag, kSiteDrainMma, false);
+    }
+  } else {
+    if (k1 > k0) {
+      if (warp == 2) {
+        if (lane == 0) late = !wait_bounded(tfull_bar, 0, tmo, abort_flag, kSiteEpiTmemFull) || *abort_flag != 0;
+        late = __shfl_sync(0xFFFFFFFFu, late, 0);
+      }
+      late = epilogue_any<32 * L::kEpi>(late);
+      tc_fence_after();
+    }
+    // Block (q, cc) of the tile, 32 rows x 32 columns, at 4096 (4 q + cc): row
+    // r's 16-byte chunk c at c ^ (r & 7) of its 128 bytes.
+    const int q = warp & 3, set = (warp - 2) >> 2;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      EpiTile t;
+      t.t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + set * 64;
+      t.has = k1 > k0 && !late;
+      float x[32];
+      load_acc32(t, c, x);
+      const uint32_t row = ring + 4096u * (4 * q + 2 * set + c) + 128u * lane;
+#pragma unroll
+      for (int v = 0; v < 8; ++v)
+        st_shared_v4(row + 16u * (v ^ (lane & 7)), __float_as_uint(x[4 * v]), __float_as_uint(x[4 * v + 1]),
+                     __float_as_uint(x[4 * v + 2]), __float_as_uint(x[4 * v + 3]));
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();
+  if (warp >= 2 && !late) {
+    typename Epi::State st = Epi::begin(P.epi);
+#pragma unroll 1
+    for (int u = rank + S * (warp - 2); u < 16; u += S * L::kEpi) {
+      EpiTile t;
+      t.row = m0 + 32 * (u >> 2) + lane;
+      t.col = n0 + 32 * (u & 3);
+      t.M = t.rows = P.M;
+      t.N = P.N;
+      t.row_off = 0;
+      t.slot = slots + static_cast<uint32_t>((warp - 2) * L::kSlotBytes);
+      t.out = &P.out;
+      t.out2 = &P.out2;
+      t.has = true;
+      if (t.col >= t.N || t.row - lane >= t.M) continue;
+      float x[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[j] = 0.0f;
+#pragma unroll 1
+      for (int s = 0; s < S; ++s) {
+        const uint32_t row = mapa_shared(ring + 4096u * u + 128u * lane, s);
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const float4 f = ld_cluster_v4(row + 16u * (v ^ (lane & 7)));
+          x[4 * v] += f.x;
+          x[4 * v + 1] += f.y;
+          x[4 * v + 2] += f.z;
+          x[4 * v + 3] += f.w;
+        }
+      }
+      Epi::step(P.epi, st, t, 0, x);
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while another may read its part
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem_base, 128);
+  }
+}
+
+template <class Epi>
+cudaLaunchConfig_t fused_cluster_config(int ctas, int pieces, cudaLaunchAttribute (&attr)[2]) {
+  using L = FusedLayout<128, kClusterStages, false, 1>;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+  cfg.blockDim = dim3(L::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = L::kBytes;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(pieces);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+template <class Epi>
+cudaError_t fused_cluster_launch(const FusedParams<typename Epi::Args>& p, int tiles, int pieces, bool pdl,
+                                 cudaStream_t s) {
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = fused_cluster_config<Epi>(tiles * pieces, pieces, attr);
+  cfg.stream = s;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, fused_cluster_kernel<Epi>, p);
+}
+
 // Shared-memory limit and launch of one instantiation.
 template <class Epi, int BN, int STAGES, bool kPair, int kHalves>
 struct Fused {

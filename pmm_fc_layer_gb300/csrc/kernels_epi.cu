@@ -196,12 +196,27 @@ struct BwdEpilogue {
 
 }  // namespace
 
+namespace {
+template <template <bool, bool> class Epi>
+cudaError_t cluster_init() {
+  constexpr int kBytes = FusedLayout<128, kClusterStages, false, 1>::kBytes;
+  for (cudaError_t e : {cudaFuncSetAttribute(fused_cluster_kernel<Epi<false, true>>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes),
+                        cudaFuncSetAttribute(fused_cluster_kernel<Epi<true, true>>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes)})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
+}
+}  // namespace
+
 cudaError_t fused_init(bool* regs_ok) {
   for (cudaError_t e :
        {fused_init_all<FwdEpilogue<false, false>>(regs_ok), fused_init_all<FwdEpilogue<false, true>>(regs_ok),
         fused_init_all<FwdEpilogue<true, false>>(regs_ok), fused_init_all<FwdEpilogue<true, true>>(regs_ok),
         fused_init_all<BwdEpilogue<false, false>>(regs_ok), fused_init_all<BwdEpilogue<false, true>>(regs_ok),
         fused_init_all<BwdEpilogue<true, false>>(regs_ok), fused_init_all<BwdEpilogue<true, true>>(regs_ok)})
+    if (e != cudaSuccess) return e;
+  for (cudaError_t e : {cluster_init<FwdEpilogue>(), cluster_init<BwdEpilogue>()})
     if (e != cudaSuccess) return e;
   return cudaSuccess;
 }
@@ -222,6 +237,22 @@ cudaError_t fused_launch(FusedKind kind, int config, const FusedParams<EpilogueA
                          bool pdl, cudaStream_t stream) {
   return kind == kFusedFwd ? launch_kind<FwdEpilogue>(config, p, units, pdl, stream)
                            : launch_kind<BwdEpilogue>(config, p, units, pdl, stream);
+}
+
+cudaError_t fused_clusters_resident(int sms, int pieces, int* clusters) {
+  using Epi = FwdEpilogue<false, true>;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = fused_cluster_config<Epi>(sms / pieces * pieces, pieces, attr);
+  return cudaOccupancyMaxActiveClusters(clusters, reinterpret_cast<const void*>(fused_cluster_kernel<Epi>), &cfg);
+}
+
+cudaError_t fused_cluster(FusedKind kind, const FusedParams<EpilogueArgs>& p, int tiles, int pieces, bool pdl,
+                          cudaStream_t stream) {
+  if (kind == kFusedFwd)
+    return p.epi.out_f32 ? fused_cluster_launch<FwdEpilogue<true, true>>(p, tiles, pieces, pdl, stream)
+                         : fused_cluster_launch<FwdEpilogue<false, true>>(p, tiles, pieces, pdl, stream);
+  return p.epi.out_f32 ? fused_cluster_launch<BwdEpilogue<true, true>>(p, tiles, pieces, pdl, stream)
+                       : fused_cluster_launch<BwdEpilogue<false, true>>(p, tiles, pieces, pdl, stream);
 }
 
 cudaError_t fused_take_status(unsigned long long* word, cudaStream_t stream) {

@@ -72,7 +72,7 @@ def product_error(K, S):
 
 
 SIZES = [(1, 64, 128), (1, 520, 72), (3, 8, 1), (31, 65, 33), (130, 200, 264), (257, 130, 521), (300, 72, 1000),
-         (2, 2050, 700), (4, 4100, 333), (1, 1, 9)]
+         (2, 2050, 700), (4, 4100, 333), (1, 1, 9), (5, 1100, 130), (150, 1030, 300), (40, 4000, 72)]
 
 
 @pytest.mark.parametrize("config", [2, 0, 6, 7, -1])
