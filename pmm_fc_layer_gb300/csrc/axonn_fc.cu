@@ -1403,7 +1403,7 @@ CeLayout ce_layout(int64_t T, int64_t K, int64_t V) {
   l.index = take(4 * t);
   l.place = take(4 * t);
   l.labels = take(4 * t);
-  l.coef = take(8);  // and the combining kernel's counter
+  l.coef = take(16);  // the combining kernel's counter, and dX's parts
   l.label_logit = take(4 * t);
   l.lse2 = take(4 * t);
   l.stats = take(8 * t * static_cast<size_t>((V + axonn::kEpilogueCols - 1) / axonn::kEpilogueCols));
@@ -1481,10 +1481,11 @@ axonn_status_t check_ce(int64_t T, int64_t K, int64_t V, uint32_t flags) {
 
 // A product whose tiles are stored times a number, on the fused kernels
 // (whose extent may be the device's count).  With splits > 1 the output is
-// that many matrices, split_rows rows apart.
+// that many matrices, split_rows rows apart, or as `parts` has it on the
+// device (with room for splits * split_rows rows).
 axonn_status_t store_product(const OpView& v, FusedChoice choice, void* out, int64_t ld_out, int mode,
                              const float* scale, const int32_t* count, int count_of, int64_t split_rows,
-                             const DeviceState& dev, cudaStream_t stream) {
+                             const int2* parts, const DeviceState& dev, cudaStream_t stream) {
   if (v.M == 0 || v.N == 0) return AXONN_OK;
   axonn::FusedParams<axonn::StoreArgs> p;
   int units = 0;
@@ -1496,6 +1497,7 @@ axonn_status_t store_product(const OpView& v, FusedChoice choice, void* out, int
   const axonn::FusedConfig& c = axonn::kFusedConfig[choice.config];
   p.splits = choice.splits;
   p.split_rows = static_cast<int32_t>(choice.splits > 1 ? split_rows : 0);
+  p.parts = choice.splits > 1 ? parts : nullptr;
   units = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(p.tiles_m) * p.tiles_n * p.splits,
                                              c.pair ? dev.max_pairs : dev.sms));
   p.count = count;
@@ -2317,6 +2319,15 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
   a.ld_packed = l.ld_x;
   a.coef = reinterpret_cast<float*>(base + l.coef);
   a.done = reinterpret_cast<uint32_t*>(base + l.coef + 4);
+  a.parts = reinterpret_cast<int2*>(base + l.coef + 8);
+  if (dx_choice.splits > 1) {
+    const axonn::FusedConfig& c = axonn::kFusedConfig[dx_choice.config];
+    a.part_rows = dx_choice.splits * ce_part_rows(T);
+    a.part_units = c.pair ? dev->max_pairs : dev->sms;
+    a.part_tile = c.bm;
+    a.part_tiles_n = static_cast<int32_t>((K + c.bn - 1) / c.bn);
+    a.most_parts = static_cast<int32_t>(std::min<int64_t>(64, std::max<int64_t>(dx_choice.splits, cols / 1024)));
+  }
   a.stats = reinterpret_cast<const float2*>(base + l.stats);
   a.group_cols = axonn::kEpilogueCols;
   a.groups = (V + a.group_cols - 1) / a.group_cols;
@@ -2404,7 +2415,7 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
                        : (flags & AXONN_OUT_F32) ? axonn::kOutF32
                                                  : axonn::kOutBF16;
       st = store_product(x, choose_fused(x.M, x.N, x.R, false, false, *dev), static_cast<char*>(dW) + off * (w_f32 ? 4 : 2),
-                         lddw, mode, a.coef, kept, 2, 0, *dev, stream);
+                         lddw, mode, a.coef, kept, 2, 0, nullptr, *dev, stream);
       if (st != AXONN_OK) return st;
     }
     if (dX) {
@@ -2418,13 +2429,13 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
       v.R = n;
       st = store_product(v, dx_choice, in_place ? static_cast<void*>(a.packed_x) : static_cast<void*>(dx32), l.ld_x,
                          in_place ? axonn::kOutBF16 : (j == 0 ? axonn::kOutF32 : axonn::kOutF32Accum), a.coef,
-                         kept, 1, ce_part_rows(T), *dev, stream);
+                         kept, 1, ce_part_rows(T), a.parts, *dev, stream);
       if (st != AXONN_OK) return st;
     }
   }
   if (dX)
-    AXONN_CE_RUN(axonn::ce_unpack_launch(a, in_place ? static_cast<const void*>(a.packed_x) : dx32, l.ld_x,
-                                         in_place ? 0 : dx_choice.splits, ce_part_rows(T), dev->sms, pdl, stream), "dX");
+    AXONN_CE_RUN(axonn::ce_unpack_launch(a, in_place ? static_cast<const void*>(a.packed_x) : dx32, l.ld_x, !in_place,
+                                         dev->sms, pdl, stream), "dX");
   return ok();
 }
 

@@ -80,6 +80,7 @@ struct FusedParams {
   // The reduction in `splits` consecutive ranges, each a product of its own:
   // range s writes the rows from s * split_rows on.
   int32_t splits, split_rows;
+  const int2* parts;  // not null: {splits, split_rows} on the device instead
   int32_t M, N, num_k;
   int32_t tiles_m, tiles_n;
   uint32_t idesc;

@@ -352,8 +352,14 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
       all_k = (n + kBK - 1) / kBK;
     }
   }
+  int splits = P.splits, split_rows = P.split_rows;
+  if (P.parts) {
+    const int2 parts = *P.parts;
+    splits = parts.x;
+    split_rows = parts.y;
+  }
   const int per_split = tiles_m * P.tiles_n;
-  const int total = per_split * P.splits;
+  const int total = per_split * splits;
   // A unit's items: the tiles unit, unit + units, ...; where the last round
   // would leave half the units idle, its tiles' halves are items instead.
   const int over = total % units;
@@ -365,8 +371,8 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
   };
   // Range s of the reduction: stages [all_k s / splits, all_k (s + 1) / splits).
   auto range = [&](int split, int& k0) {
-    k0 = static_cast<int>(static_cast<int64_t>(all_k) * split / P.splits);
-    return static_cast<int>(static_cast<int64_t>(all_k) * (split + 1) / P.splits) - k0;
+    k0 = static_cast<int>(static_cast<int64_t>(all_k) * split / splits);
+    return static_cast<int>(static_cast<int64_t>(all_k) * (split + 1) / splits) - k0;
   };
 
   if constexpr (kHalves == 2) {
@@ -608,7 +614,7 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
         tile.slot = slots + static_cast<uint32_t>((warp - L::kEpiFirst) * L::kSlotBytes);
         tile.out = &P.out;
         tile.out2 = &P.out2;
-        tile.row_off = split * P.split_rows;
+        tile.row_off = split * split_rows;
         tile.has = has;
         auto ready = [&]() -> bool {
           if (!tile.has) return true;

@@ -78,6 +78,17 @@ __global__ void __launch_bounds__(1024) ce_index_kernel(CeRowArgs a) {
     *a.kept = n;
     *a.coef = n > 0 ? a.grad_scale / static_cast<float>(n) : 0.0f;
     *a.done = 0;
+    // As many parts as keep the GPU's units busy with n rows (fewer than the
+    // host, which knows only `rows`, could count on), packed n rows apart.
+    int parts = 1;
+    const int64_t apart = (n + 31) / 32 * 32;
+    if (a.part_rows > 0 && n > 0) {
+      const int64_t tiles = (n + a.part_tile - 1) / a.part_tile * static_cast<int64_t>(a.part_tiles_n);
+      parts = static_cast<int>(max(static_cast<int64_t>(1),
+                                   min(min(a.part_rows / apart, static_cast<int64_t>(a.most_parts)),
+                                       static_cast<int64_t>(a.part_units) / tiles)));
+    }
+    *a.parts = make_int2(parts, static_cast<int>(apart));
   }
 }
 
@@ -236,10 +247,11 @@ __global__ void __launch_bounds__(256) ce_scale_kernel(CeRowArgs a, uint16_t* pi
 // A block takes a row of dX at a time, a thread eight columns: the packed
 // row, the sum of its fp32 parts in order, or zeros.
 template <bool kF32>
-__global__ void __launch_bounds__(256) ce_unpack_kernel(CeRowArgs a, const void* packed, int64_t ld, int splits,
-                                                        int64_t split_rows) {
+__global__ void __launch_bounds__(256) ce_unpack_kernel(CeRowArgs a, const void* packed, int64_t ld) {
   griddep_launch_dependents();
   griddep_wait();
+  const int splits = kF32 ? a.parts->x : 0;
+  const int64_t split_rows = kF32 ? a.parts->y : 0;
   const int64_t vecs = (a.cols + 7) / 8;
   for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
     const int64_t at = a.place[t];
@@ -303,12 +315,11 @@ cudaError_t ce_scale_launch(const CeRowArgs& a, uint16_t* piece, int64_t ld_piec
   return launch_after(ce_scale_kernel, grid, 256, pdl, stream, a, piece, ld_piece, col0, cols);
 }
 
-cudaError_t ce_unpack_launch(const CeRowArgs& a, const void* packed, int64_t ld, int splits,
-                             int64_t split_rows, int sms, bool pdl, cudaStream_t stream) {
+cudaError_t ce_unpack_launch(const CeRowArgs& a, const void* packed, int64_t ld, bool f32, int sms, bool pdl,
+                             cudaStream_t stream) {
   if (a.rows == 0 || a.cols == 0) return cudaSuccess;
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.rows, int64_t{8} * sms)));
-  return launch_after(splits > 0 ? ce_unpack_kernel<true> : ce_unpack_kernel<false>, grid, 256, pdl, stream, a,
-                      packed, ld, splits, split_rows);
+  return launch_after(f32 ? ce_unpack_kernel<true> : ce_unpack_kernel<false>, grid, 256, pdl, stream, a, packed, ld);
 }
 
 }  // namespace axonn

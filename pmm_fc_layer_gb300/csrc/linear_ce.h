@@ -21,6 +21,13 @@ struct CeRowArgs {
   int64_t ld_packed;
   float* coef;            // [1] grad_scale / n
   uint32_t* done;         // [1] blocks of the combining kernel that have finished
+  // dX as fp32 parts of a split reduction: how many, and how many rows apart,
+  // follow from n (see ce_index_kernel); part_rows = 0: none.
+  int2* parts;            // [1] {parts, rows apart}
+  int64_t part_rows;      // rows of all parts together
+  int32_t part_units;     // tiles that run at once
+  int32_t part_tile, part_tiles_n;  // rows of a tile, tiles across
+  int32_t most_parts;
   const float2* stats;    // [groups x rows]
   int64_t groups;
   int32_t group_cols;
@@ -44,9 +51,9 @@ cudaError_t ce_combine_launch(const CeRowArgs& a, bool pdl, cudaStream_t stream)
 // in place.
 cudaError_t ce_scale_launch(const CeRowArgs& a, uint16_t* piece, int64_t ld_piece, int64_t col0,
                             int64_t cols, bool pdl, cudaStream_t stream);
-// dx from its packed rows: bf16 (splits = 0), or the sum of `splits` fp32
-// matrices split_rows rows apart, in order; zeros where a row does not count.
-cudaError_t ce_unpack_launch(const CeRowArgs& a, const void* packed, int64_t ld, int splits,
-                             int64_t split_rows, int sms, bool pdl, cudaStream_t stream);
+// dx from its packed rows: bf16, or the sum of fp32 parts, in order; zeros
+// where a row does not count.
+cudaError_t ce_unpack_launch(const CeRowArgs& a, const void* packed, int64_t ld, bool f32, int sms, bool pdl,
+                             cudaStream_t stream);
 
 }  // namespace axonn
