@@ -371,3 +371,51 @@ def test_repeatable(cuda_lib):
     fc.axonn_sync_status()
     for D, db in got[1:]:
         assert torch.equal(D, got[0][0]) and torch.equal(db, got[0][1])
+
+
+def test_empty_reduction_of_one_row(cuda_lib):
+    fc = cuda_lib
+    import torch
+    Y = torch.full((1, 16), 7.0, device="cuda", dtype=torch.bfloat16)
+    b = torch.linspace(-2, 2, 16, device="cuda")
+    fc.axonn_fc_fwd_epi(torch.empty((1, 0), device="cuda", dtype=torch.bfloat16),
+                        torch.empty((0, 16), device="cuda", dtype=torch.bfloat16), Y, fc.Shape(1, 0, 16),
+                        bias=b, act="relu")
+    fc.axonn_sync_status()
+    assert torch.equal(Y[0], torch.relu(b).to(torch.bfloat16))
+
+
+def test_offsets_past_32_bits(cuda_lib):
+    """Matrices of more than 2^31 elements: the last rows are where they
+    belong (checked against the same call on those rows alone)."""
+    fc = cuda_lib
+    import torch
+    T, K, N = 70016, 64, 32768
+    assert T * N > 2**31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.randn((T, K), device="cuda", generator=g).to(torch.bfloat16)
+    W = torch.randn((K, N), device="cuda", generator=g).to(torch.bfloat16)
+    R = torch.randn((T, N), device="cuda", generator=g, dtype=torch.bfloat16)
+    Y, Z = torch.empty_like(R), torch.empty_like(R)
+    tail = 300
+    fc.axonn_fc_fwd_epi(X, W, Y, fc.Shape(T, K, N), act="silu", pre=Z, residual=R)
+    y, z = (torch.empty((tail, N), device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    fc.axonn_fc_fwd_epi(X[-tail:], W, y, fc.Shape(tail, K, N), act="silu", pre=z, residual=R[-tail:])
+    fc.axonn_sync_status()
+    assert torch.equal(Y[-tail:], y) and torch.equal(Z[-tail:], z)
+    # the same rows, elementwise: the mask's counter holds the row itself
+    words_d, seed, offset = words()
+    db, part = torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+    ws = torch.empty(fc.axonn_epi_workspace_size(T, N), dtype=torch.uint8, device="cuda")
+    fc.axonn_epi_bwd(R, Y, pre=Z, act="silu", dbias=db, ws=ws)
+    d = torch.empty_like(y)
+    fc.axonn_epi_bwd(R[-tail:], d, pre=Z[-tail:], act="silu", dbias=part, ws=ws)
+    fc.axonn_dropout(R, Z, 0.5, words_d)
+    fc.axonn_sync_status()
+    assert torch.equal(Y[-tail:], d)
+    keep = ep.philox4x32_10([np.arange(N // 8, dtype=np.uint64), np.full(N // 8, T - 1, np.uint64),
+                             np.full(N // 8, offset & 0xFFFFFFFF, np.uint64),
+                             np.full(N // 8, offset >> 32, np.uint64)], (seed & 0xFFFFFFFF, seed >> 32))
+    low = np.stack([(w >> np.uint64(16 * h)) & np.uint64(0xFFFF) for w in keep for h in (0, 1)], axis=1)
+    want = torch.from_numpy(low.reshape(-1) >= 32768).cuda()
+    assert torch.equal(Z[-1] != 0, want & (R[-1] != 0))

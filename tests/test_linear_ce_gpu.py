@@ -250,3 +250,45 @@ def test_counted_rows_at_the_edges_of_a_tile(cuda_lib, n, piece):
     for config in (6, 2, 0, 7):
         cuda_lib.axonn_set_kernel_config(config)
         check(run(cuda_lib, X, W, labels, keep, piece=piece), X, W, labels, keep)
+
+
+def test_no_features(cuda_lib):
+    """K = 0: every logit is 0 and the loss is ln V."""
+    X, W = np.zeros((20, 0)), np.zeros((0, 300))
+    got = run(cuda_lib, X, W, np.arange(20), grad=False)
+    assert np.abs(got["token_loss"] - np.log(300.0)).max() < 1e-5 and got["kept"][0] == 20
+
+
+def test_offsets_past_32_bits(cuda_lib):
+    """A piece of more than 2^31 entries: the losses and dX of the last rows,
+    and dW of the last columns, against 64 bits."""
+    fc = cuda_lib
+    import torch
+    T, K, V, tail = 16800, 64, 128256, 40
+    assert T * V > 2**31
+    g = torch.Generator(device="cuda").manual_seed(2)
+    X = torch.randn((T, K), device="cuda", generator=g).to(torch.bfloat16)
+    W = torch.randn((K, V), device="cuda", generator=g).mul_(0.1).to(torch.bfloat16)
+    labels = torch.randint(0, V, (T,), device="cuda", generator=g, dtype=torch.int32)
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    tl, loss = torch.empty(T, device="cuda"), torch.empty(1, device="cuda")
+    kept = torch.empty(1, device="cuda", dtype=torch.int32)
+    ws = torch.empty(fc.axonn_linear_ce_workspace_size(T, K, V, piece=V), device="cuda", dtype=torch.uint8)
+    fc.axonn_linear_ce(X, W, labels, tl, loss, kept, ws, dX=dX, dW=dW)
+    fc.axonn_sync_status()
+    z = X[-tail:].double() @ W.double()
+    logp = torch.log_softmax(z, dim=1)
+    y = labels[-tail:].long()
+    at = torch.arange(tail, device="cuda")
+    assert float((tl[-tail:].double() + logp[at, y]).abs().max()) < 1e-4
+    P = logp.exp()
+    P[at, y] -= 1
+    ref = P @ W.double().T / T
+    assert float((dX[-tail:].double() - ref).norm() / ref.norm()) < 2 * 2.0**-8
+    # dW's last columns: every row's probabilities there
+    lse = torch.cat([torch.logsumexp(X[i:i + 2100].double() @ W.double(), dim=1) for i in range(0, T, 2100)])
+    cols = W[:, -24:].double()
+    P = torch.exp(X.double() @ cols - lse[:, None])
+    hit = labels.long()[:, None] == torch.arange(V - 24, V, device="cuda")
+    ref = X.double().T @ (P - hit.double()) / T
+    assert float((dW[:, -24:].double() - ref).norm() / ref.norm()) < 2 * 2.0**-8
