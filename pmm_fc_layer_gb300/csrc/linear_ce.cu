@@ -16,9 +16,9 @@
 // rounding.
 #include <algorithm>
 
-#include "epilogue_math.cuh"
 #include "launch.h"
 #include "linear_ce.h"
+#include "vec8.cuh"
 
 namespace axonn {
 namespace {
@@ -187,59 +187,54 @@ __global__ void __launch_bounds__(1024) ce_combine_kernel(CeRowArgs a) {
   }
 }
 
-// Eight columns a thread, blocks over (row, 2048 columns).  HBM-bound: 4
-// bytes an element.
+// Blocks over (row, 4096 columns), a thread two vectors of eight columns,
+// both loaded before either is used.  HBM-bound: 4 bytes an element.
+constexpr int kScaleVecs = 2;
+constexpr int kScaleCols = 2048 * kScaleVecs;
 __global__ void __launch_bounds__(256) ce_scale_kernel(CeRowArgs a, uint16_t* piece, int64_t ld,
                                                        int64_t col0, int64_t cols) {
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t c = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
-  if (c >= cols) return;
-  const int n = static_cast<int>(min(static_cast<int64_t>(8), cols - c));
   const int kept = *a.kept;
   const int64_t pad = min(a.rows, (static_cast<int64_t>(kept) + 63) / 64 * 64);
-  const float2* stats = a.stats + (col0 + c) / a.group_cols * a.rows;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kScaleCols + 8 * threadIdx.x;
   for (int64_t row = blockIdx.y; row < pad; row += gridDim.y) {
-    uint16_t* p = piece + row * ld + c;
-    float x[8] = {};
-    if (row < kept) {
-      uint32_t q[8];
-      if (n >= 8) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    Vec8<uint16_t> v[kScaleVecs];
+    float top[kScaleVecs];
+    const bool in = row < kept;
+    const float lse2 = in ? a.lse2[row] : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          q[2 * j] = w[j] & 0xFFFFu;
-          q[2 * j + 1] = w[j] >> 16;
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = j < n ? p[j] : kCeFar;
-      }
-      const float lse2 = a.lse2[row];
-      const float top = fmaf(stats[row].x, kEpiLog2e, -lse2);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // q as a float: the low bits of 2^23 + q
-        const float f = __uint_as_float(0x4B000000u | q[j]) - 8388608.0f;
-        x[j] = q[j] == kCeFar ? 0.0f : ex2_approx(fmaf(f, -1.0f / kCeStep, top));
-      }
-      const int64_t d = a.packed_labels[row] - col0 - c;
-      if (d >= 0 && d < 8) {
-        const float py = ex2_approx(fmaf(a.label_logit[row], kEpiLog2e, -lse2)) - 1.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j == d) x[j] = py;
+    for (int u = 0; u < kScaleVecs; ++u) {
+      const int64_t c = first + 2048 * u;
+      if (in && c < cols) {
+        v[u].load(piece + row * ld + c, static_cast<int>(min(static_cast<int64_t>(8), cols - c)));
+        top[u] = fmaf(a.stats[(col0 + c) / a.group_cols * a.rows + row].x, kEpiLog2e, -lse2);
       }
     }
-    const uint32_t o[4] = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
-                           pack_bf16(x[6], x[7])};
-    if (n >= 8) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
+    const int64_t label = in ? a.packed_labels[row] - col0 : -1;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) p[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+    for (int u = 0; u < kScaleVecs; ++u) {
+      const int64_t c = first + 2048 * u;
+      if (c < cols) {
+        float x[8] = {};
+        if (in) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t q = (j & 1) ? v[u].w[j >> 1] >> 16 : v[u].w[j >> 1] & 0xFFFFu;
+            // q as a float: the low bits of 2^23 + q
+            const float f = __uint_as_float(0x4B000000u | q) - 8388608.0f;
+            x[j] = q == kCeFar ? 0.0f : ex2_approx(fmaf(f, -1.0f / kCeStep, top[u]));
+          }
+          const int64_t d = label - c;
+          if (d >= 0 && d < 8) {
+            const float py = ex2_approx(fmaf(a.label_logit[row], kEpiLog2e, -lse2)) - 1.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j == d) x[j] = py;
+          }
+        }
+        store8(piece + row * ld + c, static_cast<int>(min(static_cast<int64_t>(8), cols - c)), x);
+      }
     }
   }
 }
@@ -310,7 +305,7 @@ cudaError_t ce_combine_launch(const CeRowArgs& a, bool pdl, cudaStream_t stream)
 cudaError_t ce_scale_launch(const CeRowArgs& a, uint16_t* piece, int64_t ld_piece, int64_t col0,
                             int64_t cols, bool pdl, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>((cols + 2047) / 2048),
+  const dim3 grid(static_cast<unsigned>((cols + kScaleCols - 1) / kScaleCols),
                   static_cast<unsigned>(std::min<int64_t>(a.rows, 65535)));
   return launch_after(ce_scale_kernel, grid, 256, pdl, stream, a, piece, ld_piece, col0, cols);
 }
