@@ -113,8 +113,8 @@ struct ProbEpilogue {
     const int col = t.col + 32 * c;
     const int64_t d = in ? a.labels[t.row] - a.col0 - col : -1;
     const float lse2 = in ? a.lse2[t.row] : 0.0f;
-    // Rows past the last, up to the next multiple of 64, are zeros: the
-    // weight gradient's reduction runs over them.
+    // Rows past the last, up to the next multiple of 64 (of those there are),
+    // are zeros: the weight gradient's reduction runs over them.
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
       float p = ex2_approx(fmaf(x[j], kEpiLog2e, -lse2));
@@ -122,7 +122,7 @@ struct ProbEpilogue {
       x[j] = in ? p : 0.0f;
     }
     EpiTile padded = t;
-    padded.rows = (t.M + 63) & ~63;
+    padded.rows = static_cast<int>(min(static_cast<int64_t>((t.M + 63) & ~63), a.rows));
     store_bf16(padded, t.out, col, x);
   }
 

@@ -203,6 +203,7 @@ __global__ void __launch_bounds__(256) ce_scale_kernel(CeRowArgs a, uint16_t* pi
     float top[kScaleVecs];
     const bool in = row < kept;
     const float lse2 = in ? a.lse2[row] : 0.0f;
+    const float far = lse2 - lse2;  // 0, or NaN throughout a row whose sum is not a number
 #pragma unroll
     for (int u = 0; u < kScaleVecs; ++u) {
       const int64_t c = first + 2048 * u;
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(256) ce_scale_kernel(CeRowArgs a, uint16_t* pi
             const uint32_t q = (j & 1) ? v[u].w[j >> 1] >> 16 : v[u].w[j >> 1] & 0xFFFFu;
             // q as a float: the low bits of 2^23 + q
             const float f = __uint_as_float(0x4B000000u | q) - 8388608.0f;
-            x[j] = q == kCeFar ? 0.0f : ex2_approx(fmaf(f, -1.0f / kCeStep, top[u]));
+            x[j] = q == kCeFar ? far : ex2_approx(fmaf(f, -1.0f / kCeStep, top[u]));
           }
           const int64_t d = label - c;
           if (d >= 0 && d < 8) {

@@ -292,3 +292,27 @@ def test_offsets_past_32_bits(cuda_lib):
     hit = labels.long()[:, None] == torch.arange(V - 24, V, device="cuda")
     ref = X.double().T @ (P - hit.double()) / T
     assert float((dW[:, -24:].double() - ref).norm() / ref.norm()) < 2 * 2.0**-8
+
+
+@pytest.mark.parametrize("piece", [0, 256])
+@pytest.mark.parametrize("where", ["row", "column"])
+def test_nan_reaches_every_entry_it_should(cuda_lib, where, piece):
+    """Logits so far apart that most probabilities are 0: a NaN in a counted
+    row or in a column of W still shows in all the gradients that contain it,
+    and in no other."""
+    rng = np.random.default_rng(11)
+    T, K, V = 40, 64, 700
+    X, W = bf16(20 * rng.standard_normal((T, K))), bf16(rng.standard_normal((K, V)))
+    labels = rng.integers(0, V, T)
+    labels[5] = -1
+    if where == "row":
+        X[7, 3] = np.nan
+        X[5] = np.nan  # does not count
+    else:
+        W[9, 17] = np.nan
+    got = run(cuda_lib, X, W, labels, piece=piece)
+    counted = labels >= 0
+    hit = counted & (np.arange(T) == 7) if where == "row" else counted
+    assert (np.isnan(got["token_loss"]) == hit).all() and np.isnan(got["loss"]).all()
+    assert (np.isnan(got["dX"]) == hit[:, None]).all() and (got["dX"][5] == 0).all()
+    assert np.isnan(got["dW"]).all()
