@@ -1340,7 +1340,7 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
   if (v.M > 0) {
     const axonn::FusedKind kind = fwd ? axonn::kFusedFwd : axonn::kFusedBwd;
     cudaError_t ce;
-    if (g_forced_config.load() < 0 && axonn::gemv_wins(v.M, v.N, v.R, dev->sms)) {
+    if (g_forced_config.load() < 0 && axonn::gemv_wins(v.M, v.R)) {
       axonn::GemvArgs p{};
       p.A = reinterpret_cast<const uint16_t*>(v.A);
       p.lda = v.lda;

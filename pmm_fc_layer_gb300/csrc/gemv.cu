@@ -1,13 +1,14 @@
-// Products of one to four rows, with the epilogues of the fused products:
-// a layer answering single tokens.  B is read once and nothing else counts
-// (T = 1, 6144 x 24576: 302 MB), so there are no tiles and no tensor cores:
+// Products of one or two rows, with the epilogues of the fused products: a
+// layer answering single tokens.  B is read once and nothing else counts (one
+// row, 6144 x 24576: 302 MB), so there are no tiles and no tensor cores:
 // every thread streams 16-byte vectors of B and multiplies them into fp32
 // sums, and what is designed is the number of bytes in flight.  The
-// reduction is cut over the kSplit CTAs of a cluster, so that a few hundred
-// CTAs of both short and wide layers keep every SM loading; their partial
-// sums meet in shared memory, in a fixed order, and each CTA finishes its
-// share of the columns.  The tensor-core product with 128 x 128 tiles took
-// 72 us for the layer above: 192 tiles are 1.3 rounds.
+// reduction is cut over the CTAs of a cluster (see gemv_launch), so that
+// short layers keep every SM loading too; their partial sums meet in shared
+// memory, in a fixed order, and each CTA finishes its share of the columns.
+// HBM-bound: the layer above with GELU takes 50.2 us called again and again
+// and 61.4 after other work has filled L2, 6.0 and 4.9 TB/s; 128 x 128 tiles
+// of the fused product take 86 (192 tiles are 1.3 rounds).
 #include <algorithm>
 #include <type_traits>
 
@@ -109,7 +110,7 @@ __device__ __forceinline__ void finish_columns(const GemvArgs& p, int64_t col, i
 // Six CTAs an SM for one row: 768 of them (6144 x 24576) are then resident at
 // once; at four, the last 160 ran as a second wave.
 template <bool kMN, int TM>
-constexpr int kResident = TM == 1 ? (kMN ? 6 : 4) : (TM == 2 ? 3 : 2);
+constexpr int kResident = TM == 1 ? (kMN ? 6 : 4) : 3;
 template <bool kFwd, bool kF32, bool kMN, int TM, int CB>
 __global__ void __launch_bounds__(kThreads, kResident<kMN, TM>) gemv_kernel(const GemvArgs p) {
   extern __shared__ float smem[];
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, kResident<kMN, TM>) gemv_kernel(cons
     }
   } else {
     static_assert(CB == 8 * kWarps, "a warp's eight columns");
-    constexpr int kCols = TM == 1 ? 8 : 4, kUnroll = 8 / kCols;  // columns at a time, 256-element steps in flight
+    constexpr int kCols = 4, kUnroll = 8 / kCols;  // columns at a time, 256-element steps in flight
 #pragma unroll 1
     for (int half = 0; half < 8 / kCols; ++half) {
       const int64_t n0 = col0 + 8 * warp + kCols * half;
@@ -304,26 +305,34 @@ cudaError_t start(const GemvArgs& p, int splits, bool pdl, cudaStream_t stream) 
 template <bool kFwd, bool kF32, int TM>
 cudaError_t start_layout(const GemvArgs& p, bool b_mn, int cols, int splits, bool pdl, cudaStream_t stream) {
   if (!b_mn) return start<kFwd, kF32, false, TM, 64>(p, splits, pdl, stream);
-  if (cols == 256) return start<kFwd, kF32, true, TM, 256>(p, splits, pdl, stream);
+  if constexpr (TM == 1)
+    if (cols == 256) return start<kFwd, kF32, true, 1, 256>(p, splits, pdl, stream);
   return start<kFwd, kF32, true, TM, 64>(p, splits, pdl, stream);
 }
 
 template <bool kFwd, bool kF32>
 cudaError_t start_rows(const GemvArgs& p, bool b_mn, int cols, int splits, bool pdl, cudaStream_t stream) {
   if (p.M == 1) return start_layout<kFwd, kF32, 1>(p, b_mn, cols, splits, pdl, stream);
-  if (p.M == 2) return start_layout<kFwd, kF32, 2>(p, b_mn, cols, splits, pdl, stream);
-  return start_layout<kFwd, kF32, 4>(p, b_mn, cols, splits, pdl, stream);
+  return start_layout<kFwd, kF32, 2>(p, b_mn, cols, splits, pdl, stream);
 }
 
 }  // namespace
 
 cudaError_t gemv_launch(FusedKind kind, GemvArgs p, bool b_mn, int sms, bool pdl, cudaStream_t stream) {
-  // The reduction in up to eight pieces of at least 256; 256 columns a CTA
-  // (whole 512-byte rows) where that still leaves four CTAs for every SM.
-  int splits = 1;
-  while (splits < 8 && p.R / (2 * splits) >= 256) splits *= 2;
+  // The reduction in at most eight pieces of at least 256.  One row of a
+  // row-major B takes them all, with 256 columns a CTA (whole 512-byte rows)
+  // where that still leaves four CTAs for every SM.  The others stop at two
+  // CTAs an SM (of pieces that leave several room in shared memory): a longer
+  // piece starts its stream and meets its cluster less often.  Two rows, us
+  // by 1, 2, 4 and 8 pieces: 6144 x 24576 64, 68, 74 and 65 (68, 70, 74 and 93
+  // stored transposed), 24576 x 6144 137, 111, 66 and 70.
+  const bool wide = b_mn && p.M == 1;
+  int most = 1;
+  while (most < 8 && p.R / (2 * most) >= 256) most *= 2;
+  int splits = wide ? most : 1;
+  while (splits < most && ((p.N + 63) / 64 * splits < 2 * sms || p.R > kGemvPiece * splits)) splits *= 2;
   p.piece = static_cast<int>(((p.R + splits - 1) / splits + 7) / 8 * 8);
-  const int cols = b_mn && (p.N + 255) / 256 * splits >= 4 * sms ? 256 : 64;
+  const int cols = wide && (p.N + 255) / 256 * splits >= 4 * sms ? 256 : 64;
   if (kind == kFusedFwd)
     return p.epi.out_f32 ? start_rows<true, true>(p, b_mn, cols, splits, pdl, stream)
                          : start_rows<true, false>(p, b_mn, cols, splits, pdl, stream);
@@ -331,15 +340,10 @@ cudaError_t gemv_launch(FusedKind kind, GemvArgs p, bool b_mn, int sms, bool pdl
                        : start_rows<false, false>(p, b_mn, cols, splits, pdl, stream);
 }
 
-// One or two rows always; three or four where 64-column tiles of the fused
-// product would leave SMs idle over a long reduction.  GELU product, us, here
-// and with the best tile (B cold in L2): one row 6144 x 24576 66 and 86,
-// 24576 x 6144 72 and 126, 768 x 768 12.3 and 12.3; four rows 6144 x 24576
-// 90 and 87 (162 and 90 with B stored transposed), 24576 x 6144 98 and 126,
-// 4096 x 1000 16 and 29.
-bool gemv_wins(int64_t M, int64_t N, int64_t R, int sms) {
-  if (M < 1 || M > kGemvRows || R > kGemvReduction) return false;
-  return M <= 2 || (R >= N && R >= 2048 && (N + 63) / 64 < sms);
-}
+// One and two rows always.  GELU product, us, here and with the best of the
+// fused forms (B cold in L2): one row 6144 x 24576 61 and 86, 24576 x 6144 66
+// and 78, 768 x 768 10.3 and 12.5; two rows 6144 x 24576 64 and 86, 24576 x
+// 6144 66 and 78.  Four rows have too much to multiply: 90 and 86, 96 and 78.
+bool gemv_wins(int64_t M, int64_t R) { return M >= 1 && M <= kGemvRows && R <= kGemvReduction; }
 
 }  // namespace axonn

@@ -1,4 +1,4 @@
-// Host interface of the products of a few rows (gemv.cu).
+// Host interface of the products of one or two rows (gemv.cu).
 #pragma once
 #include "epilogue.h"
 
@@ -19,11 +19,12 @@ struct GemvArgs {
   EpilogueArgs epi;
 };
 
-constexpr int64_t kGemvRows = 4;
-constexpr int64_t kGemvReduction = 65536;  // 128 KB of x a CTA for four rows
+constexpr int64_t kGemvRows = 2;
+constexpr int64_t kGemvPiece = 8192;  // 64 KB of x a CTA for two rows
+constexpr int64_t kGemvReduction = 8 * kGemvPiece;
 
 // Whether these kernels are the faster ones for a product.
-bool gemv_wins(int64_t M, int64_t N, int64_t R, int sms);
+bool gemv_wins(int64_t M, int64_t R);
 cudaError_t gemv_launch(FusedKind kind, GemvArgs p, bool b_mn, int sms, bool pdl, cudaStream_t stream);
 
 }  // namespace axonn
