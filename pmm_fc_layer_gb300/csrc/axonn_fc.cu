@@ -1111,24 +1111,28 @@ struct FusedChoice {
   int splits = 1;
   double us = 0;  // the estimate
 };
-// TFLOP/s of each tile on full waves (GB300, 8192 x 24576 x 6144 and
-// multiples of whole waves), shared by the units that run at once.
-constexpr double kFusedRate[axonn::kFusedConfigs] = {1580, 1100, 630, 1720};
+// TFLOP/s of each tile on full waves, shared by the units that run at once.
+// This and the next two are the numbers by which the choice came nearest the
+// best of the four tiles over 240 products of 2e6 outputs and up (each side
+// 32 to 24576, drawn log-uniformly; activation, dropout and residual, residual,
+// backward with column sums; GB300): within 0.8 % on average, 14 % at most.
+constexpr double kFusedRate[axonn::kFusedConfigs] = {1470, 900, 560, 1900};
 constexpr int kFusedPlain[axonn::kFusedConfigs] = {2, 0, 7, 6};  // the plain products' configuration of that tile
-// What a tile takes at least, however short its reduction: its epilogue, a
-// light one (stores; an activation) and a heavy one (the cross entropy's
-// statistics, dropout or a residual).  512 x 256 tiles also wait for part of
-// it at every tile's end.  us, GB300: 7877 x 728 x 8292 with 512 x 256 tiles
-// takes 17 a tile, the statistics of 490 x 768 x 50257 28 and with 256 x 256
-// tiles 9.8.
-constexpr double kFusedFloor[2][axonn::kFusedConfigs] = {{6.5, 4, 2.5, 13}, {10, 6, 4, 26}};
-constexpr double kFusedExposed = 3;
+// What a tile takes at least, however short its reduction (us): its epilogue,
+// light (stores, an activation and its slope), heavy (dropout or a residual),
+// or the cross entropy's statistics.  The last tile's is not hidden.  512 x 256
+// tiles also wait for part of it at every tile's end.
+enum EpilogueWeight { kLight = 0, kHeavy = 1, kStatistics = 2 };
+constexpr double kFusedFloor[3][axonn::kFusedConfigs] = {
+    {3.4, 2.4, 2, 9}, {7.2, 5, 4, 16.6}, {9, 6, 4.5, 26}};
+constexpr double kFusedExposed = 2;
 constexpr double kFusedBytes = 6e6;  // bytes a microsecond that the parts of a split are written and read at
 constexpr int kFusedMostSplits = 16;
 // The choice of least estimated time: rounds of tiles over the units that run
 // at once, each as long as a tile's share of the reduction, and for a split
 // its parts' traffic (8 bytes an element and part).
-FusedChoice choose_fused(int64_t M, int64_t N, int64_t R, bool heavy, bool split, const DeviceState& dev) {
+FusedChoice choose_fused(int64_t M, int64_t N, int64_t R, EpilogueWeight weight, bool split,
+                         const DeviceState& dev) {
   const int forced = g_forced_config.load();
   int only = -1;
   for (int i = 0; i < axonn::kFusedConfigs; ++i)
@@ -1150,8 +1154,8 @@ FusedChoice choose_fused(int64_t M, int64_t N, int64_t R, bool heavy, bool split
       const int64_t over = tiles * s % slots;
       const double rounds = static_cast<double>(tiles * s / slots) +
                             (over == 0 ? 0.0 : (c.bm == 512 && 2 * over <= slots ? 0.6 : 1.0));
-      const double each = std::max(tile_us / s, kFusedFloor[heavy ? 1 : 0][i]) + (c.bm == 512 ? kFusedExposed : 0.0);
-      const double us = rounds * each +
+      const double each = std::max(tile_us / s, kFusedFloor[weight][i]) + (c.bm == 512 ? kFusedExposed : 0.0);
+      const double us = rounds * each + kFusedFloor[weight][i] +
                         (s > 1 ? s * 8.0 * M * N / kFusedBytes : 0.0);
       if (first || us < least) {
         first = false;
@@ -1167,8 +1171,9 @@ FusedChoice choose_fused(int64_t M, int64_t N, int64_t R, bool heavy, bool split
 
 // Pieces of the reduction for a product whose 128 x 128 tiles leave most SMs
 // idle, each tile's CTAs a cluster (fused_cluster_kernel): as many as leave
-// all clusters resident at once, of at least eight stages, where the estimate (kFusedExchange
-// for the parts' way through shared memory) is below that of `whole`; else 1.
+// all clusters resident at once, of at least eight stages, where the estimate
+// (kFusedExchange for the parts' way through shared memory) is below that of
+// `whole`; else 1.
 constexpr double kFusedExchange = 4;
 int cluster_pieces(int64_t M, int64_t N, int64_t R, const FusedChoice& whole, const DeviceState& dev) {
   if (g_forced_config.load() >= 0) return 1;
@@ -1177,7 +1182,7 @@ int cluster_pieces(int64_t M, int64_t N, int64_t R, const FusedChoice& whole, co
   while (most > 1 && tiles > dev.fused_clusters[most]) --most;
   if (most < 2) return 1;
   const double tile_us = 2.0 * 128 * 128 * static_cast<double>(R) * dev.sms / (kFusedRate[1] * 1e6);
-  return tile_us / most + kFusedFloor[0][1] + kFusedExchange < whole.us ? static_cast<int>(most) : 1;
+  return tile_us / most + kFusedFloor[kLight][1] + kFusedExchange < whole.us ? static_cast<int>(most) : 1;
 }
 
 // The map by which epilogues write a [rows x cols] matrix of bf16, fp32 or
@@ -1360,7 +1365,7 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
     } else {
       axonn::FusedParams<axonn::EpilogueArgs> p;
       int units = 0;
-      const FusedChoice choice = choose_fused(v.M, v.N, v.R, e.residual || e.drop.thr != 0, false, *dev);
+      const FusedChoice choice = choose_fused(v.M, v.N, v.R, e.residual || e.drop.thr != 0 ? kHeavy : kLight, false, *dev);
       const int pieces = cluster_pieces(v.M, v.N, v.R, choice, *dev);
       const int config = pieces > 1 ? 1 : choice.config;
       st = fused_fill(p, v, config, 16, *dev, &units);
@@ -1512,7 +1517,7 @@ axonn_status_t store_product(const OpView& v, FusedChoice choice, void* out, int
 FusedChoice choose_dx(int64_t T, int64_t K, int64_t V) {
   DeviceState* dev = nullptr;
   if (T == 0 || K == 0 || device_state(&dev) != AXONN_OK) return {};
-  return choose_fused(T, K, V, false, true, *dev);
+  return choose_fused(T, K, V, kLight, true, *dev);
 }
 
 }  // namespace
@@ -2295,12 +2300,12 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
   DeviceState* dev = nullptr;
   st = device_state(&dev);
   if (st != AXONN_OK) return st;
-  if (plan.splits != dx_choice.splits) dx_choice = choose_fused(T, K, cols, false, false, *dev);
+  if (plan.splits != dx_choice.splits) dx_choice = choose_fused(T, K, cols, kLight, false, *dev);
   char* base = static_cast<char*>(ws);
   const int64_t ld_piece = (cols + 7) / 8 * 8;
   float* dx32 = reinterpret_cast<float*>(base + l.end);
   uint16_t* piece = reinterpret_cast<uint16_t*>(base + l.end + plan.dx_bytes);
-  const int config = choose_fused(T, cols, K, true, false, *dev).config;
+  const int config = choose_fused(T, cols, K, kStatistics, false, *dev).config;
   const bool pdl = g_pdl.load() != 0;
 
   axonn::CeRowArgs a{};
@@ -2414,7 +2419,7 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
       const int mode = (flags & AXONN_ACCUM_F32) ? axonn::kOutF32Accum
                        : (flags & AXONN_OUT_F32) ? axonn::kOutF32
                                                  : axonn::kOutBF16;
-      st = store_product(x, choose_fused(x.M, x.N, x.R, false, false, *dev), static_cast<char*>(dW) + off * (w_f32 ? 4 : 2),
+      st = store_product(x, choose_fused(x.M, x.N, x.R, kLight, false, *dev), static_cast<char*>(dW) + off * (w_f32 ? 4 : 2),
                          lddw, mode, a.coef, kept, 2, 0, nullptr, *dev, stream);
       if (st != AXONN_OK) return st;
     }

@@ -30,6 +30,7 @@ __device__ __forceinline__ void store_distances(const EpiTile& t, int col, const
 struct StatsEpilogue {
   using Args = CeArgs;
   using State = NoState;
+  static constexpr int kEachStages = 16;
   static __device__ __forceinline__ State begin(const Args&) { return {}; }
 
   template <int kCols, bool kHold, class Ready, class Release>
@@ -104,6 +105,7 @@ struct StatsEpilogue {
 struct ProbEpilogue {
   using Args = CeArgs;
   using State = NoState;
+  static constexpr int kEachStages = 16;
   static __device__ __forceinline__ State begin(const Args&) { return {}; }
   static __device__ __forceinline__ void prefetch(const Args&, const EpiTile&, int) {}
 
@@ -137,6 +139,7 @@ struct ProbEpilogue {
 struct StoreEpilogue {
   using Args = StoreArgs;
   using State = float;  // the scale
+  static constexpr int kEachStages = 8;
   static __device__ __forceinline__ State begin(const Args& a) { return a.scale ? *a.scale : 1.0f; }
 
   static __device__ __forceinline__ void prefetch(const Args&, const EpiTile&, int) {}

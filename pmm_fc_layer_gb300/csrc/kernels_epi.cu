@@ -78,6 +78,7 @@ template <bool kF32, bool kJoin>
 struct FwdEpilogue {
   using Args = EpilogueArgs;
   using State = DropRng;
+  static constexpr int kEachStages = kJoin ? 16 : 8;
   static __device__ __forceinline__ State begin(const Args& a) { return load_rng(a.drop); }
 
   static __device__ __forceinline__ void prefetch(const Args& a, const EpiTile& t, int cols) {
@@ -135,6 +136,7 @@ template <bool kF32, bool kJoin>
 struct BwdEpilogue {
   using Args = EpilogueArgs;
   using State = DropRng;
+  static constexpr int kEachStages = kJoin ? 16 : 8;
   static __device__ __forceinline__ State begin(const Args& a) { return load_rng(a.drop); }
 
   static __device__ __forceinline__ void prefetch(const Args& a, const EpiTile& t, int cols) {
