@@ -285,9 +285,10 @@ axonn_status_t axonn_goldfish_ce(const void* logits, int64_t ld_logits, const in
  * word col & 7 of the output's eight 16-bit words, lowest first.  With
  * thr = floor(65536 p + 1/2) an element is dropped (set to 0, whatever it
  * is) where its bits are below thr and is multiplied by the fp32 number
- * nearest 65536/(65536 - thr) elsewhere; thr = 65536 drops all.  (seed, offset) are two 64-bit words on
- * the DEVICE, so that a captured graph draws a new mask when they are
- * changed between replays; the library only reads them.  Calls that must
+ * nearest 65536/(65536 - thr) elsewhere; thr = 65536 drops all.
+ * (seed, offset) are two 64-bit words on the DEVICE, so that a captured graph
+ * draws a new mask when they are changed between replays; the library only
+ * reads them.  Calls that must
  * draw alike, as a forward and its backward, get the same words and rows.
  */
 #define AXONN_BIAS_F32 0x200u     /* axonn_fc_fwd_epi: the bias is fp32 (else bf16) */
@@ -380,8 +381,9 @@ axonn_status_t axonn_dropout(const void* X, int64_t ldx, const void* residual, i
  * it from there.  The last piece of the forward sweep stays, each logit as
  * its distance below a maximum of its row in 16 bits (which changes an entry
  * of P by at most 2^-12 of itself, and by 2^-32 of that maximum's), and
- * opens the backward one; the others are computed again.  The piece is as large as the workspace allows: with one
- * that holds the whole vocabulary nothing is computed twice.
+ * opens the backward one; the others are computed again.  The piece is as
+ * large as the workspace allows: with one that holds the whole vocabulary
+ * nothing is computed twice.  A NaN logit shows in its whole row's gradient.
  *   ws       256-byte aligned; axonn_linear_ce_workspace_size gives its
  *            bytes for pieces of `piece` columns (rounded up to 256; 0: at
  *            most 2 GiB of P at a time).  Anything from the size for
@@ -396,7 +398,9 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
                                cudaStream_t stream);
 
 /* Workspace bytes of axonn_linear_ce; grad != 0 when dX or dW is asked for.
- * Host-only. */
+ * They include room for dX as fp32 parts where its few tiles leave SMs idle
+ * over a long vocabulary, which depends on the current device (without one:
+ * none, and the call then runs without them).  Launches nothing. */
 axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, uint32_t flags,
                                               int grad, int64_t piece, size_t* bytes);
 
@@ -527,9 +531,12 @@ void axonn_debug_set_inject(int mode);
  * axonn_set_kernel_config(c) forces configuration c for all later calls in
  * the process (-1 restores automatic choice); AXONN_ERR_INVALID_ARG if c is
  * out of range.  The products with an epilogue and those of the linear
- * cross-entropy have the tiles 0, 2, 6 and 7 and choose among them when another is forced.
+ * cross-entropy have the tiles 0, 2, 6 and 7 and choose among them when
+ * another is forced; while any is forced, their forms for one or two rows and
+ * for a reduction cut over a cluster are not used.
  * axonn_last_kernel_config() is the configuration the last
- * GEMM launch on this thread used (-1 before any). */
+ * GEMM launch on this thread used (-1 before any, and after a product with an
+ * epilogue that ran without tiles, for one or two rows). */
 axonn_status_t axonn_set_kernel_config(int config);
 /* SM count of the current device and how many CTA pairs (clusters of 2
  * running configuration 2) it keeps resident at once. */

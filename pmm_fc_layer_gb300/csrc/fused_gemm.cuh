@@ -25,6 +25,13 @@
 // rows of A and its half of B.
 // Waits are bounded, and an expired one is recorded and reported, as in the
 // plain products.
+//
+// Measured (8192 x 6144 x 24576, 512 x 256 tiles): GELU with Z kept 1535 us,
+// 1610 TFLOP/s, the tensor pipe busy 86 % of the cycles; under the power cap
+// the clock falls as the pipe fills, so the rest is not all idle time.  Short
+// reductions are bound by the epilogue's instructions and stores: 8192 x 64 x
+// 8192 takes 41 us (3.3 TB/s) plain, 56 with GELU, 94 with dropout and a
+// residual, of which the stores are 10 (256 x 256 tiles).
 #pragma once
 #include "epilogue.h"
 #include "epilogue_math.cuh"
@@ -702,7 +709,9 @@ __global__ void __launch_bounds__(FusedLayout<BN, STAGES, kPair, kHalves>::kThre
 // 32 x 32 are then dealt out to the cluster's warps; a warp adds up the S
 // parts of its block in the order of the ranges and runs the epilogue on it.
 // One tile a cluster, nothing persistent: it is launched where all CTAs fit
-// the GPU at once.
+// the GPU at once.  What bounds it is the operands' way into each SM: 64 x
+// 24576 x 6144 (302 MB of weights) takes 65 us, 4.6 TB/s, where the best whole
+// tile takes 121; 16 x 6144 x 6144 20.5 and 33.5, 512 x 8192 x 512 22.6 and 43.
 constexpr int kClusterStages = 6;
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
   float4 v;
