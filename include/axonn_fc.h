@@ -381,8 +381,9 @@ axonn_status_t axonn_dropout(const void* X, int64_t ldx, const void* residual, i
  * it from there.  The last piece of the forward sweep stays, each logit as
  * its distance below a maximum of its row in 16 bits (which changes an entry
  * of P by at most 2^-12 of itself, and by 2^-32 of that maximum's), and
- * opens the backward one; the others are computed again.  The piece is as
- * large as the workspace allows: with one that holds the whole vocabulary
+ * opens the backward one; the others are computed again (the last one too
+ * where the features are so few that this is sooner).  The piece is as large
+ * as the workspace allows: with one that holds the whole vocabulary
  * nothing is computed twice.  A NaN logit shows in its whole row's gradient.
  *   ws       256-byte aligned; axonn_linear_ce_workspace_size gives its
  *            bytes for pieces of `piece` columns (rounded up to 256; 0: at

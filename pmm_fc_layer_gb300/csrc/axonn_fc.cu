@@ -1390,6 +1390,15 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
 // The workspace, carved in order.
 constexpr int64_t kCePieceStep = 256;               // columns: whole tiles of every configuration
 constexpr size_t kCePieceDefault = size_t{2} << 30;  // bytes of one piece of the vocabulary
+// Features up to which the piece is not kept from the forward sweep but
+// computed again: a short product costs less than writing distances and
+// turning them into probabilities, more so where the piece does not stay in
+// L2.  All of the loss and gradients, us, kept and again: 512 rows x 50257
+// words, 64 features 104 and 98, 256 117 and 114, 512 143 and 146; 4096 x
+// 128256, 64 features 1351 and 1026, 256 1402 and 1130, 512 1714 and 1564, 768
+// 2066 and 2135.
+constexpr int64_t kCeAgain = 256, kCeAgainFar = 512;
+constexpr int64_t kCeInL2 = int64_t{128} << 20;  // bytes
 struct CeLayout {
   size_t index, place, labels, coef, label_logit, lse2, stats, x, end;
   int64_t ld_x;
@@ -2383,10 +2392,12 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
     AXONN_CE_RUN(axonn::ce_launch(kind, config, p, units, pdl, stream), "logits product");
     return AXONN_OK;
   };
-  // Forward over the pieces; the last one stays.
+  // Forward over the pieces; the last one stays, unless it is sooner computed
+  // again.
+  const bool stays = K > (2 * T * cols > kCeInL2 ? kCeAgainFar : kCeAgain);
   for (int64_t i = 0; i < pieces; ++i) {
     const int64_t c0 = i * cols, n = std::min(cols, V - c0);
-    st = logits(axonn::kCeStats, c0, n, grad && i == pieces - 1);
+    st = logits(axonn::kCeStats, c0, n, grad && stays && i == pieces - 1);
     if (st != AXONN_OK) return st;
   }
   AXONN_CE_RUN(axonn::ce_combine_launch(a, pdl, stream), "logsumexp");
@@ -2397,7 +2408,7 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
   for (int64_t j = 0; j < pieces; ++j) {
     const int64_t i = j == 0 ? pieces - 1 : j - 1;
     const int64_t c0 = i * cols, n = std::min(cols, V - c0);
-    if (j == 0) {
+    if (j == 0 && stays) {
       AXONN_CE_RUN(axonn::ce_scale_launch(a, piece, ld_piece, c0, n, pdl, stream), "probabilities");
     } else {
       st = logits(axonn::kCeProb, c0, n, true);

@@ -316,3 +316,105 @@ def test_nan_reaches_every_entry_it_should(cuda_lib, where, piece):
     assert (np.isnan(got["token_loss"]) == hit).all() and np.isnan(got["loss"]).all()
     assert (np.isnan(got["dX"]) == hit[:, None]).all() and (got["dX"][5] == 0).all()
     assert np.isnan(got["dW"]).all()
+
+
+# Above 256 features the last piece of the vocabulary is kept as distances
+# (above 512 where it is larger than L2) instead of being computed again.
+KEPT = [(1, 264, 1000), (33, 272, 300), (130, 520, 1003), (300, 300, 2000), (257, 264, 4097)]
+
+
+@pytest.mark.parametrize("config", [2, 0, 6, 7])
+@pytest.mark.parametrize("tied", [False, True])
+@pytest.mark.parametrize("size", KEPT)
+def test_kept_piece_against_64_bits(cuda_lib, size, tied, config):
+    X, W, labels, rng = case(*size, seed=31)
+    cuda_lib.axonn_set_kernel_config(config)
+    check(run(cuda_lib, X, W, labels, tied=tied), X, W, labels)
+
+
+@pytest.mark.parametrize("K", [256, 257, 264])
+@pytest.mark.parametrize("n", [0, 1, 31, 64, 65, 129])
+def test_kept_piece_and_counted_rows(cuda_lib, K, n):
+    """Both sides of the number of features up to which the piece is computed
+    again, with a vocabulary that ends inside 16 bytes; the other rows hold
+    NaN."""
+    T, V = 150, 701
+    X, W, labels, rng = case(T, K, V, seed=40 + n)
+    keep = np.zeros(T, dtype=np.uint8)
+    keep[rng.permutation(T)[:n]] = 1
+    dirty = X.copy()
+    dirty[keep == 0] = np.nan
+    for piece in (0, 256):
+        check(run(cuda_lib, dirty, W, labels, keep, piece=piece), X, W, labels, keep)
+
+
+@pytest.mark.parametrize("dw", ["f32", "add"])
+@pytest.mark.parametrize("piece", [0, 256])
+def test_kept_piece_fp32_weight_gradient(cuda_lib, dw, piece):
+    X, W, labels, rng = case(150, 264, 700, seed=36)
+    old = rng.normal(size=W.shape).astype(np.float32).astype(np.float64)
+    got = run(cuda_lib, X, W, labels, dw=dw, piece=piece, scale=64.0, old=old)
+    check(got, X, W, labels, scale=64.0, dw=dw, old=old if dw == "add" else 0.0)
+
+
+@pytest.mark.parametrize("piece", [0, 256])
+def test_kept_piece_confident_rows(cuda_lib, piece):
+    """Logits so far apart that most probabilities are 0 and a label's is
+    near 1, or near 0."""
+    T, K, V = 64, 264, 900
+    X, W, labels, rng = case(T, K, V, seed=33, spread=20.0)
+    labels[::2] = (X @ W).argmax(axis=1)[::2]
+    check(run(cuda_lib, X, W, labels, piece=piece), X, W, labels)
+
+
+@pytest.mark.parametrize("where", ["row", "column"])
+def test_kept_piece_nan(cuda_lib, where):
+    """As test_nan_reaches_every_entry_it_should, with a kept piece."""
+    T, K, V = 40, 264, 700
+    X, W, labels, rng = case(T, K, V, seed=37, spread=20.0)
+    labels[5] = -1
+    if where == "row":
+        X[7, 3] = np.nan
+        X[5] = np.nan  # does not count
+    else:
+        W[9, 17] = np.nan
+    got = run(cuda_lib, X, W, labels)
+    counted = labels >= 0
+    hit = counted & (np.arange(T) == 7) if where == "row" else counted
+    assert (np.isnan(got["token_loss"]) == hit).all() and np.isnan(got["loss"]).all()
+    assert (np.isnan(got["dX"]) == hit[:, None]).all() and (got["dX"][5] == 0).all()
+    assert np.isnan(got["dW"]).all()
+
+
+def test_kept_piece_offsets_past_32_bits(cuda_lib):
+    """A kept piece of more than 2^31 entries: dX of the last rows, and dW of
+    the last columns, against 64 bits."""
+    fc = cuda_lib
+    import torch
+    T, K, V, tail = 16800, 520, 128256, 40
+    assert T * V > 2**31
+    g = torch.Generator(device="cuda").manual_seed(3)
+    X = torch.randn((T, K), device="cuda", generator=g).to(torch.bfloat16)
+    W = torch.randn((K, V), device="cuda", generator=g).mul_(0.04).to(torch.bfloat16)
+    labels = torch.randint(0, V, (T,), device="cuda", generator=g, dtype=torch.int32)
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    tl, loss = torch.empty(T, device="cuda"), torch.empty(1, device="cuda")
+    kept = torch.empty(1, device="cuda", dtype=torch.int32)
+    ws = torch.empty(fc.axonn_linear_ce_workspace_size(T, K, V, piece=V), device="cuda", dtype=torch.uint8)
+    fc.axonn_linear_ce(X, W, labels, tl, loss, kept, ws, dX=dX, dW=dW)
+    fc.axonn_sync_status()
+    z = X[-tail:].double() @ W.double()
+    logp = torch.log_softmax(z, dim=1)
+    y = labels[-tail:].long()
+    at = torch.arange(tail, device="cuda")
+    assert float((tl[-tail:].double() + logp[at, y]).abs().max()) < 1e-4
+    P = logp.exp()
+    P[at, y] -= 1
+    ref = P @ W.double().T / T
+    assert float((dX[-tail:].double() - ref).norm() / ref.norm()) < 2 * 2.0**-8
+    cols = W[:, -24:].float()
+    lse = torch.cat([torch.logsumexp(X[i:i + 2100].float() @ W.float(), dim=1) for i in range(0, T, 2100)])
+    P = torch.exp(X.double() @ cols.double() - lse.double()[:, None])
+    hit = labels.long()[:, None] == torch.arange(V - 24, V, device="cuda")
+    ref = X.double().T @ (P - hit.double()) / T
+    assert float((dW[:, -24:].double() - ref).norm() / ref.norm()) < 2 * 2.0**-8
