@@ -18,16 +18,27 @@ namespace {
 
 struct NoState {};
 
-// 32 distances of each row in steps of 1 / kCeStep, up to kCeFar.
+// The distances -x of 32 logits below their maximum, x <= 0 in powers of two,
+// in steps of 1 / kCeStep up to kCeFar: a saturating product (also of the
+// rounding that leaves x above 0), then the low bits of 2^23 + q.
 __device__ __forceinline__ void store_distances(const EpiTile& t, int col, const float (&x)[32]) {
   uint32_t w[16];
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
-    const uint32_t lo = __float2uint_rn(fminf(x[2 * j] * kCeStep, static_cast<float>(kCeFar)));
-    const uint32_t hi = __float2uint_rn(fminf(x[2 * j + 1] * kCeStep, static_cast<float>(kCeFar)));
-    w[j] = __byte_perm(lo, hi, 0x5410);
+    float lo = __saturatef(x[2 * j] * (-kCeStep / static_cast<float>(kCeFar)));
+    float hi = __saturatef(x[2 * j + 1] * (-kCeStep / static_cast<float>(kCeFar)));
+    split(fma2(f2(lo, hi), f2(static_cast<float>(kCeFar)), f2(8388608.0f)), lo, hi);
+    w[j] = __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x5410);
   }
   store_segment<uint16_t>(t, t.out, col, w);
+}
+
+// Columns past the vocabulary's end become -inf: no maximum, nothing in the
+// sum, far in the piece.
+__device__ __forceinline__ void drop_columns(float (&x)[32], int width) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    if (j >= width) x[j] = -INFINITY;
 }
 
 struct StatsEpilogue {
@@ -45,10 +56,10 @@ struct StatsEpilogue {
     const int64_t y = in ? a.labels[t.row] - a.col0 - t.col : -1;
     if (!ready()) return false;
     float m = -INFINITY, s = 0.0f, mb = 0.0f;
-    auto take_max = [&](int c, const float(&x)[32]) {
+    auto take_max = [&](int c, float(&x)[32]) {
+      if (32 * c + 32 > width) drop_columns(x, width - 32 * c);
 #pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (32 * c + j < width) m = fmaxf(m, x[j]);  // skips NaN, which the sum then shows
+      for (int j = 0; j < 32; ++j) m = fmaxf(m, x[j]);  // skips NaN, which the sum then shows
     };
     auto take_sum = [&](int c, float(&x)[32]) {
       const int64_t d = y - 32 * c;
@@ -59,16 +70,16 @@ struct StatsEpilogue {
           if (j == d) zy = x[j];
         a.label_logit[t.row] = zy;
       }
-      // distance below the maximum, in powers of two
+      // minus the distance below the maximum, in powers of two
 #pragma unroll
-      for (int j = 0; j < 32; ++j) x[j] = 32 * c + j < width ? fmaf(x[j], -kEpiLog2e, mb) : INFINITY;
+      for (int j = 0; j < 32; j += 2)
+        split(fma2(f2(x[j], x[j + 1]), f2(kEpiLog2e), f2(-mb)), x[j], x[j + 1]);
       if (a.keep_piece) store_distances(t, t.col + 32 * c, x);
-      float s0 = 0.0f, s1 = 0.0f;
+      F2 sum = f2(0.0f);
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        s0 += ex2_approx(-x[j]);
-        s1 += ex2_approx(-x[j + 1]);
-      }
+      for (int j = 0; j < 32; j += 2) sum = add2(sum, f2(ex2_approx(x[j]), ex2_approx(x[j + 1])));
+      float s0, s1;
+      split(sum, s0, s1);
       s += s0 + s1;
     };
     // A row whose every logit is -inf sums to 0 (not to e^(-inf + inf)).
@@ -77,8 +88,10 @@ struct StatsEpilogue {
       float x[kCols / 32][32];
 #pragma unroll
       for (int c = 0; c < kCols / 32; ++c) {
-        if (32 * c < width) load_acc32(t, c, x[c]);
-        take_max(c, x[c]);
+        if (32 * c < width) {
+          load_acc32(t, c, x[c]);
+          take_max(c, x[c]);
+        }
       }
       release();
       set_base();
@@ -96,6 +109,7 @@ struct StatsEpilogue {
 #pragma unroll 1
       for (int c = 0; c < kCols / 32 && 32 * c < width; ++c) {
         load_acc32(t, c, x);
+        if (32 * c + 32 > width) drop_columns(x, width - 32 * c);
         take_sum(c, x);
       }
     }
