@@ -2409,7 +2409,7 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
     const int64_t i = j == 0 ? pieces - 1 : j - 1;
     const int64_t c0 = i * cols, n = std::min(cols, V - c0);
     if (j == 0 && stays) {
-      AXONN_CE_RUN(axonn::ce_scale_launch(a, piece, ld_piece, c0, n, pdl, stream), "probabilities");
+      AXONN_CE_RUN(axonn::ce_scale_launch(a, piece, ld_piece, c0, n, dev->sms, pdl, stream), "probabilities");
     } else {
       st = logits(axonn::kCeProb, c0, n, true);
       if (st != AXONN_OK) return st;

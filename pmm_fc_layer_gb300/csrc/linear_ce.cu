@@ -309,10 +309,14 @@ cudaError_t ce_combine_launch(const CeRowArgs& a, bool pdl, cudaStream_t stream)
 }
 
 cudaError_t ce_scale_launch(const CeRowArgs& a, uint16_t* piece, int64_t ld_piece, int64_t col0,
-                            int64_t cols, bool pdl, cudaStream_t stream) {
+                            int64_t cols, int sms, bool pdl, cudaStream_t stream) {
   if (a.rows == 0) return cudaSuccess;
-  const dim3 grid(static_cast<unsigned>((cols + kScaleCols - 1) / kScaleCols),
-                  static_cast<unsigned>(std::min<int64_t>(a.rows, 65535)));
+  // About 48 blocks an SM: a block a row leaves one idle for each row that
+  // does not count (1003 x 768 x 50257, half masked: 165 us in all, 159 so),
+  // and even without a mask takes 3 % more over 4096 x 50304.
+  const int64_t across = (cols + kScaleCols - 1) / kScaleCols;
+  const dim3 grid(static_cast<unsigned>(across),
+                  static_cast<unsigned>(std::min<int64_t>(a.rows, std::max<int64_t>(1, 48 * sms / across))));
   return launch_after(ce_scale_kernel, grid, 256, pdl, stream, a, piece, ld_piece, col0, cols);
 }
 

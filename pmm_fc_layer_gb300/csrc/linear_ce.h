@@ -50,7 +50,7 @@ cudaError_t ce_combine_launch(const CeRowArgs& a, bool pdl, cudaStream_t stream)
 // The kept distances of columns [col0, col0 + cols) to P = softmax - onehot,
 // in place.
 cudaError_t ce_scale_launch(const CeRowArgs& a, uint16_t* piece, int64_t ld_piece, int64_t col0,
-                            int64_t cols, bool pdl, cudaStream_t stream);
+                            int64_t cols, int sms, bool pdl, cudaStream_t stream);
 // dx from its packed rows: bf16, or the sum of fp32 parts, in order; zeros
 // where a row does not count.
 cudaError_t ce_unpack_launch(const CeRowArgs& a, const void* packed, int64_t ld, bool f32, int sms, bool pdl,
