@@ -9,8 +9,9 @@
 // All in fp32 up to that one rounding.  A thread owns a row, so neither the
 // maximum nor the sum needs another lane.  Tensor-bound at long reductions:
 // the statistics of 4096 x 6144 x 128256 take 3.4 to 3.5 ms (1.85 to 1.9
-// PFLOP/s); 490 x 768 x 50257 takes 48 us, three times its flops, the epilogue
-// being all there is to see (its plain product takes 42).
+// PFLOP/s).  490 x 768 x 50257 takes 52 us with cold caches, two and a half
+// times its flops: a short reduction leaves its epilogue to be seen (a plain
+// product there takes 42).
 #include "fused_gemm.cuh"
 
 namespace axonn {

@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(1024) ce_combine_kernel(CeRowArgs a) {
 
 // Blocks over (row, 4096 columns), a thread two vectors of eight columns,
 // both loaded before either is used.  HBM-bound: 4 bytes an element; 4096 x
-// 128256 takes 411 us (5.1 TB/s; one vector a thread 451).
+// 128256 takes 410 to 465 us (4.5 to 5.1 TB/s; one vector a thread 451 where
+// two took 411), 490 x 50257, which L2 holds, 26 (3.8 TB/s).
 constexpr int kScaleVecs = 2;
 constexpr int kScaleCols = 2048 * kScaleVecs;
 __global__ void __launch_bounds__(256) ce_scale_kernel(CeRowArgs a, uint16_t* piece, int64_t ld,
