@@ -419,3 +419,52 @@ def test_offsets_past_32_bits(cuda_lib):
     low = np.stack([(w >> np.uint64(16 * h)) & np.uint64(0xFFFF) for w in keep for h in (0, 1)], axis=1)
     want = torch.from_numpy(low.reshape(-1) >= 32768).cuda()
     assert torch.equal(Z[-1] != 0, want & (R[-1] != 0))
+
+
+@pytest.mark.parametrize("tied", [False, True])
+@pytest.mark.parametrize("size", [(2, 20000, 19464), (1, 9000, 19464), (2, 65536, 24), (1, 65544, 24)])
+def test_few_rows_over_long_reductions(cuda_lib, size, tied):
+    """One or two rows whose pieces of the reduction are bounded by shared
+    memory, up to the longest reduction and past it."""
+    import torch
+    fc = cuda_lib
+    T, K, N = size
+    g = torch.Generator(device="cuda").manual_seed(T + K)
+    X = torch.randn((T, K), device="cuda", generator=g).to(torch.bfloat16)
+    W = torch.randn((N, K) if tied else (K, N), device="cuda", generator=g).mul_(0.02).to(torch.bfloat16)
+    Y = torch.full((T, N), float("nan"), device="cuda")
+    fc.axonn_fc_fwd_epi(X, W, Y, fc.Shape(T, K, N), fc.OUT_F32 | (fc.B_T if tied else 0))
+    fc.axonn_sync_status()
+    Wd = (W.T if tied else W).double()
+    ref, S = X.double() @ Wd, X.double().abs() @ Wd.abs()
+    inside(host(Y), host(ref), product_error(K, host(S)), "Y")
+
+
+@pytest.mark.parametrize("config,size", [(2, (300, 64, 520)), (2, (300, 1500, 520)), (0, (130, 64, 264)),
+                                         (0, (130, 1500, 264)), (6, (600, 64, 520)), (6, (600, 1500, 520)),
+                                         (7, (130, 1500, 264)), (-1, (40, 4000, 72))])
+def test_expired_wait_is_reported(cuda_lib, config, size):
+    """Operand loads withheld, short and long reductions and one cut over a
+    cluster: the bounded waits expire, the status says so, and the next call
+    is right."""
+    import torch
+    fc = cuda_lib
+    T, K, N = size
+    rng = np.random.default_rng(3)
+    X, W = bf16(rng.normal(size=(T, K))), bf16(rng.normal(size=(K, N)) * 0.05)
+    Xd, Wd, Y = dev(X, torch.bfloat16), dev(W, torch.bfloat16), dev(np.zeros((T, N)), torch.bfloat16)
+    fc.axonn_set_kernel_config(config)
+    fc.axonn_set_wait_timeout_ns(2_000_000)
+    fc.axonn_debug_set_inject(1)
+    try:
+        with pytest.raises(fc.AxonnError) as e:
+            fc.axonn_fc_fwd_epi(Xd, Wd, Y, fc.Shape(T, K, N))
+            fc.axonn_sync_status()
+        assert e.value.status == fc.ERR_TIMEOUT
+    finally:
+        fc.axonn_debug_set_inject(0)
+        fc.axonn_set_wait_timeout_ns(4_000_000_000)
+    fc.axonn_fc_fwd_epi(Xd, Wd, Y, fc.Shape(T, K, N))
+    fc.axonn_sync_status()
+    ref = X @ W
+    inside(host(Y), ref, product_error(K, np.abs(X) @ np.abs(W)) + 2.0**-8 * np.abs(ref) + 1e-30, "Y")
