@@ -128,7 +128,7 @@ axonn_status_t device_state(DeviceState** out) {
     for (cudaError_t x : es)
       if (x != cudaSuccess)
         return fail(AXONN_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(x));
-    for (cudaError_t x : {axonn::fused_init(&split_ok), axonn::ce_init(&split_ok)})
+    for (cudaError_t x : {axonn::fused_init(&split_ok), axonn::ce_init(&split_ok), axonn::gemv_init()})
       if (x != cudaSuccess)
         return fail(AXONN_ERR_CUDA, "fused kernel attributes: %s", cudaGetErrorString(x));
     if (!split_ok)

@@ -273,18 +273,35 @@ __global__ void __launch_bounds__(kThreads, kResident<kMN, TM>) gemv_kernel(cons
 }
 
 template <bool kMN, int TM, int CB>
-int smem_bytes(int piece) {
+constexpr int smem_bytes(int piece) {
   return 4 * (TM * piece + TM * CB + (kMN ? kWarps * TM * CB : 0));
+}
+constexpr int kDefaultSmem = 48 * 1024;  // what a kernel has without asking
+
+// The most that a call can need (see gemv_launch), asked for once: the limit
+// is the kernel's, not the launch's, so that a call that set its own would
+// change it under another thread's.
+template <bool kFwd, bool kF32, bool kMN, int TM, int CB>
+cudaError_t allow_smem() {
+  constexpr int kMost = smem_bytes<kMN, TM, CB>(static_cast<int>(kGemvPiece));
+  if (kMost <= kDefaultSmem) return cudaSuccess;
+  return cudaFuncSetAttribute(gemv_kernel<kFwd, kF32, kMN, TM, CB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kMost);
+}
+
+template <bool kFwd, bool kF32>
+cudaError_t allow_layouts() {
+  for (cudaError_t e : {allow_smem<kFwd, kF32, true, 1, 256>(), allow_smem<kFwd, kF32, true, 1, 64>(),
+                        allow_smem<kFwd, kF32, false, 1, 64>(), allow_smem<kFwd, kF32, true, 2, 64>(),
+                        allow_smem<kFwd, kF32, false, 2, 64>()})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
 }
 
 template <bool kFwd, bool kF32, bool kMN, int TM, int CB>
 cudaError_t start(const GemvArgs& p, int splits, bool pdl, cudaStream_t stream) {
   auto kernel = gemv_kernel<kFwd, kF32, kMN, TM, CB>;
   const int smem = smem_bytes<kMN, TM, CB>(p.piece);
-  if (smem > 48 * 1024) {  // more than a kernel has by default
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.N + CB - 1) / CB * splits), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -317,6 +334,13 @@ cudaError_t start_rows(const GemvArgs& p, bool b_mn, int cols, int splits, bool 
 }
 
 }  // namespace
+
+cudaError_t gemv_init() {
+  for (cudaError_t e : {allow_layouts<false, false>(), allow_layouts<false, true>(), allow_layouts<true, false>(),
+                        allow_layouts<true, true>()})
+    if (e != cudaSuccess) return e;
+  return cudaSuccess;
+}
 
 cudaError_t gemv_launch(FusedKind kind, GemvArgs p, bool b_mn, int sms, bool pdl, cudaStream_t stream) {
   // The reduction in at most eight pieces of at least 256.  One row of a

@@ -25,6 +25,8 @@ constexpr int64_t kGemvReduction = 8 * kGemvPiece;
 
 // Whether these kernels are the faster ones for a product.
 bool gemv_wins(int64_t M, int64_t R);
+// Shared-memory limits on the current device.
+cudaError_t gemv_init();
 cudaError_t gemv_launch(FusedKind kind, GemvArgs p, bool b_mn, int sms, bool pdl, cudaStream_t stream);
 
 }  // namespace axonn

@@ -44,3 +44,47 @@ def test_concurrent_calls_on_separate_streams(cuda_lib):
     assert not errors, errors
     for i, case in enumerate(cases):
         assert np.array_equal(results[i], case[-1]), i
+
+
+def test_rows_of_different_reductions_from_several_threads(cuda_lib):
+    """Products of two rows need shared memory by the length of their
+    reduction; calls of different lengths at once, each on its own stream, are
+    all taken.  The calls are short and made through the C interface, so that
+    the threads spend their time inside it."""
+    import ctypes
+
+    import torch
+    fc = cuda_lib
+    N, calls = 64, 4000
+    lib, epilogue = fc.load(), fc.Epilogue()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    cases = []
+    for K in (65536, 49152, 65536, 49152, 57344, 65536):
+        X = torch.randn((2, K), device="cuda", generator=g).to(torch.bfloat16)
+        W = torch.randn((K, N), device="cuda", generator=g).mul_(0.02).to(torch.bfloat16)
+        cases.append((K, X, W, torch.empty((2, N), device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    refused = []
+    start = threading.Barrier(len(cases))
+
+    def worker(K, X, W, Y, s):
+        shape = fc.Shape(2, K, N)
+        args = (X.data_ptr(), W.data_ptr(), Y.data_ptr(), K, N, N, ctypes.byref(shape), fc.OUT_F32,
+                ctypes.byref(epilogue), s.cuda_stream)
+        start.wait()
+        for _ in range(calls):
+            st = lib.axonn_fc_fwd_epi(*args)
+            if st != fc.OK:
+                refused.append((K, st, lib.axonn_last_error()))
+
+    threads = [threading.Thread(target=worker, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not refused, (len(refused), refused[0])
+    for K, X, W, Y, _ in cases:
+        ref = X.double() @ W.double()
+        # products of bf16 numbers are exact in fp32; K of them are added up
+        assert bool(((Y.double() - ref).abs() <= K * 2.0**-24 * (X.double().abs() @ W.double().abs())).all())
