@@ -1112,10 +1112,12 @@ struct FusedChoice {
   double us = 0;  // the estimate
 };
 // TFLOP/s of each tile on full waves, shared by the units that run at once.
-// This and the next two are the numbers by which the choice came nearest the
-// best of the four tiles over 240 products of 2e6 outputs and up (each side
-// 32 to 24576, drawn log-uniformly; activation, dropout and residual, residual,
-// backward with column sums; GB300): within 0.8 % on average, 14 % at most.
+// This and the next two were fitted to 60 drawn shapes (223 to 7846 rows,
+// reductions of 34 to 8160, 564 to 23290 columns, at least 2e6 outputs) with
+// four epilogues each.  Over 120 others (3 to 8192 rows, reductions and columns
+// of 32 to 24576, drawn log-uniformly; activation, dropout and residual,
+// backward with column sums; GB300) the choice is 0.9 % slower than the best of
+// the four tiles on average, a fifth or more (28 %) in one of the 360.
 constexpr double kFusedRate[axonn::kFusedConfigs] = {1470, 900, 560, 1900};
 constexpr int kFusedPlain[axonn::kFusedConfigs] = {2, 0, 7, 6};  // the plain products' configuration of that tile
 // What a tile takes at least, however short its reduction (us): its epilogue,
@@ -1150,10 +1152,13 @@ FusedChoice choose_fused(int64_t M, int64_t N, int64_t R, EpilogueWeight weight,
     for (int s = 1; s <= (split ? kFusedMostSplits : 1); ++s) {
       if (s > 1 && R / s < 1024) break;
       // a last round of the 512-row tiles that fills at most half the units
-      // runs their halves side by side
+      // runs their halves side by side, but an only round does not: one unit is
+      // launched a tile, and for so few tiles 256 x 256 ones are the faster way
+      // to have that (400 x 24576 x 6144, 48 units: 127 us, by halves 150)
       const int64_t over = tiles * s % slots;
-      const double rounds = static_cast<double>(tiles * s / slots) +
-                            (over == 0 ? 0.0 : (c.bm == 512 && 2 * over <= slots ? 0.6 : 1.0));
+      const bool halves = c.bm == 512 && tiles * s > slots && 2 * over <= slots;
+      const double rounds =
+          static_cast<double>(tiles * s / slots) + (over == 0 ? 0.0 : (halves ? 0.6 : 1.0));
       const double each = std::max(tile_us / s, kFusedFloor[weight][i]) + (c.bm == 512 ? kFusedExposed : 0.0);
       const double us = rounds * each + kFusedFloor[weight][i] +
                         (s > 1 ? s * 8.0 * M * N / kFusedBytes : 0.0);
