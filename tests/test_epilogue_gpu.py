@@ -501,3 +501,33 @@ def test_choice_of_few_large_tiles(cuda_lib, size):
             t = time_us(lambda: fc.axonn_fc_fwd_epi(X, W, Y, fc.Shape(T, K, N), act="gelu_tanh"))
             best[config] = min(best.get(config, t), t)
     assert best[-1] <= 1.2 * min(v for c, v in best.items() if c >= 0), best
+
+
+def test_gelu_tail_relatively(cuda_lib):
+    """GELU and its slope where both are nearly 0: against 64 bits, relative
+    to their values, in fp32 outputs.
+
+    Bound.  The exponent of e^(-z^2/2) is a product of three fp32 factors:
+    3 roundings of 2^-24 of z^2/2.  Everything else (the tail's rational form,
+    the SFU's exponential and reciprocal, the polynomial's roundings) is within
+    2^-19.  The slope is z times the density plus the distribution function, of
+    opposite signs; below -2 the sum of their magnitudes is at most 1.6 times
+    their difference."""
+    import torch
+    fc = cuda_lib
+    z = torch.arange(-10.0, -2.0 + 1e-9, 1 / 64, device="cuda").to(torch.bfloat16).unique()
+    N = z.numel() // 8 * 8
+    z = z[:N]
+    zd = z.double()
+    cdf = 0.5 * torch.erfc(-zd * 0.5**0.5)
+    slope = cdf + zd * torch.exp(-0.5 * zd * zd) / (2 * np.pi) ** 0.5
+    bound = 1.5 * zd * zd * 2.0**-24 + 2.0**-19
+    for T in (1, 5):  # without tiles, and with them
+        X = torch.ones((T, 8), device="cuda", dtype=torch.bfloat16)[:, :1]
+        Y, D = (torch.empty((T, N), device="cuda") for _ in range(2))
+        fc.axonn_fc_fwd_epi(X, z[None, :], Y, fc.Shape(T, 1, N), fc.OUT_F32, act="gelu")
+        fc.axonn_fc_dgrad_epi(X, torch.ones((N, 8), device="cuda", dtype=torch.bfloat16)[:, :1], D,
+                              fc.Shape(T, N, 1), fc.OUT_F32, pre=z.expand(T, N).contiguous(), act="gelu")
+        fc.axonn_sync_status()
+        assert float(((Y.double() / (zd * cdf) - 1).abs() / bound).max()) <= 1.0
+        assert float(((D.double() / slope - 1).abs() / (1.6 * bound)).max()) <= 1.0
