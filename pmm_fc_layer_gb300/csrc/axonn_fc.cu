@@ -87,6 +87,7 @@ struct DeviceState {
   // Clusters of 2..8 CTAs of fused_cluster_kernel resident at once.
   int fused_clusters[9] = {};
   bool attrs_set = false;
+  bool fused_set = false;  // fused_clusters and the fused kernels' attributes
 };
 
 // Per-device state lives in a fixed table so that pointers handed out stay
@@ -128,12 +129,10 @@ axonn_status_t device_state(DeviceState** out) {
     for (cudaError_t x : es)
       if (x != cudaSuccess)
         return fail(AXONN_ERR_CUDA, "kernel attributes: %s", cudaGetErrorString(x));
-    for (cudaError_t x : {axonn::fused_init(&split_ok), axonn::ce_init(&split_ok), axonn::gemv_init()})
-      if (x != cudaSuccess)
-        return fail(AXONN_ERR_CUDA, "fused kernel attributes: %s", cudaGetErrorString(x));
     if (!split_ok)
       return fail(AXONN_ERR_UNSUPPORTED,
-                  "a GEMM kernel was not built with the registers per thread its split assumes");
+                  "a 12-warp GEMM kernel was not built with %d registers per thread",
+                  axonn::kRegsAtLaunch);
     int clusters = 0;
     if (axonn::pair_clusters_resident(d.sms, &clusters) != cudaSuccess || clusters <= 0) {
       (void)cudaGetLastError();
@@ -153,14 +152,35 @@ axonn_status_t device_state(DeviceState** out) {
         }
         d.split_clusters[t][lg] = n;
       }
-    for (int pieces = 2; pieces <= 8; ++pieces)
-      if (axonn::fused_clusters_resident(d.sms, pieces, &d.fused_clusters[pieces]) != cudaSuccess) {
-        (void)cudaGetLastError();
-        d.fused_clusters[pieces] = 0;
-      }
     d.attrs_set = true;
   }
   *out = &d;
+  return AXONN_OK;
+}
+
+// The same for the products with a fused epilogue and of the linear cross
+// entropy, at the first of them: their kernels take three times as long to set
+// up as all the others (15 ms), and what is wrong with one of them is no
+// reason to refuse a plain product.
+axonn_status_t fused_state(DeviceState** out) {
+  const axonn_status_t st = device_state(out);
+  if (st != AXONN_OK) return st;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  DeviceState& d = **out;
+  if (d.fused_set) return AXONN_OK;
+  bool regs_ok = true;
+  for (cudaError_t x : {axonn::fused_init(&regs_ok), axonn::ce_init(&regs_ok), axonn::gemv_init()})
+    if (x != cudaSuccess)
+      return fail(AXONN_ERR_CUDA, "fused kernel attributes: %s", cudaGetErrorString(x));
+  if (!regs_ok)
+    return fail(AXONN_ERR_UNSUPPORTED,
+                "a fused kernel was not built with the registers per thread that its split assumes");
+  for (int pieces = 2; pieces <= 8; ++pieces)
+    if (axonn::fused_clusters_resident(d.sms, pieces, &d.fused_clusters[pieces]) != cudaSuccess) {
+      (void)cudaGetLastError();
+      d.fused_clusters[pieces] = 0;
+    }
+  d.fused_set = true;
   return AXONN_OK;
 }
 
@@ -1345,7 +1365,7 @@ axonn_status_t fused_op(int op, const void* P, const void* Q, void* C, int64_t l
   }
   if (v.N == 0 || (v.M == 0 && !epi->dbias)) return ok();
   DeviceState* dev = nullptr;
-  st = device_state(&dev);
+  st = fused_state(&dev);
   if (st != AXONN_OK) return st;
   if (v.M > 0) {
     const axonn::FusedKind kind = fwd ? axonn::kFusedFwd : axonn::kFusedBwd;
@@ -2312,7 +2332,7 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
   const int64_t cols = plan.cols;
   const int64_t pieces = (V + cols - 1) / cols;
   DeviceState* dev = nullptr;
-  st = device_state(&dev);
+  st = fused_state(&dev);
   if (st != AXONN_OK) return st;
   if (plan.splits != dx_choice.splits) dx_choice = choose_fused(T, K, cols, kLight, false, *dev);
   char* base = static_cast<char*>(ws);
