@@ -184,6 +184,14 @@ axonn_status_t fused_state(DeviceState** out) {
   return AXONN_OK;
 }
 
+// Whether they have been set up on the current device.
+bool fused_in_use() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  return g_devs[dev].fused_set;
+}
+
 // ------------------------------------------------------------------ grid
 void split_range(int64_t D, int64_t G, int64_t b, int64_t* s, int64_t* e) {
   const int64_t units = (D + 7) / 8;
@@ -2497,15 +2505,18 @@ axonn_status_t axonn_sync_status(cudaStream_t stream, uint64_t* detail) {
   if (detail) *detail = 0;
   cudaError_t e = cudaStreamSynchronize(stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "stream: %s", cudaGetErrorString(e));
-  // One error word per kernel translation unit; report the first set.
+  // One error word per kernel translation unit, a device-to-host copy each;
+  // report the first set.  Fused kernels that were never set up on this device
+  // have not run there.
+  const bool fused = fused_in_use();
   unsigned long long word = 0, w1 = 0, w8 = 0, w64 = 0;
   unsigned long long wg = 0, we = 0, wc = 0;
   e = axonn::kernels_take_status<1>(&w1, stream);
   if (e == cudaSuccess) e = axonn::kernels_take_status<kFewProblems>(&w8, stream);
   if (e == cudaSuccess) e = axonn::kernels_take_status<kMaxProblems>(&w64, stream);
   if (e == cudaSuccess) e = axonn::goldfish_take_status(&wg, stream);
-  if (e == cudaSuccess) e = axonn::fused_take_status(&we, stream);
-  if (e == cudaSuccess) e = axonn::ce_take_status(&wc, stream);
+  if (e == cudaSuccess && fused) e = axonn::fused_take_status(&we, stream);
+  if (e == cudaSuccess && fused) e = axonn::ce_take_status(&wc, stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
   for (unsigned long long w : {w1, w8, w64, wg, we, wc})
     if (word == 0) word = w;

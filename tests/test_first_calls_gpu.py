@@ -61,3 +61,20 @@ fc.axonn_sync_status()
 print(json.dumps(bool(torch.equal(y.float(), torch.eye(64, device="cuda") + 1.0))))
 """)
     assert got is True
+
+
+def test_status_of_plain_products_waits_for_their_words_alone(cuda_lib):
+    """Each group of kernels has a status word that is copied to the host; a
+    process without fused products does not wait for theirs: four copies where
+    the others make six."""
+    got = run("""
+def status_us():
+    fc.axonn_sync_status()
+    n = 200
+    return min(ms(lambda: [fc.axonn_sync_status() for _ in range(n)]) for _ in range(5)) / n * 1e3
+fc.axonn_fc_fwd(x, x, y, shape)
+plain = status_us()
+fc.axonn_fc_fwd_epi(x, x, y, shape, bias=b)
+print(json.dumps([plain, status_us()]))
+""")
+    assert got[0] < 0.75 * got[1], got
