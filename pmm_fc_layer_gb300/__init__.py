@@ -321,8 +321,18 @@ def axonn_goldfish_ce(logits, input_ids, labels, keep, token_loss, loss, kept, k
                                     _stream(stream)))
 
 
+def _on_device(name, t):
+    """The kernels read and write through the pointers: memory that the device
+    cannot reach is refused here."""
+    if not t.is_cuda and not t.is_pinned():
+        raise ValueError(f"{name} must be on the device, got {t.device}")
+
+
 def _ws(ws):
-    return (ws.data_ptr(), ws.numel() * ws.element_size()) if ws is not None else (None, 0)
+    if ws is None:
+        return None, 0
+    _on_device("ws", ws)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 _dtypes = {}
@@ -346,6 +356,7 @@ def _matrix(name, t, dtype, rows, cols):
         raise ValueError(f"{name} must be {_dtype(dtype)}, got {t.dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(t.shape)}")
+    _on_device(name, t)
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
@@ -360,6 +371,7 @@ def _vector(name, t, dtype, n):
         raise ValueError(f"{name} must be {_dtype(dtype)}, got {t.dtype}")
     if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be contiguous of {n} elements")
+    _on_device(name, t)
     return t.data_ptr()
 
 
@@ -368,6 +380,7 @@ def _rng(rng):
         return None
     if rng.dtype not in _dtype("words") or rng.shape != (2,) or rng.stride(0) != 1:
         raise ValueError("rng must be two contiguous 64-bit integers on the device: seed and offset")
+    _on_device("rng", rng)
     return rng.data_ptr()
 
 

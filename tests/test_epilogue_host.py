@@ -213,3 +213,54 @@ def test_binding_checks(fc):
         fc.axonn_dropout(B, B, 0.5, torch.zeros(2), stream=0)
     with pytest.raises(ValueError):
         fc.axonn_epi_bwd(B, B.float(), stream=0)
+
+
+class Elsewhere:
+    """A tensor's face, without its memory on the device: everything but the
+    device is as a call wants it."""
+
+    def __init__(self, shape, kind, device="cpu"):
+        import torch
+        self.t = torch.zeros(shape, dtype=getattr(torch, kind))
+        self.is_cuda = device == "cuda"
+
+    def is_pinned(self):
+        return False
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+@pytest.mark.parametrize("host", ["X", "W", "Y", "bias", "pre", "residual", "rng"])
+def test_host_memory_is_refused_forward(fc, host):
+    m = lambda n, shape, kind: Elsewhere(shape, kind, "cpu" if n == host else "cuda")  # noqa: E731
+    b = "bfloat16"
+    with pytest.raises(ValueError, match=f"{host} must be on the device"):
+        fc.axonn_fc_fwd_epi(m("X", (8, 8), b), m("W", (8, 8), b), m("Y", (8, 8), b), fc.Shape(8, 8, 8),
+                            bias=m("bias", (8,), "float32"), pre=m("pre", (8, 8), b),
+                            residual=m("residual", (8, 8), b), p=0.5, rng=m("rng", (2,), "int64"), stream=0)
+
+
+@pytest.mark.parametrize("host", ["dY", "W", "dX", "pre", "dbias", "ws"])
+def test_host_memory_is_refused_backward(fc, host):
+    m = lambda n, shape, kind: Elsewhere(shape, kind, "cpu" if n == host else "cuda")  # noqa: E731
+    b = "bfloat16"
+    with pytest.raises(ValueError, match=f"{host} must be on the device"):
+        fc.axonn_fc_dgrad_epi(m("dY", (8, 8), b), m("W", (8, 8), b), m("dX", (8, 8), b), fc.Shape(8, 8, 8),
+                              pre=m("pre", (8, 8), b), act="gelu", dbias=m("dbias", (8,), "float32"),
+                              ws=m("ws", (64,), "uint8"), stream=0)
+    if host in ("dY", "pre", "dbias", "ws"):
+        with pytest.raises(ValueError, match=f"{host} must be on the device"):
+            fc.axonn_epi_bwd(m("dY", (8, 8), b), m("dZ", (8, 8), b), pre=m("pre", (8, 8), b), act="gelu",
+                             dbias=m("dbias", (8,), "float32"), ws=m("ws", (64,), "uint8"), stream=0)
+
+
+@pytest.mark.parametrize("host", ["X", "W", "labels", "keep", "token_loss", "lse", "loss", "kept", "dX", "dW", "ws"])
+def test_host_memory_is_refused_linear_ce(fc, host):
+    m = lambda n, shape, kind: Elsewhere(shape, kind, "cpu" if n == host else "cuda")  # noqa: E731
+    b, f = "bfloat16", "float32"
+    with pytest.raises(ValueError, match=f"{host} must be on the device"):
+        fc.axonn_linear_ce(m("X", (8, 8), b), m("W", (8, 16), b), m("labels", (8,), "int32"),
+                           m("token_loss", (8,), f), m("loss", (1,), f), m("kept", (1,), "int32"),
+                           m("ws", (1 << 20,), "uint8"), keep=m("keep", (8,), "uint8"), lse=m("lse", (8,), f),
+                           dX=m("dX", (8, 8), b), dW=m("dW", (8, 16), b), stream=0)
