@@ -11,6 +11,8 @@ bf16 (8 significant bits) and 2^-24 in fp32, where one more bit is allowed for
 the sum with the residual.
 A column sum over T rows adds T 2^-24 of the sum of magnitudes.
 """
+import functools
+
 import numpy as np
 import pytest
 
@@ -531,3 +533,94 @@ def test_gelu_tail_relatively(cuda_lib):
         fc.axonn_sync_status()
         assert float(((Y.double() / (zd * cdf) - 1).abs() / bound).max()) <= 1.0
         assert float(((D.double() / slope - 1).abs() / (1.6 * bound)).max()) <= 1.0
+
+
+# Configuration -> tile and how many of them run at once (of CTAs or pairs).
+TILES = {2: (256, 256, 1), 0: (128, 128, 2), 7: (128, 64, 2), 6: (512, 256, 1)}
+
+
+def device_act(z, name):
+    """act and its slope in 64 bits on the device."""
+    import torch
+    z = z.detach().requires_grad_(True)
+    F = torch.nn.functional
+    a = {"none": lambda v: v * 1.0, "relu": F.relu, "gelu": F.gelu, "silu": F.silu,
+         "gelu_tanh": lambda v: F.gelu(v, approximate="tanh")}[name](z)
+    return a.detach(), torch.autograd.grad(a.sum(), z)[0]
+
+
+@functools.lru_cache(maxsize=2)
+def mask_of(T, N, p, seed, offset):
+    import torch
+    keep, scale = ep.keep_mask(T, N, p, seed, offset)
+    return torch.from_numpy(keep).cuda(), scale
+
+
+@pytest.mark.parametrize("K", [72, 200, 512, 1500])
+@pytest.mark.parametrize("rounds", [1.05, 1.7, 3.3])
+@pytest.mark.parametrize("config", [6, 2, 0, 7])
+def test_tiles_in_rounds(cuda_lib, config, rounds, K):
+    """More tiles than run at once, so that accumulators, operand stages and
+    staging slots pass from one tile to the next, with a last round that fills
+    less and more than half of the units (the 512-row tiles then run by halves,
+    or whole), over reductions shorter and longer than the ring of stages.
+    Every element, forward and backward, with and without dropout and residual.
+    """
+    import torch
+    fc = cuda_lib
+    bm, bn, per_pair = TILES[config]
+    sms, pairs = fc.axonn_device_info()
+    units = pairs if per_pair == 1 else sms
+    tiles_n = 10
+    tiles_m = max(2, round(rounds * units / tiles_n))
+    T, N = tiles_m * bm - bm // 2 + 3, tiles_n * bn - 19
+    g = torch.Generator(device="cuda").manual_seed(config + K)
+
+    def rand(rows, cols, scale=1.0, kind=torch.bfloat16):
+        ld = (cols + 7) // 8 * 8
+        return torch.randn((rows, ld), device="cuda", generator=g).mul_(scale).to(kind)[:, :cols]
+
+    def close(got, ref, bound, what):
+        worst = float(((got.double() - ref).abs() / bound).max())
+        assert worst <= 1.0, f"{what}: {worst:.3f} of the bound"
+
+    fc.axonn_set_kernel_config(config)
+    words_d, seed, offset = words()
+    keep, scale = mask_of(T, N, 0.3, seed, offset)
+    X, W, R, Z = rand(T, K), rand(K, N, 0.2), rand(T, N), rand(T, N, 2.0)
+    b = torch.randn(N, device="cuda", generator=g)
+    acc, S = X.double() @ W.double(), X.double().abs() @ W.double().abs()
+    err = product_error(K, S + b.double().abs())
+    # forward: bias, activation, the pre-activation kept
+    Y, pre = rand(T, N), rand(T, N)
+    fc.axonn_fc_fwd_epi(X, W, Y, fc.Shape(T, K, N), bias=b, act="silu", pre=pre)
+    assert fc.axonn_last_kernel_config() == config
+    z = acc + b.double()
+    a, _ = device_act(z, "silu")
+    close(pre, z, err + 2.0**-8 * z.abs() + 1e-30, "pre")
+    close(Y, a, 1.13 * err + 2.0**-20 * a.abs() + 2.0**-21 + 2.0**-8 * a.abs(), "forward")
+    # forward: dropout and residual, fp32
+    Yf, Rf = rand(T, N, kind=torch.float32), rand(T, N, kind=torch.float32)
+    fc.axonn_fc_fwd_epi(X, W, Yf, fc.Shape(T, K, N), fc.OUT_F32, act="relu", residual=Rf, p=0.3, rng=words_d)
+    a = torch.where(keep, torch.relu(acc) * scale, 0.0)
+    ref = a + Rf.double()
+    close(Yf, ref, scale * product_error(K, S) + 2.0**-20 * a.abs() + 2.0**-21 + 2.0**-23 * ref.abs(), "joined")
+    del Yf, Rf, Y, pre, z
+    # backward: slope and column sums; with dropout and residual
+    ws = torch.empty(fc.axonn_epi_workspace_size(T, N), dtype=torch.uint8, device="cuda")
+    db = torch.empty(N, device="cuda")
+    Wn = W.t().contiguous() if K % 8 == 0 else None
+    _, slope = device_act(Z.double(), "gelu_tanh")
+    for p, res in ((0.0, None), (0.3, R)):
+        D = rand(T, N)
+        db.fill_(float("nan"))
+        fc.axonn_fc_dgrad_epi(X, W if Wn is None else Wn, D, fc.Shape(T, N, K), fc.B_T if Wn is None else 0, pre=Z,
+                              act="gelu_tanh", residual=res, dbias=db, p=p, rng=words_d if p else None, ws=ws)
+        s = scale if p else 1.0
+        d = torch.where(keep, acc * s, 0.0) if p else acc
+        e = s * 1.13 * product_error(K, S) + d.abs() * 2.0**-20 + 1e-30
+        d = d * slope
+        ref = d if res is None else d + res.double()
+        close(D, ref, e + 2.0**-8 * ref.abs(), f"backward {p}")
+        close(db, d.sum(0), e.sum(0) + T * 2.0**-24 * d.abs().sum(0), f"column sums {p}")
+    fc.axonn_sync_status()

@@ -418,3 +418,114 @@ def test_kept_piece_offsets_past_32_bits(cuda_lib):
     hit = labels.long()[:, None] == torch.arange(V - 24, V, device="cuda")
     ref = X.double().T @ (P - hit.double()) / T
     assert float((dW[:, -24:].double() - ref).norm() / ref.norm()) < 2 * 2.0**-8
+
+
+@pytest.mark.parametrize("K", [72, 264, 520])
+@pytest.mark.parametrize("n", [0, 1, 31, 32, 33, 65, 149])
+@pytest.mark.parametrize("V", [4097, 20000])
+def test_parts_of_dx_follow_the_counted_rows(cuda_lib, V, n, K):
+    """dX as fp32 parts of a reduction over a long vocabulary: how many, and
+    how far apart, follows on the device from the rows that count.  The other
+    rows hold NaN, and so does the workspace at the start."""
+    T = 150
+    X, W, labels, rng = case(T, K, V, seed=50 + n)
+    size = lambda v: (cuda_lib.axonn_linear_ce_workspace_size(T, K, v)  # noqa: E731
+                      - cuda_lib.axonn_linear_ce_workspace_size(T, K, v, grad=False))
+    assert size(V) >= 2 * T * V + 2 * 4 * T * K  # at least two parts
+    keep = np.zeros(T, dtype=np.uint8)
+    keep[rng.permutation(T)[:n]] = 1
+    dirty = X.copy()
+    dirty[keep == 0] = np.nan
+    check(run(cuda_lib, dirty, W, labels, keep, tied=n % 2 == 1), X, W, labels, keep)
+
+
+@pytest.mark.parametrize("K", [72, 264])
+@pytest.mark.parametrize("size", [(1100, 14000), (1100, 11000), (600, 14003)])
+@pytest.mark.parametrize("config", [6, 2, 0, 7])
+def test_tiles_in_rounds(cuda_lib, config, size, K):
+    """More tiles than run at once: statistics, probabilities (computed again,
+    and from the kept piece) and the two gradients, with a last round that
+    fills less and more than half of the units."""
+    T, V = size
+    X, W, labels, rng = case(T, K, V, seed=60)
+    labels[::9] = -100
+    cuda_lib.axonn_set_kernel_config(config)
+    check(run(cuda_lib, X, W, labels), X, W, labels)
+
+
+@pytest.mark.parametrize("piece", [0, 512])
+@pytest.mark.parametrize("tied", [False, True])
+def test_one_gradient_alone(cuda_lib, tied, piece):
+    """dX without dW and dW without dX are the same numbers as together."""
+    import torch
+    fc = cuda_lib
+    T, K, V = 130, 264, 5003
+    X, W, labels, rng = case(T, K, V, seed=70)
+    labels[::5] = -1
+    Xd, Wd = dev(X, torch.bfloat16), dev(W.T.copy() if tied else W, torch.bfloat16)
+    y = torch.from_numpy(labels.astype(np.int32)).cuda()
+    flags = fc.B_T if tied else 0
+    ws = torch.full((fc.axonn_linear_ce_workspace_size(T, K, V, flags, True, piece),), 255, dtype=torch.uint8,
+                    device="cuda")
+    got = []
+    for want in ("both", "dX", "dW"):
+        dX, dW = (torch.zeros_like(t) if want in ("both", n) else None for n, t in (("dX", Xd), ("dW", Wd)))
+        if dX is not None:
+            dX = dev(np.full((T, K), 7.0), torch.bfloat16)
+        if dW is not None:
+            dW = dev(np.full(Wd.shape, 7.0), torch.bfloat16)
+        out = [torch.empty(T, device="cuda"), torch.empty(1, device="cuda"),
+               torch.empty(1, device="cuda", dtype=torch.int32)]
+        fc.axonn_linear_ce(Xd, Wd, y, *out, ws, dX=dX, dW=dW, flags=flags)
+        fc.axonn_sync_status()
+        got.append((out, dX, dW))
+    for out, dX, dW in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(out, got[0][0]))
+        assert dX is None or torch.equal(dX, got[0][1])
+        assert dW is None or torch.equal(dW, got[0][2])
+
+
+def test_two_streams_at_once(cuda_lib):
+    """A loss with gradients and a layer with its epilogue on two streams,
+    again and again: each as when it runs alone."""
+    import torch
+    fc = cuda_lib
+    g = torch.Generator(device="cuda").manual_seed(9)
+    T, K, V, N = 700, 264, 9000, 1040
+
+    def rand(*shape):
+        return torch.randn(shape, device="cuda", generator=g).to(torch.bfloat16)
+
+    X, W, W1, Z = rand(T, K), rand(K, V).mul_(0.05), rand(K, N).mul_(0.05), rand(T, N)
+    labels = torch.randint(0, V, (T,), device="cuda", generator=g, dtype=torch.int32)
+    ws = torch.empty(fc.axonn_linear_ce_workspace_size(T, K, V), dtype=torch.uint8, device="cuda")
+    epi_ws = torch.empty(fc.axonn_epi_workspace_size(T, K), dtype=torch.uint8, device="cuda")
+    rng = torch.tensor([5, 6], device="cuda")
+
+    def loss(o, s):
+        fc.axonn_linear_ce(X, W, labels, o[0], o[1], o[2], ws, dX=o[3], dW=o[4], stream=s)
+
+    def layer(o, s):
+        fc.axonn_fc_fwd_epi(X, W1, o[0], fc.Shape(T, K, N), act="gelu", residual=Z, p=0.2, rng=rng, stream=s)
+        fc.axonn_fc_dgrad_epi(o[0], W1, o[1], fc.Shape(T, K, N), pre=X, act="silu", dbias=o[2], ws=epi_ws, stream=s)
+        fc.axonn_fc_fwd_epi(X[:2], W1, o[3], fc.Shape(2, K, N), act="silu", stream=s)
+
+    def outputs():
+        e = lambda *shape, t=torch.float32: torch.empty(shape, device="cuda", dtype=t)  # noqa: E731
+        b = torch.bfloat16
+        return ([e(T), e(1), e(1, t=torch.int32), e(T, K, t=b), e(K, V, t=b)],
+                [e(T, N, t=b), e(T, K, t=b), e(K), e(2, N, t=b)])
+
+    alone, both = outputs(), outputs()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    loss(alone[0], None)
+    layer(alone[1], None)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        loss(both[0], streams[0])
+        for _ in range(4):
+            layer(both[1], streams[1])
+    for s in streams:
+        fc.axonn_sync_status(s)
+    for a, b in zip(alone, both):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
