@@ -321,30 +321,32 @@ def axonn_goldfish_ce(logits, input_ids, labels, keep, token_loss, loss, kept, k
                                     _stream(stream)))
 
 
-def _on_device(name, t):
-    """The kernels read and write through the pointers: memory that the device
-    cannot reach is refused here."""
-    if not t.is_cuda and not t.is_pinned():
+def _host_memory(name, t):
+    """A tensor that is not on the device: the kernels read and write through
+    its pointer, so memory that they cannot reach is refused."""
+    if not t.is_pinned():
         raise ValueError(f"{name} must be on the device, got {t.device}")
 
 
 def _ws(ws):
     if ws is None:
         return None, 0
-    _on_device("ws", ws)
+    if not ws.is_cuda:
+        _host_memory("ws", ws)
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-_dtypes = {}
+class _Dtypes(dict):
+    """torch's dtype of a name (torch is imported at the first one asked for)."""
 
-
-def _dtype(name):
-    """torch's dtype of that name (torch is imported at the first call)."""
-    if not _dtypes:
+    def __missing__(self, name):
         import torch
-        _dtypes.update(bf16=torch.bfloat16, f32=torch.float32, i32=torch.int32, u8=torch.uint8,
-                       words=(torch.int64, torch.uint64))
-    return _dtypes[name]
+        self.update(bf16=torch.bfloat16, f32=torch.float32, i32=torch.int32, u8=torch.uint8,
+                    words=(torch.int64, torch.uint64))
+        return self[name]
+
+
+_dtypes = _Dtypes()
 
 
 def _matrix(name, t, dtype, rows, cols):
@@ -352,11 +354,12 @@ def _matrix(name, t, dtype, rows, cols):
     (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.dtype is not _dtype(dtype):
-        raise ValueError(f"{name} must be {_dtype(dtype)}, got {t.dtype}")
+    if t.dtype is not _dtypes[dtype]:
+        raise ValueError(f"{name} must be {_dtypes[dtype]}, got {t.dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(t.shape)}")
-    _on_device(name, t)
+    if not t.is_cuda:
+        _host_memory(name, t)
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have unit column stride")
@@ -367,20 +370,22 @@ def _vector(name, t, dtype, n):
     """Pointer of a contiguous vector of n elements of that type, or None."""
     if t is None:
         return None
-    if t.dtype is not _dtype(dtype):
-        raise ValueError(f"{name} must be {_dtype(dtype)}, got {t.dtype}")
+    if t.dtype is not _dtypes[dtype]:
+        raise ValueError(f"{name} must be {_dtypes[dtype]}, got {t.dtype}")
     if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be contiguous of {n} elements")
-    _on_device(name, t)
+    if not t.is_cuda:
+        _host_memory(name, t)
     return t.data_ptr()
 
 
 def _rng(rng):
     if rng is None:
         return None
-    if rng.dtype not in _dtype("words") or rng.shape != (2,) or rng.stride(0) != 1:
+    if rng.dtype not in _dtypes["words"] or rng.shape != (2,) or rng.stride(0) != 1:
         raise ValueError("rng must be two contiguous 64-bit integers on the device: seed and offset")
-    _on_device("rng", rng)
+    if not rng.is_cuda:
+        _host_memory("rng", rng)
     return rng.data_ptr()
 
 
@@ -406,7 +411,7 @@ def axonn_fc_fwd_epi(X, W, Y, shape: Shape, flags: int = 0, bias=None, act="none
     type sets BIAS_F32); residual has Y's type.  D is dropout with probability
     p and ``rng``, two 64-bit words on the device (seed, offset)."""
     T, N = shape.T, shape.N
-    if bias is not None and bias.dtype is _dtype("f32"):
+    if bias is not None and bias.dtype is _dtypes["f32"]:
         flags |= BIAS_F32
     out = "f32" if flags & OUT_F32 else "bf16"
     x, w = _layer(shape, flags, "X", X, T, shape.K, W)
@@ -438,7 +443,7 @@ def axonn_epi_bwd(dY, dZ, pre=None, act="none", dbias=None, p=0.0, rng=None, ws=
     """dZ (bf16) = act'(pre) D(dY) and dbias (fp32) = its column sums, for
     dY [rows x cols] in bf16 or fp32 (the tensor's type sets IN_F32)."""
     rows, cols = dY.shape
-    f32 = dY.dtype is _dtype("f32")
+    f32 = dY.dtype is _dtypes["f32"]
     e = Epilogue(None, *_matrix("pre", pre, "bf16", rows, cols), None, 0,
                  _vector("dbias", dbias, "f32", cols), _rng(rng), _act(act), p)
     _check(load().axonn_epi_bwd(*_matrix("dY", dY, "f32" if f32 else "bf16", rows, cols),
@@ -456,7 +461,7 @@ def axonn_dropout(X, Y, p, rng, residual=None, stream=None):
     """Y = residual + D(X), bf16 or fp32 (X's type); its backward is the same
     call on the gradient."""
     rows, cols = X.shape
-    f32 = X.dtype is _dtype("f32")
+    f32 = X.dtype is _dtypes["f32"]
     kind = "f32" if f32 else "bf16"
     _check(load().axonn_dropout(*_matrix("X", X, kind, rows, cols),
                                 *_matrix("residual", residual, kind, rows, cols),

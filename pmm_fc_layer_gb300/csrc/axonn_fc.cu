@@ -87,7 +87,7 @@ struct DeviceState {
   // Clusters of 2..8 CTAs of fused_cluster_kernel resident at once.
   int fused_clusters[9] = {};
   bool attrs_set = false;
-  bool fused_set = false;  // fused_clusters and the fused kernels' attributes
+  std::atomic<bool> fused_set{false};  // fused_clusters and the fused kernels' attributes
 };
 
 // Per-device state lives in a fixed table so that pointers handed out stay
@@ -165,8 +165,9 @@ axonn_status_t device_state(DeviceState** out) {
 axonn_status_t fused_state(DeviceState** out) {
   const axonn_status_t st = device_state(out);
   if (st != AXONN_OK) return st;
-  std::lock_guard<std::mutex> lk(g_dev_mu);
   DeviceState& d = **out;
+  if (d.fused_set) return AXONN_OK;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
   if (d.fused_set) return AXONN_OK;
   bool regs_ok = true;
   for (cudaError_t x : {axonn::fused_init(&regs_ok), axonn::ce_init(&regs_ok), axonn::gemv_init()})
@@ -187,9 +188,7 @@ axonn_status_t fused_state(DeviceState** out) {
 // Whether they have been set up on the current device.
 bool fused_in_use() {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
-  std::lock_guard<std::mutex> lk(g_dev_mu);
-  return g_devs[dev].fused_set;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices && g_devs[dev].fused_set;
 }
 
 // ------------------------------------------------------------------ grid
