@@ -61,6 +61,14 @@ __device__ __forceinline__ F2 min2(F2 a, float b) {
   split(a, x, y);
   return f2(fminf(x, b), fminf(y, b));
 }
+// Each half's magnitude at most b > 0, its sign kept; NaN stays.
+__device__ __forceinline__ F2 clamp2(F2 a, float b) {
+  float x, y;
+  split(a, x, y);
+  asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(x) : "f"(b));
+  asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(y) : "f"(b));
+  return f2(x, y);
+}
 __device__ __forceinline__ F2 ex2_2(F2 a) {
   float x, y;
   split(a, x, y);
@@ -77,17 +85,16 @@ __device__ __forceinline__ F2 rcp_2(F2 a) {
 __device__ __forceinline__ F2 logistic2(F2 neg) { return rcp_2(add2(ex2_2(neg), f2(1.0f))); }
 
 // The tanh form of GELU, 0.5 z (1 + tanh(u)) with u = c0 (z + c1 z^3), is
-// z sigmoid(2u); -2u log2 e = z (kTanhA + kTanhB z^2).  z^2 is clamped where
-// the gate has long saturated, so that nothing overflows.
+// z s, s = sigmoid(2u) = 1 / (1 + e), e = 2^(-2u log2 e); -2u log2 e = z
+// (kTanhA + kTanhB z^2).
 constexpr float kGeluC0 = 0.7978845608028654f;  // sqrt(2/pi)
 constexpr float kGeluC1 = 0.044715f;
 constexpr float kTanhA = -2.0f * kGeluC0 * kEpiLog2e;
 constexpr float kTanhB = kTanhA * kGeluC1;
 constexpr float kRsqrt2 = 0.7071067811865476f;
 constexpr float kRsqrt2Pi = 0.3989422804014327f;
-__device__ __forceinline__ F2 gelu_tanh_gate2(F2 z, F2& zz) {
-  zz = min2(mul2(z, z), 4096.0f);
-  return logistic2(mul2(z, fma2(zz, f2(kTanhB), f2(kTanhA))));
+__device__ __forceinline__ F2 gelu_tanh_exponent2(F2 z, F2 zz) {
+  return mul2(z, fma2(zz, f2(kTanhB), f2(kTanhA)));
 }
 
 // The normal distribution function at z, and e = e^(-z^2 / 2).  Its tail
@@ -132,8 +139,8 @@ __device__ __forceinline__ F2 act_value2(F2 z) {
     return mul2(z, normal_cdf2(z, e));
   }
   if constexpr (ACT == kActGeluTanh) {
-    F2 zz;
-    return mul2(z, gelu_tanh_gate2(z, zz));
+    // z^2 stops where the gate has long saturated, so that nothing overflows
+    return mul2(z, logistic2(gelu_tanh_exponent2(z, min2(mul2(z, z), 4096.0f))));
   }
   if constexpr (ACT == kActSilu) return mul2(z, logistic2(mul2(z, f2(-kEpiLog2e))));
   return z;
@@ -152,10 +159,13 @@ __device__ __forceinline__ F2 act_slope2(F2 z) {
     return fma2(mul2(z, f2(kRsqrt2Pi)), e, cdf);
   }
   if constexpr (ACT == kActGeluTanh) {
-    // with s = sigmoid(2u): s + z s (1 - s) 2 u'(z)
-    F2 zz;
-    const F2 s = gelu_tanh_gate2(z, zz);
-    const F2 w = mul2(z, fma2(mul2(s, f2(-1.0f)), s, s));  // 0 where the gate has saturated
+    // s + z s (1 - s) 2 u'(z).  1 - s = e s: as a difference it would keep
+    // s's rounding, which z 2 u'(z) makes 2^-19 of at z = 5.  At z = 10 the slope
+    // is 1 and at -10 it is 0 in fp32, with e at 2^-126 and 2^126: there z stops.
+    z = clamp2(z, 10.0f);
+    const F2 zz = mul2(z, z);
+    const F2 e = ex2_2(gelu_tanh_exponent2(z, zz)), s = rcp_2(add2(e, f2(1.0f)));
+    const F2 w = mul2(z, mul2(mul2(e, s), s));
     return fma2(w, fma2(zz, f2(6.0f * kGeluC0 * kGeluC1), f2(2.0f * kGeluC0)), s);
   }
   if constexpr (ACT == kActSilu) {

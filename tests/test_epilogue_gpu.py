@@ -624,3 +624,31 @@ def test_tiles_in_rounds(cuda_lib, config, rounds, K):
         close(D, ref, e + 2.0**-8 * ref.abs(), f"backward {p}")
         close(db, d.sum(0), e.sum(0) + T * 2.0**-24 * d.abs().sum(0), f"column sums {p}")
     fc.axonn_sync_status()
+
+
+@pytest.mark.parametrize("act", ep.ACTS)
+def test_slopes_everywhere(cuda_lib, act):
+    """Every bf16 pre-activation between -16 and 16 whose magnitude is at least
+    1/256: the slope is within 2^-20, in the products' epilogues (with tiles
+    and without) and in the elementwise backward (the column sum of one row)."""
+    import torch
+    fc = cuda_lib
+    z = torch.arange(-16, 16, 1 / 256, device="cuda").to(torch.bfloat16).unique()
+    z = z[:z.numel() // 8 * 8]
+    N = z.numel()
+    _, slope = device_act(z.double(), act)
+    got = {}
+    for T in (1, 5):
+        D = torch.empty((T, N), device="cuda")
+        fc.axonn_fc_dgrad_epi(torch.ones((T, 8), device="cuda", dtype=torch.bfloat16)[:, :1],
+                              torch.ones((N, 8), device="cuda", dtype=torch.bfloat16)[:, :1], D, fc.Shape(T, N, 1),
+                              fc.OUT_F32, pre=z.expand(T, N).contiguous(), act=act)
+        got[f"{T} rows"] = D
+    db = torch.empty(N, device="cuda")
+    one = torch.ones((1, N), device="cuda", dtype=torch.bfloat16)
+    ws = torch.empty(fc.axonn_epi_workspace_size(1, N), dtype=torch.uint8, device="cuda")
+    fc.axonn_epi_bwd(one, torch.empty_like(one), pre=z[None, :], act=act, dbias=db, ws=ws)
+    got["elementwise"] = db
+    fc.axonn_sync_status()
+    for what, d in got.items():
+        assert float((d.double() - slope).abs().max()) <= 2.0**-20, what
