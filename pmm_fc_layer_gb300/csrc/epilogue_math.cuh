@@ -1,6 +1,6 @@
 // Device arithmetic shared by the fused epilogues and the elementwise
 // kernels: the activations with their derivatives, the counter-based
-// generator behind dropout, and 32-column row segments in bf16 and fp32.
+// generator behind dropout, and 16-column row segments in bf16 and fp32.
 // Everything is fp32 between the loads and the one rounding at the store.
 #pragma once
 #include <cuda_bf16.h>

@@ -26,12 +26,12 @@
 // Waits are bounded, and an expired one is recorded and reported, as in the
 // plain products.
 //
-// Measured (8192 x 6144 x 24576, 512 x 256 tiles): GELU with Z kept 1535 us,
-// 1610 TFLOP/s, the tensor pipe busy 86 % of the cycles; under the power cap
+// Measured (8192 x 6144 x 24576, 512 x 256 tiles): GELU with Z kept 1545 us,
+// 1601 TFLOP/s, the tensor pipe busy 86 % of the cycles; under the power cap
 // the clock falls as the pipe fills, so the rest is not all idle time.  Short
 // reductions are bound by the epilogue's instructions and stores: 8192 x 64 x
-// 8192 takes 41 us (3.3 TB/s) plain, 56 with GELU, 94 with dropout and a
-// residual, of which the stores are 10 (256 x 256 tiles).
+// 8192 takes 42 us (3.2 TB/s) plain, 56 with GELU, 94 with dropout and a
+// residual, of which the stores are 11, 9 and 5 (256 x 256 tiles).
 #pragma once
 #include "epilogue.h"
 #include "epilogue_math.cuh"

@@ -4,9 +4,10 @@
 // Both are bound by the tensor cores wherever the reduction is long; the
 // epilogue's arithmetic and its reads of R and Z run beside the next tile's
 // mainloop.  A thread owns one row and walks its columns 32 at a time.
-// Measured, 2.47e12 flops each: GELU + Z 8192 x 6144 x 24576 1535 us, dropout +
-// residual 8192 x 24576 x 6144 1540, backward with GELU' and column sums 8192 x
-// 6144 x 24576 1605 (1610, 1605 and 1540 TFLOP/s).
+// Measured, 2.47e12 flops each, medians over four GPUs under the power cap
+// (within 3 %): GELU + Z 8192 x 6144 x 24576 1545 us, dropout + residual 8192 x
+// 24576 x 6144 1549, backward with GELU' and column sums 8192 x 6144 x 24576
+// 1624 (1601, 1597 and 1523 TFLOP/s).
 #include "fused_gemm.cuh"
 
 namespace axonn {
