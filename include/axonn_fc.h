@@ -297,7 +297,8 @@ axonn_status_t axonn_goldfish_ce(const void* logits, int64_t ld_logits, const in
  */
 #define AXONN_BIAS_F32 0x200u     /* axonn_fc_fwd_epi: the bias is fp32 (else bf16) */
 #define AXONN_IN_F32 0x400u       /* axonn_epi_bwd: dY is fp32 (else bf16); axonn_dropout: X,
-                                     residual and Y are fp32 (else bf16) */
+                                     residual and Y are fp32 (else bf16); operators over rows
+                                     of logits: logits and dlogits are fp32 (else bf16) */
 typedef enum {
   AXONN_ACT_NONE = 0,
   AXONN_ACT_RELU = 1,
@@ -408,6 +409,84 @@ axonn_status_t axonn_linear_ce(const void* X, int64_t ldx, const void* W, int64_
  * none, and the call then runs without them).  Launches nothing. */
 axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, uint32_t flags,
                                               int grad, int64_t piece, size_t* bytes);
+
+/*
+ * Rows of vocabulary logits: log probabilities of given tokens with their
+ * entropy and top alternatives, the way back through them, and distillation
+ * from a teacher's lists.  With x a row of logits [V], tau the temperature,
+ *   z = x / tau;  lse = ln sum_v e^(z_v);  ln p_v = z_v - lse
+ *   H = -sum_v p_v ln p_v
+ * Common to the three calls:
+ *   logits   bf16, or fp32 with AXONN_IN_F32, [T x V] (ld_logits).  Columns
+ *            behind V are neither read nor written.
+ *   keep     uint8 [T] or NULL: a row whose byte is 0 counts for nothing and
+ *            is not read
+ *   temperature  in [1e-4, 1e4]
+ * A logit of -inf has probability 0.  In a row of nothing else every
+ * probability is 0: ln p = lse = -inf, H = 0, and no gradient.  A NaN or +inf
+ * among the logits makes the row's numbers NaN.  Arithmetic and sums are fp32,
+ * sums in an order that depends on the sizes alone, exponentials the special
+ * function units' (2^-22; 0 below 2^-126); differences are taken from the row's
+ * maximum before they are scaled, so a row of finite logits of any size gives
+ * its own probabilities.  No workspace.
+ *
+ * axonn_token_logprobs -- scoring, answering and a teacher's lists, in one
+ * launch that reads the logits once.  Each output may be NULL:
+ *   tokens   int32 [T], given with logprob: a token outside [0, V) (padding)
+ *            has logprob 0; the row's other outputs are as for any row
+ *   logprob  out, fp32 [T]: ln p of the row's token
+ *   entropy  out, fp32 [T]: H;   lse  out, fp32 [T]
+ *   top_index, top_logprob  out, int32 and fp32 [T x k] (ld_top >= k, 4-byte
+ *            aligned): the row's k largest logits, best first, equal ones by
+ *            index, and their ln p.  0 <= k <= min(V, 128).  -0 equals 0, and
+ *            a NaN comes before every number.
+ * Rows that keep leaves out get 0, and -1 as indices.
+ *
+ * axonn_token_logprobs_bwd -- with g and h the gradients of logprob and
+ * entropy (a policy loss and its entropy bonus),
+ *   dlogits_v = (g ([v = token] - p_v) - h p_v (ln p_v + H)) / tau
+ *   tokens, dlogprob   int32 and fp32 [T], or both NULL; a token outside
+ *                      [0, V) has no gradient
+ *   lse                fp32 [T], as the forward left it for these logits and
+ *                      this temperature (p comes from it: it is off by
+ *                      2^-24 |lse| of itself)
+ *   entropy, dentropy  fp32 [T], H as the forward left it, and h; or both NULL
+ *   dlogits            out, of the logits' type, rounded once; may be the
+ *                      logits themselves (same ld), else must not overlap them
+ * Rows left out, and rows with g = h = 0, are written as zeros and not read.
+ *
+ * axonn_distill -- a student's loss against a teacher's lists of k logits
+ * (or log probabilities: a list may be shifted by any number), renormalised:
+ *   q = softmax(top_logit / tau) over the list
+ *   KL_t = sum_j q_j (ln q_j - ln p[top_index_j]);  token_loss_t = tau^2 KL_t
+ *   loss = sum over counted t of token_loss_t / n, n = number counted
+ *   dlogits_v = grad_scale tau (p_v - sum of q_j with top_index_j = v) / n
+ *   top_index, top_logit  int32 and fp32 [T x k] (ld_top >= k, 4-byte aligned),
+ *              1 <= k <= 1024; a list ends at its first index outside [0, V).
+ *              An index given twice teaches twice.  Entries of -inf have q = 0;
+ *              a list of nothing else has loss and gradient 0, but counts.
+ *   A row counts when keep does not leave it out and its list is not empty.
+ *   token_loss out, fp32 [T]: 0 where not counted; +inf where q > 0 at p = 0
+ *   loss, kept out, fp32 [1] and int32 [1] (n); loss is 0 for n = 0, and its
+ *              word counts finished blocks during the call
+ *   dlogits    out, of the logits' type, or NULL for the loss alone; rows not
+ *              counted get zeros; in place as above
+ * Two launches; the second reads the logits twice, the second time from L2.
+ */
+axonn_status_t axonn_token_logprobs(const void* logits, int64_t ld_logits, const int32_t* tokens,
+                                    const uint8_t* keep, int64_t T, int64_t V, float temperature,
+                                    uint32_t flags, float* logprob, float* entropy, float* lse, int32_t k,
+                                    int32_t* top_index, float* top_logprob, int64_t ld_top,
+                                    cudaStream_t stream);
+axonn_status_t axonn_token_logprobs_bwd(const void* logits, int64_t ld_logits, const int32_t* tokens,
+                                        const uint8_t* keep, int64_t T, int64_t V, float temperature,
+                                        uint32_t flags, const float* lse, const float* dlogprob,
+                                        const float* entropy, const float* dentropy, void* dlogits,
+                                        int64_t ld_dlogits, cudaStream_t stream);
+axonn_status_t axonn_distill(const void* logits, int64_t ld_logits, const int32_t* top_index,
+                             const float* top_logit, int64_t ld_top, const uint8_t* keep, int64_t T, int64_t V,
+                             int32_t k, float temperature, float grad_scale, uint32_t flags, float* token_loss,
+                             float* loss, int32_t* kept, void* dlogits, int64_t ld_dlogits, cudaStream_t stream);
 
 /*
  * Per-shape tuning -- the GB300 counterpart of the automatic tuning of BLAS

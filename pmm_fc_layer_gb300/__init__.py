@@ -37,6 +37,7 @@ EXPORTS = ("axonn_fc_fwd", "axonn_fc_dgrad", "axonn_fc_wgrad", "axonn_fc_vgrid_s
            "axonn_shards_gather", "axonn_fc_wgrad_zsharded", "axonn_goldfish_ce",
            "axonn_fc_fwd_epi", "axonn_fc_dgrad_epi", "axonn_epi_bwd", "axonn_epi_workspace_size",
            "axonn_dropout", "axonn_linear_ce", "axonn_linear_ce_workspace_size",
+           "axonn_token_logprobs", "axonn_token_logprobs_bwd", "axonn_distill",
            "axonn_fc_workspace_size", "axonn_fc_tune", "axonn_tune_cache_save",
            "axonn_tune_cache_load", "axonn_tune_cache_clear", "axonn_tune_cache_size",
            "axonn_tune_lookup",
@@ -144,6 +145,13 @@ def load(path: str | None = None):
         lib.axonn_tune_lookup.restype = ctypes.c_int
         lib.axonn_last_choice.argtypes = [ctypes.POINTER(ctypes.c_int)] * 3
         lib.axonn_last_choice.restype = None
+        f32 = ctypes.c_float
+        lib.axonn_token_logprobs.argtypes = [vp, i64, vp, vp, i64, i64, f32, u32, vp, vp, vp, i32, vp, vp, i64, vp]
+        lib.axonn_token_logprobs.restype = ctypes.c_int
+        lib.axonn_token_logprobs_bwd.argtypes = [vp, i64, vp, vp, i64, i64, f32, u32, vp, vp, vp, vp, vp, i64, vp]
+        lib.axonn_token_logprobs_bwd.restype = ctypes.c_int
+        lib.axonn_distill.argtypes = [vp, i64, vp, vp, i64, vp, i64, i64, i32, f32, f32, u32, vp, vp, vp, vp, i64, vp]
+        lib.axonn_distill.restype = ctypes.c_int
         lib.axonn_fc_workspace_size.argtypes = [ctypes.c_int, ctypes.POINTER(Shape), u32,
                                                 ctypes.POINTER(sz)]
         lib.axonn_fc_workspace_size.restype = ctypes.c_int
@@ -226,6 +234,18 @@ def _current_stream() -> int:
         else:
             _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
     return _raw_stream()
+
+
+_device = None
+
+
+def _current_device() -> int:
+    global _device
+    if _device is None:
+        import torch
+        torch.cuda.init()
+        _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    return _device()
 
 
 def _stream(stream) -> int:
@@ -495,6 +515,91 @@ def axonn_linear_ce_workspace_size(T: int, K: int, V: int, flags: int = 0, grad:
     n = ctypes.c_size_t(0)
     _check(load().axonn_linear_ce_workspace_size(T, K, V, flags, int(grad), piece, ctypes.byref(n)))
     return n.value
+
+
+def _logits(logits, *others):
+    """(rows, columns, type name) of logits; every other tensor that is given
+    must be on their device, which must be the current one."""
+    rows, cols = logits.shape
+    if logits.is_cuda:
+        here = logits.get_device()
+        for t in others:
+            if t is not None and t.is_cuda and t.get_device() != here:
+                raise ValueError(f"tensors on devices {here} and {t.get_device()}")
+        if here != _current_device():
+            raise ValueError(f"logits are on device {here}, which is not the current one")
+    return rows, cols, "f32" if logits.dtype is _dtypes["f32"] else "bf16"
+
+
+def _logit_rows(name, t, kind, rows, cols):
+    """(pointer, leading dimension) of rows of logits, or (None, 0) for None;
+    the stride of a single row says nothing."""
+    at, ld = _matrix(name, t, kind, rows, cols)
+    return at, ld if rows > 1 else (cols + 7) // 8 * 8
+
+
+def _lists(name, t, dtype, rows, k):
+    """(pointer, leading dimension) of [rows x k] list entries of that type, or
+    (None, 0) for None."""
+    if t is None:
+        return None, 0
+    at, ld = _matrix(name, t, dtype, rows, k)
+    return at, ld if rows > 1 else k
+
+
+def axonn_token_logprobs(logits, tokens=None, logprob=None, entropy=None, lse=None, top_index=None,
+                         top_logprob=None, keep=None, temperature=1.0, stream=None):
+    """ln p of int32 tokens [T] under softmax(logits / temperature), logits
+    [T x V] in bf16 or fp32 (the tensor's type sets IN_F32): fills, where given,
+    logprob [T], entropy [T], lse [T], and the rows' largest logits, best first,
+    as top_index (int32) and top_logprob [T x k].  Rows with keep (uint8 [T]) 0
+    get zeros and indices of -1."""
+    T, V, kind = _logits(logits, tokens, logprob, entropy, lse, top_index, top_logprob, keep)
+    top = top_index if top_index is not None else top_logprob
+    k = 0 if top is None else top.shape[1]
+    index, ld = _lists("top_index", top_index, "i32", T, k)
+    value, ld_value = _lists("top_logprob", top_logprob, "f32", T, k)
+    if index and value and ld != ld_value:
+        raise ValueError("top_index and top_logprob must have the same row stride")
+    _check(load().axonn_token_logprobs(
+        *_logit_rows("logits", logits, kind, T, V), _vector("tokens", tokens, "i32", T), _vector("keep", keep, "u8", T),
+        T, V, temperature, IN_F32 if kind == "f32" else 0, _vector("logprob", logprob, "f32", T),
+        _vector("entropy", entropy, "f32", T), _vector("lse", lse, "f32", T), k, index, value, ld or ld_value,
+        _stream(stream)))
+
+
+def axonn_token_logprobs_bwd(logits, lse, dlogits, tokens=None, dlogprob=None, entropy=None, dentropy=None,
+                             keep=None, temperature=1.0, stream=None):
+    """dlogits (the logits' type; may be the logits) = (dlogprob (onehot(tokens)
+    - p) - dentropy p (ln p + entropy)) / temperature, for lse and entropy as
+    axonn_token_logprobs left them."""
+    T, V, kind = _logits(logits, lse, dlogits, tokens, dlogprob, entropy, dentropy, keep)
+    _check(load().axonn_token_logprobs_bwd(
+        *_logit_rows("logits", logits, kind, T, V), _vector("tokens", tokens, "i32", T), _vector("keep", keep, "u8", T),
+        T, V, temperature, IN_F32 if kind == "f32" else 0, _vector("lse", lse, "f32", T),
+        _vector("dlogprob", dlogprob, "f32", T), _vector("entropy", entropy, "f32", T),
+        _vector("dentropy", dentropy, "f32", T), *_logit_rows("dlogits", dlogits, kind, T, V), _stream(stream)))
+
+
+def axonn_distill(logits, top_index, top_logit, token_loss, loss, kept, dlogits=None, keep=None, temperature=1.0,
+                  grad_scale=1.0, stream=None):
+    """tau^2 KL of softmax(top_logit / tau) over a teacher's lists (int32
+    top_index and fp32 top_logit [T x k], ended by an index outside the
+    vocabulary) against softmax(logits / tau), tau the temperature: fills
+    token_loss [T], loss [1], kept [1] (int32) and, if given, dlogits (the
+    logits' type; may be the logits), the gradient of the mean loss times
+    grad_scale."""
+    T, V, kind = _logits(logits, top_index, top_logit, token_loss, loss, kept, dlogits, keep)
+    k = top_index.shape[1]
+    index, ld = _lists("top_index", top_index, "i32", T, k)
+    value, ld_value = _lists("top_logit", top_logit, "f32", T, k)
+    if ld != ld_value:
+        raise ValueError("top_index and top_logit must have the same row stride")
+    _check(load().axonn_distill(
+        *_logit_rows("logits", logits, kind, T, V), index, value, ld, _vector("keep", keep, "u8", T), T, V, k,
+        temperature, grad_scale, IN_F32 if kind == "f32" else 0, _vector("token_loss", token_loss, "f32", T),
+        _vector("loss", loss, "f32", 1), _vector("kept", kept, "i32", 1), *_logit_rows("dlogits", dlogits, kind, T, V),
+        _stream(stream)))
 
 
 def axonn_fc_tune(op, P, Q, C, shape: Shape, flags: int = 0, ws=None, ldp=None, ldq=None,

@@ -27,6 +27,7 @@
 #include "goldfish.h"
 #include "kernel_launch.h"
 #include "linear_ce.h"
+#include "vocab_rows.h"
 
 namespace {
 
@@ -1561,6 +1562,34 @@ FusedChoice choose_dx(int64_t T, int64_t K, int64_t V) {
   return choose_fused(T, K, V, kLight, true, *dev);
 }
 
+// ------------------------------------------------------------------ rows of logits
+// What the operators over rows of logits have in common: types, sizes, the
+// temperature and the logits themselves.
+axonn_status_t logit_rows(const void* logits, int64_t ld, const uint8_t* keep, int64_t T, int64_t V,
+                          float temperature, uint32_t flags, axonn::LogitRows* rows) {
+  if (flags & ~AXONN_IN_F32)
+    return fail(AXONN_ERR_INVALID_ARG, "flag bits 0x%x do not apply here", flags & ~AXONN_IN_F32);
+  axonn_status_t st = check_rows_cols(T, V);
+  if (st != AXONN_OK) return st;
+  if (V < 1) return fail(AXONN_ERR_INVALID_ARG, "vocabulary size %lld", (long long)V);
+  if (!(temperature >= 1e-4f && temperature <= 1e4f))
+    return fail(AXONN_ERR_INVALID_ARG, "temperature not in [1e-4, 1e4]");
+  const bool f32 = (flags & AXONN_IN_F32) != 0;
+  st = check_matrix("logits", logits, ld, T, V, f32);
+  if (st != AXONN_OK) return st;
+  *rows = axonn::LogitRows{logits, ld, keep, T, V, temperature, f32 ? 1 : 0};
+  return AXONN_OK;
+}
+
+// Their gradient, which may be the logits themselves.
+axonn_status_t check_dlogits(const axonn::LogitRows& rows, const void* d, int64_t ld) {
+  const axonn_status_t st = check_matrix("dlogits", d, ld, rows.rows, rows.vocab, rows.f32 != 0);
+  if (st != AXONN_OK) return st;
+  if (d == rows.logits && ld != rows.ld && rows.rows > 1)
+    return fail(AXONN_ERR_INVALID_ARG, "dlogits is the logits' memory with another leading dimension");
+  return AXONN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1744,6 +1773,105 @@ axonn_status_t axonn_fc_wgrad_zsharded(const void* X, const void* dY, void* cons
   }
   st = run_blocks(v, last, *dev, stream);
   if (st != AXONN_OK) return st;
+  return ok();
+}
+
+axonn_status_t axonn_token_logprobs(const void* logits, int64_t ld_logits, const int32_t* tokens,
+                                    const uint8_t* keep, int64_t T, int64_t V, float temperature,
+                                    uint32_t flags, float* logprob, float* entropy, float* lse, int32_t k,
+                                    int32_t* top_index, float* top_logprob, int64_t ld_top,
+                                    cudaStream_t stream) {
+  axonn::LogprobArgs a{};
+  axonn_status_t st = logit_rows(logits, ld_logits, keep, T, V, temperature, flags, &a.in);
+  if (st != AXONN_OK) return st;
+  if (T > 0 && (tokens == nullptr) != (logprob == nullptr))
+    return fail(AXONN_ERR_INVALID_ARG, "tokens and logprob go together");
+  if (k < 0 || k > V) return fail(AXONN_ERR_INVALID_ARG, "a list of %d entries of %lld", k, (long long)V);
+  if (k > axonn::kMaxTop) return fail(AXONN_ERR_UNSUPPORTED, "lists of more than %d entries", axonn::kMaxTop);
+  if (k == 0 && (top_index || top_logprob))
+    return fail(AXONN_ERR_INVALID_ARG, "top_index or top_logprob without k");
+  if (k > 0 && T > 0 && !top_index && !top_logprob)
+    return fail(AXONN_ERR_INVALID_ARG, "k without top_index or top_logprob");
+  if (k > 0 && ld_top < k)
+    return fail(AXONN_ERR_INVALID_ARG, "lists: leading dimension %lld < %d", (long long)ld_top, k);
+  if (T > 0 && !logprob && !entropy && !lse && k == 0) return fail(AXONN_ERR_INVALID_ARG, "no output is asked for");
+  if (T == 0) return ok();
+  DeviceState* dev = nullptr;
+  st = device_state(&dev);
+  if (st != AXONN_OK) return st;
+  a.tokens = tokens;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.lse = lse;
+  a.top_index = top_index;
+  a.top_logprob = top_logprob;
+  a.ld_top = ld_top;
+  a.k = k;
+  const cudaError_t e = axonn::logprobs_launch(a, dev->sms, g_pdl.load() != 0, stream);
+  if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "log probabilities: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+axonn_status_t axonn_token_logprobs_bwd(const void* logits, int64_t ld_logits, const int32_t* tokens,
+                                        const uint8_t* keep, int64_t T, int64_t V, float temperature,
+                                        uint32_t flags, const float* lse, const float* dlogprob,
+                                        const float* entropy, const float* dentropy, void* dlogits,
+                                        int64_t ld_dlogits, cudaStream_t stream) {
+  axonn::LogprobBwdArgs a{};
+  axonn_status_t st = logit_rows(logits, ld_logits, keep, T, V, temperature, flags, &a.in);
+  if (st == AXONN_OK) st = check_dlogits(a.in, dlogits, ld_dlogits);
+  if (st != AXONN_OK) return st;
+  if (T > 0 && !lse) return fail(AXONN_ERR_INVALID_ARG, "lse is NULL");
+  if (T > 0 && (tokens == nullptr) != (dlogprob == nullptr))
+    return fail(AXONN_ERR_INVALID_ARG, "tokens and dlogprob go together");
+  if (T > 0 && (entropy == nullptr) != (dentropy == nullptr))
+    return fail(AXONN_ERR_INVALID_ARG, "entropy and dentropy go together");
+  if (T > 0 && !dlogprob && !dentropy) return fail(AXONN_ERR_INVALID_ARG, "no gradient comes in");
+  if (T == 0) return ok();
+  DeviceState* dev = nullptr;
+  st = device_state(&dev);
+  if (st != AXONN_OK) return st;
+  a.tokens = tokens;
+  a.lse = lse;
+  a.dlogprob = dlogprob;
+  a.entropy = entropy;
+  a.dentropy = dentropy;
+  a.dlogits = dlogits;
+  a.ld_dlogits = ld_dlogits;
+  const cudaError_t e = axonn::logprobs_bwd_launch(a, g_pdl.load() != 0, stream);
+  if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "log probabilities, backward: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+axonn_status_t axonn_distill(const void* logits, int64_t ld_logits, const int32_t* top_index,
+                             const float* top_logit, int64_t ld_top, const uint8_t* keep, int64_t T, int64_t V,
+                             int32_t k, float temperature, float grad_scale, uint32_t flags, float* token_loss,
+                             float* loss, int32_t* kept, void* dlogits, int64_t ld_dlogits, cudaStream_t stream) {
+  axonn::DistillArgs a{};
+  axonn_status_t st = logit_rows(logits, ld_logits, keep, T, V, temperature, flags, &a.in);
+  if (st == AXONN_OK && dlogits) st = check_dlogits(a.in, dlogits, ld_dlogits);
+  if (st != AXONN_OK) return st;
+  if (!loss || !kept) return fail(AXONN_ERR_INVALID_ARG, "loss or kept is NULL");
+  if (T > 0 && (!top_index || !top_logit || !token_loss))
+    return fail(AXONN_ERR_INVALID_ARG, "top_index, top_logit or token_loss is NULL");
+  if (k < 1) return fail(AXONN_ERR_INVALID_ARG, "lists of %d entries", k);
+  if (k > axonn::kMaxList) return fail(AXONN_ERR_UNSUPPORTED, "lists of more than %d entries", axonn::kMaxList);
+  if (ld_top < k) return fail(AXONN_ERR_INVALID_ARG, "lists: leading dimension %lld < %d", (long long)ld_top, k);
+  DeviceState* dev = nullptr;
+  st = device_state(&dev);
+  if (st != AXONN_OK) return st;
+  a.top_index = top_index;
+  a.top_logit = top_logit;
+  a.ld_top = ld_top;
+  a.k = k;
+  a.grad_scale = grad_scale;
+  a.token_loss = token_loss;
+  a.loss = loss;
+  a.kept = kept;
+  a.dlogits = dlogits;
+  a.ld_dlogits = ld_dlogits;
+  const cudaError_t e = axonn::distill_launch(a, dev->sms, g_pdl.load() != 0, stream);
+  if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "distillation: %s", cudaGetErrorString(e));
   return ok();
 }
 

@@ -1,0 +1,194 @@
+"""The operators over rows of vocabulary logits, without a GPU: the 64-bit
+forms against torch and differences, and every refusal of the entry points
+(which comes before any device work)."""
+import numpy as np
+import pytest
+
+from oracle import vocab as vo
+
+FAKE = 0x10000000  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def fc():
+    from pmm_fc_layer_gb300 import build as _build
+    _build.build()
+    import pmm_fc_layer_gb300 as mod
+    mod.load()
+    return mod
+
+
+# ------------------------------------------------------------------ the 64-bit forms
+@pytest.mark.parametrize("tau", [1.0, 0.7, 2.0])
+def test_logprobs_against_torch(tau):
+    import torch
+    rng = np.random.default_rng(1)
+    x = rng.normal(size=(6, 50)) * 3
+    x[1, 10:] = -np.inf
+    x[2] = np.round(x[2])  # ties
+    tokens = np.array([3, 5, -100, 49, 50, 0])
+    got = vo.token_logprobs(x, tokens, np.array([1, 1, 1, 1, 1, 0]), tau, 7)
+    z = torch.from_numpy(x) / tau
+    logp = torch.log_softmax(z, dim=1).numpy()
+    want = [logp[0, 3], logp[1, 5], 0, logp[3, 49], 0, 0]
+    assert np.allclose(got["logprob"], want, rtol=1e-13, atol=0)
+    ent = torch.special.entr(torch.softmax(z, dim=1)).sum(1).numpy()
+    assert np.allclose(got["entropy"][:5], ent[:5], rtol=1e-12) and got["entropy"][5] == 0
+    assert np.allclose(got["lse"][:5], torch.logsumexp(z, 1).numpy()[:5], rtol=1e-13) and got["lse"][5] == 0
+    order = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :7].numpy()
+    assert np.array_equal(got["top_index"][:5], order[:5]) and (got["top_index"][5] == -1).all()
+    assert np.allclose(got["top_logprob"][:5], np.take_along_axis(logp, order, 1)[:5], rtol=1e-13)
+
+
+def test_rows_without_a_distribution():
+    x = np.array([[-np.inf, -np.inf], [np.nan, 1.0], [np.inf, 0.0], [0.0, -0.0]])
+    got = vo.token_logprobs(x, np.array([0, 1, 1, 1]), None, 1.0, 2)
+    assert got["lse"][0] == got["logprob"][0] == -np.inf and got["entropy"][0] == 0
+    assert np.isnan(got["lse"][1:3]).all() and np.isnan(got["entropy"][1:3]).all()
+    assert np.array_equal(got["top_index"], [[0, 1], [0, 1], [0, 1], [0, 1]])
+
+
+@pytest.mark.parametrize("tau", [1.0, 0.6])
+def test_logprobs_backward_against_differences(tau):
+    rng = np.random.default_rng(2)
+    x = rng.normal(size=(4, 6))
+    tokens = np.array([2, -1, 5, 0])
+    keep = np.array([1, 1, 1, 0])
+    g, h = rng.normal(size=4), rng.normal(size=4)
+    f = vo.token_logprobs(x, tokens, keep, tau)
+    d = vo.token_logprobs_bwd(x, f["lse"], tokens, g, f["entropy"], h, keep, tau)
+
+    def value():
+        r = vo.token_logprobs(x, tokens, keep, tau)
+        return (g * r["logprob"] + h * r["entropy"]).sum()
+    step = 1e-5
+    for at in np.ndindex(*x.shape):
+        old = x[at]
+        x[at] = old + step
+        up = value()
+        x[at] = old - step
+        down = value()
+        x[at] = old
+        assert abs((up - down) / (2 * step) - d[at]) < 1e-8  # step^2 f'''/6, and 1e-16 / step
+
+
+@pytest.mark.parametrize("tau", [1.0, 2.5])
+def test_distill_against_differences_and_torch(tau):
+    import torch
+    rng = np.random.default_rng(3)
+    x = rng.normal(size=(6, 9))
+    at = np.array([[1, 4, 7], [3, 3, 0], [8, -1, 2], [-1, 0, 1], [5, 6, 9], [0, 1, 2]])
+    t = rng.normal(size=(6, 3))
+    t[4, 1] = -np.inf
+    keep = np.array([1, 1, 1, 1, 1, 0])
+    r = vo.distill(x, at, t, keep, tau, 1.5)
+    assert r["n"] == 4 and np.array_equal(r["counted"], [1, 1, 1, 0, 1, 0])
+    # row 0 in torch's own words
+    q = torch.softmax(torch.from_numpy(t[0]) / tau, 0)
+    logp = torch.log_softmax(torch.from_numpy(x[0]) / tau, 0)[at[0]]
+    kl = torch.nn.functional.kl_div(logp, q, reduction="sum")
+    assert abs(r["token_loss"][0] - float(kl) * tau**2) < 1e-13
+    # lists of one entry: cross entropy at the temperature
+    assert abs(r["token_loss"][2] + tau**2 * vo.log_softmax(x, tau)[2, 8]) < 1e-13
+    step = 1e-5
+    for i in np.ndindex(*x.shape):
+        old = x[i]
+        x[i] = old + step
+        up = vo.distill(x, at, t, keep, tau)["loss"]
+        x[i] = old - step
+        down = vo.distill(x, at, t, keep, tau)["loss"]
+        x[i] = old
+        assert abs(1.5 * (up - down) / (2 * step) - r["dlogits"][i]) < 1e-8
+
+
+# ------------------------------------------------------------------ refusals
+LOG = dict(logits=FAKE, ld=64, tokens=FAKE, keep=0, T=4, V=60, tau=1.0, flags=0, logprob=FAKE, entropy=0, lse=0,
+           k=0, top_index=0, top_logprob=0, ld_top=0, stream=0)
+BWD = dict(logits=FAKE, ld=64, tokens=FAKE, keep=0, T=4, V=60, tau=1.0, flags=0, lse=FAKE, dlogprob=FAKE, entropy=0,
+           dentropy=0, dlogits=FAKE, ld_d=64, stream=0)
+DIS = dict(logits=FAKE, ld=64, top_index=FAKE, top_logit=FAKE, ld_top=8, keep=0, T=4, V=60, k=8, tau=1.0, scale=1.0,
+           flags=0, token_loss=FAKE, loss=FAKE, kept=FAKE, dlogits=FAKE, ld_d=64, stream=0)
+COMMON = [
+    (dict(V=0), 1), (dict(V=-1), 1), (dict(T=-1), 1), (dict(T=1 << 31), 3), (dict(V=1 << 31, ld=1 << 31), 3),
+    (dict(tau=0.0), 1), (dict(tau=-1.0), 1), (dict(tau=float("nan")), 1), (dict(tau=float("inf")), 1),
+    (dict(tau=1e-5), 1), (dict(tau=1e5), 1), (dict(flags=0x20), 1), (dict(flags=0x2), 1),
+    (dict(logits=0), 1), (dict(logits=FAKE + 8), 2), (dict(ld=56), 1), (dict(ld=68), 2),
+    (dict(flags=0x400, ld=62), 2), (dict(ld=1 << 40), 3),
+]
+
+
+def refuse(fc, fn, base, change, expect):
+    st = getattr(fc.load(), fn)(*{**base, **change}.values())
+    assert st == expect, (change, fc.axonn_last_error())
+    assert fc.axonn_last_error()
+
+
+@pytest.mark.parametrize("fn,base", [("axonn_token_logprobs", LOG), ("axonn_token_logprobs_bwd", BWD),
+                                     ("axonn_distill", DIS)])
+@pytest.mark.parametrize("change,expect", COMMON)
+def test_common_refusals(fc, fn, base, change, expect):
+    refuse(fc, fn, base, change, expect)
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(tokens=0), 1), (dict(logprob=0), 1), (dict(tokens=0, logprob=0), 1),
+    (dict(k=-1), 1), (dict(k=61, top_index=FAKE, ld_top=61), 1),
+    (dict(V=1000, ld=1000, k=129, top_index=FAKE, ld_top=129), 3),
+    (dict(top_index=FAKE), 1), (dict(top_logprob=FAKE), 1), (dict(k=2, ld_top=2), 1),
+    (dict(k=8, top_index=FAKE, ld_top=7), 1),
+])
+def test_logprobs_refusals(fc, change, expect):
+    refuse(fc, "axonn_token_logprobs", LOG, change, expect)
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(lse=0), 1), (dict(tokens=0), 1), (dict(dlogprob=0), 1), (dict(entropy=FAKE), 1), (dict(dentropy=FAKE), 1),
+    (dict(tokens=0, dlogprob=0), 1), (dict(dlogits=0), 1), (dict(dlogits=FAKE + 4), 2), (dict(ld_d=68), 2),
+    (dict(ld_d=56), 1), (dict(ld_d=72), 1),  # in place with another leading dimension
+])
+def test_backward_refusals(fc, change, expect):
+    refuse(fc, "axonn_token_logprobs_bwd", BWD, change, expect)
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(top_index=0), 1), (dict(top_logit=0), 1), (dict(token_loss=0), 1), (dict(loss=0), 1), (dict(kept=0), 1),
+    (dict(k=0), 1), (dict(k=-3), 1), (dict(k=1025, ld_top=1025), 3), (dict(ld_top=7), 1),
+    (dict(dlogits=FAKE + 2), 2), (dict(ld_d=60), 2), (dict(ld_d=72), 1),
+])
+def test_distill_refusals(fc, change, expect):
+    refuse(fc, "axonn_distill", DIS, change, expect)
+
+
+def test_binding_refuses_wrong_tensors(fc):
+    import torch
+    bf = torch.zeros(4, 64, dtype=torch.bfloat16)
+    f, i = torch.zeros(4), torch.zeros(4, dtype=torch.int32)
+    lists = torch.zeros(4, 8, dtype=torch.int32)
+    with pytest.raises(ValueError):  # memory that the GPU cannot reach
+        fc.axonn_token_logprobs(bf, tokens=i, logprob=f)
+    with pytest.raises(ValueError):  # half precision
+        fc.axonn_token_logprobs(bf.half(), tokens=i, logprob=f)
+    with pytest.raises(ValueError):  # 64-bit indices
+        fc.axonn_token_logprobs(bf, top_index=lists.long())
+    with pytest.raises(ValueError):
+        fc.axonn_token_logprobs_bwd(bf, f, bf.float(), tokens=i, dlogprob=f)
+    with pytest.raises(ValueError):
+        fc.axonn_distill(bf, lists, torch.zeros(4, 7), f, f[:1], i[:1])
+
+
+def test_binding_refuses_other_devices(fc, monkeypatch):
+    class Other:
+        """A tensor of device 1, as far as the check looks."""
+        shape, is_cuda, dtype = (4, 64), True, None
+
+        def get_device(self):
+            return 1
+
+    class Here(Other):
+        def get_device(self):
+            return 0
+    monkeypatch.setattr(fc, "_current_device", lambda: 0)
+    with pytest.raises(ValueError, match="not the current one"):
+        fc.axonn_token_logprobs(Other(), lse=Other())
+    with pytest.raises(ValueError, match="devices 0 and 1"):
+        fc.axonn_token_logprobs(Here(), lse=Other())
