@@ -22,6 +22,7 @@ namespace {
 
 constexpr float kRowLn2 = 0.6931471805599453f;
 constexpr unsigned kAll = 0xFFFFFFFFu;
+constexpr int kStatThreads = 256;
 
 template <typename T>
 __device__ __forceinline__ float logit_at(const T* p) {
@@ -37,9 +38,9 @@ struct RowSums {
   float m = -INFINITY, s = 0.0f, a = 0.0f;
 };
 
-// Adds eight logits.
+// Adds eight logits; returns the largest of them.
 template <bool kEntropy>
-__device__ __forceinline__ void add8(RowSums& r, const float (&x)[8], float c) {
+__device__ __forceinline__ float add8(RowSums& r, const float (&x)[8], float c) {
   const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
   if (top > r.m) {
     if (r.m > -INFINITY) {
@@ -70,6 +71,7 @@ __device__ __forceinline__ void add8(RowSums& r, const float (&x)[8], float c) {
     split(a, s0, s1);
     r.a += s0 + s1;
   }
+  return top;
 }
 
 // Joins two parts.  A part without a finite logit has S = 0, or NaN, which stays.
@@ -103,61 +105,141 @@ __device__ __forceinline__ RowSums join_block(RowSums r, float c, RowSums* parts
   return r;
 }
 
-// ------------------------------------------------------------------ logprobs
-constexpr int kStatThreads = 512;
-constexpr int kBatch = 4;  // vectors of eight a thread loads before it uses them
-
-// Adds a row's logits to the threads' parts: a thread every kThreads-th vector.
-template <bool kEntropy, int kThreads, typename T>
-__device__ __forceinline__ RowSums row_sums(const T* row, int64_t V, float c) {
-  RowSums r;
-  for (int64_t base = 8 * threadIdx.x; base < V; base += 8 * kThreads * kBatch) {
-    Vec8<T> v[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int64_t i = base + 8 * kThreads * u;
-      if (i < V) v[u].load(row + i, static_cast<int>(min(static_cast<int64_t>(8), V - i)));
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int64_t i = base + 8 * kThreads * u;
-      if (i < V) {
-        float x[8];
-        v[u].values(x);
-        if (V - i < 8) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j >= V - i) x[j] = -INFINITY;
-        }
-        add8<kEntropy>(r, x, c);
-      }
-    }
-  }
-  return r;
+// ------------------------------------------------------------------ shares of a row
+// A row is cut over the CTAs of a cluster, whole vectors of eight to each; the
+// last one has the row's last V mod 8 logits too.
+struct Share {
+  int first, end;  // its vectors
+  int tail;        // logits behind the last whole vector, or 0
+  int64_t tail_at;
+};
+__device__ __forceinline__ Share share_of(int64_t V) {
+  const int whole = static_cast<int>(V >> 3), ctas = static_cast<int>(cluster_nctarank());
+  const int rank = static_cast<int>(cluster_ctarank()), each = (whole + ctas - 1) / ctas;
+  Share s;
+  s.first = min(whole, rank * each);
+  s.end = min(whole, s.first + each);
+  s.tail = rank == ctas - 1 ? static_cast<int>(V & 7) : 0;
+  s.tail_at = V & ~static_cast<int64_t>(7);
+  return s;
 }
 
+// The halves of a cluster's barrier: CTAs must have begun before their shared
+// memory is written to, which the first pair makes sure of at no cost.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Writes into the shared memory of a CTA of the cluster.
+__device__ __forceinline__ void put_remote(const RowSums* at, int rank, const RowSums& r) {
+  const uint32_t a = mapa_shared(smem_addr(at), static_cast<uint32_t>(rank));
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(r.m) : "memory");
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 4), "f"(r.s) : "memory");
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a + 8), "f"(r.a) : "memory");
+}
+__device__ __forceinline__ void put_remote(const uint64_t* at, int rank, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_addr(at), static_cast<uint32_t>(rank))),
+               "l"(v)
+               : "memory");
+}
+
+constexpr int kMaxCluster = 8;
+constexpr int kUnroll = 2;  // vectors a thread loads at a time; the next ones are on their way meanwhile
+
+// Streams a share: f(logits, vector) for every whole vector, a thread every
+// kThreads-th, ascending; next(batch) before each batch of kUnroll of them.
+template <int kThreads, typename T, class Next, class F>
+__device__ __forceinline__ void stream_share(const T* row, const Share& sh, Next&& next, F&& f) {
+  constexpr int kStep = kThreads * kUnroll;
+  auto load = [&](Vec8<T>(&v)[kUnroll], int i0) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (i0 + kThreads * u < sh.end) v[u].load(row + static_cast<int64_t>(i0 + kThreads * u) * 8, 8);
+  };
+  auto use = [&](const Vec8<T>(&v)[kUnroll], int i0) {
+    next(i0);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (i0 + kThreads * u < sh.end) {
+        float x[8];
+        v[u].values(x);
+        f(x, i0 + kThreads * u);
+      }
+  };
+  Vec8<T> v[kUnroll], w[kUnroll];
+  int i = sh.first + static_cast<int>(threadIdx.x);
+  load(v, i);
+  while (i < sh.end) {
+    load(w, i + kStep);
+    use(v, i);
+    i += kStep;
+    if (i >= sh.end) break;
+    load(v, i + kStep);
+    use(w, i);
+    i += kStep;
+  }
+}
+
+// The eight places of a share's tail; -inf where there is none.
+template <typename T>
+__device__ __forceinline__ void tail_values(const T* row, const Share& sh, float (&x)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = j < sh.tail ? logit_at(row + sh.tail_at + j) : -INFINITY;
+}
+
+// ------------------------------------------------------------------ lists
 // The order of a list as whole numbers: a NaN above every number, -0 as 0,
 // and of equal logits the lower index first.  0 is below every entry, and
 // 2^64 - 1 above.
 constexpr uint32_t kNanKey = 0xFFC00000u;  // an infinity's is 0xFF800000
-__device__ __forceinline__ uint64_t rank_of(float x, int64_t index) {
+__device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
-  const uint32_t key = x != x ? kNanKey : b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
-  return (static_cast<uint64_t>(key) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(index));
+  return x != x ? kNanKey : b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
-__device__ __forceinline__ int64_t rank_index(uint64_t r) { return 0xFFFFFFFFu - static_cast<uint32_t>(r); }
+__device__ __forceinline__ uint64_t rank_of(uint32_t key, uint32_t index) {
+  return (static_cast<uint64_t>(key) << 32) | (0xFFFFFFFFu - index);
+}
+__device__ __forceinline__ uint32_t rank_index(uint64_t r) { return 0xFFFFFFFFu - static_cast<uint32_t>(r); }
 __device__ __forceinline__ float rank_value(uint64_t r) {
   const uint32_t key = static_cast<uint32_t>(r >> 32);
   if (key == kNanKey) return __uint_as_float(0x7FC00000u);
   return __uint_as_float((key >> 31) ? key ^ 0x80000000u : ~key);
 }
 
-// The largest entry of the row below `below`, known to every thread.
+// How the k largest of a share are found, in work that the logits' values do
+// not change: while it streams, a thread keeps for each of its kSegments
+// segments (vectors that follow each other in its own sequence) the largest
+// logit, as the rank of the last index of the first vector that has it.  A
+// segment has an entry at least that good, so the k-th best of these numbers
+// is a bound that k entries reach.  An entry that reaches it lies in a segment
+// that does: only those are read again, and what reaches the bound is the
+// candidates.  The bound is sought among the threads' best segments alone,
+// between the k-th and the (1.5 k + 4)-th.
+constexpr int kSegments = 8;
+
+template <int kThreads>
+struct TopShared {
+  union {
+    uint64_t segment[kSegments][kThreads];
+    uint64_t entry[kSegments * kThreads];  // the candidates, after the segments
+  };
+  uint16_t again[kSegments * kThreads];  // segments that reach the bound
+  uint64_t part[kThreads / 32];
+  uint64_t list[kMaxTop];
+  int segments, entries, listed;
+};
+
+// The largest entry of a share below `below`, known to every thread.
 template <int kThreads, typename T>
-__device__ __forceinline__ uint64_t next_entry(const T* row, int64_t V, uint64_t below, uint64_t* parts) {
+__device__ __noinline__ uint64_t next_entry(const T* row, const Share sh, uint64_t below, uint64_t* parts) {
   uint64_t best = 0;
-  for (int64_t i = threadIdx.x; i < V; i += kThreads) {
-    const uint64_t r = rank_of(logit_at(row + i), i);
+  const int64_t end = sh.tail ? sh.tail_at + sh.tail : static_cast<int64_t>(sh.end) * 8;
+  for (int64_t i = static_cast<int64_t>(sh.first) * 8 + threadIdx.x; i < end; i += kThreads) {
+    const uint64_t r = rank_of(key_of(logit_at(row + i)), static_cast<uint32_t>(i));
     if (r < below && r > best) best = r;
   }
 #pragma unroll
@@ -169,51 +251,288 @@ __device__ __forceinline__ uint64_t next_entry(const T* row, int64_t V, uint64_t
   return best;
 }
 
-template <typename T, bool kEntropy>
-__global__ void __launch_bounds__(kStatThreads) logprobs_kernel(const LogprobArgs p) {
+// A number that at least k (or else all) of the threads' numbers reach, and at
+// most `most` unless fewer numbers than k are not 0.  All are different, and
+// below `hi`.
+__device__ __forceinline__ uint64_t bound_of(uint64_t mine, int k, int most, uint64_t hi) {
+  int n = __syncthreads_count(mine != 0);
+  if (n <= most) return 1;
+  // downwards from hi in growing steps, then by halves: n reach lo, fewer than k hi
+  uint64_t lo = hi, step = static_cast<uint64_t>(1) << 50;
+  for (n = 0; n < k; step <<= 2) {
+    hi = lo;
+    lo = step < hi && step < (static_cast<uint64_t>(1) << 62) ? hi - step : 1;
+    n = __syncthreads_count(mine >= lo);
+  }
+  while (n > most && hi - lo > 1) {
+    const uint64_t mid = lo + (hi - lo) / 2;
+    const int at = __syncthreads_count(mine >= mid);
+    if (at >= k) {
+      lo = mid;
+      n = at;
+    } else {
+      hi = mid;
+    }
+  }
+  return lo;
+}
+
+// Leaves the k largest of n > k entries, all different, in sh.list.
+template <int kThreads>
+__device__ __noinline__ void cut_entries(TopShared<kThreads>& sh, int n, int k) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t lo = 1, hi = ~static_cast<uint64_t>(0);
+  int reach = n;
+  while (reach > k) {
+    const uint64_t mid = lo + (hi - lo) / 2;
+    int c = 0;
+    for (int i = threadIdx.x; i < n; i += kThreads) c += sh.entry[i] >= mid ? 1 : 0;
+    c = __reduce_add_sync(kAll, c);
+    if (lane == 0) sh.part[warp] = static_cast<uint64_t>(c);
+    __syncthreads();
+    c = 0;
+    for (int w = 0; w < kThreads / 32; ++w) c += static_cast<int>(sh.part[w]);
+    __syncthreads();
+    if (c >= k) {
+      lo = mid;
+      reach = c;
+    } else {
+      hi = mid;
+    }
+  }
+  for (int i = threadIdx.x; i < n; i += kThreads)
+    if (sh.entry[i] >= lo) sh.list[atomicAdd(&sh.listed, 1)] = sh.entry[i];
+  __syncthreads();
+}
+
+// The best segments of a share by whole-number order, for rows with a NaN,
+// which comparisons of floats pass over.
+template <int kThreads, typename T>
+__device__ __noinline__ uint64_t segments_of_nan(const T* row, const Share sh, int batches, TopShared<kThreads>& top) {
+  uint64_t best = 0;
+  for (int j = 0; j < kSegments; ++j) {
+    uint64_t seg = 0;
+    for (int b = 0; b < batches * kUnroll; ++b) {
+      const int i = sh.first + static_cast<int>(threadIdx.x) + kThreads * (j * batches * kUnroll + b);
+      if (i >= sh.end) break;
+      uint32_t key = 0;
+      for (int e = 0; e < 8; ++e) key = max(key, key_of(logit_at(row + static_cast<int64_t>(i) * 8 + e)));
+      seg = max(seg, rank_of(key, static_cast<uint32_t>(i) * 8u + 7u));
+    }
+    top.segment[j][threadIdx.x] = seg;
+    best = max(best, seg);
+  }
+  __syncthreads();
+  return best;
+}
+
+// ------------------------------------------------------------------ logprobs
+// A cluster takes a row, a CTA a share of it.  Each CTA sums its share and
+// finds its own list; they meet in the shared memory of the cluster's first
+// CTA, which joins them in order and writes.
+template <typename T, bool kEntropy, bool kTop, int kThreads, int kResident>
+__global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const LogprobArgs p) {
   griddep_launch_dependents();
   griddep_wait();
-  __shared__ RowSums parts[kStatThreads / 32];
-  __shared__ uint64_t best[kStatThreads / 32];
+  constexpr int kWarps = kThreads / 32;
+  __shared__ RowSums parts[kWarps];
+  __shared__ RowSums shares[kMaxCluster];                        // the first CTA's: the others' sums
+  __shared__ uint64_t lists[kTop ? kMaxCluster * kMaxTop : 1];   // and lists, each in order
+  __shared__ TopShared<kTop ? kThreads : 32> top;
   const int64_t V = p.in.vocab;
+  const int64_t t = cluster_id_x();
+  const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
+  const int tid = static_cast<int>(threadIdx.x);
   const float inv = 1.0f / p.in.temperature, c = kEpiLog2e * inv;
-  for (int64_t t = blockIdx.x; t < p.in.rows; t += gridDim.x) {
-    if (p.in.keep && p.in.keep[t] == 0) {
-      if (threadIdx.x == 0) {
-        if (p.logprob) p.logprob[t] = 0.0f;
-        if (p.entropy) p.entropy[t] = 0.0f;
-        if (p.lse) p.lse[t] = 0.0f;
-      }
-      for (int j = threadIdx.x; j < p.k; j += kStatThreads) {
-        if (p.top_index) p.top_index[t * p.ld_top + j] = -1;
-        if (p.top_logprob) p.top_logprob[t * p.ld_top + j] = 0.0f;
-      }
-      continue;
+  if (p.in.keep && p.in.keep[t] == 0) {
+    if (rank != 0) return;
+    if (tid == 0) {
+      if (p.logprob) p.logprob[t] = 0.0f;
+      if (p.entropy) p.entropy[t] = 0.0f;
+      if (p.lse) p.lse[t] = 0.0f;
     }
-    const T* row = static_cast<const T*>(p.in.logits) + t * p.in.ld;
-    const RowSums r = join_block<kEntropy, kStatThreads / 32>(row_sums<kEntropy, kStatThreads>(row, V, c), c, parts);
-    const float log2s = log2f(r.s), lns = log2s * kRowLn2;  // -inf for a row of -inf
-    // ln p of a logit x, which may be as far below the maximum as fp32 reaches
-    auto lnp = [&](float x) {
-      return r.s == 0.0f ? -INFINITY : fmaf(x - r.m, inv, -lns);
+    for (int j = tid; j < p.k; j += kThreads) {
+      if (p.top_index) p.top_index[t * p.ld_top + j] = -1;
+      if (p.top_logprob) p.top_logprob[t * p.ld_top + j] = 0.0f;
+    }
+    return;
+  }
+  if (ctas > 1) cluster_arrive();
+  const T* row = static_cast<const T*>(p.in.logits) + t * p.in.ld;
+  const Share sh = share_of(V);
+  float own = -INFINITY;  // the token's logit
+  bool inside = false;
+  if (rank == 0 && tid == 0 && p.logprob) {
+    const int32_t y = p.tokens[t];
+    inside = y >= 0 && y < V;
+    if (inside) own = logit_at(row + y);
+  }
+
+  // the sums, and the largest logit of each segment
+  RowSums r;
+  uint64_t best = 0;
+  int batches = 1;  // of a segment, a power of two
+  if constexpr (kTop) {
+    const int all = (sh.end - sh.first + kThreads * kUnroll - 1) / (kThreads * kUnroll);
+    while (batches * kSegments < all) batches *= 2;
+    if (tid == 0) top.segments = top.entries = top.listed = 0;
+    float seg_m = -INFINITY;
+    int seg_at = 0, j = -1, left = 0;
+    auto flush = [&]() {
+      const uint64_t seg = rank_of(key_of(seg_m), static_cast<uint32_t>(seg_at) * 8u + 7u);
+      top.segment[j][tid] = seg;
+      best = max(best, seg);
     };
-    if (threadIdx.x == 0) {
-      if (p.logprob) {
-        const int32_t y = p.tokens[t];
-        p.logprob[t] = y >= 0 && y < V ? lnp(logit_at(row + y)) : 0.0f;
-      }
-      if (p.lse) p.lse[t] = fmaf(r.m, inv, lns);
-      if (kEntropy) p.entropy[t] = r.s == 0.0f ? 0.0f : (log2s - r.a / r.s) * kRowLn2;
+    stream_share<kThreads>(
+        row, sh,
+        [&](int i) {
+          if (left == 0) {
+            if (j >= 0) flush();
+            ++j;
+            left = batches;
+            seg_m = -INFINITY;
+            seg_at = i;
+          }
+          --left;
+        },
+        [&](const float(&x)[8], int i) {
+          const float m = add8<kEntropy>(r, x, c);
+          if (m > seg_m) {
+            seg_m = m;
+            seg_at = i;
+          }
+        });
+    if (j >= 0) flush();
+    for (++j; j < kSegments; ++j) top.segment[j][tid] = 0;
+  } else {
+    stream_share<kThreads>(row, sh, [](int) {}, [&](const float(&x)[8], int) { add8<kEntropy>(r, x, c); });
+  }
+  if (sh.tail && tid == kThreads - 1) {
+    float x[8];
+    tail_values(row, sh, x);
+    add8<kEntropy>(r, x, c);
+  }
+  r = join_block<kEntropy, kWarps>(r, c, parts);
+
+  if (ctas > 1) {
+    cluster_wait();  // every CTA has begun
+    if (tid == 0) put_remote(&shares[rank], 0, r);
+  }
+  if constexpr (kTop) {
+    const int64_t have = static_cast<int64_t>(sh.end - sh.first) * 8 + sh.tail;
+    const int k = static_cast<int>(min(static_cast<int64_t>(p.k), have));  // of this share
+    uint64_t hi = rank_of(key_of(r.m), 0) + 1;
+    if (r.s != r.s) {
+      best = segments_of_nan<kThreads>(row, sh, batches, top);
+      hi = ~static_cast<uint64_t>(0);
     }
-    uint64_t at = ~static_cast<uint64_t>(0);
-    for (int j = 0; j < p.k; ++j) {
-      at = next_entry<kStatThreads>(row, V, at, best);
-      if (threadIdx.x == 0) {
-        if (p.top_index) p.top_index[t * p.ld_top + j] = static_cast<int32_t>(rank_index(at));
-        if (p.top_logprob) p.top_logprob[t * p.ld_top + j] = lnp(rank_value(at));
+    const uint64_t bound = bound_of(best, k, k + k / 2 + 4, hi);
+    unsigned reach = 0;
+#pragma unroll
+    for (int j = 0; j < kSegments; ++j)
+      if (best >= bound && top.segment[j][tid] >= bound) reach |= 1u << j;
+    for (; reach; reach &= reach - 1)
+      top.again[atomicAdd(&top.segments, 1)] = static_cast<uint16_t>((__ffs(static_cast<int>(reach)) - 1) * kThreads + tid);
+    __syncthreads();
+    // from here the segments' memory takes the candidates
+    constexpr int kRoom = kSegments * kThreads;
+    auto offer = [&](float x, int64_t at) {
+      const uint64_t e = rank_of(key_of(x), static_cast<uint32_t>(at));
+      if (e >= bound) {
+        const int place = atomicAdd(&top.entries, 1);
+        if (place < kRoom) top.entry[place] = e;
+      }
+    };
+    const int each = __ffs(batches * kUnroll) - 1;  // log2 of a segment's vectors
+    for (int w = tid; w < top.segments << each; w += kThreads) {
+      const int s = top.again[w >> each], j = s / kThreads;
+      const int i = sh.first + s % kThreads + kThreads * ((j << each) + (w & ((1 << each) - 1)));
+      if (i < sh.end) {
+        Vec8<T> v;
+        v.load(row + static_cast<int64_t>(i) * 8, 8);
+        float x[8];
+        v.values(x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) offer(x[e], static_cast<int64_t>(i) * 8 + e);
       }
     }
-    __syncthreads();  // parts and best are written again for the next row
+    if (tid < sh.tail) offer(logit_at(row + sh.tail_at + tid), sh.tail_at + tid);
+    __syncthreads();
+    int n = top.entries;
+    const uint64_t* entry = top.entry;
+    if (n > kRoom) {
+      // more candidates than there is room for (a share of which a few segments
+      // hold nearly everything that is large): one by one
+      uint64_t at = ~static_cast<uint64_t>(0);
+      for (int j = 0; j < k; ++j) {
+        at = next_entry<kThreads>(row, sh, at, top.part);
+        if (tid == 0) top.list[j] = at;
+      }
+      __syncthreads();
+      n = k;
+      entry = top.list;
+    } else if (n > kThreads) {
+      cut_entries(top, n, k);
+      n = k;
+      entry = top.list;
+    }
+    // each candidate's place is the number of larger ones
+    const float lns = log2f(r.s) * kRowLn2;
+    auto write = [&](int place, uint64_t e, float m, float s, float ln_s) {
+      const int64_t at = t * p.ld_top + place;
+      if (p.top_index) p.top_index[at] = static_cast<int32_t>(rank_index(e));
+      // as far below the maximum as fp32 reaches
+      if (p.top_logprob) p.top_logprob[at] = s == 0.0f ? -INFINITY : fmaf(rank_value(e) - m, inv, -ln_s);
+    };
+    if (tid < n) {
+      const uint64_t e = entry[tid];
+      int place = 0;
+#pragma unroll 4
+      for (int i = 0; i < n; ++i) place += entry[i] > e ? 1 : 0;
+      if (place < k) {
+        if (ctas == 1) write(place, e, r.m, r.s, lns);
+        else put_remote(&lists[rank * p.k + place], 0, e);
+      }
+    }
+    if (ctas > 1) {
+      for (int j = k + tid; j < p.k; j += kThreads) put_remote(&lists[rank * p.k + j], 0, 0);
+      __syncwarp();
+      cluster_sync();
+      if (rank != 0) return;
+      r = shares[0];
+      for (int i = 1; i < ctas; ++i) join<kEntropy>(r, shares[i], c);
+      const float ln_s = log2f(r.s) * kRowLn2;
+      // an entry's place: its own in its list, and those before it in the others
+      for (int i = tid; i < ctas * p.k; i += kThreads) {
+        const uint64_t e = lists[i];
+        const int of = i / p.k;
+        int place = i - of * p.k;
+        if (e == 0) continue;
+        for (int l = 0; l < ctas; ++l) {
+          if (l == of) continue;
+          int before = 0, behind = p.k;  // entries above e: a prefix of the list
+          while (before < behind) {
+            const int mid = (before + behind) / 2;
+            if (lists[l * p.k + mid] > e) before = mid + 1;
+            else behind = mid;
+          }
+          place += before;
+        }
+        if (place < p.k) write(place, e, r.m, r.s, ln_s);
+      }
+    }
+  } else if (ctas > 1) {
+    __syncwarp();
+    cluster_sync();
+    if (rank != 0) return;
+    r = shares[0];
+    for (int i = 1; i < ctas; ++i) join<kEntropy>(r, shares[i], c);
+  }
+  if (tid == 0) {
+    const float log2s = log2f(r.s), lns = log2s * kRowLn2;  // -inf for a row of -inf
+    if (p.logprob) p.logprob[t] = !inside ? 0.0f : r.s == 0.0f ? -INFINITY : fmaf(own - r.m, inv, -lns);
+    if (p.lse) p.lse[t] = fmaf(r.m, inv, lns);
+    if (kEntropy) p.entropy[t] = r.s == 0.0f ? 0.0f : (log2s - r.a / r.s) * kRowLn2;
   }
 }
 
@@ -306,6 +625,36 @@ __global__ void __launch_bounds__(1024) distill_count_kernel(const DistillArgs p
 }
 
 constexpr int kDistThreads = 512;
+constexpr int kBatch = 4;  // vectors of eight a thread loads before it uses them
+
+// Adds a row's logits to the threads' parts: a thread every kThreads-th vector.
+template <bool kEntropy, int kThreads, typename T>
+__device__ __forceinline__ RowSums row_sums(const T* row, int64_t V, float c) {
+  RowSums r;
+  for (int64_t base = 8 * threadIdx.x; base < V; base += 8 * kThreads * kBatch) {
+    Vec8<T> v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t i = base + 8 * kThreads * u;
+      if (i < V) v[u].load(row + i, static_cast<int>(min(static_cast<int64_t>(8), V - i)));
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t i = base + 8 * kThreads * u;
+      if (i < V) {
+        float x[8];
+        v[u].values(x);
+        if (V - i < 8) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j >= V - i) x[j] = -INFINITY;
+        }
+        add8<kEntropy>(r, x, c);
+      }
+    }
+  }
+  return r;
+}
 
 // The sums of the row's softmax and of the list's, the row's loss, and (in a
 // second pass over the row, which L2 still has) the gradient: p everywhere,
@@ -428,14 +777,27 @@ __global__ void __launch_bounds__(kDistThreads) distill_kernel(const DistillArgs
   }
 }
 
+// CTAs a row: as many as fill the GPU's places a few times over, each with
+// some thousands of logits.
+int row_cluster(int64_t rows, int64_t vocab, int sms) {
+  int cluster = 1;
+  while (cluster < kMaxCluster && rows * cluster < int64_t{12} * sms && vocab / (2 * cluster) >= 4096) cluster *= 2;
+  return cluster;
+}
+
 }  // namespace
 
 cudaError_t logprobs_launch(const LogprobArgs& a, int sms, bool pdl, cudaStream_t stream) {
-  (void)sms;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.in.rows, INT32_MAX)));
-  auto kernel = a.in.f32 ? (a.entropy ? logprobs_kernel<float, true> : logprobs_kernel<float, false>)
-                         : (a.entropy ? logprobs_kernel<uint16_t, true> : logprobs_kernel<uint16_t, false>);
-  return launch_after(kernel, grid, kStatThreads, pdl, stream, a);
+  const int cluster = row_cluster(a.in.rows, a.in.vocab, sms);
+  const dim3 grid(static_cast<unsigned>(a.in.rows * cluster));
+  const int which = (a.in.f32 ? 4 : 0) + (a.entropy ? 2 : 0) + (a.k > 0 ? 1 : 0);
+  using Kernel = void (*)(LogprobArgs);
+  static constexpr Kernel kKernels[8] = {
+      logprobs_kernel<uint16_t, false, false, kStatThreads, 6>, logprobs_kernel<uint16_t, false, true, kStatThreads, 5>,
+      logprobs_kernel<uint16_t, true, false, kStatThreads, 5>,  logprobs_kernel<uint16_t, true, true, kStatThreads, 4>,
+      logprobs_kernel<float, false, false, kStatThreads, 4>,    logprobs_kernel<float, false, true, kStatThreads, 4>,
+      logprobs_kernel<float, true, false, kStatThreads, 4>,     logprobs_kernel<float, true, true, kStatThreads, 4>};
+  return launch_clusters(kKernels[which], grid, static_cast<unsigned>(cluster), kStatThreads, pdl, stream, a);
 }
 
 cudaError_t logprobs_bwd_launch(const LogprobBwdArgs& a, bool pdl, cudaStream_t stream) {

@@ -216,6 +216,21 @@ def test_logprobs_special_rows(cuda_lib, V, kind, k):
     check_logprobs({n: v[fine] for n, v in got.items()}, x[fine], tokens[fine], None, 1.0, k)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [3, 2000])
+def test_lists_of_rows_with_what_is_large_in_a_few_threads(cuda_lib, T, kind):
+    """More logits reach the bound that the threads' best give than a block
+    holds: one vector of eight in four, at a stride that gives them to 60
+    threads."""
+    V, k = 65541, 100
+    rng = np.random.default_rng(15)
+    x = rng.normal(size=(3, V)) + np.where(np.arange(V) // 8 % 256 < 60, 9.0, 0.0)
+    x = stored(np.repeat(x, T // 3 + 1, axis=0)[:T], kind)
+    got = run_logprobs(cuda_lib, x, kind, np.zeros(T, int), k=k)
+    pick = np.unique([0, 1, 2, T // 2, T - 1])
+    check_logprobs({n: v[pick] for n, v in got.items()}, x[pick], np.zeros(len(pick), int), k=k)
+
+
 def test_logprobs_each_output_alone(cuda_lib):
     import torch
     x, tokens, _ = logits_of(6, 3001, "bf16", seed=3)
