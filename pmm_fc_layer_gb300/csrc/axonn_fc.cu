@@ -89,6 +89,7 @@ struct DeviceState {
   int fused_clusters[9] = {};
   bool attrs_set = false;
   std::atomic<bool> fused_set{false};  // fused_clusters and the fused kernels' attributes
+  std::atomic<bool> distill_set{false};  // the distillation kernels' attributes
 };
 
 // Per-device state lives in a fixed table so that pointers handed out stay
@@ -186,7 +187,20 @@ axonn_status_t fused_state(DeviceState** out) {
   return AXONN_OK;
 }
 
-// Whether they have been set up on the current device.
+// The same for the distillation.
+axonn_status_t distill_state(DeviceState** out) {
+  const axonn_status_t st = device_state(out);
+  if (st != AXONN_OK) return st;
+  DeviceState& d = **out;
+  if (d.distill_set) return AXONN_OK;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  const cudaError_t e = axonn::distill_init();
+  if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "distillation kernel attributes: %s", cudaGetErrorString(e));
+  d.distill_set = true;
+  return AXONN_OK;
+}
+
+// Whether the fused kernels have been set up on the current device.
 bool fused_in_use() {
   int dev = 0;
   return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices && g_devs[dev].fused_set;
@@ -1858,7 +1872,7 @@ axonn_status_t axonn_distill(const void* logits, int64_t ld_logits, const int32_
   if (k > axonn::kMaxList) return fail(AXONN_ERR_UNSUPPORTED, "lists of more than %d entries", axonn::kMaxList);
   if (ld_top < k) return fail(AXONN_ERR_INVALID_ARG, "lists: leading dimension %lld < %d", (long long)ld_top, k);
   DeviceState* dev = nullptr;
-  st = device_state(&dev);
+  st = distill_state(&dev);
   if (st != AXONN_OK) return st;
   a.top_index = top_index;
   a.top_logit = top_logit;

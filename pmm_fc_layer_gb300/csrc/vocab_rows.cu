@@ -38,10 +38,12 @@ struct RowSums {
   float m = -INFINITY, s = 0.0f, a = 0.0f;
 };
 
-// Adds eight logits; returns the largest of them.
-template <bool kEntropy>
-__device__ __forceinline__ float add8(RowSums& r, const float (&x)[8], float c) {
-  const float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+// Adds N logits; returns the largest of them.
+template <bool kEntropy, int N>
+__device__ __forceinline__ float add(RowSums& r, const float (&x)[N], float c) {
+  float top = x[0];
+#pragma unroll
+  for (int j = 1; j < N; ++j) top = fmaxf(top, x[j]);
   if (top > r.m) {
     if (r.m > -INFINITY) {
       const float d = (r.m - top) * c, f = ex2_approx(d);
@@ -53,7 +55,7 @@ __device__ __forceinline__ float add8(RowSums& r, const float (&x)[8], float c) 
   const F2 m = f2(r.m > -INFINITY ? -r.m : 0.0f), c2 = f2(c);
   F2 s = f2(0.0f), a = f2(0.0f);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int j = 0; j < N / 2; ++j) {
     const F2 d = mul2(add2(f2(x[2 * j], x[2 * j + 1]), m), c2);
     const F2 e = ex2_2(d);
     s = add2(s, e);
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
           --left;
         },
         [&](const float(&x)[8], int i) {
-          const float m = add8<kEntropy>(r, x, c);
+          const float m = add<kEntropy>(r, x, c);
           if (m > seg_m) {
             seg_m = m;
             seg_at = i;
@@ -405,12 +407,12 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
     if (j >= 0) flush();
     for (++j; j < kSegments; ++j) top.segment[j][tid] = 0;
   } else {
-    stream_share<kThreads>(row, sh, [](int) {}, [&](const float(&x)[8], int) { add8<kEntropy>(r, x, c); });
+    stream_share<kThreads>(row, sh, [](int) {}, [&](const float(&x)[8], int) { add<kEntropy>(r, x, c); });
   }
   if (sh.tail && tid == kThreads - 1) {
     float x[8];
     tail_values(row, sh, x);
-    add8<kEntropy>(r, x, c);
+    add<kEntropy>(r, x, c);
   }
   r = join_block<kEntropy, kWarps>(r, c, parts);
 
@@ -624,155 +626,229 @@ __global__ void __launch_bounds__(1024) distill_count_kernel(const DistillArgs p
   }
 }
 
-constexpr int kDistThreads = 512;
-constexpr int kBatch = 4;  // vectors of eight a thread loads before it uses them
+constexpr int kDistThreads = 256;
+constexpr int kHeldBytes = 64 << 10;  // of a row that a CTA holds, where 8 CTAs can hold a row so
+constexpr int kMostHeld = 200 << 10;
 
-// Adds a row's logits to the threads' parts: a thread every kThreads-th vector.
-template <bool kEntropy, int kThreads, typename T>
-__device__ __forceinline__ RowSums row_sums(const T* row, int64_t V, float c) {
-  RowSums r;
-  for (int64_t base = 8 * threadIdx.x; base < V; base += 8 * kThreads * kBatch) {
-    Vec8<T> v[kBatch];
+// 16 bytes of a row: 8 bf16 or 4 fp32 logits.
+template <typename T>
+constexpr int kUnit = 16 / static_cast<int>(sizeof(T));
+template <typename T>
+__device__ __forceinline__ void unit_values(const uint4& v, float (&x)[kUnit<T>]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int64_t i = base + 8 * kThreads * u;
-      if (i < V) v[u].load(row + i, static_cast<int>(min(static_cast<int64_t>(8), V - i)));
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int64_t i = base + 8 * kThreads * u;
-      if (i < V) {
-        float x[8];
-        v[u].values(x);
-        if (V - i < 8) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j >= V - i) x[j] = -INFINITY;
-        }
-        add8<kEntropy>(r, x, c);
-      }
-    }
-  }
-  return r;
+  for (int j = 0; j < kUnit<T>; ++j)
+    x[j] = __uint_as_float(sizeof(T) == 4 ? w[j] : (j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
+}
+__device__ __forceinline__ uint4 unit_of(const float (&x)[8]) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+__device__ __forceinline__ uint4 unit_of(const float (&x)[4]) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
 
-// The sums of the row's softmax and of the list's, the row's loss, and (in a
-// second pass over the row, which L2 still has) the gradient: p everywhere,
-// then the list's entries, p - q, by the threads that have them.  The block
-// that finishes last adds up the losses in a fixed order.
-template <typename T>
-__global__ void __launch_bounds__(kDistThreads) distill_kernel(const DistillArgs p) {
+// Asynchronous copies of 16 bytes into shared memory, in groups of the thread
+// that asks for them.
+__device__ __forceinline__ void copy_unit(uint4* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// A cluster takes a row, a CTA a share of it, which it copies to its shared
+// memory (as much of it as there is room for: `room` units; a thread copies
+// what it will use itself, so nothing waits for another).  The softmax's sums
+// meet in every CTA's shared memory; then the gradient comes from the copy: p
+// everywhere, and the list's entries, p - q, by the threads that have them.
+// Without a gradient nothing is kept.  The row whose cluster finishes last
+// adds up the losses in a fixed order.
+template <typename T, bool kGrad>
+__global__ void __launch_bounds__(kDistThreads) distill_kernel(const DistillArgs p, int room) {
   griddep_launch_dependents();
   griddep_wait();
-  __shared__ RowSums parts[kDistThreads / 32];
-  __shared__ float list_q[kMaxList];       // log2 of the list's weights, then q
-  __shared__ float list_x[kMaxList];       // the row's logits there
-  __shared__ int32_t list_at[kMaxList];
+  constexpr int kWarps = kDistThreads / 32, kPer = kUnit<T>, kGroups = 4;
+  extern __shared__ __align__(16) uint4 held[];
+  __shared__ RowSums parts[kWarps];
+  __shared__ RowSums shares[kMaxCluster];  // of every CTA of the cluster
   __shared__ int length;
   __shared__ bool last, teaches;
+  float* list_q = reinterpret_cast<float*>(held + room);  // log2 of the list's weights, then q
+  float* list_x = list_q + p.k;                           // the row's logits there
+  int32_t* list_at = reinterpret_cast<int32_t*>(list_x + p.k);
   const int64_t V = p.in.vocab;
+  const int64_t t = cluster_id_x();
+  const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
+  const int tid = static_cast<int>(threadIdx.x);
   const float c = kEpiLog2e * (1.0f / p.in.temperature);
   const int n = *p.kept;
-  const float scale = n > 0 ? p.grad_scale * p.in.temperature / static_cast<float>(n) : 0.0f;
-  for (int64_t t = blockIdx.x; t < p.in.rows; t += gridDim.x) {
-    const T* row = static_cast<const T*>(p.in.logits) + t * p.in.ld;
-    T* out = p.dlogits ? static_cast<T*>(p.dlogits) + t * p.ld_dlogits : nullptr;
-    if (!row_counts(p, t)) {
-      if (threadIdx.x == 0) p.token_loss[t] = 0.0f;
-      if (out) {
-        const float none[8] = {};
-        for (int64_t i = 8 * threadIdx.x; i < V; i += 8 * kDistThreads)
-          store8(out + i, static_cast<int>(min(static_cast<int64_t>(8), V - i)), none);
+  const T* row = static_cast<const T*>(p.in.logits) + t * p.in.ld;
+  T* out = kGrad ? static_cast<T*>(p.dlogits) + t * p.ld_dlogits : nullptr;
+  const Share sh = share_of(V);
+  // the share in units; its logits are those from `lo` to before `hi`
+  const int units = (sh.end - sh.first) * (8 / kPer);
+  const int64_t lo = static_cast<int64_t>(sh.first) * 8, hi = sh.tail ? V : static_cast<int64_t>(sh.end) * 8;
+  const uint4* src = reinterpret_cast<const uint4*>(row + lo);
+  const bool counts = row_counts(p, t);
+  if (counts) {
+    if (ctas > 1) cluster_arrive();
+    if (tid == 0) length = p.k;
+    const int keep = kGrad ? min(units, room) : 0;
+    const int each = (keep + kGroups * kDistThreads - 1) / (kGroups * kDistThreads);  // units of a thread and group
+    if (kGrad) {
+#pragma unroll
+      for (int g = 0; g < kGroups; ++g) {
+        for (int e = 0; e < each; ++e) {
+          const int i = tid + kDistThreads * (g * each + e);
+          if (i < keep) copy_unit(held + i, src + i);
+        }
+        copy_commit();
       }
-      continue;
     }
-    if (threadIdx.x == 0) length = p.k;
     __syncthreads();
-    for (int j = threadIdx.x; j < p.k; j += kDistThreads) {
+    // the list; every CTA has all of it, with the logits that it needs: the
+    // first CTA all of them, for the loss
+    for (int j = tid; j < p.k; j += kDistThreads) {
       const int32_t at = p.top_index[t * p.ld_top + j];
       list_at[j] = at;
       if (at >= 0 && at < V) {
         list_q[j] = p.top_logit[t * p.ld_top + j];
-        list_x[j] = logit_at(row + at);
+        if (rank == 0 || (at >= lo && at < hi)) list_x[j] = logit_at(row + at);
       } else {
         atomicMin(&length, j);
       }
     }
-    const RowSums r = join_block<false, kDistThreads / 32>(row_sums<false, kDistThreads>(row, V, c), c, parts);
+    // the sums of the share: what is held as it arrives, the rest from memory
+    RowSums r;
+    auto take = [&](const uint4& v) {
+      float x[kPer];
+      unit_values<T>(v, x);
+      add<false>(r, x, c);
+    };
+    if (kGrad) {
+      auto take_group = [&](int g) {
+        for (int e = 0; e < each; ++e) {
+          const int i = tid + kDistThreads * (g * each + e);
+          if (i < keep) take(held[i]);
+        }
+      };
+      copy_wait<3>();
+      take_group(0);
+      copy_wait<2>();
+      take_group(1);
+      copy_wait<1>();
+      take_group(2);
+      copy_wait<0>();
+      take_group(3);
+      for (int i = keep + tid; i < units; i += kDistThreads) take(src[i]);
+    } else {
+      stream_share<kDistThreads>(row, sh, [](int) {}, [&](const float(&x)[8], int) { add<false>(r, x, c); });
+    }
+    if (sh.tail && tid == kDistThreads - 1) {
+      float x[8];
+      tail_values(row, sh, x);
+      add<false>(r, x, c);
+    }
+    r = join_block<false, kWarps>(r, c, parts);
+    if (ctas > 1) {
+      cluster_wait();  // every CTA has begun
+      if (tid < ctas) put_remote(&shares[rank], tid, r);
+      __syncwarp();
+      cluster_sync();
+      r = shares[0];
+      for (int i = 1; i < ctas; ++i) join<false>(r, shares[i], c);
+    }
     const int len = length;  // at least 1
-    const float log2s = log2f(r.s);
-    if (threadIdx.x < 32) {
+    if (tid < 32) {
       float top = -INFINITY;
-      for (int j = threadIdx.x; j < len; j += 32) top = fmaxf(top, list_q[j]);
+      for (int j = tid; j < len; j += 32) top = fmaxf(top, list_q[j]);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
       const float base = top > -INFINITY ? top : 0.0f;
       float sum = 0.0f;
-      for (int j = threadIdx.x; j < len; j += 32) {
+      for (int j = tid; j < len; j += 32) {
         const float d = (list_q[j] - base) * c;
         list_q[j] = d;
         sum += ex2_approx(d);
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(kAll, sum, o);
-      const float log2w = log2f(sum);
+      const float log2w = log2f(sum), log2s = log2f(r.s);
       float kl = 0.0f;
-      for (int j = threadIdx.x; j < len; j += 32) {
+      for (int j = tid; j < len; j += 32) {
         const float lq = list_q[j] - log2w;
         const float q = sum == 0.0f ? 0.0f : ex2_approx(list_q[j]) / sum;
-        const float lp = r.s == 0.0f ? -INFINITY : (list_x[j] - r.m) * c - log2s;
-        if (q != 0.0f) kl = fmaf(q, lq - lp, kl);
         list_q[j] = q;
+        if (rank == 0) {
+          const float lp = r.s == 0.0f ? -INFINITY : (list_x[j] - r.m) * c - log2s;
+          if (q != 0.0f) kl = fmaf(q, lq - lp, kl);
+        }
       }
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) kl += __shfl_xor_sync(kAll, kl, o);
-      if (threadIdx.x == 0) {
-        p.token_loss[t] = kl * (kRowLn2 * p.in.temperature * p.in.temperature);
+      if (tid == 0) {
+        if (rank == 0) p.token_loss[t] = kl * (kRowLn2 * p.in.temperature * p.in.temperature);
         teaches = sum != 0.0f;
       }
     }
-    __syncthreads();
-    if (out) {
+    if (kGrad) {
+      __syncthreads();
+      const float scale = p.grad_scale * p.in.temperature / static_cast<float>(n);
       const float share = r.s == 0.0f || !teaches ? 0.0f : scale / r.s;
       const float m = r.m > -INFINITY ? r.m : 0.0f;
-      for (int64_t i = 8 * threadIdx.x; i < V; i += 8 * kDistThreads) {
-        const int w = static_cast<int>(min(static_cast<int64_t>(8), V - i));
-        Vec8<T> v;
-        v.load(row + i, w);
-        float x[8];
-        v.values(x);
+      const F2 m2 = f2(-m), c2 = f2(c), share2 = f2(share);
+      uint4* dst = reinterpret_cast<uint4*>(out + lo);
+      auto give = [&](int i, const uint4& v) {
+        float x[kPer];
+        unit_values<T>(v, x);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = ex2_approx((x[j] - m) * c) * share;
-        store8(out + i, w, x);
-      }
+        for (int j = 0; j < kPer; j += 2)
+          split(mul2(ex2_2(mul2(add2(f2(x[j], x[j + 1]), m2), c2)), share2), x[j], x[j + 1]);
+        __stcs(dst + i, unit_of(x));
+      };
+#pragma unroll 4
+      for (int i = tid; i < keep; i += kDistThreads) give(i, held[i]);
+      for (int i = keep + tid; i < units; i += kDistThreads) give(i, src[i]);
+      if (tid < sh.tail)
+        put_logit(out + sh.tail_at + tid, ex2_approx((logit_at(row + sh.tail_at + tid) - m) * c) * share);
       __syncthreads();
-      for (int j = threadIdx.x; j < len; j += kDistThreads) {
+      for (int j = tid; j < len; j += kDistThreads) {
         const int32_t at = list_at[j];
+        if (at < lo || at >= hi) continue;
         float q = 0.0f;
         for (int i = 0; i < len; ++i)  // an index given twice teaches twice
           if (list_at[i] == at) q += list_q[i];
         put_logit(out + at, fmaf(ex2_approx((list_x[j] - m) * c), share, -scale * q));
       }
     }
-    __syncthreads();  // the shared arrays are written again for the next row
+  } else {
+    if (rank == 0 && tid == 0) p.token_loss[t] = 0.0f;
+    if (kGrad) {
+      uint4* dst = reinterpret_cast<uint4*>(out + lo);
+      for (int i = tid; i < units; i += kDistThreads) __stcs(dst + i, make_uint4(0, 0, 0, 0));
+      if (tid < sh.tail) put_logit(out + sh.tail_at + tid, 0.0f);
+    }
   }
-  // the mean: token_loss in order, by the block that finishes last
-  __shared__ float sums[kDistThreads / 32];
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(reinterpret_cast<unsigned*>(p.loss), 1u) == gridDim.x - 1;
+  if (rank != 0) return;
+  // the mean: token_loss in order, by the row that finishes last
+  if (tid == 0) {
+    __threadfence();
+    last = atomicAdd(reinterpret_cast<unsigned*>(p.loss), 1u) == static_cast<unsigned>(p.in.rows) - 1;
+  }
   __syncthreads();
   if (!last) return;
   __threadfence();
   float sum = 0.0f;
-  for (int64_t t = threadIdx.x; t < p.in.rows; t += kDistThreads) sum += __ldcg(p.token_loss + t);
+  for (int64_t i = tid; i < p.in.rows; i += kDistThreads) sum += __ldcg(p.token_loss + i);
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(kAll, sum, o);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = sum;
+  if ((tid & 31) == 0) parts[tid >> 5].s = sum;
   __syncthreads();
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     float total = 0.0f;
-    for (int w = 0; w < kDistThreads / 32; ++w) total += sums[w];
+    for (int w = 0; w < kWarps; ++w) total += parts[w].s;
     *p.loss = n > 0 ? total / static_cast<float>(n) : 0.0f;
   }
 }
@@ -797,7 +873,7 @@ cudaError_t logprobs_launch(const LogprobArgs& a, int sms, bool pdl, cudaStream_
       logprobs_kernel<uint16_t, true, false, kStatThreads, 5>,  logprobs_kernel<uint16_t, true, true, kStatThreads, 4>,
       logprobs_kernel<float, false, false, kStatThreads, 4>,    logprobs_kernel<float, false, true, kStatThreads, 4>,
       logprobs_kernel<float, true, false, kStatThreads, 4>,     logprobs_kernel<float, true, true, kStatThreads, 4>};
-  return launch_clusters(kKernels[which], grid, static_cast<unsigned>(cluster), kStatThreads, pdl, stream, a);
+  return launch_clusters(kKernels[which], grid, static_cast<unsigned>(cluster), kStatThreads, pdl, stream, 0, a);
 }
 
 cudaError_t logprobs_bwd_launch(const LogprobBwdArgs& a, bool pdl, cudaStream_t stream) {
@@ -808,12 +884,31 @@ cudaError_t logprobs_bwd_launch(const LogprobBwdArgs& a, bool pdl, cudaStream_t 
   return launch_after(kernel, grid, kBwdThreads, pdl, stream, a);
 }
 
+cudaError_t distill_init() {
+  for (auto kernel : {distill_kernel<float, true>, distill_kernel<uint16_t, true>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kMostHeld + 12 * kMaxList);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 cudaError_t distill_launch(const DistillArgs& a, int sms, bool pdl, cudaStream_t stream) {
-  (void)sms;
   const cudaError_t e = launch_after(distill_count_kernel, dim3(1), 1024, pdl, stream, a);
   if (e != cudaSuccess || a.in.rows == 0) return e;
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(a.in.rows, INT32_MAX)));
-  return launch_after(a.in.f32 ? distill_kernel<float> : distill_kernel<uint16_t>, grid, kDistThreads, pdl, stream, a);
+  int cluster = row_cluster(a.in.rows, a.in.vocab, sms);
+  int held = 0;
+  if (a.dlogits) {
+    const int64_t vectors = a.in.vocab / 8, bytes = a.in.f32 ? 32 : 16;
+    auto share = [&] { return (vectors + cluster - 1) / cluster * bytes; };
+    while (cluster < kMaxCluster && share() > kHeldBytes) cluster *= 2;
+    held = static_cast<int>(std::min<int64_t>(share(), kMostHeld));
+  }
+  const dim3 grid(static_cast<unsigned>(a.in.rows * cluster));
+  auto kernel = a.in.f32 ? (a.dlogits ? distill_kernel<float, true> : distill_kernel<float, false>)
+                         : (a.dlogits ? distill_kernel<uint16_t, true> : distill_kernel<uint16_t, false>);
+  return launch_clusters(kernel, grid, static_cast<unsigned>(cluster), kDistThreads, pdl, stream,
+                         static_cast<size_t>(held + 12 * a.k), a, held / 16);
 }
 
 }  // namespace axonn

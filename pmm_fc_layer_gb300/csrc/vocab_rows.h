@@ -62,6 +62,7 @@ struct DistillArgs {
 
 cudaError_t logprobs_launch(const LogprobArgs& a, int sms, bool pdl, cudaStream_t stream);
 cudaError_t logprobs_bwd_launch(const LogprobBwdArgs& a, bool pdl, cudaStream_t stream);
+cudaError_t distill_init();  // once for each device, before the first launch
 cudaError_t distill_launch(const DistillArgs& a, int sms, bool pdl, cudaStream_t stream);
 
 }  // namespace axonn
