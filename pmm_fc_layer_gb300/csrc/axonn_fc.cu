@@ -200,10 +200,11 @@ axonn_status_t distill_state(DeviceState** out) {
   return AXONN_OK;
 }
 
-// Whether the fused kernels have been set up on the current device.
-bool fused_in_use() {
+// Whether kernels that are set up at their first call have been, on the
+// current device.
+bool in_use(std::atomic<bool> DeviceState::*set) {
   int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices && g_devs[dev].fused_set;
+  return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kMaxDevices && g_devs[dev].*set;
 }
 
 // ------------------------------------------------------------------ grid
@@ -1884,7 +1885,8 @@ axonn_status_t axonn_distill(const void* logits, int64_t ld_logits, const int32_
   a.kept = kept;
   a.dlogits = dlogits;
   a.ld_dlogits = ld_dlogits;
-  const cudaError_t e = axonn::distill_launch(a, dev->sms, g_pdl.load() != 0, stream);
+  const cudaError_t e = axonn::distill_launch(a, dev->sms, g_timeout_ns.load(), g_inject.load(), g_pdl.load() != 0,
+                                              stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "distillation: %s", cudaGetErrorString(e));
   return ok();
 }
@@ -2647,19 +2649,20 @@ axonn_status_t axonn_sync_status(cudaStream_t stream, uint64_t* detail) {
   cudaError_t e = cudaStreamSynchronize(stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "stream: %s", cudaGetErrorString(e));
   // One error word per kernel translation unit, a device-to-host copy each;
-  // report the first set.  Fused kernels that were never set up on this device
-  // have not run there.
-  const bool fused = fused_in_use();
+  // report the first set.  Fused kernels and distillations that were never set up
+  // on this device have not run there.
+  const bool fused = in_use(&DeviceState::fused_set), distill = in_use(&DeviceState::distill_set);
   unsigned long long word = 0, w1 = 0, w8 = 0, w64 = 0;
-  unsigned long long wg = 0, we = 0, wc = 0;
+  unsigned long long wg = 0, we = 0, wc = 0, wd = 0;
   e = axonn::kernels_take_status<1>(&w1, stream);
   if (e == cudaSuccess) e = axonn::kernels_take_status<kFewProblems>(&w8, stream);
   if (e == cudaSuccess) e = axonn::kernels_take_status<kMaxProblems>(&w64, stream);
   if (e == cudaSuccess) e = axonn::goldfish_take_status(&wg, stream);
   if (e == cudaSuccess && fused) e = axonn::fused_take_status(&we, stream);
   if (e == cudaSuccess && fused) e = axonn::ce_take_status(&wc, stream);
+  if (e == cudaSuccess && distill) e = axonn::distill_take_status(&wd, stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
-  for (unsigned long long w : {w1, w8, w64, wg, we, wc})
+  for (unsigned long long w : {w1, w8, w64, wg, we, wc, wd})
     if (word == 0) word = w;
   if (word == 0) return ok();
   if (detail) *detail = word;

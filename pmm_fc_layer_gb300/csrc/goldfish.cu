@@ -85,18 +85,6 @@ __device__ __forceinline__ bool gf_wait(uint32_t bar, uint32_t parity, uint64_t 
   }
 }
 
-// 1-D bulk copy global -> this CTA's shared memory with an L2 cache policy,
-// completion counted on `bar` in bytes (both addresses 16-byte aligned, size
-// a multiple of 16).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1], %2, [%3], %4;" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "l"(policy)
-      : "memory");
-}
-
 // Bounded wait of a whole warp: lane 0 polls, then every lane tests the
 // completed phase once (each lane's own acquire of the data it guards).  The
 // barriers waited on this way cannot complete their next phase before this
@@ -108,13 +96,6 @@ __device__ __forceinline__ bool gf_warp_wait(uint32_t bar, uint32_t parity, uint
   got = __shfl_sync(0xFFFFFFFFu, got, 0) != 0;
   if (got) (void)mbar_test_wait(bar, parity);
   return got;
-}
-
-// L2 policy marking every line of an access evict-first.
-__device__ __forceinline__ uint64_t evict_first_policy() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
-  return p;
 }
 
 // 1-D bulk copy of this CTA's shared memory to global memory with an L2

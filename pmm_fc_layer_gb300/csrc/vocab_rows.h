@@ -1,5 +1,5 @@
 // Host interface of the kernels over rows of vocabulary logits
-// (vocab_rows.cu): log probabilities of given tokens with entropy and top
+// (vocab_rows.cu, distill.cu): log probabilities of given tokens with entropy and top
 // alternatives, their way back, and distillation from a teacher's lists.  The
 // C entry points that validate arguments and call these are
 // axonn_token_logprobs, axonn_token_logprobs_bwd and axonn_distill in
@@ -54,7 +54,7 @@ struct DistillArgs {
   int32_t k;
   float grad_scale;
   float* token_loss;  // [rows]
-  float* loss;        // [1]; during the call the count of finished blocks
+  float* loss;        // [1]; during the call the kernels' counter
   int32_t* kept;      // [1]
   void* dlogits;      // of the logits' type, may be the logits; or null
   int64_t ld_dlogits;
@@ -63,6 +63,9 @@ struct DistillArgs {
 cudaError_t logprobs_launch(const LogprobArgs& a, int sms, bool pdl, cudaStream_t stream);
 cudaError_t logprobs_bwd_launch(const LogprobBwdArgs& a, bool pdl, cudaStream_t stream);
 cudaError_t distill_init();  // once for each device, before the first launch
-cudaError_t distill_launch(const DistillArgs& a, int sms, bool pdl, cudaStream_t stream);
+cudaError_t distill_launch(const DistillArgs& a, int sms, uint64_t timeout_ns, int inject, bool pdl,
+                           cudaStream_t stream);
+// Reads (and clears if set) the device error word of the distillation.
+cudaError_t distill_take_status(unsigned long long* word, cudaStream_t stream);
 
 }  // namespace axonn

@@ -492,6 +492,71 @@ def test_distill_longest_lists(cuda_lib):
     check_distill(run_distill(cuda_lib, x, "bf16", at, t), x, "bf16", at, t)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("kind,V", [("bf16", 33003), ("f32", 17001), ("bf16", 81920), ("f32", 70007), ("bf16", 131076)])
+def test_distill_many_long_rows(cuda_lib, V, kind, in_place):
+    """Enough long rows that an SM takes several: rows that fit its buffers and
+    rows that do not, whole chunks and odd ends, rows that do not count between
+    them.  Thirteen kinds of row repeat: the first of each is compared with 64
+    bits, the others with it."""
+    T, kinds, k, tau = 330, 13, 70, 1.4
+    x, _, rng = logits_of(kinds, V, kind, seed=26)
+    at, t = lists_of(x, k, rng)
+    length = rng.integers(1, k + 1, size=kinds)
+    length[2] = k
+    at[np.arange(k) >= length[:, None]] = V
+    at[3, 5:60] = at[3, :55]
+    length[3] = 60
+    at[3, 60:] = -1
+    x[4, V // 2:] = -np.inf
+    t[5, :3] = -np.inf
+    keep = np.ones(T, np.uint8)
+    pick = np.arange(T) % kinds
+    at, t = at[pick], t[pick]
+    at[pick == 6, 0] = -1
+    keep[pick == 7] = 0
+    keep[40:100] = 0
+    x_all = x[pick]
+    x_all[(keep == 0) | (pick == 6)] = np.nan  # never read
+    got = run_distill(cuda_lib, x_all, kind, at, t, keep, tau, 2.0, in_place=in_place)
+    counted = (keep != 0) & (pick != 6)
+    n = counted.sum()
+    assert got["kept"] == n
+    assert (got["token_loss"][~counted] == 0).all() and (got["dlogits"][~counted] == 0).all()
+    one = np.array([np.nonzero(counted & (pick == r))[0][0] for r in range(kinds) if r not in (6, 7)])
+    for r in one:
+        same = counted & (pick == pick[r])
+        assert (got["dlogits"][same] == got["dlogits"][r]).all() and (got["token_loss"][same] == got["token_loss"][r]).all()
+    part = {"token_loss": got["token_loss"][one], "dlogits": got["dlogits"][one], "kept": len(one)}
+    want = vo.distill(x[pick[one]], at[one], t[one], None, float(np.float32(tau)), 2.0 * len(one) / n)
+    part["loss"] = want["loss"]
+    check_distill(part, x[pick[one]], kind, at[one], t[one], None, tau, 2.0 * len(one) / n)
+    # a masked word in the teacher's list of kind 4: its loss is infinite, and so is the mean
+    assert got["token_loss"][pick == 4][0] == np.inf and got["loss"] == np.inf
+
+
+def test_distill_expired_wait_is_reported(cuda_lib):
+    """The producer withholds its copies: the waits run out, the call reports
+    it, and the next one is right."""
+    fc = cuda_lib
+    x, _, rng = logits_of(310, 33000, "bf16", seed=27)
+    at, t = lists_of(x, 8, rng)
+    want = run_distill(fc, x, "bf16", at, t)
+    mean = want["token_loss"].sum() / 310
+    assert abs(want["loss"] - mean) <= 2.0**-24 * (310 / 576 + 32) * mean
+    fc.axonn_set_wait_timeout_ns(20_000_000)
+    fc.axonn_debug_set_inject(1)
+    try:
+        with pytest.raises(fc.AxonnError) as e:
+            run_distill(fc, x, "bf16", at, t)
+        assert e.value.status == fc.ERR_TIMEOUT
+    finally:
+        fc.axonn_debug_set_inject(0)
+        fc.axonn_set_wait_timeout_ns(4_000_000_000)
+    again = run_distill(fc, x, "bf16", at, t)
+    assert all(np.array_equal(want[n], again[n]) for n in want)
+
+
 def test_distill_against_differences(cuda_lib):
     """The mean's gradient by differences of the kernel's own loss along random
     directions: step^2 f'''/6, and the loss's error over the step, both below
