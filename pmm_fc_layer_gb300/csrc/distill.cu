@@ -272,15 +272,19 @@ __global__ void __launch_bounds__(kDistThreads) distill_kernel(const DistillArgs
 // barriers: the next row arrives while this one's gradient is written.  The
 // consumer warps take a row's sums, then its gradient: from the buffers, as far
 // as the ring holds the row (its last chunks), the rest from L2 through the
-// ring again.  A list warp works one row ahead: it reads the list, gathers the
-// row's logits there, makes the weights, and when the sums are known the loss;
-// when the gradient p is written it writes the list's entries, p - q, over it.
+// ring again.  Two list warps take the rows in turn, each one row of its own
+// ahead: it reads the list, gathers the row's logits there, makes the weights,
+// and when the sums are known the loss; when the gradient p is written it
+// writes the list's entries, p - q, over it.
 // Rows are claimed one by one (the first ones by block), since those that do
 // not count cost half.
 constexpr int kRowWarps = 16, kRowConsumers = 32 * kRowWarps;
-constexpr int kRowThreads = kRowConsumers + 64;  // + the producer and the list warp
-constexpr int kChunk = 1024;                     // units: 16 KB
-constexpr int kRing = 12;
+constexpr int kListWarps = 2;
+constexpr int kFirstConsumer = 32 * (1 + kListWarps);  // after the producer and the list warps
+constexpr int kRowThreads = kRowConsumers + kFirstConsumer;
+constexpr int kChunk = 2048;                     // units: 32 KB
+constexpr int kTake = kChunk / kRowConsumers;    // of a thread
+constexpr int kRing = 6;
 constexpr int kSpare = 2;   // buffers that stay free for what comes next
 constexpr int kRowSlots = 4;
 constexpr int kStreamList = 256;  // longest list
@@ -288,7 +292,9 @@ constexpr int kStreamList = 256;  // longest list
 __device__ unsigned long long g_distill_status;
 
 // Bounded wait on an mbarrier phase by polling; false (and an error word) on
-// expiry.
+// expiry.  Every lane that reads what the barrier guards waits itself.  No
+// barrier waited on so can complete its next phase before its waiters have
+// gone on.
 __device__ __noinline__ bool row_wait_long(uint32_t bar, uint32_t parity, uint64_t timeout_ns, uint32_t site) {
   const uint64_t t0 = global_timer_ns();
   while (true) {
@@ -303,17 +309,6 @@ __device__ __noinline__ bool row_wait_long(uint32_t bar, uint32_t parity, uint64
 }
 __device__ __forceinline__ bool row_wait(const uint64_t& bar, uint32_t parity, uint64_t timeout_ns, uint32_t site) {
   return mbar_test_wait(smem_addr(&bar), parity) || row_wait_long(smem_addr(&bar), parity, timeout_ns, site);
-}
-// The same for a whole warp: lane 0 polls, then every lane tests the phase
-// (its own acquire).  No barrier waited on so can complete its next phase
-// before this warp has gone on.
-__device__ __forceinline__ bool row_warp_wait(const uint64_t& bar, uint32_t parity, uint64_t timeout_ns,
-                                              uint32_t site) {
-  bool got = true;
-  if ((threadIdx.x & 31) == 0) got = row_wait(bar, parity, timeout_ns, site);
-  got = __shfl_sync(kAll, got, 0) != 0;
-  if (got) (void)mbar_test_wait(smem_addr(&bar), parity);
-  return got;
 }
 __device__ __forceinline__ void arrive(uint64_t& bar) { mbar_arrive(smem_addr(&bar)); }
 
@@ -504,6 +499,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
         row = next < T_ ? next : -1;
         counts = row >= 0 && row_counts(a, row);
         post(r + 1, row, counts);
+        if (row < 0)  // each list warp is told
+          for (uint32_t i = 2; i <= kListWarps; ++i) post(r + i, row, false);
         if (copies)
           for (int i = 0; i < again && ok; ++i) copy(at, i, drop_pol);
       }
@@ -514,24 +511,24 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
           row_wait(tl->full[i % kRing], (i / kRing) & 1u, tmo, 3);
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp <= kListWarps) {
     // ------------------------------------------------------------ lists
     auto prepare = [&](uint32_t r) {
       RowSlot& slot = tl->slot[r % kRowSlots];
-      ok = ok && row_warp_wait(tl->row_full[r % kRowSlots], parity(r), tmo, 4);
+      ok = ok && row_wait(tl->row_full[r % kRowSlots], parity(r), tmo, 4);
       if (!ok || slot.row < 0) return false;
       if (slot.counts) take_list<T>(a, slot.row, list_of(r), slot, c);
       if (lane == 0) arrive(tl->list_full[r % kRowSlots]);
       return true;
     };
-    bool more = prepare(0);
-    for (uint32_t r = 0; more; ++r) {
+    uint32_t r = static_cast<uint32_t>(warp - 1);
+    for (bool more = prepare(r); more; r += kListWarps) {
       const RowSlot& slot = tl->slot[r % kRowSlots];
       const RowList l = list_of(r);
       const int64_t t = slot.row;
       const bool counts = slot.counts;
-      more = prepare(r + 1);
-      ok = ok && row_warp_wait(tl->sums_full[r % kRowSlots], parity(r), tmo, 5);
+      more = prepare(r + kListWarps);
+      ok = ok && row_wait(tl->sums_full[r % kRowSlots], parity(r), tmo, 5);
       if (ok && !counts && lane == 0) a.token_loss[t] = 0.0f;
       if (ok && counts) {
         const float log2w = log2f(slot.sum), log2s = log2f(slot.s);
@@ -545,7 +542,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
         for (int o = 1; o < 32; o <<= 1) kl += __shfl_xor_sync(kAll, kl, o);
         if (lane == 0) a.token_loss[t] = kl * (kRowLn2 * a.in.temperature * a.in.temperature);
       }
-      ok = ok && row_warp_wait(tl->written[r % kRowSlots], parity(r), tmo, 6);
+      ok = ok && row_wait(tl->written[r % kRowSlots], parity(r), tmo, 6);
       if (ok && counts) {
         const float scale = a.grad_scale * a.in.temperature / static_cast<float>(*a.kept);
         const float share = slot.s == 0.0f || slot.sum == 0.0f ? 0.0f : scale / slot.s;
@@ -561,7 +558,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
     }
   } else {
     // ------------------------------------------------------------ consumers
-    const int cw = warp - 2, ct = static_cast<int>(threadIdx.x) - 64;
+    const int cw = warp - 1 - kListWarps, ct = static_cast<int>(threadIdx.x) - kFirstConsumer;
     const int n = *a.kept;
     const float scale = n > 0 ? a.grad_scale * a.in.temperature / static_cast<float>(n) : 0.0f;
     const int tail = static_cast<int>(V & 7);
@@ -569,7 +566,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
     uint32_t seq = 0;
     for (uint32_t r = 0;; ++r) {
       RowSlot& slot = tl->slot[r % kRowSlots];
-      ok = ok && row_warp_wait(tl->row_full[r % kRowSlots], parity(r), tmo, 7);
+      ok = ok && row_wait(tl->row_full[r % kRowSlots], parity(r), tmo, 7);
       if (consumers_any(!ok || slot.row < 0)) break;
       const int64_t t = slot.row;
       const T* row = static_cast<const T*>(a.in.logits) + t * a.in.ld;
@@ -580,17 +577,19 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
         if (ct < tail) put_logit(out + tail_at + ct, 0.0f);
         if (ct == 0) arrive(tl->sums_full[r % kRowSlots]);
       } else {
-        // f on every unit of a chunk that has arrived as the s-th
+        // f(units, first, n) on a thread's units of a chunk that arrived as the
+        // s-th: the first of them at `first`, the others kRowConsumers apart, those
+        // from n on of -inf
         auto chunk = [&](uint32_t s, int i, bool arrived, bool release, auto&& f) {
           const int b = static_cast<int>(s % kRing);
-          if (!arrived) ok = ok && row_warp_wait(tl->full[b], (s / kRing) & 1u, tmo, 8);
+          if (!arrived) ok = ok && row_wait(tl->full[b], (s / kRing) & 1u, tmo, 8);
           const uint4* buf = ring + b * kChunk;
-          const int units = min(kChunk, p.units - i * kChunk);
-          if (ok) {
+          const int n = ok ? min(kChunk, p.units - i * kChunk) : 0;
+          uint4 v[kTake];
 #pragma unroll
-            for (int u = 0; u < kChunk / kRowConsumers; ++u)
-              if (ct + kRowConsumers * u < units) f(i * kChunk + ct + kRowConsumers * u, buf[ct + kRowConsumers * u]);
-          }
+          for (int u = 0; u < kTake; ++u)
+            v[u] = ct + kRowConsumers * u < n ? buf[ct + kRowConsumers * u] : no_unit<T>();
+          f(v, i * kChunk + ct, i * kChunk + n);
           if (release) {
             __syncwarp();
             if (lane == 0) arrive(tl->empty[b]);
@@ -599,11 +598,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
         const int again = p.chunks - p.held;
         RowSums sums;
         for (int i = 0; i < p.chunks; ++i)
-          chunk(seq + i, i, false, i < again, [&](int, const uint4& v) {
-            float x[kPer];
-            unit_values<T>(v, x);
-            add<false>(sums, x, c);
-          });
+          chunk(seq + i, i, false, i < again,
+                [&](const uint4(&v)[kTake], int, int) { add_units<T>(sums, v, c); });
         float last[8];  // the row's last logits, one thread
         if (ct == kRowConsumers - 1 && tail) {
 #pragma unroll
@@ -619,18 +615,21 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
           slot.s = sums.s;
           arrive(tl->sums_full[r % kRowSlots]);
         }
-        // in place, the list warp must have read before anything is written
-        ok = ok && row_warp_wait(tl->list_full[r % kRowSlots], parity(r), tmo, 9);
+        // in place, a list warp must have read before anything is written
+        ok = ok && row_wait(tl->list_full[r % kRowSlots], parity(r), tmo, 9);
         const float share = sums.s == 0.0f || slot.sum == 0.0f ? 0.0f : scale / sums.s;
         const float m = sums.m > -INFINITY ? sums.m : 0.0f;
         const F2 m2 = f2(-m), c2 = f2(c), share2 = f2(share);
-        auto give = [&](int i, const uint4& v) {
-          float x[kPer];
-          unit_values<T>(v, x);
+        auto give = [&](const uint4(&v)[kTake], int first, int end) {
 #pragma unroll
-          for (int j = 0; j < kPer; j += 2)
-            split(mul2(ex2_2(mul2(add2(f2(x[j], x[j + 1]), m2), c2)), share2), x[j], x[j + 1]);
-          __stcs(dst + i, unit_of(x));
+          for (int u = 0; u < kTake; ++u) {
+            float x[kPer];
+            unit_values<T>(v[u], x);
+#pragma unroll
+            for (int j = 0; j < kPer; j += 2)
+              split(mul2(ex2_2(mul2(add2(f2(x[j], x[j + 1]), m2), c2)), share2), x[j], x[j + 1]);
+            if (first + kRowConsumers * u < end) __stcs(dst + first + kRowConsumers * u, unit_of(x));
+          }
         };
         for (int i = again; i < p.chunks; ++i) chunk(seq + i, i, true, true, give);
         for (int i = 0; i < again; ++i) chunk(seq + p.chunks + i, i, false, true, give);

@@ -222,11 +222,63 @@ __device__ __forceinline__ void unit_values(const uint4& v, float (&x)[kUnit<T>]
   for (int j = 0; j < kUnit<T>; ++j)
     x[j] = __uint_as_float(sizeof(T) == 4 ? w[j] : (j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16);
 }
+template <typename T>
+__device__ __forceinline__ uint4 no_unit() {  // of -inf
+  const uint32_t w = sizeof(T) == 4 ? 0xFF800000u : 0xFF80FF80u;
+  return make_uint4(w, w, w, w);
+}
+// Their largest logit, two bf16 at a time (a NaN is passed over).
+__device__ __forceinline__ __nv_bfloat162 pair_max(uint32_t a, uint32_t b) {
+  return __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+}
+template <typename T, int U>
+__device__ __forceinline__ float units_max(const uint4 (&v)[U]) {
+  float top = -INFINITY;
+  if constexpr (sizeof(T) == 2) {
+    __nv_bfloat162 m = __hmax2(pair_max(v[0].x, v[0].y), pair_max(v[0].z, v[0].w));
+#pragma unroll
+    for (int u = 1; u < U; ++u) m = __hmax2(m, __hmax2(pair_max(v[u].x, v[u].y), pair_max(v[u].z, v[u].w)));
+    top = fmaxf(__low2float(m), __high2float(m));
+  } else {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[4];
+      unit_values<T>(v[u], x);
+      top = fmaxf(top, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+    }
+  }
+  return top;
+}
 __device__ __forceinline__ uint4 unit_of(const float (&x)[8]) {
   return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 __device__ __forceinline__ uint4 unit_of(const float (&x)[4]) {
   return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+
+// Adds units, without A.
+template <typename T, int U>
+__device__ __forceinline__ void add_units(RowSums& r, const uint4 (&v)[U], float c) {
+  const float top = units_max<T>(v);
+  if (top > r.m) {
+    if (r.m > -INFINITY) r.s *= ex2_approx((r.m - top) * c);
+    r.m = top;
+  }
+  const F2 m = f2(r.m > -INFINITY ? -r.m : 0.0f), c2 = f2(c);
+  F2 s[2] = {f2(0.0f), f2(0.0f)};
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float x[kUnit<T>];
+    unit_values<T>(v[u], x);
+#pragma unroll
+    for (int j = 0; j < kUnit<T>; j += 2) {
+      F2& to = s[(j / 2) & 1];
+      to = add2(to, ex2_2(mul2(add2(f2(x[j], x[j + 1]), m), c2)));
+    }
+  }
+  float s0, s1;
+  split(add2(s[0], s[1]), s0, s1);
+  r.s += s0 + s1;
 }
 
 // CTAs a row: as many as fill the GPU's places a few times over, each with
