@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
         sums = join_warp<false>(sums, c);
         if (lane == 0) tl->parts[cw] = sums;
         (void)consumers_any(false);
-        sums = join_parts<false, kRowWarps>(tl->parts, kRowWarps, c);
+        sums = join_parts_warp<false, kRowWarps>(tl->parts, c);
         if (ct == 0) {
           slot.m = sums.m;
           slot.s = sums.s;

@@ -9,7 +9,7 @@
 namespace axonn {
 namespace {
 
-constexpr int kStatThreads = 256;
+constexpr int kStatThreads = 256;  // the most, and those of blocks in clusters
 
 // ------------------------------------------------------------------ lists
 // The order of a list as whole numbers: a NaN above every number, -0 as 0,
@@ -38,7 +38,7 @@ __device__ __forceinline__ float rank_value(uint64_t r) {
 // is a bound that k entries reach.  An entry that reaches it lies in a segment
 // that does: only those are read again, and what reaches the bound is the
 // candidates.  The bound is sought among the threads' best segments alone,
-// between the k-th and the (1.5 k + 4)-th.
+// between the k-th and a few places (half of k, at most 16, and 4) behind it.
 constexpr int kSegments = 8;
 
 template <int kThreads>
@@ -47,6 +47,8 @@ struct TopShared {
     uint64_t segment[kSegments][kThreads];
     uint64_t entry[kSegments * kThreads];  // the candidates, after the segments
   };
+  uint64_t best[kThreads];  // of each thread's segments
+  uint64_t bound;
   uint16_t again[kSegments * kThreads];  // segments that reach the bound
   uint64_t part[kThreads / 32];
   uint64_t list[kMaxTop];
@@ -71,22 +73,34 @@ __device__ __noinline__ uint64_t next_entry(const T* row, const Share sh, uint64
   return best;
 }
 
-// A number that at least k (or else all) of the threads' numbers reach, and at
+// A number that at least k (or else all) of the block's numbers reach, and at
 // most `most` unless fewer numbers than k are not 0.  All are different, and
-// below `hi`.
-__device__ __forceinline__ uint64_t bound_of(uint64_t mine, int k, int most, uint64_t hi) {
-  int n = __syncthreads_count(mine != 0);
+// below `hi`.  One warp's work: it reads them all, and the others wait (every
+// warp counting its own, with a barrier for each step, took four times the
+// instructions).
+template <int kThreads>
+__device__ __forceinline__ uint64_t bound_of(const uint64_t* numbers, int k, int most, uint64_t hi) {
+  uint64_t mine[kThreads / 32];
+#pragma unroll
+  for (int j = 0; j < kThreads / 32; ++j) mine[j] = numbers[(threadIdx.x & 31) + 32 * j];
+  auto reach = [&](uint64_t x) {
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < kThreads / 32; ++j) n += mine[j] >= x ? 1 : 0;
+    return __reduce_add_sync(kAll, n);
+  };
+  int n = reach(1);
   if (n <= most) return 1;
   // downwards from hi in growing steps, then by halves: n reach lo, fewer than k hi
   uint64_t lo = hi, step = static_cast<uint64_t>(1) << 50;
   for (n = 0; n < k; step <<= 2) {
     hi = lo;
     lo = step < hi && step < (static_cast<uint64_t>(1) << 62) ? hi - step : 1;
-    n = __syncthreads_count(mine >= lo);
+    n = reach(lo);
   }
   while (n > most && hi - lo > 1) {
     const uint64_t mid = lo + (hi - lo) / 2;
-    const int at = __syncthreads_count(mine >= mid);
+    const int at = reach(mid);
     if (at >= k) {
       lo = mid;
       n = at;
@@ -97,7 +111,7 @@ __device__ __forceinline__ uint64_t bound_of(uint64_t mine, int k, int most, uin
   return lo;
 }
 
-// Leaves the k largest of n > k entries, all different, in sh.list.
+// Leaves the k largest of n > k entries, all different, as the first ones.
 template <int kThreads>
 __device__ __noinline__ void cut_entries(TopShared<kThreads>& sh, int n, int k) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -122,6 +136,8 @@ __device__ __noinline__ void cut_entries(TopShared<kThreads>& sh, int n, int k) 
   }
   for (int i = threadIdx.x; i < n; i += kThreads)
     if (sh.entry[i] >= lo) sh.list[atomicAdd(&sh.listed, 1)] = sh.entry[i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < k; i += kThreads) sh.entry[i] = sh.list[i];
   __syncthreads();
 }
 
@@ -155,13 +171,15 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
   griddep_launch_dependents();
   griddep_wait();
   constexpr int kWarps = kThreads / 32;
+  constexpr bool kClusters = kThreads == kStatThreads;
   __shared__ RowSums parts[kWarps];
   __shared__ RowSums shares[kMaxCluster];                        // the first CTA's: the others' sums
-  __shared__ uint64_t lists[kTop ? kMaxCluster * kMaxTop : 1];   // and lists, each in order
+  __shared__ uint64_t lists[kTop && kClusters ? kMaxCluster * kMaxTop : 1];  // and lists, each in order
   __shared__ TopShared<kTop ? kThreads : 32> top;
   const int64_t V = p.in.vocab;
   const int64_t t = cluster_id_x();
-  const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
+  const int rank = kClusters ? static_cast<int>(cluster_ctarank()) : 0;
+  const int ctas = kClusters ? static_cast<int>(cluster_nctarank()) : 1;
   const int tid = static_cast<int>(threadIdx.x);
   const float inv = 1.0f / p.in.temperature, c = kEpiLog2e * inv;
   if (p.in.keep && p.in.keep[t] == 0) {
@@ -246,16 +264,25 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
       best = segments_of_nan<kThreads>(row, sh, batches, top);
       hi = ~static_cast<uint64_t>(0);
     }
-    const uint64_t bound = bound_of(best, k, k + k / 2 + 4, hi);
+    top.best[tid] = best;
+    __syncthreads();
+    if (tid < 32) {
+      const uint64_t b = bound_of<kThreads>(top.best, k, k + min(k / 2, 16) + 4, hi);
+      if (tid == 0) top.bound = b;
+    }
+    __syncthreads();
+    const uint64_t bound = top.bound;
     unsigned reach = 0;
+    if (best >= bound) {
 #pragma unroll
-    for (int j = 0; j < kSegments; ++j)
-      if (best >= bound && top.segment[j][tid] >= bound) reach |= 1u << j;
+      for (int j = 0; j < kSegments; ++j) reach |= top.segment[j][tid] >= bound ? 1u << j : 0u;
+    }
     for (; reach; reach &= reach - 1)
       top.again[atomicAdd(&top.segments, 1)] = static_cast<uint16_t>((__ffs(static_cast<int>(reach)) - 1) * kThreads + tid);
     __syncthreads();
     // from here the segments' memory takes the candidates
     constexpr int kRoom = kSegments * kThreads;
+    const float least = rank_value(bound);  // a NaN where the bound is one, or none
     auto offer = [&](float x, int64_t at) {
       const uint64_t e = rank_of(key_of(x), static_cast<uint32_t>(at));
       if (e >= bound) {
@@ -272,31 +299,34 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
         v.load(row + static_cast<int64_t>(i) * 8, 8);
         float x[8];
         v.values(x);
+        unsigned large = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) offer(x[e], static_cast<int64_t>(i) * 8 + e);
+        for (int e = 0; e < 8; ++e) large |= x[e] < least ? 0u : 1u << e;
+        for (; large; large &= large - 1) {
+          const int64_t at = static_cast<int64_t>(i) * 8 + __ffs(static_cast<int>(large)) - 1;
+          offer(logit_at(row + at), at);
+        }
       }
     }
     if (tid < sh.tail) offer(logit_at(row + sh.tail_at + tid), sh.tail_at + tid);
     __syncthreads();
     int n = top.entries;
-    const uint64_t* entry = top.entry;
     if (n > kRoom) {
       // more candidates than there is room for (a share of which a few segments
       // hold nearly everything that is large): one by one
       uint64_t at = ~static_cast<uint64_t>(0);
       for (int j = 0; j < k; ++j) {
         at = next_entry<kThreads>(row, sh, at, top.part);
-        if (tid == 0) top.list[j] = at;
+        if (tid == 0) top.entry[j] = at;
       }
-      __syncthreads();
       n = k;
-      entry = top.list;
-    } else if (n > kThreads) {
+      __syncthreads();
+    } else if (n > 2 * kThreads) {
       cut_entries(top, n, k);
       n = k;
-      entry = top.list;
     }
-    // each candidate's place is the number of larger ones
+    // each candidate's place is the number of larger ones, counted by as many
+    // threads as there are for it
     const float lns = log2f(r.s) * kRowLn2;
     auto write = [&](int place, uint64_t e, float m, float s, float ln_s) {
       const int64_t at = t * p.ld_top + place;
@@ -304,12 +334,16 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
       // as far below the maximum as fp32 reaches
       if (p.top_logprob) p.top_logprob[at] = s == 0.0f ? -INFINITY : fmaf(rank_value(e) - m, inv, -ln_s);
     };
-    if (tid < n) {
-      const uint64_t e = entry[tid];
+    int share = 0;  // log2 of a candidate's threads
+    while (share < 5 && n << (share + 1) <= kThreads) ++share;
+    const int lanes = 1 << share;
+    for (int at = tid >> share; at < n; at += kThreads >> share) {
+      const uint64_t e = top.entry[at];
       int place = 0;
 #pragma unroll 4
-      for (int i = 0; i < n; ++i) place += entry[i] > e ? 1 : 0;
-      if (place < k) {
+      for (int i = tid & (lanes - 1); i < n; i += lanes) place += top.entry[i] > e ? 1 : 0;
+      for (int o = 1; o < lanes; o <<= 1) place += __shfl_xor_sync(__activemask(), place, o);
+      if (place < k && (tid & (lanes - 1)) == 0) {
         if (ctas == 1) write(place, e, r.m, r.s, lns);
         else put_remote(&lists[rank * p.k + place], 0, e);
       }
@@ -414,19 +448,45 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const Logprob
   }
 }
 
+// Blocks of kThreads, as many on an SM as their registers allow: 1536 threads
+// where a thread does least, 1280 or 1024 otherwise.
+template <int kThreads>
+cudaError_t logprobs_launch_blocks(const LogprobArgs& a, int cluster, bool pdl, cudaStream_t stream) {
+  constexpr int kAt6 = 1536 / kThreads, kAt5 = 1280 / kThreads, kAt4 = 1024 / kThreads;
+  using Kernel = void (*)(LogprobArgs);
+  static constexpr Kernel kKernels[8] = {
+      logprobs_kernel<uint16_t, false, false, kThreads, kAt6>, logprobs_kernel<uint16_t, false, true, kThreads, kAt5>,
+      logprobs_kernel<uint16_t, true, false, kThreads, kAt5>,  logprobs_kernel<uint16_t, true, true, kThreads, kAt4>,
+      logprobs_kernel<float, false, false, kThreads, kAt4>,    logprobs_kernel<float, false, true, kThreads, kAt4>,
+      logprobs_kernel<float, true, false, kThreads, kAt4>,     logprobs_kernel<float, true, true, kThreads, kAt4>};
+  const int which = (a.in.f32 ? 4 : 0) + (a.entropy ? 2 : 0) + (a.k > 0 ? 1 : 0);
+  const dim3 grid(static_cast<unsigned>(a.in.rows * cluster));
+  return launch_clusters(kKernels[which], grid, static_cast<unsigned>(cluster), kThreads, pdl, stream, 0, a);
+}
+cudaError_t logprobs_launch_with(const LogprobArgs& a, int threads, int cluster, bool pdl, cudaStream_t stream) {
+  if (threads == 64) return logprobs_launch_blocks<64>(a, cluster, pdl, stream);
+  if (threads == 128) return logprobs_launch_blocks<128>(a, cluster, pdl, stream);
+  return logprobs_launch_blocks<kStatThreads>(a, cluster, pdl, stream);
+}
+
+// Threads a block: what a block costs whatever its row is the work of its
+// warps, so short rows have few (8192 rows, lists of 8 of 2000 words: 21.5 us
+// by 64 threads, 30 by 128, 56 by 256; lists of 20 of 32000 words 123, 111 and
+// 134).  Long rows, and rows that come one to an SM, want as many loads on
+// their way as a block can have (4096 x 128256, lists of 20: 271, 196, 189; 64
+// rows of 128256 words 39, 21, 12), and a list of k comes from the best of at
+// least 2 k threads.
+int row_threads(const LogprobArgs& a, int cluster, int sms) {
+  const int64_t V = a.in.vocab;
+  if (cluster > 1 || a.k > 64 || V >= 65536 || (V > 8192 && a.in.rows < 4 * sms)) return kStatThreads;
+  return V <= 8192 && a.k <= 16 && a.in.rows >= 12 * sms ? 64 : 128;
+}
+
 }  // namespace
 
 cudaError_t logprobs_launch(const LogprobArgs& a, int sms, bool pdl, cudaStream_t stream) {
   const int cluster = row_cluster(a.in.rows, a.in.vocab, sms);
-  const dim3 grid(static_cast<unsigned>(a.in.rows * cluster));
-  const int which = (a.in.f32 ? 4 : 0) + (a.entropy ? 2 : 0) + (a.k > 0 ? 1 : 0);
-  using Kernel = void (*)(LogprobArgs);
-  static constexpr Kernel kKernels[8] = {
-      logprobs_kernel<uint16_t, false, false, kStatThreads, 6>, logprobs_kernel<uint16_t, false, true, kStatThreads, 5>,
-      logprobs_kernel<uint16_t, true, false, kStatThreads, 5>,  logprobs_kernel<uint16_t, true, true, kStatThreads, 4>,
-      logprobs_kernel<float, false, false, kStatThreads, 4>,    logprobs_kernel<float, false, true, kStatThreads, 4>,
-      logprobs_kernel<float, true, false, kStatThreads, 4>,     logprobs_kernel<float, true, true, kStatThreads, 4>};
-  return launch_clusters(kKernels[which], grid, static_cast<unsigned>(cluster), kStatThreads, pdl, stream, 0, a);
+  return logprobs_launch_with(a, row_threads(a, cluster, sms), cluster, pdl, stream);
 }
 
 cudaError_t logprobs_bwd_launch(const LogprobBwdArgs& a, bool pdl, cudaStream_t stream) {

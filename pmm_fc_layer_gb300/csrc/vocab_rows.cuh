@@ -117,13 +117,30 @@ __device__ __forceinline__ RowSums join_warp(RowSums r, float c) {
   return r;
 }
 
+// The sum of kParts parts that every lane of a warp can read (a power of two),
+// known to every lane: a lane takes one, and they join as a tree.
+template <bool kEntropy, int kParts>
+__device__ __forceinline__ RowSums join_parts_warp(const RowSums* parts, float c) {
+  RowSums r = parts[threadIdx.x % kParts];
+  float m = r.m;
+#pragma unroll
+  for (int o = 1; o < kParts; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+  shift_to<kEntropy>(r, m, c);
+#pragma unroll
+  for (int o = 1; o < kParts; o <<= 1) {
+    r.s += __shfl_xor_sync(kAll, r.s, o);
+    if (kEntropy) r.a += __shfl_xor_sync(kAll, r.a, o);
+  }
+  return r;
+}
+
 // The block's sum of the threads' parts, known to every thread.
 template <bool kEntropy, int kWarps>
 __device__ __forceinline__ RowSums join_block(RowSums r, float c, RowSums* parts) {
   r = join_warp<kEntropy>(r, c);
   if ((threadIdx.x & 31) == 0) parts[threadIdx.x >> 5] = r;
   __syncthreads();
-  return join_parts<kEntropy, kWarps>(parts, kWarps, c);
+  return join_parts_warp<kEntropy, kWarps>(parts, c);
 }
 
 // ------------------------------------------------------------------ shares of a row
@@ -281,11 +298,12 @@ __device__ __forceinline__ void add_units(RowSums& r, const uint4 (&v)[U], float
   r.s += s0 + s1;
 }
 
-// CTAs a row: as many as fill the GPU's places a few times over, each with
-// some thousands of logits.
+// CTAs a row: as many as fill the GPU once, each with some thousands of logits.
+// More only add to what a CTA costs whatever its share (8 a row instead of 2:
+// 256 x 128256, lists of 20, 36 us against 25; 64 rows of fp32 12 against 15).
 inline int row_cluster(int64_t rows, int64_t vocab, int sms) {
   int cluster = 1;
-  while (cluster < kMaxCluster && rows * cluster < int64_t{12} * sms && vocab / (2 * cluster) >= 4096) cluster *= 2;
+  while (cluster < kMaxCluster && rows * cluster * 2 <= int64_t{4} * sms && vocab / (2 * cluster) >= 4096) cluster *= 2;
   return cluster;
 }
 

@@ -167,6 +167,21 @@ def test_logprobs_temperature_mask_and_padding(cuda_lib, kind, tau):
         check_logprobs(got, clean, tokens, keep, tau, 9)
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,ks", [(650, 700, (1, 64, 65)), (700, 9001, (3, 64)), (2000, 300, (2, 16, 17)),
+                                    (2000, 4099, (8,)), (610, 20003, (20,))])
+def test_logprobs_many_rows(cuda_lib, T, V, ks, kind):
+    """Blocks of every size: few threads for many short rows."""
+    x, tokens, _ = logits_of(min(T, 97), V, kind, seed=16)
+    x[::5] = np.round(x[::5])  # ties
+    pick = np.arange(T) % len(x)
+    for k in ks:
+        got = run_logprobs(cuda_lib, x[pick], kind, tokens[pick], k=k)
+        check_logprobs({n: v[:len(x)] for n, v in got.items()}, x, tokens, k=k)
+        for n, v in got.items():
+            assert np.array_equal(v, v[:len(x)][pick]), n
+
+
 def special_rows(V, kind):
     """Rows that are hard on a maximum, a sum or an order."""
     rng = np.random.default_rng(9)
