@@ -473,20 +473,62 @@ axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, u
  *              counted get zeros; in place as above
  * Two launches; the second reads the logits twice, the second time from L2.
  */
-axonn_status_t axonn_token_logprobs(const void* logits, int64_t ld_logits, const int32_t* tokens,
-                                    const uint8_t* keep, int64_t T, int64_t V, float temperature,
-                                    uint32_t flags, float* logprob, float* entropy, float* lse, int32_t k,
-                                    int32_t* top_index, float* top_logprob, int64_t ld_top,
-                                    cudaStream_t stream);
-axonn_status_t axonn_token_logprobs_bwd(const void* logits, int64_t ld_logits, const int32_t* tokens,
-                                        const uint8_t* keep, int64_t T, int64_t V, float temperature,
-                                        uint32_t flags, const float* lse, const float* dlogprob,
-                                        const float* entropy, const float* dentropy, void* dlogits,
-                                        int64_t ld_dlogits, cudaStream_t stream);
-axonn_status_t axonn_distill(const void* logits, int64_t ld_logits, const int32_t* top_index,
-                             const float* top_logit, int64_t ld_top, const uint8_t* keep, int64_t T, int64_t V,
-                             int32_t k, float temperature, float grad_scale, uint32_t flags, float* token_loss,
-                             float* loss, int32_t* kept, void* dlogits, int64_t ld_dlogits, cudaStream_t stream);
+typedef struct {
+  const void* logits;
+  int64_t ld_logits;
+  const int32_t* tokens;
+  const uint8_t* keep;
+  int64_t T, V;
+  float temperature;
+  uint32_t flags;      /* 0 or AXONN_IN_F32 */
+  float* logprob;
+  float* entropy;
+  float* lse;
+  int32_t* top_index;
+  float* top_logprob;
+  int64_t ld_top;
+  int32_t k;
+} axonn_token_logprobs_t;
+
+typedef struct {
+  const void* logits;
+  int64_t ld_logits;
+  const int32_t* tokens;
+  const uint8_t* keep;
+  int64_t T, V;
+  float temperature;
+  uint32_t flags;
+  const float* lse;
+  const float* dlogprob;
+  const float* entropy;
+  const float* dentropy;
+  void* dlogits;
+  int64_t ld_dlogits;
+} axonn_token_logprobs_bwd_t;
+
+typedef struct {
+  const void* logits;
+  int64_t ld_logits;
+  const int32_t* top_index;
+  const float* top_logit;
+  int64_t ld_top;
+  const uint8_t* keep;
+  int64_t T, V;
+  float temperature;
+  uint32_t flags;
+  float* token_loss;
+  float* loss;
+  int32_t* kept;
+  void* dlogits;
+  int64_t ld_dlogits;
+  float grad_scale;
+  int32_t k;
+} axonn_distill_t;
+
+/* The arguments are read during the call and not kept. */
+axonn_status_t axonn_token_logprobs(const axonn_token_logprobs_t* args, cudaStream_t stream);
+axonn_status_t axonn_token_logprobs_bwd(const axonn_token_logprobs_bwd_t* args, cudaStream_t stream);
+axonn_status_t axonn_distill(const axonn_distill_t* args, cudaStream_t stream);
 
 /*
  * Per-shape tuning -- the GB300 counterpart of the automatic tuning of BLAS

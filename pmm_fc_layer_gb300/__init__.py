@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from . import build as _build
@@ -145,13 +146,10 @@ def load(path: str | None = None):
         lib.axonn_tune_lookup.restype = ctypes.c_int
         lib.axonn_last_choice.argtypes = [ctypes.POINTER(ctypes.c_int)] * 3
         lib.axonn_last_choice.restype = None
-        f32 = ctypes.c_float
-        lib.axonn_token_logprobs.argtypes = [vp, i64, vp, vp, i64, i64, f32, u32, vp, vp, vp, i32, vp, vp, i64, vp]
-        lib.axonn_token_logprobs.restype = ctypes.c_int
-        lib.axonn_token_logprobs_bwd.argtypes = [vp, i64, vp, vp, i64, i64, f32, u32, vp, vp, vp, vp, vp, i64, vp]
-        lib.axonn_token_logprobs_bwd.restype = ctypes.c_int
-        lib.axonn_distill.argtypes = [vp, i64, vp, vp, i64, vp, i64, i64, i32, f32, f32, u32, vp, vp, vp, vp, i64, vp]
-        lib.axonn_distill.restype = ctypes.c_int
+        for name in ("axonn_token_logprobs", "axonn_token_logprobs_bwd", "axonn_distill"):
+            f = getattr(lib, name)
+            f.argtypes = [ctypes.c_char_p, vp]  # the packed argument struct
+            f.restype = ctypes.c_int
         lib.axonn_fc_workspace_size.argtypes = [ctypes.c_int, ctypes.POINTER(Shape), u32,
                                                 ctypes.POINTER(sz)]
         lib.axonn_fc_workspace_size.restype = ctypes.c_int
@@ -517,34 +515,69 @@ def axonn_linear_ce_workspace_size(T: int, K: int, V: int, flags: int = 0, grad:
     return n.value
 
 
-def _logits(logits, *others):
-    """(rows, columns, type name) of logits; every other tensor that is given
-    must be on their device, which must be the current one."""
+# The argument structs of the operators over rows of logits, packed as C lays
+# them out: one conversion for all of a call's arguments (ctypes takes a fifth
+# of a microsecond for each).
+_TOKEN_LOGPROBS = struct.Struct("@PqPPqqfIPPPPPqi4x")
+_TOKEN_LOGPROBS_BWD = struct.Struct("@PqPPqqfIPPPPPq")
+_DISTILL = struct.Struct("@PqPPqPqqfIPPPPqfi")
+
+
+def _logits(logits):
+    """(device, rows, columns, dtype, IN_F32 or 0) of logits, whose device must
+    be the current one."""
+    here = logits.get_device()
+    if here >= 0 and here != _current_device():
+        raise ValueError(f"logits are on device {here}, which is not the current one")
     rows, cols = logits.shape
-    if logits.is_cuda:
-        here = logits.get_device()
-        for t in others:
-            if t is not None and t.is_cuda and t.get_device() != here:
-                raise ValueError(f"tensors on devices {here} and {t.get_device()}")
-        if here != _current_device():
-            raise ValueError(f"logits are on device {here}, which is not the current one")
-    return rows, cols, "f32" if logits.dtype is _dtypes["f32"] else "bf16"
+    f32 = _dtypes["f32"]
+    return (here, rows, cols, f32, IN_F32) if logits.dtype is f32 else (here, rows, cols, _dtypes["bf16"], 0)
 
 
-def _logit_rows(name, t, kind, rows, cols):
-    """(pointer, leading dimension) of rows of logits, or (None, 0) for None;
-    the stride of a single row says nothing."""
-    at, ld = _matrix(name, t, kind, rows, cols)
-    return at, ld if rows > 1 else (cols + 7) // 8 * 8
+def _beside(name, t, dtype, shape, here):
+    """Checks a tensor's type, shape and place beside logits on device `here`."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    at = t.get_device()
+    if at != here:
+        if at >= 0 and here >= 0:
+            raise ValueError(f"{name} is on device {at}, the logits on {here}")
+    if at < 0:
+        _host_memory(name, t)
 
 
-def _lists(name, t, dtype, rows, k):
-    """(pointer, leading dimension) of [rows x k] list entries of that type, or
-    (None, 0) for None."""
+def _whole(name, t, dtype, shape, here):
+    """Address of a contiguous tensor beside the logits, 0 for None."""
     if t is None:
-        return None, 0
-    at, ld = _matrix(name, t, dtype, rows, k)
-    return at, ld if rows > 1 else k
+        return 0
+    _beside(name, t, dtype, shape, here)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(name, t, dtype, shape, here, single):
+    """(address, leading dimension) of rows beside the logits, (0, 0) for None.
+    The stride of a single row says nothing: it counts as `single`."""
+    if t is None:
+        return 0, 0
+    _beside(name, t, dtype, shape, here)
+    ld, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), ld if shape[0] > 1 else single
+
+
+def _lists(index_name, index, value_name, value, T, here):
+    """(k, address of the indices, of the values, leading dimension)."""
+    k = (index if index is not None else value).shape[1]
+    index, ld = _rows(index_name, index, _dtypes["i32"], (T, k), here, k)
+    value, ld_value = _rows(value_name, value, _dtypes["f32"], (T, k), here, k)
+    if index and value and ld != ld_value:
+        raise ValueError(f"{index_name} and {value_name} must have the same row stride")
+    return k, index, value, ld or ld_value
 
 
 def axonn_token_logprobs(logits, tokens=None, logprob=None, entropy=None, lse=None, top_index=None,
@@ -554,18 +587,16 @@ def axonn_token_logprobs(logits, tokens=None, logprob=None, entropy=None, lse=No
     logprob [T], entropy [T], lse [T], and the rows' largest logits, best first,
     as top_index (int32) and top_logprob [T x k].  Rows with keep (uint8 [T]) 0
     get zeros and indices of -1."""
-    T, V, kind = _logits(logits, tokens, logprob, entropy, lse, top_index, top_logprob, keep)
-    top = top_index if top_index is not None else top_logprob
-    k = 0 if top is None else top.shape[1]
-    index, ld = _lists("top_index", top_index, "i32", T, k)
-    value, ld_value = _lists("top_logprob", top_logprob, "f32", T, k)
-    if index and value and ld != ld_value:
-        raise ValueError("top_index and top_logprob must have the same row stride")
-    _check(load().axonn_token_logprobs(
-        *_logit_rows("logits", logits, kind, T, V), _vector("tokens", tokens, "i32", T), _vector("keep", keep, "u8", T),
-        T, V, temperature, IN_F32 if kind == "f32" else 0, _vector("logprob", logprob, "f32", T),
-        _vector("entropy", entropy, "f32", T), _vector("lse", lse, "f32", T), k, index, value, ld or ld_value,
-        _stream(stream)))
+    here, T, V, kind, flags = _logits(logits)
+    f32, per_row, single = _dtypes["f32"], (T,), (V + 7) // 8 * 8
+    k = index = value = ld_top = 0
+    if top_index is not None or top_logprob is not None:
+        k, index, value, ld_top = _lists("top_index", top_index, "top_logprob", top_logprob, T, here)
+    _check(load().axonn_token_logprobs(_TOKEN_LOGPROBS.pack(
+        *_rows("logits", logits, kind, (T, V), here, single), _whole("tokens", tokens, _dtypes["i32"], per_row, here),
+        _whole("keep", keep, _dtypes["u8"], per_row, here), T, V, temperature, flags,
+        _whole("logprob", logprob, f32, per_row, here), _whole("entropy", entropy, f32, per_row, here),
+        _whole("lse", lse, f32, per_row, here), index, value, ld_top, k), _stream(stream)))
 
 
 def axonn_token_logprobs_bwd(logits, lse, dlogits, tokens=None, dlogprob=None, entropy=None, dentropy=None,
@@ -573,12 +604,14 @@ def axonn_token_logprobs_bwd(logits, lse, dlogits, tokens=None, dlogprob=None, e
     """dlogits (the logits' type; may be the logits) = (dlogprob (onehot(tokens)
     - p) - dentropy p (ln p + entropy)) / temperature, for lse and entropy as
     axonn_token_logprobs left them."""
-    T, V, kind = _logits(logits, lse, dlogits, tokens, dlogprob, entropy, dentropy, keep)
-    _check(load().axonn_token_logprobs_bwd(
-        *_logit_rows("logits", logits, kind, T, V), _vector("tokens", tokens, "i32", T), _vector("keep", keep, "u8", T),
-        T, V, temperature, IN_F32 if kind == "f32" else 0, _vector("lse", lse, "f32", T),
-        _vector("dlogprob", dlogprob, "f32", T), _vector("entropy", entropy, "f32", T),
-        _vector("dentropy", dentropy, "f32", T), *_logit_rows("dlogits", dlogits, kind, T, V), _stream(stream)))
+    here, T, V, kind, flags = _logits(logits)
+    f32, per_row, single = _dtypes["f32"], (T,), (V + 7) // 8 * 8
+    _check(load().axonn_token_logprobs_bwd(_TOKEN_LOGPROBS_BWD.pack(
+        *_rows("logits", logits, kind, (T, V), here, single), _whole("tokens", tokens, _dtypes["i32"], per_row, here),
+        _whole("keep", keep, _dtypes["u8"], per_row, here), T, V, temperature, flags,
+        _whole("lse", lse, f32, per_row, here), _whole("dlogprob", dlogprob, f32, per_row, here),
+        _whole("entropy", entropy, f32, per_row, here), _whole("dentropy", dentropy, f32, per_row, here),
+        *_rows("dlogits", dlogits, kind, (T, V), here, single)), _stream(stream)))
 
 
 def axonn_distill(logits, top_index, top_logit, token_loss, loss, kept, dlogits=None, keep=None, temperature=1.0,
@@ -589,16 +622,14 @@ def axonn_distill(logits, top_index, top_logit, token_loss, loss, kept, dlogits=
     token_loss [T], loss [1], kept [1] (int32) and, if given, dlogits (the
     logits' type; may be the logits), the gradient of the mean loss times
     grad_scale."""
-    T, V, kind = _logits(logits, top_index, top_logit, token_loss, loss, kept, dlogits, keep)
-    k = top_index.shape[1]
-    index, ld = _lists("top_index", top_index, "i32", T, k)
-    value, ld_value = _lists("top_logit", top_logit, "f32", T, k)
-    if ld != ld_value:
-        raise ValueError("top_index and top_logit must have the same row stride")
-    _check(load().axonn_distill(
-        *_logit_rows("logits", logits, kind, T, V), index, value, ld, _vector("keep", keep, "u8", T), T, V, k,
-        temperature, grad_scale, IN_F32 if kind == "f32" else 0, _vector("token_loss", token_loss, "f32", T),
-        _vector("loss", loss, "f32", 1), _vector("kept", kept, "i32", 1), *_logit_rows("dlogits", dlogits, kind, T, V),
+    here, T, V, kind, flags = _logits(logits)
+    f32, i32, single = _dtypes["f32"], _dtypes["i32"], (V + 7) // 8 * 8
+    k, index, value, ld_top = _lists("top_index", top_index, "top_logit", top_logit, T, here)
+    _check(load().axonn_distill(_DISTILL.pack(
+        *_rows("logits", logits, kind, (T, V), here, single), index, value, ld_top,
+        _whole("keep", keep, _dtypes["u8"], (T,), here), T, V, temperature, flags,
+        _whole("token_loss", token_loss, f32, (T,), here), _whole("loss", loss, f32, (1,), here),
+        _whole("kept", kept, i32, (1,), here), *_rows("dlogits", dlogits, kind, (T, V), here, single), grad_scale, k),
         _stream(stream)))
 
 

@@ -1580,19 +1580,20 @@ FusedChoice choose_dx(int64_t T, int64_t K, int64_t V) {
 // ------------------------------------------------------------------ rows of logits
 // What the operators over rows of logits have in common: types, sizes, the
 // temperature and the logits themselves.
-axonn_status_t logit_rows(const void* logits, int64_t ld, const uint8_t* keep, int64_t T, int64_t V,
-                          float temperature, uint32_t flags, axonn::LogitRows* rows) {
-  if (flags & ~AXONN_IN_F32)
-    return fail(AXONN_ERR_INVALID_ARG, "flag bits 0x%x do not apply here", flags & ~AXONN_IN_F32);
-  axonn_status_t st = check_rows_cols(T, V);
+template <class Args>
+axonn_status_t logit_rows(const Args* a, axonn::LogitRows* rows) {
+  if (!a) return fail(AXONN_ERR_INVALID_ARG, "the arguments are NULL");
+  if (a->flags & ~AXONN_IN_F32)
+    return fail(AXONN_ERR_INVALID_ARG, "flag bits 0x%x do not apply here", a->flags & ~AXONN_IN_F32);
+  axonn_status_t st = check_rows_cols(a->T, a->V);
   if (st != AXONN_OK) return st;
-  if (V < 1) return fail(AXONN_ERR_INVALID_ARG, "vocabulary size %lld", (long long)V);
-  if (!(temperature >= 1e-4f && temperature <= 1e4f))
+  if (a->V < 1) return fail(AXONN_ERR_INVALID_ARG, "vocabulary size %lld", (long long)a->V);
+  if (!(a->temperature >= 1e-4f && a->temperature <= 1e4f))
     return fail(AXONN_ERR_INVALID_ARG, "temperature not in [1e-4, 1e4]");
-  const bool f32 = (flags & AXONN_IN_F32) != 0;
-  st = check_matrix("logits", logits, ld, T, V, f32);
+  const bool f32 = (a->flags & AXONN_IN_F32) != 0;
+  st = check_matrix("logits", a->logits, a->ld_logits, a->T, a->V, f32);
   if (st != AXONN_OK) return st;
-  *rows = axonn::LogitRows{logits, ld, keep, T, V, temperature, f32 ? 1 : 0};
+  *rows = axonn::LogitRows{a->logits, a->ld_logits, a->keep, a->T, a->V, a->temperature, f32 ? 1 : 0};
   return AXONN_OK;
 }
 
@@ -1791,100 +1792,96 @@ axonn_status_t axonn_fc_wgrad_zsharded(const void* X, const void* dY, void* cons
   return ok();
 }
 
-axonn_status_t axonn_token_logprobs(const void* logits, int64_t ld_logits, const int32_t* tokens,
-                                    const uint8_t* keep, int64_t T, int64_t V, float temperature,
-                                    uint32_t flags, float* logprob, float* entropy, float* lse, int32_t k,
-                                    int32_t* top_index, float* top_logprob, int64_t ld_top,
-                                    cudaStream_t stream) {
+axonn_status_t axonn_token_logprobs(const axonn_token_logprobs_t* args, cudaStream_t stream) {
   axonn::LogprobArgs a{};
-  axonn_status_t st = logit_rows(logits, ld_logits, keep, T, V, temperature, flags, &a.in);
+  axonn_status_t st = logit_rows(args, &a.in);
   if (st != AXONN_OK) return st;
-  if (T > 0 && (tokens == nullptr) != (logprob == nullptr))
+  const axonn_token_logprobs_t& p = *args;
+  if (p.T > 0 && (p.tokens == nullptr) != (p.logprob == nullptr))
     return fail(AXONN_ERR_INVALID_ARG, "tokens and logprob go together");
-  if (k < 0 || k > V) return fail(AXONN_ERR_INVALID_ARG, "a list of %d entries of %lld", k, (long long)V);
-  if (k > axonn::kMaxTop) return fail(AXONN_ERR_UNSUPPORTED, "lists of more than %d entries", axonn::kMaxTop);
-  if (k == 0 && (top_index || top_logprob))
+  if (p.k < 0 || p.k > p.V) return fail(AXONN_ERR_INVALID_ARG, "a list of %d entries of %lld", p.k, (long long)p.V);
+  if (p.k > axonn::kMaxTop) return fail(AXONN_ERR_UNSUPPORTED, "lists of more than %d entries", axonn::kMaxTop);
+  if (p.k == 0 && (p.top_index || p.top_logprob))
     return fail(AXONN_ERR_INVALID_ARG, "top_index or top_logprob without k");
-  if (k > 0 && T > 0 && !top_index && !top_logprob)
+  if (p.k > 0 && p.T > 0 && !p.top_index && !p.top_logprob)
     return fail(AXONN_ERR_INVALID_ARG, "k without top_index or top_logprob");
-  if (k > 0 && ld_top < k)
-    return fail(AXONN_ERR_INVALID_ARG, "lists: leading dimension %lld < %d", (long long)ld_top, k);
-  if (T > 0 && !logprob && !entropy && !lse && k == 0) return fail(AXONN_ERR_INVALID_ARG, "no output is asked for");
-  if (T == 0) return ok();
+  if (p.k > 0 && p.ld_top < p.k)
+    return fail(AXONN_ERR_INVALID_ARG, "lists: leading dimension %lld < %d", (long long)p.ld_top, p.k);
+  if (p.T > 0 && !p.logprob && !p.entropy && !p.lse && p.k == 0)
+    return fail(AXONN_ERR_INVALID_ARG, "no output is asked for");
+  if (p.T == 0) return ok();
   DeviceState* dev = nullptr;
   st = device_state(&dev);
   if (st != AXONN_OK) return st;
-  a.tokens = tokens;
-  a.logprob = logprob;
-  a.entropy = entropy;
-  a.lse = lse;
-  a.top_index = top_index;
-  a.top_logprob = top_logprob;
-  a.ld_top = ld_top;
-  a.k = k;
+  a.tokens = p.tokens;
+  a.logprob = p.logprob;
+  a.entropy = p.entropy;
+  a.lse = p.lse;
+  a.top_index = p.top_index;
+  a.top_logprob = p.top_logprob;
+  a.ld_top = p.ld_top;
+  a.k = p.k;
   const cudaError_t e = axonn::logprobs_launch(a, dev->sms, g_pdl.load() != 0, stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "log probabilities: %s", cudaGetErrorString(e));
   return ok();
 }
 
-axonn_status_t axonn_token_logprobs_bwd(const void* logits, int64_t ld_logits, const int32_t* tokens,
-                                        const uint8_t* keep, int64_t T, int64_t V, float temperature,
-                                        uint32_t flags, const float* lse, const float* dlogprob,
-                                        const float* entropy, const float* dentropy, void* dlogits,
-                                        int64_t ld_dlogits, cudaStream_t stream) {
+axonn_status_t axonn_token_logprobs_bwd(const axonn_token_logprobs_bwd_t* args, cudaStream_t stream) {
   axonn::LogprobBwdArgs a{};
-  axonn_status_t st = logit_rows(logits, ld_logits, keep, T, V, temperature, flags, &a.in);
-  if (st == AXONN_OK) st = check_dlogits(a.in, dlogits, ld_dlogits);
+  axonn_status_t st = logit_rows(args, &a.in);
   if (st != AXONN_OK) return st;
-  if (T > 0 && !lse) return fail(AXONN_ERR_INVALID_ARG, "lse is NULL");
-  if (T > 0 && (tokens == nullptr) != (dlogprob == nullptr))
+  const axonn_token_logprobs_bwd_t& p = *args;
+  st = check_dlogits(a.in, p.dlogits, p.ld_dlogits);
+  if (st != AXONN_OK) return st;
+  if (p.T > 0 && !p.lse) return fail(AXONN_ERR_INVALID_ARG, "lse is NULL");
+  if (p.T > 0 && (p.tokens == nullptr) != (p.dlogprob == nullptr))
     return fail(AXONN_ERR_INVALID_ARG, "tokens and dlogprob go together");
-  if (T > 0 && (entropy == nullptr) != (dentropy == nullptr))
+  if (p.T > 0 && (p.entropy == nullptr) != (p.dentropy == nullptr))
     return fail(AXONN_ERR_INVALID_ARG, "entropy and dentropy go together");
-  if (T > 0 && !dlogprob && !dentropy) return fail(AXONN_ERR_INVALID_ARG, "no gradient comes in");
-  if (T == 0) return ok();
+  if (p.T > 0 && !p.dlogprob && !p.dentropy) return fail(AXONN_ERR_INVALID_ARG, "no gradient comes in");
+  if (p.T == 0) return ok();
   DeviceState* dev = nullptr;
   st = device_state(&dev);
   if (st != AXONN_OK) return st;
-  a.tokens = tokens;
-  a.lse = lse;
-  a.dlogprob = dlogprob;
-  a.entropy = entropy;
-  a.dentropy = dentropy;
-  a.dlogits = dlogits;
-  a.ld_dlogits = ld_dlogits;
+  a.tokens = p.tokens;
+  a.lse = p.lse;
+  a.dlogprob = p.dlogprob;
+  a.entropy = p.entropy;
+  a.dentropy = p.dentropy;
+  a.dlogits = p.dlogits;
+  a.ld_dlogits = p.ld_dlogits;
   const cudaError_t e = axonn::logprobs_bwd_launch(a, g_pdl.load() != 0, stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "log probabilities, backward: %s", cudaGetErrorString(e));
   return ok();
 }
 
-axonn_status_t axonn_distill(const void* logits, int64_t ld_logits, const int32_t* top_index,
-                             const float* top_logit, int64_t ld_top, const uint8_t* keep, int64_t T, int64_t V,
-                             int32_t k, float temperature, float grad_scale, uint32_t flags, float* token_loss,
-                             float* loss, int32_t* kept, void* dlogits, int64_t ld_dlogits, cudaStream_t stream) {
+axonn_status_t axonn_distill(const axonn_distill_t* args, cudaStream_t stream) {
   axonn::DistillArgs a{};
-  axonn_status_t st = logit_rows(logits, ld_logits, keep, T, V, temperature, flags, &a.in);
-  if (st == AXONN_OK && dlogits) st = check_dlogits(a.in, dlogits, ld_dlogits);
+  axonn_status_t st = logit_rows(args, &a.in);
   if (st != AXONN_OK) return st;
-  if (!loss || !kept) return fail(AXONN_ERR_INVALID_ARG, "loss or kept is NULL");
-  if (T > 0 && (!top_index || !top_logit || !token_loss))
+  const axonn_distill_t& p = *args;
+  if (p.dlogits) st = check_dlogits(a.in, p.dlogits, p.ld_dlogits);
+  if (st != AXONN_OK) return st;
+  if (!p.loss || !p.kept) return fail(AXONN_ERR_INVALID_ARG, "loss or kept is NULL");
+  if (p.T > 0 && (!p.top_index || !p.top_logit || !p.token_loss))
     return fail(AXONN_ERR_INVALID_ARG, "top_index, top_logit or token_loss is NULL");
-  if (k < 1) return fail(AXONN_ERR_INVALID_ARG, "lists of %d entries", k);
-  if (k > axonn::kMaxList) return fail(AXONN_ERR_UNSUPPORTED, "lists of more than %d entries", axonn::kMaxList);
-  if (ld_top < k) return fail(AXONN_ERR_INVALID_ARG, "lists: leading dimension %lld < %d", (long long)ld_top, k);
+  if (p.k < 1) return fail(AXONN_ERR_INVALID_ARG, "lists of %d entries", p.k);
+  if (p.k > axonn::kMaxList) return fail(AXONN_ERR_UNSUPPORTED, "lists of more than %d entries", axonn::kMaxList);
+  if (p.ld_top < p.k)
+    return fail(AXONN_ERR_INVALID_ARG, "lists: leading dimension %lld < %d", (long long)p.ld_top, p.k);
   DeviceState* dev = nullptr;
   st = distill_state(&dev);
   if (st != AXONN_OK) return st;
-  a.top_index = top_index;
-  a.top_logit = top_logit;
-  a.ld_top = ld_top;
-  a.k = k;
-  a.grad_scale = grad_scale;
-  a.token_loss = token_loss;
-  a.loss = loss;
-  a.kept = kept;
-  a.dlogits = dlogits;
-  a.ld_dlogits = ld_dlogits;
+  a.top_index = p.top_index;
+  a.top_logit = p.top_logit;
+  a.ld_top = p.ld_top;
+  a.k = p.k;
+  a.grad_scale = p.grad_scale;
+  a.token_loss = p.token_loss;
+  a.loss = p.loss;
+  a.kept = p.kept;
+  a.dlogits = p.dlogits;
+  a.ld_dlogits = p.ld_dlogits;
   const cudaError_t e = axonn::distill_launch(a, dev->sms, g_timeout_ns.load(), g_inject.load(), g_pdl.load() != 0,
                                               stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "distillation: %s", cudaGetErrorString(e));

@@ -103,11 +103,11 @@ def test_distill_against_differences_and_torch(tau):
 
 # ------------------------------------------------------------------ refusals
 LOG = dict(logits=FAKE, ld=64, tokens=FAKE, keep=0, T=4, V=60, tau=1.0, flags=0, logprob=FAKE, entropy=0, lse=0,
-           k=0, top_index=0, top_logprob=0, ld_top=0, stream=0)
+           top_index=0, top_logprob=0, ld_top=0, k=0)
 BWD = dict(logits=FAKE, ld=64, tokens=FAKE, keep=0, T=4, V=60, tau=1.0, flags=0, lse=FAKE, dlogprob=FAKE, entropy=0,
-           dentropy=0, dlogits=FAKE, ld_d=64, stream=0)
-DIS = dict(logits=FAKE, ld=64, top_index=FAKE, top_logit=FAKE, ld_top=8, keep=0, T=4, V=60, k=8, tau=1.0, scale=1.0,
-           flags=0, token_loss=FAKE, loss=FAKE, kept=FAKE, dlogits=FAKE, ld_d=64, stream=0)
+           dentropy=0, dlogits=FAKE, ld_d=64)
+DIS = dict(logits=FAKE, ld=64, top_index=FAKE, top_logit=FAKE, ld_top=8, keep=0, T=4, V=60, tau=1.0, flags=0,
+           token_loss=FAKE, loss=FAKE, kept=FAKE, dlogits=FAKE, ld_d=64, scale=1.0, k=8)
 COMMON = [
     (dict(V=0), 1), (dict(V=-1), 1), (dict(T=-1), 1), (dict(T=1 << 31), 3), (dict(V=1 << 31, ld=1 << 31), 3),
     (dict(tau=0.0), 1), (dict(tau=-1.0), 1), (dict(tau=float("nan")), 1), (dict(tau=float("inf")), 1),
@@ -118,7 +118,9 @@ COMMON = [
 
 
 def refuse(fc, fn, base, change, expect):
-    st = getattr(fc.load(), fn)(*{**base, **change}.values())
+    packed = {"axonn_token_logprobs": fc._TOKEN_LOGPROBS, "axonn_token_logprobs_bwd": fc._TOKEN_LOGPROBS_BWD,
+              "axonn_distill": fc._DISTILL}[fn].pack(*{**base, **change}.values())
+    st = getattr(fc.load(), fn)(packed, 0)
     assert st == expect, (change, fc.axonn_last_error())
     assert fc.axonn_last_error()
 
@@ -128,6 +130,35 @@ def refuse(fc, fn, base, change, expect):
 @pytest.mark.parametrize("change,expect", COMMON)
 def test_common_refusals(fc, fn, base, change, expect):
     refuse(fc, fn, base, change, expect)
+
+
+def test_packed_arguments_are_the_header_s_structs(fc, tmp_path):
+    """Sizes and offsets of the packed structs, against the C compiler's."""
+    import os
+    import subprocess
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    lasts = [("axonn_token_logprobs_t", "k", fc._TOKEN_LOGPROBS, "i4x"), ("axonn_token_logprobs_t", "logprob", None, 56),
+             ("axonn_token_logprobs_bwd_t", "ld_dlogits", fc._TOKEN_LOGPROBS_BWD, "q"),
+             ("axonn_token_logprobs_bwd_t", "lse", None, 56),
+             ("axonn_distill_t", "k", fc._DISTILL, "i"), ("axonn_distill_t", "token_loss", None, 72)]
+    body = "".join(f'printf("%zu %zu\\n", sizeof({t}), offsetof({t}, {f}));' for t, f, _, _ in lasts)
+    src = tmp_path / "sizes.c"
+    src.write_text(f'#include <stdio.h>\n#include "axonn_fc.h"\nint main(void) {{{body} return 0;}}\n')
+    subprocess.check_call(["gcc", "-I", include, "-I", cuda, str(src), "-o", str(tmp_path / "sizes")])
+    out = subprocess.check_output([str(tmp_path / "sizes")], text=True).split()
+    for (t, f, packed, tail), size, at in zip(lasts, map(int, out[::2]), map(int, out[1::2])):
+        if packed is None:
+            assert at == tail, (t, f)
+        else:
+            assert size == packed.size, t
+            import struct
+            assert at == packed.size - struct.calcsize(tail), (t, f)
+
+
+@pytest.mark.parametrize("fn", ["axonn_token_logprobs", "axonn_token_logprobs_bwd", "axonn_distill"])
+def test_null_arguments(fc, fn):
+    assert getattr(fc.load(), fn)(None, 0) == 1
 
 
 @pytest.mark.parametrize("change,expect", [
@@ -177,18 +208,26 @@ def test_binding_refuses_wrong_tensors(fc):
 
 
 def test_binding_refuses_other_devices(fc, monkeypatch):
-    class Other:
-        """A tensor of device 1, as far as the check looks."""
-        shape, is_cuda, dtype = (4, 64), True, None
+    import torch
+
+    class At:
+        """A tensor of some device, as far as the checks look before the call."""
+        def __init__(self, device, shape, dtype):
+            self.device, self.shape, self.dtype = device, shape, dtype
 
         def get_device(self):
-            return 1
+            return self.device
 
-    class Here(Other):
-        def get_device(self):
-            return 0
+        def stride(self):
+            return self.shape[1], 1
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return FAKE
     monkeypatch.setattr(fc, "_current_device", lambda: 0)
     with pytest.raises(ValueError, match="not the current one"):
-        fc.axonn_token_logprobs(Other(), lse=Other())
-    with pytest.raises(ValueError, match="devices 0 and 1"):
-        fc.axonn_token_logprobs(Here(), lse=Other())
+        fc.axonn_token_logprobs(At(1, (4, 64), torch.bfloat16), lse=At(1, (4,), torch.float32))
+    with pytest.raises(ValueError, match="lse is on device 1"):
+        fc.axonn_token_logprobs(At(0, (4, 64), torch.bfloat16), lse=At(1, (4,), torch.float32))
