@@ -42,10 +42,10 @@ __device__ __forceinline__ float rank_value(uint64_t r) {
 constexpr int kSegments = 8;
 
 template <int kThreads>
-struct TopShared {
+struct alignas(16) TopShared {
   union {
     uint64_t segment[kSegments][kThreads];
-    uint64_t entry[kSegments * kThreads];  // the candidates, after the segments
+    uint64_t entry[kSegments * kThreads + 2];  // the candidates, after the segments
   };
   uint64_t best[kThreads];  // of each thread's segments
   uint64_t bound;
@@ -325,8 +325,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
       cut_entries(top, n, k);
       n = k;
     }
-    // each candidate's place is the number of larger ones, counted by as many
-    // threads as there are for it
+    // each candidate's place is the number of larger ones
     const float lns = log2f(r.s) * kRowLn2;
     auto write = [&](int place, uint64_t e, float m, float s, float ln_s) {
       const int64_t at = t * p.ld_top + place;
@@ -334,16 +333,18 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
       // as far below the maximum as fp32 reaches
       if (p.top_logprob) p.top_logprob[at] = s == 0.0f ? -INFINITY : fmaf(rank_value(e) - m, inv, -ln_s);
     };
-    int share = 0;  // log2 of a candidate's threads
-    while (share < 5 && n << (share + 1) <= kThreads) ++share;
-    const int lanes = 1 << share;
-    for (int at = tid >> share; at < n; at += kThreads >> share) {
+    if (tid == 0 && (n & 1)) top.entry[n] = 0;  // two are read at a time
+    __syncthreads();
+    for (int at = tid; at < n; at += kThreads) {
       const uint64_t e = top.entry[at];
       int place = 0;
 #pragma unroll 4
-      for (int i = tid & (lanes - 1); i < n; i += lanes) place += top.entry[i] > e ? 1 : 0;
-      for (int o = 1; o < lanes; o <<= 1) place += __shfl_xor_sync(__activemask(), place, o);
-      if (place < k && (tid & (lanes - 1)) == 0) {
+      for (int i = 0; i < n; i += 2) {
+        const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(top.entry + i);
+        place += two.x > e ? 1 : 0;
+        place += two.y > e ? 1 : 0;
+      }
+      if (place < k) {
         if (ctas == 1) write(place, e, r.m, r.s, lns);
         else put_remote(&lists[rank * p.k + place], 0, e);
       }
@@ -355,22 +356,22 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
       if (rank != 0) return;
       r = join_parts<kEntropy, kMaxCluster>(shares, ctas, c);
       const float ln_s = log2f(r.s) * kRowLn2;
-      // an entry's place: its own in its list, and those before it in the others
+      // an entry's place: its own in its list, and those above it in the others,
+      // a prefix of each; the lists are searched side by side
+      int half = 1;
+      while (2 * half <= p.k) half *= 2;
       for (int i = tid; i < ctas * p.k; i += kThreads) {
         const uint64_t e = lists[i];
-        const int of = i / p.k;
-        int place = i - of * p.k;
         if (e == 0) continue;
-        for (int l = 0; l < ctas; ++l) {
-          if (l == of) continue;
-          int before = 0, behind = p.k;  // entries above e: a prefix of the list
-          while (before < behind) {
-            const int mid = (before + behind) / 2;
-            if (lists[l * p.k + mid] > e) before = mid + 1;
-            else behind = mid;
-          }
-          place += before;
+        int above[kMaxCluster] = {};
+        for (int step = half; step; step /= 2) {
+#pragma unroll
+          for (int l = 0; l < kMaxCluster; ++l)
+            if (l < ctas && above[l] + step <= p.k && lists[l * p.k + above[l] + step - 1] > e) above[l] += step;
         }
+        int place = 0;
+#pragma unroll
+        for (int l = 0; l < kMaxCluster; ++l) place += above[l];
         if (place < p.k) write(place, e, r.m, r.s, ln_s);
       }
     }
