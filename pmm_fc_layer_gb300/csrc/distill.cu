@@ -35,7 +35,6 @@ __global__ void __launch_bounds__(1024) distill_count_kernel(const DistillArgs p
   }
 }
 
-constexpr int kDistThreads = 256;
 constexpr int kHeldBytes = 64 << 10;  // of a row that a CTA holds, where 8 CTAs can hold a row so
 constexpr int kMostHeld = 200 << 10;
 
@@ -83,7 +82,7 @@ __device__ __forceinline__ void mean_of_rows(const DistillArgs& p, RowSums* part
 // everywhere, and the list's entries, p - q, by the threads that have them.
 // Without a gradient nothing is kept.  The row whose cluster finishes last
 // adds up the losses in a fixed order.
-template <typename T, bool kGrad>
+template <typename T, bool kGrad, int kDistThreads>
 __global__ void __launch_bounds__(kDistThreads) distill_kernel(const DistillArgs p, int room) {
   griddep_launch_dependents();
   griddep_wait();
@@ -660,17 +659,62 @@ int stream_shared(int k) {
   return kRing * kChunk * 16 + static_cast<int>(sizeof(RowTail)) + kRowSlots * 16 * ((k + 3) / 4 * 4);
 }
 
-// Which rows go through the ring: long ones, and enough of them that an SM gets
-// several.
+// Which rows go through the ring: long ones, of which an SM gets several
+// (gradients of 4096 rows: 98 us against 90 in shares at 24000 bf16 words, 105
+// against 117 at 32000, 323 against 428 at 128256; of 64000 words 30.3 against
+// 30.5 for 400 rows, 17.7 against 16.7 for 200), with lists that one warp
+// prepares while others take a row.
 bool streams_rows(int64_t rows, int64_t row_bytes, int k, int sms) {
-  return k <= kStreamList && rows >= 2 * sms && row_bytes >= (64 << 10);
+  return k <= kStreamList && rows >= 2 * sms && row_bytes >= (56 << 10);
+}
+
+cudaError_t distill_ring_launch(const DistillArgs& a, int sms, uint64_t timeout_ns, int inject, bool pdl,
+                                cudaStream_t stream) {
+  StreamArgs p{};
+  p.a = a;
+  p.units = static_cast<int>(a.in.vocab / 8 * (a.in.f32 ? 2 : 1));
+  p.chunks = (p.units + kChunk - 1) / kChunk;
+  p.held = std::min(p.chunks, kRing - kSpare);
+  p.list = (a.k + 3) / 4 * 4;
+  p.timeout_ns = timeout_ns;
+  p.inject = inject;
+  return launch_clusters(a.in.f32 ? distill_rows_kernel<float> : distill_rows_kernel<uint16_t>,
+                         dim3(static_cast<unsigned>(std::min<int64_t>(a.in.rows, sms))), 1, kRowThreads, pdl, stream,
+                         static_cast<size_t>(stream_shared(a.k)), p);
+}
+
+template <int kThreads>
+cudaError_t distill_shares_blocks(const DistillArgs& a, int cluster, bool pdl, cudaStream_t stream) {
+  int held = 0;
+  if (a.dlogits) {
+    const int64_t vectors = (a.in.vocab / 8 + cluster - 1) / cluster;
+    held = static_cast<int>(std::min<int64_t>(vectors * (a.in.f32 ? 32 : 16), kMostHeld));
+  }
+  auto kernel = a.in.f32 ? (a.dlogits ? distill_kernel<float, true, kThreads> : distill_kernel<float, false, kThreads>)
+                         : (a.dlogits ? distill_kernel<uint16_t, true, kThreads>
+                                      : distill_kernel<uint16_t, false, kThreads>);
+  return launch_clusters(kernel, dim3(static_cast<unsigned>(a.in.rows * cluster)), static_cast<unsigned>(cluster),
+                         kThreads, pdl, stream, static_cast<size_t>(held + 12 * a.k), a, held / 16);
+}
+cudaError_t distill_shares_launch(const DistillArgs& a, int threads, int cluster, bool pdl, cudaStream_t stream) {
+  return threads == 128 ? distill_shares_blocks<128>(a, cluster, pdl, stream)
+                        : distill_shares_blocks<256>(a, cluster, pdl, stream);
+}
+
+// Threads a block: fewer for many short rows (gradients of 4096 x 4000: 33 us by
+// 128, 43 by 256; 4096 x 16000 72 and 69), and for many rows of which only the
+// sums are wanted (1024 x 128256 55 us and 63).
+int row_threads(const DistillArgs& a, int64_t bytes, int sms) {
+  if (!a.dlogits) return a.in.rows >= 4 * sms ? 128 : 256;
+  return bytes <= (16 << 10) && a.in.rows >= 12 * sms ? 128 : 256;
 }
 
 }  // namespace
 
 cudaError_t distill_init() {
   cudaError_t e = cudaSuccess;
-  for (auto kernel : {distill_kernel<float, true>, distill_kernel<uint16_t, true>})
+  for (auto kernel : {distill_kernel<float, true, 128>, distill_kernel<uint16_t, true, 128>,
+                      distill_kernel<float, true, 256>, distill_kernel<uint16_t, true, 256>})
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostHeld + 12 * kMaxList);
   for (auto kernel : {distill_rows_kernel<float>, distill_rows_kernel<uint16_t>})
@@ -683,32 +727,12 @@ cudaError_t distill_launch(const DistillArgs& a, int sms, uint64_t timeout_ns, i
                            cudaStream_t stream) {
   const cudaError_t e = launch_after(distill_count_kernel, dim3(1), 1024, pdl, stream, a);
   if (e != cudaSuccess || a.in.rows == 0) return e;
-  const int64_t vectors = a.in.vocab / 8, bytes = a.in.f32 ? 32 : 16;
-  if (a.dlogits && streams_rows(a.in.rows, vectors * bytes, a.k, sms)) {
-    StreamArgs p{};
-    p.a = a;
-    p.units = static_cast<int>(vectors * bytes / 16);
-    p.chunks = (p.units + kChunk - 1) / kChunk;
-    p.held = std::min(p.chunks, kRing - kSpare);
-    p.list = (a.k + 3) / 4 * 4;
-    p.timeout_ns = timeout_ns;
-    p.inject = inject;
-    return launch_clusters(a.in.f32 ? distill_rows_kernel<float> : distill_rows_kernel<uint16_t>,
-                           dim3(static_cast<unsigned>(std::min<int64_t>(a.in.rows, sms))), 1, kRowThreads, pdl, stream,
-                           static_cast<size_t>(stream_shared(a.k)), p);
-  }
-  int cluster = row_cluster(a.in.rows, a.in.vocab, sms);
-  int held = 0;
-  if (a.dlogits) {
-    auto share = [&] { return (vectors + cluster - 1) / cluster * bytes; };
-    while (cluster < kMaxCluster && share() > kHeldBytes) cluster *= 2;
-    held = static_cast<int>(std::min<int64_t>(share(), kMostHeld));
-  }
-  const dim3 grid(static_cast<unsigned>(a.in.rows * cluster));
-  auto kernel = a.in.f32 ? (a.dlogits ? distill_kernel<float, true> : distill_kernel<float, false>)
-                         : (a.dlogits ? distill_kernel<uint16_t, true> : distill_kernel<uint16_t, false>);
-  return launch_clusters(kernel, grid, static_cast<unsigned>(cluster), kDistThreads, pdl, stream,
-                         static_cast<size_t>(held + 12 * a.k), a, held / 16);
+  const int64_t bytes = a.in.vocab / 8 * (a.in.f32 ? 32 : 16);
+  if (a.dlogits && streams_rows(a.in.rows, bytes, a.k, sms))
+    return distill_ring_launch(a, sms, timeout_ns, inject, pdl, stream);
+  int cluster = row_cluster(a.in.rows, a.in.vocab, a.dlogits ? 4 : 8, sms);
+  while (a.dlogits && cluster < kMaxCluster && bytes / cluster > kHeldBytes) cluster *= 2;
+  return distill_shares_launch(a, row_threads(a, bytes, sms), cluster, pdl, stream);
 }
 
 cudaError_t distill_take_status(unsigned long long* word, cudaStream_t stream) {

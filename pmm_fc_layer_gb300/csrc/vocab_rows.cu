@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
 }
 
 // ------------------------------------------------------------------ logprobs, backward
-constexpr int kBwdThreads = 256;
+constexpr int kBwdThreads = 64;
 constexpr int kBwdVecs = 4;
 constexpr int kBwdCols = 8 * kBwdThreads * kBwdVecs;
 
@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const Logprob
       h = p.dentropy[t] * inv;
       entropy = p.entropy[t];
     }
+    const F2 inv2 = f2(inv), lse2 = f2(-lse), g2 = f2(-g), h2 = f2(-h), entropy2 = f2(entropy);
     // nothing to say, or a row of -inf: zeros, and nothing is read
     const bool zero = (p.in.keep && p.in.keep[t] == 0) || lse == -INFINITY || (g == 0.0f && h == 0.0f);
     Vec8<T> v[kBwdVecs];
@@ -432,15 +433,23 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const Logprob
         float x[8] = {};
         if (!zero) {
           v[u].values(x);
-          const int64_t at = y - i;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float lnp = fmaf(x[j], inv, -lse);
-            const float prob = ex2_approx(lnp * kEpiLog2e);
-            float w = g;
-            if (kEntropy) w = fmaf(h, fmaxf(lnp, -256.0f) + entropy, g);
-            x[j] = -w * prob;
-            if (at == j) x[j] += g;
+          for (int j = 0; j < 8; j += 2) {
+            const F2 lnp = fma2(f2(x[j], x[j + 1]), inv2, lse2);
+            const F2 prob = ex2_2(mul2(lnp, f2(kEpiLog2e)));
+            F2 w = g2;  // -(g + h (ln p + H)), where p is not 0
+            if (kEntropy) {
+              float a, b;
+              split(lnp, a, b);
+              w = fma2(h2, add2(f2(fmaxf(a, -256.0f), fmaxf(b, -256.0f)), entropy2), g2);
+            }
+            split(mul2(w, prob), x[j], x[j + 1]);
+          }
+          const int64_t at = y - i;
+          if (at >= 0 && at < 8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (at == j) x[j] += g;
           }
         }
         store8(out + i, static_cast<int>(min(static_cast<int64_t>(8), V - i)), x);
@@ -475,18 +484,18 @@ cudaError_t logprobs_launch_with(const LogprobArgs& a, int threads, int cluster,
 // by 64 threads, 30 by 128, 56 by 256; lists of 20 of 32000 words 123, 111 and
 // 134).  Long rows, and rows that come one to an SM, want as many loads on
 // their way as a block can have (4096 x 128256, lists of 20: 271, 196, 189; 64
-// rows of 128256 words 39, 21, 12), and a list of k comes from the best of at
-// least 2 k threads.
+// rows of 128256 words 39, 21, 12; a mask that leaves few rows does the same
+// to long ones), and a list of k comes from the best of at least 2 k threads.
 int row_threads(const LogprobArgs& a, int cluster, int sms) {
-  const int64_t V = a.in.vocab;
-  if (cluster > 1 || a.k > 64 || V >= 65536 || (V > 8192 && a.in.rows < 4 * sms)) return kStatThreads;
+  const int64_t V = a.in.vocab, bytes = V * (a.in.f32 ? 4 : 2);
+  if (cluster > 1 || a.k > 64 || bytes >= (96 << 10) || (V > 8192 && a.in.rows < 4 * sms)) return kStatThreads;
   return V <= 8192 && a.k <= 16 && a.in.rows >= 12 * sms ? 64 : 128;
 }
 
 }  // namespace
 
 cudaError_t logprobs_launch(const LogprobArgs& a, int sms, bool pdl, cudaStream_t stream) {
-  const int cluster = row_cluster(a.in.rows, a.in.vocab, sms);
+  const int cluster = row_cluster(a.in.rows, a.in.vocab, a.k > 0 ? 4 : 8, sms);
   return logprobs_launch_with(a, row_threads(a, cluster, sms), cluster, pdl, stream);
 }
 

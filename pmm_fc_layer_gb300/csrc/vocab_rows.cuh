@@ -298,12 +298,16 @@ __device__ __forceinline__ void add_units(RowSums& r, const uint4 (&v)[U], float
   r.s += s0 + s1;
 }
 
-// CTAs a row: as many as fill the GPU once, each with some thousands of logits.
-// More only add to what a CTA costs whatever its share (8 a row instead of 2:
-// 256 x 128256, lists of 20, 36 us against 25; 64 rows of fp32 12 against 15).
-inline int row_cluster(int64_t rows, int64_t vocab, int sms) {
+// CTAs a row: up to `per_sm` of them on each SM in all, each with some
+// thousands of logits.  More only add to what a CTA costs whatever its share;
+// that is more where a list is made or a gradient written (4 an SM: 256 x
+// 128256 with lists of 20 takes 25 us by 2 CTAs a row, 36 by 8) than for sums
+// alone (8 an SM: the loss alone of 256 x 128256 19.5 us by 4, 22.9 by 2).
+inline int row_cluster(int64_t rows, int64_t vocab, int per_sm, int sms) {
   int cluster = 1;
-  while (cluster < kMaxCluster && rows * cluster * 2 <= int64_t{4} * sms && vocab / (2 * cluster) >= 4096) cluster *= 2;
+  while (cluster < kMaxCluster && rows * cluster * 2 <= static_cast<int64_t>(per_sm) * sms &&
+         vocab / (2 * cluster) >= 4096)
+    cluster *= 2;
   return cluster;
 }
 
