@@ -453,7 +453,8 @@ axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, u
  *   entropy, dentropy  fp32 [T], H as the forward left it, and h; or both NULL
  *   dlogits            out, of the logits' type, rounded once; may be the
  *                      logits themselves (same ld), else must not overlap them
- * Rows left out, and rows with g = h = 0, are written as zeros and not read.
+ * Rows left out are written as zeros, and so are rows with g = h = 0, whatever
+ * is in them.
  *
  * axonn_distill -- a student's loss against a teacher's lists of k logits
  * (or log probabilities: a list may be shifted by any number), renormalised:

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
       top.segment[j][tid] = seg;
       best = max(best, seg);
     };
-    stream_share<kThreads>(
+    stream_share<kThreads, kUnroll>(
         row, sh,
         [&](int i) {
           if (left == 0) {
@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
     if (j >= 0) flush();
     for (++j; j < kSegments; ++j) top.segment[j][tid] = 0;
   } else {
-    stream_share<kThreads>(row, sh, [](int) {}, [&](const float(&x)[8], int) { add<kEntropy>(r, x, c); });
+    stream_share<kThreads, kUnrollSums<T>>(row, sh, [](int) {},
+                                           [&](const float(&x)[8], int) { add<kEntropy>(r, x, c); });
   }
   if (sh.tail && tid == kThreads - 1) {
     float x[8];
@@ -405,6 +406,13 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const Logprob
   for (int64_t t = blockIdx.y; t < p.in.rows; t += gridDim.y) {
     const T* row = static_cast<const T*>(p.in.logits) + t * p.in.ld;
     T* out = static_cast<T*>(p.dlogits) + t * p.ld_dlogits;
+    const bool kept = !p.in.keep || p.in.keep[t] != 0;
+    Vec8<T> v[kBwdVecs];
+#pragma unroll
+    for (int u = 0; u < kBwdVecs; ++u) {
+      const int64_t i = first + 8 * kBwdThreads * u;
+      if (i < V && kept) v[u].load(row + i, static_cast<int>(min(static_cast<int64_t>(8), V - i)));
+    }
     const float lse = p.lse[t];
     float g = 0.0f, h = 0.0f, entropy = 0.0f;
     int64_t y = -1;
@@ -418,14 +426,8 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const Logprob
       entropy = p.entropy[t];
     }
     const F2 inv2 = f2(inv), lse2 = f2(-lse), g2 = f2(-g), h2 = f2(-h), entropy2 = f2(entropy);
-    // nothing to say, or a row of -inf: zeros, and nothing is read
-    const bool zero = (p.in.keep && p.in.keep[t] == 0) || lse == -INFINITY || (g == 0.0f && h == 0.0f);
-    Vec8<T> v[kBwdVecs];
-#pragma unroll
-    for (int u = 0; u < kBwdVecs; ++u) {
-      const int64_t i = first + 8 * kBwdThreads * u;
-      if (i < V && !zero) v[u].load(row + i, static_cast<int>(min(static_cast<int64_t>(8), V - i)));
-    }
+    // nothing to say, or a row of -inf: zeros
+    const bool zero = !kept || lse == -INFINITY || (g == 0.0f && h == 0.0f);
 #pragma unroll
     for (int u = 0; u < kBwdVecs; ++u) {
       const int64_t i = first + 8 * kBwdThreads * u;
@@ -458,15 +460,15 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const Logprob
   }
 }
 
-// Blocks of kThreads, as many on an SM as their registers allow: 1536 threads
-// where a thread does least, 1280 or 1024 otherwise.
+// Blocks of kThreads, as many on an SM as their registers allow: 1280 or 1024
+// threads.
 template <int kThreads>
 cudaError_t logprobs_launch_blocks(const LogprobArgs& a, int cluster, bool pdl, cudaStream_t stream) {
-  constexpr int kAt6 = 1536 / kThreads, kAt5 = 1280 / kThreads, kAt4 = 1024 / kThreads;
+  constexpr int kAt5 = 1280 / kThreads, kAt4 = 1024 / kThreads;
   using Kernel = void (*)(LogprobArgs);
   static constexpr Kernel kKernels[8] = {
-      logprobs_kernel<uint16_t, false, false, kThreads, kAt6>, logprobs_kernel<uint16_t, false, true, kThreads, kAt5>,
-      logprobs_kernel<uint16_t, true, false, kThreads, kAt5>,  logprobs_kernel<uint16_t, true, true, kThreads, kAt4>,
+      logprobs_kernel<uint16_t, false, false, kThreads, kAt5>, logprobs_kernel<uint16_t, false, true, kThreads, kAt5>,
+      logprobs_kernel<uint16_t, true, false, kThreads, kAt4>,  logprobs_kernel<uint16_t, true, true, kThreads, kAt4>,
       logprobs_kernel<float, false, false, kThreads, kAt4>,    logprobs_kernel<float, false, true, kThreads, kAt4>,
       logprobs_kernel<float, true, false, kThreads, kAt4>,     logprobs_kernel<float, true, true, kThreads, kAt4>};
   const int which = (a.in.f32 ? 4 : 0) + (a.entropy ? 2 : 0) + (a.k > 0 ? 1 : 0);

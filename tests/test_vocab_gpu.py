@@ -341,7 +341,7 @@ def test_backward_masks_and_masked_logits(cuda_lib, kind):
     keep = (rng.random(30) < 0.7).astype(np.uint8)
     keep[4:8] = 1
     g[9] = h[9] = 0
-    x[9] = np.nan                          # no gradient comes in: not read
+    x[9] = np.nan                          # no gradient comes in: zeros
     x[keep == 0] = np.nan
     got = run_backward(cuda_lib, x, kind, lse, tokens, g, H, h, keep)
     assert (got[4] == 0).all() and (got[9] == 0).all() and (got[keep == 0] == 0).all()
