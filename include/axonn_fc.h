@@ -472,7 +472,8 @@ axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, u
  *              word counts finished blocks during the call
  *   dlogits    out, of the logits' type, or NULL for the loss alone; rows not
  *              counted get zeros; in place as above
- * Two launches; the second reads the logits twice, the second time from L2.
+ * Two launches; the logits are read from memory once, as far as a row fits the
+ * shared memory of the CTAs that share it, and what does not again from L2.
  */
 typedef struct {
   const void* logits;

@@ -550,6 +550,23 @@ def test_distill_many_long_rows(cuda_lib, V, kind, in_place):
     assert got["token_loss"][pick == 4][0] == np.inf and got["loss"] == np.inf
 
 
+@pytest.mark.parametrize("k", [1, 3, 255, 256, 257])
+def test_distill_many_long_rows_lists(cuda_lib, k):
+    """Lists of every length that a list warp takes, and one more."""
+    T, kinds, V = 320, 8, 30001
+    x, _, rng = logits_of(kinds, V, "bf16", seed=28)
+    at, t = lists_of(x, k, rng)
+    at[1, k // 2:] = at[1, 0]  # the same index many times
+    pick = np.arange(T) % kinds
+    got = run_distill(cuda_lib, x[pick], "bf16", at[pick], t[pick])
+    for r in range(kinds):
+        assert (got["dlogits"][pick == r] == got["dlogits"][r]).all()
+    # the first of each as a batch of their own, whose mean's gradient is T / kinds times theirs
+    one = {"token_loss": got["token_loss"][:kinds], "dlogits": got["dlogits"][:kinds], "kept": kinds,
+           "loss": vo.distill(x, at, t)["loss"]}
+    check_distill(one, x, "bf16", at, t, None, 1.0, kinds / T)
+
+
 def test_distill_expired_wait_is_reported(cuda_lib):
     """The producer withholds its copies: the waits run out, the call reports
     it, and the next one is right."""
@@ -755,6 +772,49 @@ def test_more_rows_than_a_grid_dimension(cuda_lib):
     g = rng.normal(size=70000).astype(np.float32)
     lse = got["lse"].astype(np.float32)
     check_backward(run_backward(cuda_lib, x, "f32", lse, tokens, g), x, "f32", lse, tokens, g)
+
+
+def test_a_row_past_2_31_bytes(cuda_lib):
+    """One row of 1.1e9 words, zeros but for a few: closed forms, and offsets in
+    bytes past 2^31 in every kernel that takes it."""
+    import math
+
+    import torch
+    fc = cuda_lib
+    V, k = 1_100_000_005, 4
+    X = torch.zeros((1, V + 3), dtype=torch.bfloat16, device="cuda")[:, :V]
+    places, values = [V - 1, 12, 1_073_741_830, 536_870_921], [24.0, 23.0, 22.0, 21.0]
+    for at, v in zip(places, values):
+        X[0, at] = v
+    lse = math.log(V - k + sum(math.exp(v) for v in values))
+    lp, H, out = (torch.empty(1, device="cuda") for _ in range(3))
+    index = torch.empty((1, k), dtype=torch.int32, device="cuda")
+    value = torch.empty((1, k), device="cuda")
+    fc.axonn_token_logprobs(X, tokens=i32([places[2]]), logprob=lp, entropy=H, lse=out, top_index=index,
+                            top_logprob=value)
+    assert host(index)[0].tolist() == places
+    # sums of 1.1e9 terms over 8 x 256 threads: 67138 vectors each, 2^-24 for each
+    # addition; the terms are equal, so their roundings may all go one way
+    tol = 2.0**-24 * V / (8 * 2048) * 2 + 2.0**-20
+    assert abs(host(out)[0] - lse) <= tol and abs(host(lp)[0] - (values[2] - lse)) <= tol
+    assert np.abs(host(value)[0] - (np.array(values) - lse)).max() <= tol
+    d = torch.full((1, V + 3), 7.0, dtype=torch.bfloat16, device="cuda")[:, :V]
+    fc.axonn_token_logprobs_bwd(X, out, d, tokens=i32([places[2]]), dlogprob=f32([1.0]))
+    p0 = math.exp(-lse)
+    got = host(d[0, torch.tensor([*places, 0, V - 2], device="cuda")])
+    want = np.array([-math.exp(v - lse) for v in values] + [-p0, -p0])
+    want[2] += 1
+    assert (np.abs(got - want) <= (2.0**-8 + 2 * tol) * np.abs(want) + 2 * tol).all()
+    assert bool((d[0, 100:200].double() / -p0 - 1).abs().max() <= 2.0**-8 + 2 * tol)
+    fc.axonn_distill(X, index, value, lp, H, i32([0]), dlogits=d)
+    got = host(d[0, torch.tensor([*places, 0, V - 2], device="cuda")])
+    q = np.exp(np.array(values) - 24)
+    q = q / q.sum()
+    want = np.array([math.exp(v - lse) - w for v, w in zip(values, q)] + [p0, p0])
+    assert (np.abs(got - want) <= (2.0**-8 + 2 * tol) * np.abs(want) + 4 * tol * np.append(q, [p0, p0])).all()
+    kl = float((q * (np.log(q) - (np.array(values) - lse))).sum())
+    assert abs(host(lp)[0] - kl) <= 2 * tol
+    assert bool((d._base[:, V:] == 7).all())
 
 
 def test_no_rows(cuda_lib):
