@@ -527,7 +527,9 @@ def _logits(logits):
     """(device, rows, columns, dtype, IN_F32 or 0) of logits, whose device must
     be the current one."""
     here = logits.get_device()
-    if here >= 0 and here != _current_device():
+    if here < 0:
+        raise ValueError(f"logits must be on the device, got {logits.device}")
+    if here != _current_device():
         raise ValueError(f"logits are on device {here}, which is not the current one")
     rows, cols = logits.shape
     f32 = _dtypes["f32"]
@@ -540,12 +542,8 @@ def _beside(name, t, dtype, shape, here):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
-    at = t.get_device()
-    if at != here:
-        if at >= 0 and here >= 0:
-            raise ValueError(f"{name} is on device {at}, the logits on {here}")
-    if at < 0:
-        _host_memory(name, t)
+    if t.get_device() != here:
+        raise ValueError(f"{name} must be on the logits' device {here}, got {t.device}")
 
 
 def _whole(name, t, dtype, shape, here):

@@ -513,9 +513,11 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
     __syncwarp();
   } else if (warp <= kListWarps) {
     // ------------------------------------------------------------ lists
+    // a wait that ran out for one lane has for all: they go on together
+    auto all_lanes = [](bool mine) { return __all_sync(kAll, mine) != 0; };
     auto prepare = [&](uint32_t r) {
       RowSlot& slot = tl->slot[r % kRowSlots];
-      ok = ok && row_wait(tl->row_full[r % kRowSlots], parity(r), tmo, 4);
+      ok = all_lanes(ok && row_wait(tl->row_full[r % kRowSlots], parity(r), tmo, 4));
       if (!ok || slot.row < 0) return false;
       if (slot.counts) take_list<T>(a, slot.row, list_of(r), slot, c);
       if (lane == 0) arrive(tl->list_full[r % kRowSlots]);
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
       const int64_t t = slot.row;
       const bool counts = slot.counts;
       more = prepare(r + kListWarps);
-      ok = ok && row_wait(tl->sums_full[r % kRowSlots], parity(r), tmo, 5);
+      ok = all_lanes(ok && row_wait(tl->sums_full[r % kRowSlots], parity(r), tmo, 5));
       if (ok && !counts && lane == 0) a.token_loss[t] = 0.0f;
       if (ok && counts) {
         const float log2w = log2f(slot.sum), log2s = log2f(slot.s);
@@ -542,7 +544,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
         for (int o = 1; o < 32; o <<= 1) kl += __shfl_xor_sync(kAll, kl, o);
         if (lane == 0) a.token_loss[t] = kl * (kRowLn2 * a.in.temperature * a.in.temperature);
       }
-      ok = ok && row_wait(tl->written[r % kRowSlots], parity(r), tmo, 6);
+      ok = all_lanes(ok && row_wait(tl->written[r % kRowSlots], parity(r), tmo, 6));
       if (ok && counts) {
         const float scale = a.grad_scale * a.in.temperature / static_cast<float>(*a.kept);
         const float share = slot.s == 0.0f || slot.sum == 0.0f ? 0.0f : scale / slot.s;

@@ -176,10 +176,11 @@ def test_logprobs_many_rows(cuda_lib, T, V, ks, kind):
     x[::5] = np.round(x[::5])  # ties
     pick = np.arange(T) % len(x)
     for k in ks:
-        got = run_logprobs(cuda_lib, x[pick], kind, tokens[pick], k=k)
-        check_logprobs({n: v[:len(x)] for n, v in got.items()}, x, tokens, k=k)
-        for n, v in got.items():
-            assert np.array_equal(v, v[:len(x)][pick]), n
+        for entropy in (False, True):
+            got = run_logprobs(cuda_lib, x[pick], kind, tokens[pick], k=k, entropy=entropy)
+            check_logprobs({n: v[:len(x)] for n, v in got.items()}, x, tokens, k=k)
+            for n, v in got.items():
+                assert np.array_equal(v, v[:len(x)][pick]), n
 
 
 def special_rows(V, kind):
@@ -499,6 +500,37 @@ def test_distill_nothing_counted(cuda_lib, T):
     at[:, 0] = -1
     got = run_distill(cuda_lib, x[:T], "bf16", at[:T], t[:T])
     assert got["kept"] == 0 and got["loss"] == 0 and (got["token_loss"] == 0).all() and (got["dlogits"] == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V,k", [(1900, 301, 200), (1900, 2050, 9), (700, 1003, 300)])
+def test_distill_many_short_rows(cuda_lib, T, V, k, kind):
+    """Small blocks, and lists longer than they are."""
+    x, _, rng = logits_of(53, V, kind, seed=29)
+    at, t = lists_of(x, k, rng)
+    at[7, k // 2:] = at[7, 0]
+    at[9, 0] = -1
+    pick = np.arange(T) % 53
+    n = (pick != 9).sum()
+    for grad in (False, True):
+        got = run_distill(cuda_lib, x[pick], kind, at[pick], t[pick], tau=0.9, grad=grad)
+        assert got["kept"] == n
+        one = {"token_loss": got["token_loss"][:53], "kept": 52}
+        one["loss"] = vo.distill(x, at, t, None, float(np.float32(0.9)))["loss"]
+        if grad:
+            assert (got["dlogits"] == got["dlogits"][:53][pick]).all()
+            one["dlogits"] = got["dlogits"][:53]
+        check_distill(one, x, kind, at, t, None, 0.9, 52 / n)
+        mean = got["token_loss"].sum() / n
+        assert abs(got["loss"] - mean) <= 2.0**-24 * (T / 128 + 32) * mean
+
+
+def test_distill_a_share_larger_than_shared_memory(cuda_lib):
+    """What a CTA cannot hold it reads again."""
+    x, _, rng = logits_of(2, 500003, "f32", seed=30)
+    at, t = lists_of(x, 20, rng)
+    for in_place in (False, True):
+        check_distill(run_distill(cuda_lib, x, "f32", at, t, in_place=in_place), x, "f32", at, t)
 
 
 def test_distill_longest_lists(cuda_lib):

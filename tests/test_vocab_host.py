@@ -190,44 +190,101 @@ def test_distill_refusals(fc, change, expect):
     refuse(fc, "axonn_distill", DIS, change, expect)
 
 
-def test_binding_refuses_wrong_tensors(fc):
-    import torch
-    bf = torch.zeros(4, 64, dtype=torch.bfloat16)
-    f, i = torch.zeros(4), torch.zeros(4, dtype=torch.int32)
-    lists = torch.zeros(4, 8, dtype=torch.int32)
-    with pytest.raises(ValueError):  # memory that the GPU cannot reach
-        fc.axonn_token_logprobs(bf, tokens=i, logprob=f)
-    with pytest.raises(ValueError):  # half precision
-        fc.axonn_token_logprobs(bf.half(), tokens=i, logprob=f)
-    with pytest.raises(ValueError):  # 64-bit indices
-        fc.axonn_token_logprobs(bf, top_index=lists.long())
-    with pytest.raises(ValueError):
-        fc.axonn_token_logprobs_bwd(bf, f, bf.float(), tokens=i, dlogprob=f)
-    with pytest.raises(ValueError):
-        fc.axonn_distill(bf, lists, torch.zeros(4, 7), f, f[:1], i[:1])
+class At:
+    """A tensor of some device, type, shape and strides, as far as the binding
+    looks before the call."""
+
+    def __init__(self, shape, dtype, device=0, stride=None):
+        import torch
+        self.shape, self.at = torch.Size(shape), device
+        self.dtype = getattr(torch, dtype)
+        full = torch.empty(shape, device="meta") if stride is None else torch.empty_strided(shape, stride, device="meta")
+        self.strides, self.whole = full.stride(), full.is_contiguous()
+        self.device = f"cuda:{device}" if device >= 0 else "cpu"
+
+    def get_device(self):
+        return self.at
+
+    def stride(self):
+        return self.strides
+
+    def is_contiguous(self):
+        return self.whole
+
+    def data_ptr(self):
+        return FAKE
 
 
-def test_binding_refuses_other_devices(fc, monkeypatch):
-    import torch
+@pytest.fixture
+def on_device_0(fc, monkeypatch):
+    """The checks as on device 0; a call that gets past them says so."""
+    class Past(Exception):
+        pass
 
-    class At:
-        """A tensor of some device, as far as the checks look before the call."""
-        def __init__(self, device, shape, dtype):
-            self.device, self.shape, self.dtype = device, shape, dtype
-
-        def get_device(self):
-            return self.device
-
-        def stride(self):
-            return self.shape[1], 1
-
-        def is_contiguous(self):
-            return True
-
-        def data_ptr(self):
-            return FAKE
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                raise Past(name)
+            return call
     monkeypatch.setattr(fc, "_current_device", lambda: 0)
-    with pytest.raises(ValueError, match="not the current one"):
-        fc.axonn_token_logprobs(At(1, (4, 64), torch.bfloat16), lse=At(1, (4,), torch.float32))
-    with pytest.raises(ValueError, match="lse is on device 1"):
-        fc.axonn_token_logprobs(At(0, (4, 64), torch.bfloat16), lse=At(1, (4,), torch.float32))
+    monkeypatch.setattr(fc, "_current_stream", lambda: 0)
+    monkeypatch.setattr(fc, "load", lambda: Library())
+    return Past
+
+
+BF, I4, F4 = ((4, 64), "bfloat16"), ((4,), "int32"), ((4,), "float32")
+LISTS = dict(top_index=((4, 8), "int32"), top_logprob=((4, 8), "float32"))
+
+
+@pytest.mark.parametrize("logits,others,say", [
+    (((4, 64), "float16"), dict(lse=F4), "logits must be torch.bfloat16"),
+    (((4, 64), "bfloat16", -1), dict(lse=F4), "logits must be on the device"),
+    (((4, 64), "bfloat16", 1), dict(lse=F4), "not the current one"),
+    (((4, 64), "bfloat16", 0, (1, 4)), dict(lse=F4), "unit column stride"),
+    (BF, dict(lse=((4,), "float32", 1)), "lse must be on the logits' device 0"),
+    (BF, dict(lse=((4,), "float32", -1)), "lse must be on the logits' device 0"),
+    (BF, dict(lse=((4,), "float64")), "lse must be torch.float32"),
+    (BF, dict(lse=((5,), "float32")), "lse must be"),
+    (BF, dict(lse=((4,), "float32", 0, (2,))), "lse must be contiguous"),
+    (BF, dict(tokens=((4,), "int64"), logprob=F4), "tokens must be torch.int32"),
+    (BF, dict(tokens=I4, logprob=F4, keep=((4,), "bool")), "keep must be torch.uint8"),
+    (BF, dict(top_index=((4, 8), "int64")), "top_index must be torch.int32"),
+    (BF, dict(LISTS, top_logprob=((4, 7), "float32")), "top_logprob must be"),
+    (BF, dict(LISTS, top_logprob=((4, 8), "float32", 0, (16, 1))), "same row stride"),
+    (BF, dict(LISTS, lse=F4), None),
+    (((1, 50257), "bfloat16", 0, (3, 1)), dict(lse=((1,), "float32")), None),
+])
+def test_binding_logprobs(fc, on_device_0, logits, others, say):
+    args = {name: At(*v) for name, v in others.items()}
+    with pytest.raises(ValueError if say else on_device_0, match=say):
+        fc.axonn_token_logprobs(At(*logits), **args)
+
+
+@pytest.mark.parametrize("others,say", [
+    (dict(dlogits=((4, 64), "float32")), "dlogits must be torch.bfloat16"),
+    (dict(dlogits=((4, 60), "bfloat16")), "dlogits must be"),
+    (dict(lse=((4,), "bfloat16")), "lse must be torch.float32"),
+    (dict(dlogprob=((3,), "float32")), "dlogprob must be"),
+    (dict(dentropy=((4,), "float32", 1)), "dentropy must be on"),
+    ({}, None),
+])
+def test_binding_backward(fc, on_device_0, others, say):
+    args = {name: At(*v) for name, v in {**dict(lse=F4, dlogits=BF, tokens=I4, dlogprob=F4), **others}.items()}
+    with pytest.raises(ValueError if say else on_device_0, match=say):
+        fc.axonn_token_logprobs_bwd(At(*BF), **args)
+
+
+@pytest.mark.parametrize("others,say", [
+    (dict(top_logit=((4, 7), "float32")), "top_logit must be"),
+    (dict(top_index=((4, 8), "int64")), "top_index must be torch.int32"),
+    (dict(kept=((1,), "int64")), "kept must be torch.int32"),
+    (dict(loss=((), "float32")), "loss must be"),
+    (dict(dlogits=((4, 64), "bfloat16", 0, (1, 4))), "unit column stride"),
+    ({}, None),
+])
+def test_binding_distill(fc, on_device_0, others, say):
+    base = dict(top_index=((4, 8), "int32"), top_logit=((4, 8), "float32"), token_loss=F4, loss=((1,), "float32"),
+                kept=((1,), "int32"), dlogits=BF)
+    args = {name: At(*v) for name, v in {**base, **others}.items()}
+    with pytest.raises(ValueError if say else on_device_0, match=say):
+        fc.axonn_distill(At(*BF), **args)
