@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(kDistThreads) distill_kernel(const DistillArgs
       take_group(3);
       for (int i = keep + tid; i < units; i += kDistThreads) take(src[i]);
     } else {
-      stream_share<kDistThreads, kUnrollSums<T>>(row, sh, [](int) {},
-                                                 [&](const float(&x)[8], int) { add<false>(r, x, c); });
+      stream_share<kDistThreads, kUnrollSums<T>, true>(row, sh, [](int) {},
+                                                       [&](const float(&x)[8], int) { add<false>(r, x, c); });
     }
     if (sh.tail && tid == kDistThreads - 1) {
       float x[8];

@@ -10,15 +10,18 @@ namespace axonn {
 // vectors are 16-byte aligned: base pointers and leading dimensions are
 // checked by the host and columns are multiples of 8.  Every element is
 // touched once, so loads and stores are marked streaming (not kept in the
-// caches at the expense of others).
+// caches at the expense of others); load<false> is for those that are read
+// again.
 template <typename T>
 struct Vec8;
 template <>
 struct Vec8<uint16_t> {
   uint32_t w[4];
+  template <bool kOnce = true>
   __device__ __forceinline__ void load(const uint16_t* p, int n) {
     if (n >= 8) {
-      const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+      const uint4* q = reinterpret_cast<const uint4*>(p);
+      const uint4 a = kOnce ? __ldcs(q) : *q;
       w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
     } else {
 #pragma unroll
@@ -37,9 +40,11 @@ struct Vec8<uint16_t> {
 template <>
 struct Vec8<float> {
   float w[8];
+  template <bool kOnce = true>
   __device__ __forceinline__ void load(const float* p, int n) {
     if (n >= 8) {
-      const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+      const float4* q = reinterpret_cast<const float4*>(p);
+      const float4 a = kOnce ? __ldcs(q) : q[0], b = kOnce ? __ldcs(q + 1) : q[1];
       w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
       w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
     } else {

@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
       top.segment[j][tid] = seg;
       best = max(best, seg);
     };
-    stream_share<kThreads, kUnroll>(
+    stream_share<kThreads, kUnroll, false>(
         row, sh,
         [&](int i) {
           if (left == 0) {
@@ -243,8 +243,8 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
     if (j >= 0) flush();
     for (++j; j < kSegments; ++j) top.segment[j][tid] = 0;
   } else {
-    stream_share<kThreads, kUnrollSums<T>>(row, sh, [](int) {},
-                                           [&](const float(&x)[8], int) { add<kEntropy>(r, x, c); });
+    stream_share<kThreads, kUnrollSums<T>, true>(row, sh, [](int) {},
+                                                 [&](const float(&x)[8], int) { add<kEntropy>(r, x, c); });
   }
   if (sh.tail && tid == kThreads - 1) {
     float x[8];

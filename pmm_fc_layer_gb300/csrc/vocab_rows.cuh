@@ -195,14 +195,14 @@ template <typename T>
 constexpr int kUnrollSums = sizeof(T) == 2 ? 3 : 2;
 
 // Streams a share: f(logits, vector) for every whole vector, a thread every
-// kThreads-th, ascending; next(batch) before each batch of kVectors of them.
-template <int kThreads, int kVectors, typename T, class Next, class F>
+// kThreads-th, ascending; next(batch) before each batch of kVectors of them.  kOnce: not read again.
+template <int kThreads, int kVectors, bool kOnce, typename T, class Next, class F>
 __device__ __forceinline__ void stream_share(const T* row, const Share& sh, Next&& next, F&& f) {
   constexpr int kStep = kThreads * kVectors;
   auto load = [&](Vec8<T>(&v)[kVectors], int i0) {
 #pragma unroll
     for (int u = 0; u < kVectors; ++u)
-      if (i0 + kThreads * u < sh.end) v[u].load(row + static_cast<int64_t>(i0 + kThreads * u) * 8, 8);
+      if (i0 + kThreads * u < sh.end) v[u].template load<kOnce>(row + static_cast<int64_t>(i0 + kThreads * u) * 8, 8);
   };
   auto use = [&](const Vec8<T>(&v)[kVectors], int i0) {
     next(i0);
