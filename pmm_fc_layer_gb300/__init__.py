@@ -88,6 +88,8 @@ def library_path() -> str:
 def load(path: str | None = None):
     """Load the built library (raises if it is absent)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -536,23 +538,23 @@ def _logits(logits):
     return (here, rows, cols, f32, IN_F32) if logits.dtype is f32 else (here, rows, cols, _dtypes["bf16"], 0)
 
 
-def _beside(name, t, dtype, shape, here):
-    """Checks a tensor's type, shape and place beside logits on device `here`."""
+def _refuse(name, t, dtype, shape, here):
+    """Says what is wrong with a tensor beside logits on device `here`."""
     if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
     if t.get_device() != here:
         raise ValueError(f"{name} must be on the logits' device {here}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _whole(name, t, dtype, shape, here):
     """Address of a contiguous tensor beside the logits, 0 for None."""
     if t is None:
         return 0
-    _beside(name, t, dtype, shape, here)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != here or not t.is_contiguous():
+        _refuse(name, t, dtype, shape, here)
     return t.data_ptr()
 
 
@@ -561,7 +563,8 @@ def _rows(name, t, dtype, shape, here, single):
     The stride of a single row says nothing: it counts as `single`."""
     if t is None:
         return 0, 0
-    _beside(name, t, dtype, shape, here)
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != here:
+        _refuse(name, t, dtype, shape, here)
     ld, inner = t.stride()
     if inner != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have unit column stride")
