@@ -741,7 +741,7 @@ cudaError_t distill_launch(const DistillArgs& a, int sms, uint64_t timeout_ns, i
   const int64_t bytes = a.in.vocab / 8 * (a.in.f32 ? 32 : 16);
   if (a.dlogits && streams_rows(a.in.rows, bytes, a.k, sms))
     return distill_ring_launch(a, sms, timeout_ns, inject, pdl, stream);
-  int cluster = row_cluster(a.in.rows, a.in.vocab, a.dlogits ? 4 : 8, sms);
+  int cluster = row_cluster(a.in.rows, a.in.vocab, sms);
   while (a.dlogits && cluster < kMaxCluster && bytes / cluster > kHeldBytes) cluster *= 2;
   return distill_shares_launch(a, row_threads(a, bytes, sms), cluster, pdl, stream);
 }

@@ -507,7 +507,7 @@ int row_threads(const LogprobArgs& a, int cluster, int sms) {
 }  // namespace
 
 cudaError_t logprobs_launch(const LogprobArgs& a, int sms, bool pdl, cudaStream_t stream) {
-  const int cluster = row_cluster(a.in.rows, a.in.vocab, a.k > 0 ? 4 : 8, sms);
+  const int cluster = row_cluster(a.in.rows, a.in.vocab, sms);
   return logprobs_launch_with(a, row_threads(a, cluster, sms), cluster, pdl, stream);
 }
 

@@ -304,16 +304,14 @@ __device__ __forceinline__ void add_units(RowSums& r, const uint4 (&v)[U], float
   r.s += s0 + s1;
 }
 
-// CTAs a row: up to `per_sm` of them on each SM in all, each with some
-// thousands of logits.  More only add to what a CTA costs whatever its share;
-// that is more where a list is made or a gradient written (4 an SM: 256 x
-// 128256 with lists of 20 takes 25 us by 2 CTAs a row, 36 by 8) than for sums
-// alone (8 an SM: the loss alone of 256 x 128256 19.5 us by 4, 22.9 by 2).
-inline int row_cluster(int64_t rows, int64_t vocab, int per_sm, int sms) {
+// CTAs a row: up to four on each SM in all, each with some thousands of logits.
+// More only add to what a CTA costs whatever its share, and rows in shares of
+// which some wait for a place take longer than whole rows (sums of 128256 words
+// with a cold L2: 100 rows 14.0 us by 4 CTAs a row, 16.0 by 2 or 8; 200 rows
+// 18.7 by 2, 20.8 by 4; 400 rows 26.3 whole, 32.4 by 2; lists of 20 alike).
+inline int row_cluster(int64_t rows, int64_t vocab, int sms) {
   int cluster = 1;
-  while (cluster < kMaxCluster && rows * cluster * 2 <= static_cast<int64_t>(per_sm) * sms &&
-         vocab / (2 * cluster) >= 4096)
-    cluster *= 2;
+  while (cluster < kMaxCluster && rows * cluster * 2 <= int64_t{4} * sms && vocab / (2 * cluster) >= 4096) cluster *= 2;
   return cluster;
 }
 
