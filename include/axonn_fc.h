@@ -431,7 +431,8 @@ axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, u
  * its own probabilities.  No workspace.
  *
  * axonn_token_logprobs -- scoring, answering and a teacher's lists, in one
- * launch that reads the logits once.  Each output may be NULL:
+ * launch that reads the logits once (what a list may come from, again).  Each
+ * output may be NULL:
  *   tokens   int32 [T], given with logprob: a token outside [0, V) (padding)
  *            has logprob 0; the row's other outputs are as for any row
  *   logprob  out, fp32 [T]: ln p of the row's token
@@ -469,7 +470,7 @@ axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, u
  *   A row counts when keep does not leave it out and its list is not empty.
  *   token_loss out, fp32 [T]: 0 where not counted; +inf where q > 0 at p = 0
  *   loss, kept out, fp32 [1] and int32 [1] (n); loss is 0 for n = 0, and its
- *              word counts finished blocks during the call
+ *              word is the kernels' counter during the call
  *   dlogits    out, of the logits' type, or NULL for the loss alone; rows not
  *              counted get zeros; in place as above
  * Two launches; the logits are read from memory once, as far as a row fits the
