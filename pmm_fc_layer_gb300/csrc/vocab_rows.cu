@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const Logprob
 // threads.
 template <int kThreads>
 cudaError_t logprobs_launch_blocks(const LogprobArgs& a, int cluster, bool pdl, cudaStream_t stream) {
-  constexpr int kAt5 = 1280 / kThreads, kAt4 = 1024 / kThreads;
+  constexpr int kAt5 = std::min(32, 1280 / kThreads), kAt4 = 1024 / kThreads;
   using Kernel = void (*)(LogprobArgs);
   static constexpr Kernel kKernels[8] = {
       logprobs_kernel<uint16_t, false, false, kThreads, kAt5>, logprobs_kernel<uint16_t, false, true, kThreads, kAt5>,
@@ -486,22 +486,26 @@ cudaError_t logprobs_launch_blocks(const LogprobArgs& a, int cluster, bool pdl, 
   return launch_clusters(kKernels[which], grid, static_cast<unsigned>(cluster), kThreads, pdl, stream, 0, a);
 }
 cudaError_t logprobs_launch_with(const LogprobArgs& a, int threads, int cluster, bool pdl, cudaStream_t stream) {
+  if (threads == 32) return logprobs_launch_blocks<32>(a, cluster, pdl, stream);
   if (threads == 64) return logprobs_launch_blocks<64>(a, cluster, pdl, stream);
   if (threads == 128) return logprobs_launch_blocks<128>(a, cluster, pdl, stream);
   return logprobs_launch_blocks<kStatThreads>(a, cluster, pdl, stream);
 }
 
 // Threads a block: what a block costs whatever its row is the work of its
-// warps, so short rows have few (8192 rows, lists of 8 of 2000 words: 21.5 us
-// by 64 threads, 30 by 128, 56 by 256; lists of 20 of 32000 words 123, 111 and
-// 134).  Long rows, and rows that come one to an SM, want as many loads on
-// their way as a block can have (4096 x 128256, lists of 20: 271, 196, 189; 64
-// rows of 128256 words 39, 21, 12; a mask that leaves few rows does the same
-// to long ones), and a list of k comes from the best of at least 2 k threads.
+// warps, so short rows have few (8192 rows of 2000 words, lists of 8: 15.6 us by
+// 32 threads, 21.0 by 64, 26.7 by 128, 48.8 by 256; lists of 20 of 32000 words
+// 123 by 64, 111 by 128, 134 by 256).  Long rows, and rows that come one to an
+// SM, want as many loads on their way as a block can have (4096 x 128256, lists
+// of 20: 271 by 64, 196, 189; 64 rows of 128256 words 39, 21, 12; a mask that
+// leaves few rows does the same to long ones), and a list of k comes from the
+// best of at least 2 k threads, or better 3 k (lists of 16 of 1000 words 28 by
+// 32 threads, 20 by 64; of 32 of 2000 words 42 by 64, 33 by 128).
 int row_threads(const LogprobArgs& a, int cluster, int sms) {
   const int64_t V = a.in.vocab, bytes = V * (a.in.f32 ? 4 : 2);
   if (cluster > 1 || a.k > 64 || bytes >= (96 << 10) || (V > 8192 && a.in.rows < 4 * sms)) return kStatThreads;
-  return V <= 8192 && a.k <= 16 && a.in.rows >= 12 * sms ? 64 : 128;
+  if (V > 8192 || a.k > 24 || a.in.rows < 6 * sms) return 128;
+  return V <= 4096 && a.k <= 10 ? 32 : 64;
 }
 
 }  // namespace
