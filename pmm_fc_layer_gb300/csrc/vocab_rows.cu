@@ -51,7 +51,7 @@ struct alignas(16) TopShared {
   uint64_t bound;
   uint16_t again[kSegments * kThreads];  // segments that reach the bound
   uint64_t part[kThreads / 32];
-  uint64_t list[kMaxTop];
+  uint64_t list[kThreads];
   int segments, entries, listed;
 };
 
@@ -73,27 +73,15 @@ __device__ __noinline__ uint64_t next_entry(const T* row, const Share sh, uint64
   return best;
 }
 
-// A number that at least k (or else all) of the block's numbers reach, and at
-// most `most` unless fewer numbers than k are not 0.  All are different, and
-// below `hi`.  One warp's work: it reads them all, and the others wait (every
-// warp counting its own, with a barrier for each step, took four times the
-// instructions).
-template <int kThreads>
-__device__ __forceinline__ uint64_t bound_of(const uint64_t* numbers, int k, int most, uint64_t hi) {
-  uint64_t mine[kThreads / 32];
-#pragma unroll
-  for (int j = 0; j < kThreads / 32; ++j) mine[j] = numbers[(threadIdx.x & 31) + 32 * j];
-  auto reach = [&](uint64_t x) {
-    int n = 0;
-#pragma unroll
-    for (int j = 0; j < kThreads / 32; ++j) n += mine[j] >= x ? 1 : 0;
-    return __reduce_add_sync(kAll, n);
-  };
-  int n = reach(1);
-  if (n <= most) return 1;
-  // downwards from hi in growing steps, then by halves: n reach lo, fewer than k hi
+// A number that at least k numbers reach and at most `most`, where reach(x)
+// says how many reach x; all are different and below `hi`, and more than `most`
+// reach 1.  Downwards from hi in growing steps, then by halves: n reach lo, fewer
+// than k hi.
+template <class F>
+__device__ __forceinline__ uint64_t seek_bound(int k, int most, uint64_t hi, F&& reach) {
   uint64_t lo = hi, step = static_cast<uint64_t>(1) << 50;
-  for (n = 0; n < k; step <<= 2) {
+  int n = 0;
+  for (; n < k; step <<= 2) {
     hi = lo;
     lo = step < hi && step < (static_cast<uint64_t>(1) << 62) ? hi - step : 1;
     n = reach(lo);
@@ -111,34 +99,46 @@ __device__ __forceinline__ uint64_t bound_of(const uint64_t* numbers, int k, int
   return lo;
 }
 
-// Leaves the k largest of n > k entries, all different, as the first ones.
+// That among the block's numbers, or 1 where no more than `most` are not 0.
+// One warp's work: it reads them all, and the others wait (every warp counting
+// its own, with a barrier for each step, took four times the instructions).
 template <int kThreads>
-__device__ __noinline__ void cut_entries(TopShared<kThreads>& sh, int n, int k) {
+__device__ __forceinline__ uint64_t bound_of(const uint64_t* numbers, int k, int most, uint64_t hi) {
+  uint64_t mine[kThreads / 32];
+#pragma unroll
+  for (int j = 0; j < kThreads / 32; ++j) mine[j] = numbers[(threadIdx.x & 31) + 32 * j];
+  auto reach = [&](uint64_t x) {
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < kThreads / 32; ++j) n += mine[j] >= x ? 1 : 0;
+    return __reduce_add_sync(kAll, n);
+  };
+  return reach(1) <= most ? 1 : seek_bound(k, most, hi, reach);
+}
+
+// Of n entries, all different and more than kThreads, leaves at least the k
+// largest and at most kThreads as the first ones; returns how many.
+template <int kThreads>
+__device__ __noinline__ int cut_entries(TopShared<kThreads>& sh, int n, int k, uint64_t hi) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint64_t lo = 1, hi = ~static_cast<uint64_t>(0);
-  int reach = n;
-  while (reach > k) {
-    const uint64_t mid = lo + (hi - lo) / 2;
+  const uint64_t lo = seek_bound(k, kThreads, hi, [&](uint64_t x) {
     int c = 0;
-    for (int i = threadIdx.x; i < n; i += kThreads) c += sh.entry[i] >= mid ? 1 : 0;
+    for (int i = threadIdx.x; i < n; i += kThreads) c += sh.entry[i] >= x ? 1 : 0;
     c = __reduce_add_sync(kAll, c);
     if (lane == 0) sh.part[warp] = static_cast<uint64_t>(c);
     __syncthreads();
     c = 0;
     for (int w = 0; w < kThreads / 32; ++w) c += static_cast<int>(sh.part[w]);
     __syncthreads();
-    if (c >= k) {
-      lo = mid;
-      reach = c;
-    } else {
-      hi = mid;
-    }
-  }
+    return c;
+  });
   for (int i = threadIdx.x; i < n; i += kThreads)
     if (sh.entry[i] >= lo) sh.list[atomicAdd(&sh.listed, 1)] = sh.entry[i];
   __syncthreads();
-  for (int i = threadIdx.x; i < k; i += kThreads) sh.entry[i] = sh.list[i];
+  n = sh.listed;
+  for (int i = threadIdx.x; i < n; i += kThreads) sh.entry[i] = sh.list[i];
   __syncthreads();
+  return n;
 }
 
 // The best segments of a share by whole-number order, for rows with a NaN,
@@ -329,8 +329,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
       n = k;
       __syncthreads();
     } else if (n > 2 * kThreads) {
-      cut_entries(top, n, k);
-      n = k;
+      n = cut_entries(top, n, k, hi);
     }
     // each candidate's place is the number of larger ones
     const float lns = log2f(r.s) * kRowLn2;
@@ -372,13 +371,15 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
         if (e == 0) continue;
         int above[kMaxCluster] = {};
         for (int step = half; step; step /= 2) {
+          uint64_t at[kMaxCluster];  // without a branch, so that the loads go together
 #pragma unroll
-          for (int l = 0; l < kMaxCluster; ++l)
-            if (l < ctas && above[l] + step <= p.k && lists[l * p.k + above[l] + step - 1] > e) above[l] += step;
+          for (int l = 0; l < kMaxCluster; ++l) at[l] = lists[min(l, ctas - 1) * p.k + min(above[l] + step, p.k) - 1];
+#pragma unroll
+          for (int l = 0; l < kMaxCluster; ++l) above[l] += above[l] + step <= p.k && at[l] > e ? step : 0;
         }
         int place = 0;
 #pragma unroll
-        for (int l = 0; l < kMaxCluster; ++l) place += above[l];
+        for (int l = 0; l < kMaxCluster; ++l) place += l < ctas ? above[l] : 0;
         if (place < p.k) write(place, e, r.m, r.s, ln_s);
       }
     }
@@ -500,12 +501,15 @@ cudaError_t logprobs_launch_with(const LogprobArgs& a, int threads, int cluster,
 // of 20: 271 by 64, 196, 189; 64 rows of 128256 words 39, 21, 12; a mask that
 // leaves few rows does the same to long ones), and a list of k comes from the
 // best of at least 2 k threads, or better 3 k (lists of 16 of 1000 words 28 by
-// 32 threads, 20 by 64; of 32 of 2000 words 42 by 64, 33 by 128).
+// 32 threads, 20 by 64; of 32 of 2000 words 42 by 64, 33 by 128).  In between it
+// is the number of rows (lists of 20 of 4000 words: 2000 rows 12.9 by 64, 11.0
+// by 128; 3000 rows 13.3 and 14.3).
 int row_threads(const LogprobArgs& a, int cluster, int sms) {
   const int64_t V = a.in.vocab, bytes = V * (a.in.f32 ? 4 : 2);
   if (cluster > 1 || a.k > 64 || bytes >= (96 << 10) || (V > 8192 && a.in.rows < 4 * sms)) return kStatThreads;
-  if (V > 8192 || a.k > 24 || a.in.rows < 6 * sms) return 128;
-  return V <= 4096 && a.k <= 10 ? 32 : 64;
+  if (V > 8192 || a.k > 24 || a.in.rows < 4 * sms) return 128;
+  if (a.k <= 10 && (V <= 2048 || (V <= 6144 && a.in.rows >= 24 * sms))) return 32;
+  return a.in.rows >= 16 * sms ? 64 : 128;
 }
 
 }  // namespace

@@ -168,8 +168,8 @@ def test_logprobs_temperature_mask_and_padding(cuda_lib, kind, tau):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
-@pytest.mark.parametrize("T,V,ks", [(650, 700, (1, 64, 65)), (700, 9001, (3, 64)), (2000, 300, (2, 10, 11, 24, 25)),
-                                    (1100, 4091, (1, 10, 20)), (610, 20003, (20,))])
+@pytest.mark.parametrize("T,V,ks", [(650, 700, (1, 64, 65)), (700, 9001, (3, 64)), (2500, 300, (2, 10, 11, 24, 25)),
+                                    (3700, 2100, (1, 10)), (610, 20003, (20,))])
 def test_logprobs_many_rows(cuda_lib, T, V, ks, kind):
     """Blocks of every size: few threads for many short rows."""
     x, tokens, _ = logits_of(min(T, 97), V, kind, seed=16)
