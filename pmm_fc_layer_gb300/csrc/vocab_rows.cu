@@ -171,7 +171,7 @@ __device__ __noinline__ uint64_t segments_of_nan(const T* row, const Share sh, i
 // list of 64 of 128256 costs a quarter more (4096 rows 204 us, 160 without): of
 // a block's 70000 cycles the bound takes 2000, the segments that are read again
 // 8000, at the latency of a busy memory and with 14 % more traffic, and the
-// places 2500.  One row with a list of 20, on 8 CTAs: 7.5 us, 3.4 without.
+// places 2500.  One row with a list of 20, on 8 CTAs: 6.9 us, 3.4 without.
 template <typename T, bool kEntropy, bool kTop, int kThreads, int kResident>
 __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const LogprobArgs p) {
   griddep_launch_dependents();
