@@ -299,6 +299,8 @@ axonn_status_t axonn_goldfish_ce(const void* logits, int64_t ld_logits, const in
 #define AXONN_IN_F32 0x400u       /* axonn_epi_bwd: dY is fp32 (else bf16); axonn_dropout: X,
                                      residual and Y are fp32 (else bf16); operators over rows
                                      of logits: logits and dlogits are fp32 (else bf16) */
+#define AXONN_LSE_PARTS 0x800u    /* axonn_token_logprobs and its backward: lse is [T x 2], the
+                                     row's largest logit and ln sum_v e^(z_v - max z) */
 typedef enum {
   AXONN_ACT_NONE = 0,
   AXONN_ACT_RELU = 1,
@@ -428,7 +430,7 @@ axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, u
  * sums in an order that depends on the sizes alone, exponentials the special
  * function units' (2^-22; 0 below 2^-126); differences are taken from the row's
  * maximum before they are scaled, so a row of finite logits of any size gives
- * its own probabilities.  No workspace.
+ * its own probabilities (in the way back with AXONN_LSE_PARTS).  No workspace.
  *
  * axonn_token_logprobs -- scoring, answering and a teacher's lists, in one
  * launch that reads the logits once (what a list may come from, again).  Each
@@ -436,7 +438,8 @@ axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, u
  *   tokens   int32 [T], given with logprob: a token outside [0, V) (padding)
  *            has logprob 0; the row's other outputs are as for any row
  *   logprob  out, fp32 [T]: ln p of the row's token
- *   entropy  out, fp32 [T]: H;   lse  out, fp32 [T]
+ *   entropy  out, fp32 [T]: H;   lse  out, fp32 [T], or [T x 2] with
+ *            AXONN_LSE_PARTS: m = max_v x_v and ln S = lse - m / tau
  *   top_index, top_logprob  out, int32 and fp32 [T x k] (ld_top >= k, 4-byte
  *            aligned): the row's k largest logits, best first, equal ones by
  *            index, and their ln p.  0 <= k <= min(V, 128).  -0 equals 0, and
@@ -448,9 +451,13 @@ axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, u
  *   dlogits_v = (g ([v = token] - p_v) - h p_v (ln p_v + H)) / tau
  *   tokens, dlogprob   int32 and fp32 [T], or both NULL; a token outside
  *                      [0, V) has no gradient
- *   lse                fp32 [T], as the forward left it for these logits and
- *                      this temperature (p comes from it: it is off by
- *                      2^-24 |lse| of itself)
+ *   lse                as the forward left it for these logits and this
+ *                      temperature.  [T x 2] with AXONN_LSE_PARTS: p =
+ *                      e^((x - m) / tau - ln S), right for logits of any size.
+ *                      [T]: p = e^(x / tau - lse), which is off by 2^-23 |lse|
+ *                      of itself; where |lse| is above 65536 a gradient cannot
+ *                      be had from it and is NaN (0 at logits of -inf where lse
+ *                      is -inf: a row of nothing else has no gradient)
  *   entropy, dentropy  fp32 [T], H as the forward left it, and h; or both NULL
  *   dlogits            out, of the logits' type, rounded once; may be the
  *                      logits themselves (same ld), else must not overlap them
@@ -483,7 +490,7 @@ typedef struct {
   const uint8_t* keep;
   int64_t T, V;
   float temperature;
-  uint32_t flags;      /* 0 or AXONN_IN_F32 */
+  uint32_t flags;      /* AXONN_IN_F32, AXONN_LSE_PARTS */
   float* logprob;
   float* entropy;
   float* lse;

@@ -83,6 +83,26 @@ def token_logprobs_bwd(x, lse, tokens=None, dlogprob=None, entropy=None, dentrop
     return d / tau
 
 
+def policy_gradient(x, tokens=None, g=None, h=None, tau=1.0):
+    """The gradient of sum_t g_t ln p[token_t] + h_t H_t from the logits alone,
+    finite ones of any size among them."""
+    T, V = x.shape
+    lp = log_softmax(x, tau)
+    p = np.exp(lp)
+    known = np.where(p == 0, 0.0, lp)
+    H = -np.where(p == 0, 0.0, p * known).sum(axis=1)
+    d = np.zeros((T, V))
+    for t in range(T):
+        gt = 0.0 if g is None or not 0 <= tokens[t] < V else float(g[t])
+        ht = 0.0 if h is None else float(h[t])
+        if (gt == 0 and ht == 0) or (lp[t] == -np.inf).all():
+            continue
+        d[t] = -gt * p[t] - ht * p[t] * (known[t] + H[t])
+        if gt:
+            d[t, tokens[t]] += gt
+    return d / tau
+
+
 def distill(x, top_index, top_logit, keep=None, tau=1.0, grad_scale=1.0):
     T, V = x.shape
     lp = log_softmax(x, tau)

@@ -28,6 +28,7 @@ REDUCE_ADD = 0x80
 VGRID_PARTIALS = 0x100
 BIAS_F32 = 0x200
 IN_F32 = 0x400
+LSE_PARTS = 0x800
 
 ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
@@ -558,6 +559,13 @@ def _whole(name, t, dtype, shape, here):
     return t.data_ptr()
 
 
+def _lse(t, T, here):
+    """(address, LSE_PARTS or 0) of lse [T], or [T x 2] in parts."""
+    if t is not None and len(t.shape) == 2:
+        return _whole("lse", t, _dtypes["f32"], (T, 2), here), LSE_PARTS
+    return _whole("lse", t, _dtypes["f32"], (T,), here), 0
+
+
 def _rows(name, t, dtype, shape, here, single):
     """(address, leading dimension) of rows beside the logits, (0, 0) for None.
     The stride of a single row says nothing: it counts as `single`."""
@@ -585,32 +593,36 @@ def axonn_token_logprobs(logits, tokens=None, logprob=None, entropy=None, lse=No
                          top_logprob=None, keep=None, temperature=1.0, stream=None):
     """ln p of int32 tokens [T] under softmax(logits / temperature), logits
     [T x V] in bf16 or fp32 (the tensor's type sets IN_F32): fills, where given,
-    logprob [T], entropy [T], lse [T], and the rows' largest logits, best first,
-    as top_index (int32) and top_logprob [T x k].  Rows with keep (uint8 [T]) 0
-    get zeros and indices of -1."""
+    logprob [T], entropy [T], lse [T] (or [T x 2]: the largest logit and
+    lse - it / temperature), and the rows' largest logits, best first, as
+    top_index (int32) and top_logprob [T x k].  Rows with keep (uint8 [T]) 0 get
+    zeros and indices of -1."""
     here, T, V, kind, flags = _logits(logits)
+    lse, parts = _lse(lse, T, here)
     f32, per_row, single = _dtypes["f32"], (T,), (V + 7) // 8 * 8
     k = index = value = ld_top = 0
     if top_index is not None or top_logprob is not None:
         k, index, value, ld_top = _lists("top_index", top_index, "top_logprob", top_logprob, T, here)
     _check(load().axonn_token_logprobs(_TOKEN_LOGPROBS.pack(
         *_rows("logits", logits, kind, (T, V), here, single), _whole("tokens", tokens, _dtypes["i32"], per_row, here),
-        _whole("keep", keep, _dtypes["u8"], per_row, here), T, V, temperature, flags,
+        _whole("keep", keep, _dtypes["u8"], per_row, here), T, V, temperature, flags | parts,
         _whole("logprob", logprob, f32, per_row, here), _whole("entropy", entropy, f32, per_row, here),
-        _whole("lse", lse, f32, per_row, here), index, value, ld_top, k), _stream(stream)))
+        lse, index, value, ld_top, k), _stream(stream)))
 
 
 def axonn_token_logprobs_bwd(logits, lse, dlogits, tokens=None, dlogprob=None, entropy=None, dentropy=None,
                              keep=None, temperature=1.0, stream=None):
     """dlogits (the logits' type; may be the logits) = (dlogprob (onehot(tokens)
     - p) - dentropy p (ln p + entropy)) / temperature, for lse and entropy as
-    axonn_token_logprobs left them."""
+    axonn_token_logprobs left them.  lse [T x 2] is right for logits of any size;
+    from lse [T] rows beyond 65536 in size get NaN."""
     here, T, V, kind, flags = _logits(logits)
+    lse, parts = _lse(lse, T, here)
     f32, per_row, single = _dtypes["f32"], (T,), (V + 7) // 8 * 8
     _check(load().axonn_token_logprobs_bwd(_TOKEN_LOGPROBS_BWD.pack(
         *_rows("logits", logits, kind, (T, V), here, single), _whole("tokens", tokens, _dtypes["i32"], per_row, here),
-        _whole("keep", keep, _dtypes["u8"], per_row, here), T, V, temperature, flags,
-        _whole("lse", lse, f32, per_row, here), _whole("dlogprob", dlogprob, f32, per_row, here),
+        _whole("keep", keep, _dtypes["u8"], per_row, here), T, V, temperature, flags | parts, lse,
+        _whole("dlogprob", dlogprob, f32, per_row, here),
         _whole("entropy", entropy, f32, per_row, here), _whole("dentropy", dentropy, f32, per_row, here),
         *_rows("dlogits", dlogits, kind, (T, V), here, single)), _stream(stream)))
 

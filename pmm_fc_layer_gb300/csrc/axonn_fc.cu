@@ -1581,10 +1581,9 @@ FusedChoice choose_dx(int64_t T, int64_t K, int64_t V) {
 // What the operators over rows of logits have in common: types, sizes, the
 // temperature and the logits themselves.
 template <class Args>
-axonn_status_t logit_rows(const Args* a, axonn::LogitRows* rows) {
+axonn_status_t logit_rows(const Args* a, uint32_t flags, axonn::LogitRows* rows) {
   if (!a) return fail(AXONN_ERR_INVALID_ARG, "the arguments are NULL");
-  if (a->flags & ~AXONN_IN_F32)
-    return fail(AXONN_ERR_INVALID_ARG, "flag bits 0x%x do not apply here", a->flags & ~AXONN_IN_F32);
+  if (a->flags & ~flags) return fail(AXONN_ERR_INVALID_ARG, "flag bits 0x%x do not apply here", a->flags & ~flags);
   axonn_status_t st = check_rows_cols(a->T, a->V);
   if (st != AXONN_OK) return st;
   if (a->V < 1) return fail(AXONN_ERR_INVALID_ARG, "vocabulary size %lld", (long long)a->V);
@@ -1794,11 +1793,13 @@ axonn_status_t axonn_fc_wgrad_zsharded(const void* X, const void* dY, void* cons
 
 axonn_status_t axonn_token_logprobs(const axonn_token_logprobs_t* args, cudaStream_t stream) {
   axonn::LogprobArgs a{};
-  axonn_status_t st = logit_rows(args, &a.in);
+  axonn_status_t st = logit_rows(args, AXONN_IN_F32 | AXONN_LSE_PARTS, &a.in);
   if (st != AXONN_OK) return st;
   const axonn_token_logprobs_t& p = *args;
   if (p.T > 0 && (p.tokens == nullptr) != (p.logprob == nullptr))
     return fail(AXONN_ERR_INVALID_ARG, "tokens and logprob go together");
+  if (p.T > 0 && (p.flags & AXONN_LSE_PARTS) && !p.lse)
+    return fail(AXONN_ERR_INVALID_ARG, "AXONN_LSE_PARTS without lse");
   if (p.k < 0 || p.k > p.V) return fail(AXONN_ERR_INVALID_ARG, "a list of %d entries of %lld", p.k, (long long)p.V);
   if (p.k > axonn::kMaxTop) return fail(AXONN_ERR_UNSUPPORTED, "lists of more than %d entries", axonn::kMaxTop);
   if (p.k == 0 && (p.top_index || p.top_logprob))
@@ -1821,6 +1822,7 @@ axonn_status_t axonn_token_logprobs(const axonn_token_logprobs_t* args, cudaStre
   a.top_logprob = p.top_logprob;
   a.ld_top = p.ld_top;
   a.k = p.k;
+  a.lse_parts = (p.flags & AXONN_LSE_PARTS) != 0;
   const cudaError_t e = axonn::logprobs_launch(a, dev->sms, g_pdl.load() != 0, stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "log probabilities: %s", cudaGetErrorString(e));
   return ok();
@@ -1828,7 +1830,7 @@ axonn_status_t axonn_token_logprobs(const axonn_token_logprobs_t* args, cudaStre
 
 axonn_status_t axonn_token_logprobs_bwd(const axonn_token_logprobs_bwd_t* args, cudaStream_t stream) {
   axonn::LogprobBwdArgs a{};
-  axonn_status_t st = logit_rows(args, &a.in);
+  axonn_status_t st = logit_rows(args, AXONN_IN_F32 | AXONN_LSE_PARTS, &a.in);
   if (st != AXONN_OK) return st;
   const axonn_token_logprobs_bwd_t& p = *args;
   st = check_dlogits(a.in, p.dlogits, p.ld_dlogits);
@@ -1850,6 +1852,7 @@ axonn_status_t axonn_token_logprobs_bwd(const axonn_token_logprobs_bwd_t* args, 
   a.dentropy = p.dentropy;
   a.dlogits = p.dlogits;
   a.ld_dlogits = p.ld_dlogits;
+  a.lse_parts = (p.flags & AXONN_LSE_PARTS) != 0;
   const cudaError_t e = axonn::logprobs_bwd_launch(a, g_pdl.load() != 0, stream);
   if (e != cudaSuccess) return fail(AXONN_ERR_CUDA, "log probabilities, backward: %s", cudaGetErrorString(e));
   return ok();
@@ -1857,7 +1860,7 @@ axonn_status_t axonn_token_logprobs_bwd(const axonn_token_logprobs_bwd_t* args, 
 
 axonn_status_t axonn_distill(const axonn_distill_t* args, cudaStream_t stream) {
   axonn::DistillArgs a{};
-  axonn_status_t st = logit_rows(args, &a.in);
+  axonn_status_t st = logit_rows(args, AXONN_IN_F32, &a.in);
   if (st != AXONN_OK) return st;
   const axonn_distill_t& p = *args;
   if (p.dlogits) st = check_dlogits(a.in, p.dlogits, p.ld_dlogits);

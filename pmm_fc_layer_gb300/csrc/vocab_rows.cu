@@ -188,12 +188,20 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
   const int ctas = kClusters ? static_cast<int>(cluster_nctarank()) : 1;
   const int tid = static_cast<int>(threadIdx.x);
   const float inv = 1.0f / p.in.temperature, c = kEpiLog2e * inv;
+  auto put_lse = [&](float m, float log_sum, float lse) {
+    if (p.lse_parts) {
+      p.lse[2 * t] = m;
+      p.lse[2 * t + 1] = log_sum;
+    } else {
+      p.lse[t] = lse;
+    }
+  };
   if (p.in.keep && p.in.keep[t] == 0) {
     if (rank != 0) return;
     if (tid == 0) {
       if (p.logprob) p.logprob[t] = 0.0f;
       if (p.entropy) p.entropy[t] = 0.0f;
-      if (p.lse) p.lse[t] = 0.0f;
+      if (p.lse) put_lse(0.0f, 0.0f, 0.0f);
     }
     for (int j = tid; j < p.k; j += kThreads) {
       if (p.top_index) p.top_index[t * p.ld_top + j] = -1;
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
   if (tid == 0) {
     const float log2s = log2f(r.s), lns = log2s * kRowLn2;  // -inf for a row of -inf
     if (p.logprob) p.logprob[t] = !inside ? 0.0f : r.s == 0.0f ? -INFINITY : fmaf(own - r.m, inv, -lns);
-    if (p.lse) p.lse[t] = fmaf(r.m, inv, lns);
+    if (p.lse) put_lse(r.m, lns, fmaf(r.m, inv, lns));
     if (kEntropy) p.entropy[t] = r.s == 0.0f ? 0.0f : (log2s - r.a / r.s) * kRowLn2;
   }
 }
@@ -401,13 +409,20 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
 constexpr int kBwdThreads = 64;
 constexpr int kBwdVecs = 4;
 constexpr int kBwdCols = 8 * kBwdThreads * kBwdVecs;
+// The largest |lse| in one number whose p = e^(z - lse) is worth having: half a
+// step of it is then 2^-8 of p, bf16's own rounding.  Beyond it ln S goes under in
+// lse (in a row of a mask's -1e9 throughout, p would be 1 everywhere).
+constexpr float kLseMost = 65536.0f;
 
+// p comes from the forward's sums: with kParts from the row's largest logit m and
+// ln S, as e^((x - m) / tau - ln S), which is right for logits of any size, else
+// from lse, as e^(x / tau - lse).
 // Blocks over (row, kBwdCols columns).  HBM-bound: 8192 x 128256 with entropy
-// 659 us, 6.4 TB/s.  What counts is how soon a block has its loads on their
-// way: they are issued before the row's scalars are known (after them 683 us),
-// and from small blocks, of which an SM has 24 (blocks of 256 threads 4 us more,
-// of 64 with eight vectors a thread 14).
-template <typename T, bool kEntropy>
+// 638 us, 6.6 TB/s.  What counts is how soon a block has its loads on their
+// way: they are issued before the row's scalars are known (after them 24 us
+// more), and from small blocks, of which an SM has 21 to 25 (blocks of 256 threads
+// 4 us more, of 64 with eight vectors a thread 14).
+template <typename T, bool kEntropy, bool kParts>
 __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const LogprobBwdArgs p) {
   griddep_launch_dependents();
   griddep_wait();
@@ -424,7 +439,10 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const Logprob
       const int64_t i = first + 8 * kBwdThreads * u;
       if (i < V && kept) v[u].load(row + i, static_cast<int>(min(static_cast<int64_t>(8), V - i)));
     }
-    const float lse = p.lse[t];
+    const float m = kParts ? p.lse[2 * t] : 0.0f;
+    float lse = kParts ? p.lse[2 * t + 1] : p.lse[t];
+    const bool empty = lse == -INFINITY;
+    if (!kParts && fabsf(lse) > kLseMost) lse = NAN;
     float g = 0.0f, h = 0.0f, entropy = 0.0f;
     int64_t y = -1;
     if (p.dlogprob) {
@@ -436,9 +454,18 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const Logprob
       h = p.dentropy[t] * inv;
       entropy = p.entropy[t];
     }
-    const F2 inv2 = f2(inv), lse2 = f2(-lse), g2 = f2(-g), h2 = f2(-h), entropy2 = f2(entropy);
     // nothing to say, or a row of -inf: zeros
-    const bool zero = !kept || lse == -INFINITY || (g == 0.0f && h == 0.0f);
+    const bool zero = !kept || (kParts && empty) || (g == 0.0f && h == 0.0f);
+    if (!kParts && empty && !zero) {
+      // a row of -inf, or one whose lse is below fp32's range
+#pragma unroll 1
+      for (int n = 0; n < 8 * kBwdVecs; ++n) {
+        const int64_t i = first + 8 * kBwdThreads * (n / 8) + n % 8;
+        if (i < V) put_logit(out + i, logit_at(row + i) == -INFINITY ? 0.0f : NAN);
+      }
+      continue;
+    }
+    const F2 inv2 = f2(inv), m2 = f2(-m), lse2 = f2(-lse), g2 = f2(-g), h2 = f2(-h), entropy2 = f2(entropy);
 #pragma unroll
     for (int u = 0; u < kBwdVecs; ++u) {
       const int64_t i = first + 8 * kBwdThreads * u;
@@ -448,7 +475,9 @@ __global__ void __launch_bounds__(kBwdThreads) logprobs_bwd_kernel(const Logprob
           v[u].values(x);
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
-            const F2 lnp = fma2(f2(x[j], x[j + 1]), inv2, lse2);
+            F2 z = f2(x[j], x[j + 1]);
+            if (kParts) z = add2(z, m2);
+            const F2 lnp = fma2(z, inv2, lse2);
             const F2 prob = ex2_2(mul2(lnp, f2(kEpiLog2e)));
             F2 w = g2;  // -(g + h (ln p + H)), where p is not 0
             if (kEntropy) {
@@ -522,8 +551,13 @@ cudaError_t logprobs_launch(const LogprobArgs& a, int sms, bool pdl, cudaStream_
 cudaError_t logprobs_bwd_launch(const LogprobBwdArgs& a, bool pdl, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>((a.in.vocab + kBwdCols - 1) / kBwdCols),
                   static_cast<unsigned>(std::min<int64_t>(a.in.rows, 65535)));
-  auto kernel = a.in.f32 ? (a.dentropy ? logprobs_bwd_kernel<float, true> : logprobs_bwd_kernel<float, false>)
-                         : (a.dentropy ? logprobs_bwd_kernel<uint16_t, true> : logprobs_bwd_kernel<uint16_t, false>);
+  using Kernel = void (*)(LogprobBwdArgs);
+  static constexpr Kernel kKernels[8] = {
+      logprobs_bwd_kernel<uint16_t, false, false>, logprobs_bwd_kernel<uint16_t, false, true>,
+      logprobs_bwd_kernel<uint16_t, true, false>,  logprobs_bwd_kernel<uint16_t, true, true>,
+      logprobs_bwd_kernel<float, false, false>,    logprobs_bwd_kernel<float, false, true>,
+      logprobs_bwd_kernel<float, true, false>,     logprobs_bwd_kernel<float, true, true>};
+  const Kernel kernel = kKernels[(a.in.f32 ? 4 : 0) + (a.dentropy ? 2 : 0) + (a.lse_parts ? 1 : 0)];
   return launch_after(kernel, grid, kBwdThreads, pdl, stream, a);
 }
 

@@ -28,22 +28,24 @@ struct LogprobArgs {
   const int32_t* tokens;  // [rows]; null where logprob is
   float* logprob;         // each [rows] or null
   float* entropy;
-  float* lse;
+  float* lse;             // with lse_parts [rows x 2]: the largest logit, ln S
   int32_t* top_index;     // [rows x k], row stride ld_top, or null
   float* top_logprob;     // the same, or null
   int64_t ld_top;
   int32_t k;              // 0: no list
+  int32_t lse_parts;
 };
 
 struct LogprobBwdArgs {
   LogitRows in;
   const int32_t* tokens;    // [rows] or null (dlogprob is null then)
-  const float* lse;         // [rows]
+  const float* lse;         // [rows], with lse_parts [rows x 2]
   const float* dlogprob;    // [rows] or null
   const float* entropy;     // [rows]; null where dentropy is
   const float* dentropy;    // [rows] or null
   void* dlogits;            // of the logits' type, may be the logits
   int64_t ld_dlogits;
+  int32_t lse_parts;
 };
 
 struct DistillArgs {

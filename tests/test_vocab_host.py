@@ -288,3 +288,70 @@ def test_binding_distill(fc, on_device_0, others, say):
     args = {name: At(*v) for name, v in {**base, **others}.items()}
     with pytest.raises(ValueError if say else on_device_0, match=say):
         fc.axonn_distill(At(*BF), **args)
+
+
+# ------------------------------------------------------------------ lse in parts
+def test_policy_gradient_against_differences_and_the_way_back():
+    """The gradient from the logits alone: by differences, as the way back from
+    64-bit lse and H, and for a row of any size."""
+    rng = np.random.default_rng(6)
+    tau = 0.6
+    x = rng.normal(size=(4, 6))
+    x[2, 1] = -np.inf
+    tokens, g, h = np.array([2, -1, 5, 0]), rng.normal(size=4), rng.normal(size=4)
+    f = vo.token_logprobs(x, tokens, None, tau)
+    d = vo.policy_gradient(x, tokens, g, h, tau)
+    assert np.allclose(d, vo.token_logprobs_bwd(x, f["lse"], tokens, g, f["entropy"], h, None, tau), rtol=0, atol=1e-14)
+    step = 1e-5
+    for at in np.ndindex(*x.shape):
+        sides = []
+        for s in (step, -step):
+            y = x.copy()
+            y[at] += s
+            r = vo.token_logprobs(y, tokens, None, tau)
+            sides.append((g * r["logprob"] + h * r["entropy"]).sum())
+        assert abs((sides[0] - sides[1]) / (2 * step) - d[at]) < 1e-8  # step^2 f'''/6, and 1e-16 / step
+    low = np.full((2, 5), -3.3895313892515355e38)
+    low[1] = -np.inf
+    d = vo.policy_gradient(low, np.array([1, 1]), np.ones(2), np.ones(2))
+    assert np.allclose(d[0], np.array([-0.2, 0.8, -0.2, -0.2, -0.2])) and (d[1] == 0).all()
+
+
+@pytest.mark.parametrize("fn,base,change", [
+    ("axonn_token_logprobs", LOG, dict(flags=0x800)),                       # in parts, without lse
+    ("axonn_token_logprobs_bwd", BWD, dict(flags=0x800, lse=0)),
+    ("axonn_distill", DIS, dict(flags=0x800)),                              # has no lse
+    ("axonn_token_logprobs", LOG, dict(flags=0x1800, lse=FAKE)),
+])
+def test_refusals_of_lse_in_parts(fc, fn, base, change):
+    assert fc.LSE_PARTS == 0x800
+    refuse(fc, fn, base, change, 1)
+
+
+@pytest.mark.parametrize("lse,flags,say", [
+    (((4,), "float32"), 0, None), (((4, 2), "float32"), 0x800, None),
+    (((4, 3), "float32"), 0, "lse must be"), (((4, 1), "float32"), 0, "lse must be"), (((2, 2), "float32"), 0, "lse must be"),
+    (((4, 2), "float64"), 0, "lse must be torch.float32"), (((4, 2), "float32", 0, (1, 4)), 0, "lse must be contiguous"),
+    (((4, 2), "float32", 1), 0, "lse must be on the logits' device 0"),
+])
+def test_binding_of_lse_in_parts(fc, on_device_0, monkeypatch, lse, flags, say):
+    """[T x 2] sets the flag, forward and backward."""
+    got = []
+
+    class Library:
+        def __getattr__(self, name):
+            def call(packed, stream):
+                layout = fc._TOKEN_LOGPROBS if name == "axonn_token_logprobs" else fc._TOKEN_LOGPROBS_BWD
+                got.append(layout.unpack(packed)[7])
+                return 0
+            return call
+    monkeypatch.setattr(fc, "load", lambda: Library())
+    calls = (lambda: fc.axonn_token_logprobs(At(*BF), lse=At(*lse)),
+             lambda: fc.axonn_token_logprobs_bwd(At(*BF), At(*lse), At(*BF), tokens=At(*I4), dlogprob=At(*F4)))
+    for call in calls:
+        if say:
+            with pytest.raises(ValueError, match=say):
+                call()
+        else:
+            call()
+    assert got == ([] if say else [flags, flags])
