@@ -302,7 +302,9 @@ __device__ unsigned long long g_distill_status;
 // Bounded wait on an mbarrier phase by polling; false (and an error word) on
 // expiry.  Every lane that reads what the barrier guards waits itself.  No
 // barrier waited on so can complete its next phase before its waiters have
-// gone on.
+// gone on.  A warp of which one lane's wait has run out arrives nowhere any more:
+// what it waited for may still be on its way into a buffer, which is then never
+// filled again, and the waits of those who need its arrival run out in their turn.
 __device__ __noinline__ bool row_wait_long(uint32_t bar, uint32_t parity, uint64_t timeout_ns, uint32_t site) {
   const uint64_t t0 = global_timer_ns();
   while (true) {
@@ -319,6 +321,8 @@ __device__ __forceinline__ bool row_wait(const uint64_t& bar, uint32_t parity, u
   return mbar_test_wait(smem_addr(&bar), parity) || row_wait_long(smem_addr(&bar), parity, timeout_ns, site);
 }
 __device__ __forceinline__ void arrive(uint64_t& bar) { mbar_arrive(smem_addr(&bar)); }
+// A wait that ran out for one lane has for all: they go on together.
+__device__ __forceinline__ bool all_lanes(bool mine) { return __all_sync(kAll, mine) != 0; }
 
 // The consumers' barrier, which also says whether any of them has `pred`.
 __device__ __forceinline__ bool consumers_any(bool pred) {
@@ -368,7 +372,7 @@ struct StreamArgs {
   int units, chunks, held;  // of a row: whole vectors in units, in chunks, chunks kept
   int list;                 // k rounded up to 4
   uint64_t timeout_ns;
-  int32_t inject;  // 1: the producer withholds every copy (a test of the bounded waits)
+  int32_t inject;  // tests of the bounded waits: 1 withholds every copy, 2 delays a CTA's first past the limit
 };
 
 // Reads a row's list and prepares it, a warp.
@@ -481,6 +485,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
         const int b = static_cast<int>(seq % kRing);
         ok = ok && row_wait(tl->empty[b], ((seq / kRing) & 1u) ^ 1u, tmo, 1);
         if (!ok) return;
+        if (p.inject == 2 && seq == 0)
+          for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < min(2 * tmo, uint64_t{2'000'000'000});) {}
         const uint32_t bytes = static_cast<uint32_t>(min(kChunk, p.units - chunk * kChunk)) * 16u;
         mbar_arrive_expect_tx(smem_addr(&tl->full[b]), bytes);
         bulk_load(smem_addr(ring + b * kChunk), reinterpret_cast<const uint4*>(row) + static_cast<int64_t>(chunk) * kChunk,
@@ -512,17 +518,15 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
         if (copies)
           for (int i = 0; i < again && ok; ++i) copy(at, i, drop_pol);
       }
-      // Copies nobody took exist only after an expired wait: let them land
-      // (bounded) before this CTA's shared memory goes away.
-      if (!ok)
-        for (uint32_t i = seq > kRing ? seq - kRing : 0; i < seq; ++i)
-          row_wait(tl->full[i % kRing], (i / kRing) & 1u, tmo, 3);
+      // Copies that nobody took, after an expired wait of anyone's: they land
+      // (bounded) before this CTA's shared memory goes away.  Where all were taken
+      // these waits are over at once.
+      for (uint32_t i = seq > kRing ? seq - kRing : 0; i < seq; ++i)
+        row_wait(tl->full[i % kRing], (i / kRing) & 1u, tmo, 3);
     }
     __syncwarp();
   } else if (warp <= kListWarps) {
     // ------------------------------------------------------------ lists
-    // a wait that ran out for one lane has for all: they go on together
-    auto all_lanes = [](bool mine) { return __all_sync(kAll, mine) != 0; };
     auto prepare = [&](uint32_t r) {
       RowSlot& slot = tl->slot[r % kRowSlots];
       ok = all_lanes(ok && row_wait(tl->row_full[r % kRowSlots], parity(r), tmo, 4));
@@ -563,7 +567,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
           put_logit(out + l.at[j], fmaf(ex2_approx((l.x[j] - m) * c), share, -teach * l.w[j]));
       }
       __syncwarp();
-      if (lane == 0) arrive(tl->row_empty[r % kRowSlots]);
+      if (ok && lane == 0) arrive(tl->row_empty[r % kRowSlots]);
       more = more && ok;
     }
   } else {
@@ -576,7 +580,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
     uint32_t seq = 0;
     for (uint32_t r = 0;; ++r) {
       RowSlot& slot = tl->slot[r % kRowSlots];
-      ok = ok && row_wait(tl->row_full[r % kRowSlots], parity(r), tmo, 7);
+      ok = all_lanes(ok && row_wait(tl->row_full[r % kRowSlots], parity(r), tmo, 7));
       if (consumers_any(!ok || slot.row < 0)) break;
       const int64_t t = slot.row;
       const T* row = static_cast<const T*>(a.in.logits) + t * a.in.ld;
@@ -592,7 +596,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
         // from n on of -inf
         auto chunk = [&](uint32_t s, int i, bool arrived, bool release, auto&& f) {
           const int b = static_cast<int>(s % kRing);
-          if (!arrived) ok = ok && row_wait(tl->full[b], (s / kRing) & 1u, tmo, 8);
+          if (!arrived) ok = all_lanes(ok && row_wait(tl->full[b], (s / kRing) & 1u, tmo, 8));
           const uint4* buf = ring + b * kChunk;
           const int n = ok ? min(kChunk, p.units - i * kChunk) : 0;
           uint4 v[kTake];
@@ -602,7 +606,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
           f(v, i * kChunk + ct, i * kChunk + n);
           if (release) {
             __syncwarp();
-            if (lane == 0) arrive(tl->empty[b]);
+            if (ok && lane == 0) arrive(tl->empty[b]);
           }
         };
         const int again = p.chunks - p.held;
@@ -620,13 +624,13 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
         if (lane == 0) tl->parts[cw] = sums;
         (void)consumers_any(false);
         sums = join_parts_warp<false, kRowWarps>(tl->parts, c);
-        if (ct == 0) {
+        if (ok && ct == 0) {
           slot.m = sums.m;
           slot.s = sums.s;
           arrive(tl->sums_full[r % kRowSlots]);
         }
         // in place, a list warp must have read before anything is written
-        ok = ok && row_wait(tl->list_full[r % kRowSlots], parity(r), tmo, 9);
+        ok = all_lanes(ok && row_wait(tl->list_full[r % kRowSlots], parity(r), tmo, 9));
         const float share = sums.s == 0.0f || slot.sum == 0.0f ? 0.0f : scale / sums.s;
         const float m = sums.m > -INFINITY ? sums.m : 0.0f;
         const F2 m2 = f2(-m), c2 = f2(c), share2 = f2(share);
@@ -649,7 +653,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
         seq += static_cast<uint32_t>(p.chunks + again);
       }
       __syncwarp();
-      if (lane == 0) {
+      if (ok && lane == 0) {
         arrive(tl->written[r % kRowSlots]);
         arrive(tl->row_empty[r % kRowSlots]);
       }
