@@ -643,7 +643,7 @@ void axonn_set_wait_timeout_ns(uint64_t ns);
 /* Test hook: 1 makes the next launches' producer withhold all operand
  * loads (the GEMM kernels' tiles, the Goldfish loss's kept rows, the rows of a
  * distillation of many long ones), so the bounded waits expire and
- * AXONN_ERR_TIMEOUT is reported; 2 makes the distillation's hold back the first
+ * AXONN_ERR_TIMEOUT is reported; 2 makes the latter two hold back the first
  * load of each CTA for two limits (2 s at most), so that it lands after the wait
  * for it has expired; 0 restores normal operation.  Never needed in production. */
 void axonn_debug_set_inject(int mode);

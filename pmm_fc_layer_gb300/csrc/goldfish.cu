@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(kGfThreads, 1)
       bool ok = true;
       while (true) {
         ok = ok && gf_wait(smem_addr(&tl->rq_empty[q]), qph ^ 1u, tmo, 1);
-        const int64_t r = ok ? static_cast<int64_t>(atomicAdd(counter, 1u)) : T;
+        if (!ok) break;  // the entry is not the producer's to write: the others' waits run out, too
+        const int64_t r = static_cast<int64_t>(atomicAdd(counter, 1u));
         const bool more = r < T;
         const int32_t keep = more ? a.keep[r] : 0;
         tl->rq_row[q] = more ? r : -1;
@@ -343,6 +344,8 @@ __global__ void __launch_bounds__(kGfThreads, 1)
             const int64_t e0 = c * kGfChunk;
             const uint32_t bytes = static_cast<uint32_t>(min(kGfChunk, vpad - e0) * 2);
             const uint32_t fb = smem_addr(&tl->full[b]);
+            if (a.inject == 2 && uses[0] == 0)
+              for (const uint64_t t0 = global_timer_ns(); global_timer_ns() - t0 < min(2 * tmo, uint64_t{2'000'000'000});) {}
             mbar_arrive_expect_tx(fb, bytes);
             bulk_load(buf(b), src + e0, bytes, fb, pass == 0 ? keep_pol : drop_pol);
             ++uses[b];
@@ -353,11 +356,11 @@ __global__ void __launch_bounds__(kGfThreads, 1)
           }
         }
       }
-      // Copies nobody took exist only after an expired wait: let them land
-      // (bounded) before this CTA's shared memory goes away.
-      if (!ok)
-        for (int i = 0; i < kGfRing; ++i)
-          if (uses[i] > 0) gf_wait(smem_addr(&tl->full[i]), (uses[i] - 1) & 1u, tmo, 3);
+      // Copies that nobody took, after an expired wait of anyone's: they land
+      // (bounded) before this CTA's shared memory goes away.  Where all were taken
+      // these waits are over at once.
+      for (int i = 0; i < kGfRing; ++i)
+        if (uses[i] > 0) gf_wait(smem_addr(&tl->full[i]), (uses[i] - 1) & 1u, tmo, 3);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ stores
@@ -370,7 +373,7 @@ __global__ void __launch_bounds__(kGfThreads, 1)
       const int64_t r = tl->rq_row[q];
       const bool keep = tl->rq_keep[q] != 0;
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&tl->rq_empty[q]));
+      if (ok && lane == 0) mbar_arrive(smem_addr(&tl->rq_empty[q]));
       if (++q == kGfRowQ) {
         q = 0;
         qph ^= 1u;
@@ -426,7 +429,8 @@ __global__ void __launch_bounds__(kGfThreads, 1)
     uint32_t ph = 0, qph = 0;
     bool ok = true;  // this thread's waits all completed
     // waits for chunk b, passes it to f(x, e0, n_valid) when it arrived, and
-    // reports the warp done with it
+    // reports the warp done with it; a warp whose wait ran out reports nothing
+    // more, since the copy may still be on its way into the buffer
     auto take_chunk = [&](int c, auto&& f) {
       const bool got = ok && gf_warp_wait(smem_addr(&tl->full[b]), ph, tmo, 4);
       ok = got;
@@ -434,7 +438,7 @@ __global__ void __launch_bounds__(kGfThreads, 1)
       const int64_t nv = max(int64_t{0}, min(kGfChunk, V - e0));
       if (got) f(reinterpret_cast<uint16_t*>(smem + b * kGfChunk * 2), e0, nv);
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&tl->consumed[b]));
+      if (got && lane == 0) mbar_arrive(smem_addr(&tl->consumed[b]));
       if (++b == kGfRing) {
         b = 0;
         ph ^= 1u;
@@ -446,7 +450,7 @@ __global__ void __launch_bounds__(kGfThreads, 1)
       const int32_t y = tl->rq_y[q];
       const bool keep = tl->rq_keep[q] != 0;
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&tl->rq_empty[q]));
+      if (ok && lane == 0) mbar_arrive(smem_addr(&tl->rq_empty[q]));
       if (++q == kGfRowQ) {
         q = 0;
         qph ^= 1u;

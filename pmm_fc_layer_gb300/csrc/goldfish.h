@@ -22,7 +22,7 @@ struct GoldfishArgs {
   uint16_t* dlogits;   // bf16 [T x V] or null, row stride ld_dlogits
   int64_t ld_dlogits;
   uint64_t timeout_ns;
-  int32_t inject;  // 1: the rows kernel withholds every copy (a test of the bounded waits)
+  int32_t inject;  // tests of the bounded waits: 1 withholds every copy, 2 delays a CTA's first past the limit
 };
 
 // Largest vocabulary the entry point accepts (8 x 49152 tokens).

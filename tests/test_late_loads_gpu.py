@@ -3,6 +3,8 @@ nothing that comes later is harmed."""
 import numpy as np
 import pytest
 
+from oracle import goldfish as gf
+from test_goldfish_gpu import _check, _problem, _run
 from test_vocab_gpu import lists_of, logits_of, run_distill
 
 pytestmark = pytest.mark.gpu
@@ -36,3 +38,18 @@ def test_distill(cuda_lib, kind, V, in_place):
         late(fc, lambda: run_distill(*args, in_place=in_place))
         again = run_distill(*args, in_place=in_place)
         assert all(np.array_equal(want[n], again[n]) for n in want)
+
+
+@pytest.mark.parametrize("grad", [True, False])
+@pytest.mark.parametrize("V", [20000, 128256])
+def test_goldfish(cuda_lib, V, grad):
+    """Two rows' copies fit the buffers, or one row's do not."""
+    fc = cuda_lib
+    ids, labels, logits = _problem(2, 200, V, 305)
+    want = _run(fc, ids, labels, logits, 0, 13, grad=grad)
+    few = (ids[:1, :40], labels[:1, :40], logits[:40])
+    _check(_run(fc, *few, 0, 13, grad=grad), gf.goldfish_ce(few[2], *few[:2], 0, 13), V, few[2])
+    for _ in range(2):
+        late(fc, lambda: _run(fc, ids, labels, logits, 0, 13, grad=grad))
+        again = _run(fc, ids, labels, logits, 0, 13, grad=grad)
+        assert all(np.array_equal(want[n], again[n]) for n in want if want[n] is not None)
