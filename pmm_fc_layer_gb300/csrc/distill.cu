@@ -496,7 +496,8 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
       auto post = [&](uint32_t r, int64_t row, bool counts) {
         RowSlot& slot = tl->slot[r % kRowSlots];
         ok = ok && row_wait(tl->row_empty[r % kRowSlots], parity(r) ^ 1u, tmo, 2);
-        slot.row = ok ? row : -1;
+        if (!ok) return;  // the slot is still another row's: the others' waits run out, too
+        slot.row = row;
         slot.counts = counts;
         arrive(tl->row_full[r % kRowSlots]);
       };
