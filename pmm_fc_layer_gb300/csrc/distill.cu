@@ -324,7 +324,8 @@ __device__ __forceinline__ void arrive(uint64_t& bar) { mbar_arrive(smem_addr(&b
 // A wait that ran out for one lane has for all: they go on together.
 __device__ __forceinline__ bool all_lanes(bool mine) { return __all_sync(kAll, mine) != 0; }
 
-// The consumers' barrier, which also says whether any of them has `pred`.
+// The consumers' barrier, which also says whether any of them has `pred`; a warp's
+// lanes come to it together.
 __device__ __forceinline__ bool consumers_any(bool pred) {
   uint32_t r;
   asm volatile(
@@ -623,6 +624,7 @@ __global__ void __launch_bounds__(kRowThreads, 1) distill_rows_kernel(const __gr
         }
         sums = join_warp<false>(sums, c);
         if (lane == 0) tl->parts[cw] = sums;
+        __syncwarp();
         (void)consumers_any(false);
         sums = join_parts_warp<false, kRowWarps>(tl->parts, c);
         if (ok && ct == 0) {

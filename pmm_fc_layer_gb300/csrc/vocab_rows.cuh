@@ -163,8 +163,10 @@ __device__ __forceinline__ Share share_of(int64_t V) {
 }
 
 // The halves of a cluster's barrier: CTAs must have begun before their shared
-// memory is written to, which the first pair makes sure of at no cost.
+// memory is written to, which the first pair makes sure of at no cost.  A warp's
+// lanes take an aligned barrier together, whatever branch they come from.
 __device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
