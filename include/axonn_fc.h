@@ -425,8 +425,9 @@ axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, u
  *            is not read
  *   temperature  in [1e-4, 1e4]
  * A logit of -inf has probability 0.  In a row of nothing else every
- * probability is 0: ln p = lse = -inf, H = 0, and no gradient.  A NaN or +inf
- * among the logits makes the row's numbers NaN.  Arithmetic and sums are fp32,
+ * probability is 0: ln p = lse = -inf, H = 0, and no gradient of either (the
+ * distillation's is p - q with p = 0 there, below).  A NaN or +inf among the
+ * logits makes the row's numbers NaN.  Arithmetic and sums are fp32,
  * sums in an order that depends on the sizes alone, exponentials the special
  * function units' (2^-22; 0 below 2^-126); differences are taken from the row's
  * maximum before they are scaled, so a row of finite logits of any size gives
@@ -475,7 +476,9 @@ axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, u
  *              An index given twice teaches twice.  Entries of -inf have q = 0;
  *              a list of nothing else has loss and gradient 0, but counts.
  *   A row counts when keep does not leave it out and its list is not empty.
- *   token_loss out, fp32 [T]: 0 where not counted; +inf where q > 0 at p = 0
+ *   token_loss out, fp32 [T]: 0 where not counted; +inf where q > 0 at p = 0.
+ *              The gradient stays p - q there, and -q in a row of logits that are
+ *              all -inf: finite beside an infinite loss
  *   loss, kept out, fp32 [1] and int32 [1] (n); loss is 0 for n = 0, and its
  *              word is the kernels' counter during the call
  *   dlogits    out, of the logits' type, or NULL for the loss alone; rows not

@@ -355,3 +355,24 @@ def test_binding_of_lse_in_parts(fc, on_device_0, monkeypatch, lse, flags, say):
         else:
             call()
     assert got == ([] if say else [flags, flags])
+
+
+# ------------------------------------------------------------------ a student without a word left
+def test_distill_where_the_student_has_no_probability():
+    """The loss is infinite where q > 0 at p = 0, and the gradient p - q all the
+    same: -q in a row of -inf alone, the other rows as they are without it."""
+    rng = np.random.default_rng(7)
+    x, t, tau = rng.normal(size=(3, 7)), rng.normal(size=(3, 3)), 1.5
+    at = np.array([[0, 2, 4], [1, 3, 3], [6, 5, 0]])
+    x[1] = -np.inf
+    x[2, 6] = -np.inf
+    r = vo.distill(x, at, t, None, tau, 2.0)
+    q = np.exp(vo.log_softmax(t, tau))
+    assert r["n"] == 3 and np.isfinite(r["token_loss"][0]) and (r["token_loss"][1:] == np.inf).all()
+    want = np.zeros((3, 7))
+    want[1, 1], want[1, 3] = -q[1, 0], -q[1, 1] - q[1, 2]
+    want[2] = np.exp(vo.log_softmax(x[2:], tau))[0]
+    want[2, at[2]] -= q[2]
+    assert np.allclose(r["dlogits"][1:], want[1:] * 2.0 * tau / 3, rtol=1e-13, atol=0)
+    alone = vo.distill(x[:1], at[:1], t[:1], None, tau, 2.0)
+    assert np.allclose(r["dlogits"][0], alone["dlogits"][0] / 3, rtol=1e-13)
