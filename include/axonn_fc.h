@@ -484,7 +484,9 @@ axonn_status_t axonn_linear_ce_workspace_size(int64_t T, int64_t K, int64_t V, u
  *   dlogits    out, of the logits' type, or NULL for the loss alone; rows not
  *              counted get zeros; in place as above
  * Two launches; the logits are read from memory once, as far as a row fits the
- * shared memory of the CTAs that share it, and what does not again from L2.
+ * shared memory of the CTAs that share it, and what does not again from L2.  A long
+ * list costs as its square (4096 x 128256 bf16: 332 us with lists of 64, 464 of 256,
+ * 664 of 257, 3.8 ms of 1024).
  */
 typedef struct {
   const void* logits;

@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kDistThreads) distill_kernel(const DistillArgs
 // writes the list's entries, p - q, over it.
 // Rows are claimed one by one (the first ones by block), since those that do
 // not count cost half.
-// HBM-bound: 4096 x 128256 bf16 with lists of 64 takes 333 us, 6.3 TB/s (the
+// HBM-bound: 4096 x 128256 bf16 with lists of 64 takes 332 us, 6.3 TB/s (the
 // same in shares 428); fp32 1024 x 128256 182, 5.8 TB/s (6.7 rows an SM).  What
 // it took: four units of a thread at once (one: 435), maxima of bf16 in pairs,
 // two list warps (4096 x 32000: one 149, two 107).
@@ -681,7 +681,9 @@ int stream_shared(int k) {
 // (gradients of 4096 rows: 98 us against 90 in shares at 24000 bf16 words, 105
 // against 117 at 32000, 323 against 428 at 128256; of 64000 words 30.3 against
 // 30.5 for 400 rows, 17.7 against 16.7 for 200), with lists that one warp
-// prepares while others take a row.
+// prepares while others take a row.  Each entry looks for its index in the whole
+// list, here and in shares: 4096 x 128256 with lists of 64 takes 332 us, of 256 464,
+// of 257, in shares, 664, and of 1024 3.8 ms.
 bool streams_rows(int64_t rows, int64_t row_bytes, int k, int sms) {
   return k <= kStreamList && rows >= 2 * sms && row_bytes >= (56 << 10);
 }

@@ -31,7 +31,7 @@ __device__ __forceinline__ float rank_value(uint64_t r) {
 }
 
 // How the k largest of a share are found, in work that the logits' values do
-// not change: while it streams, a thread keeps for each of its kSegments
+// not change but in one case (at the end): while it streams, a thread keeps for each of its kSegments
 // segments (vectors that follow each other in its own sequence) the largest
 // logit, as the rank of the last index of the first vector that has it.  A
 // segment has an entry at least that good, so the k-th best of these numbers
@@ -39,6 +39,9 @@ __device__ __forceinline__ float rank_value(uint64_t r) {
 // that does: only those are read again, and what reaches the bound is the
 // candidates.  The bound is sought among the threads' best segments alone,
 // between the k-th and a few places (half of k, at most 16, and 4) behind it.
+// Where more candidates reach it than kSegments * kThreads, because a few threads'
+// segments hold nearly all that is large, the share is read once for each entry of
+// the list instead (every row of 4096 x 128256 so, lists of 64: 23.8 ms for 206 us).
 constexpr int kSegments = 8;
 
 template <int kThreads>
