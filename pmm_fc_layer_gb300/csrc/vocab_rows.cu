@@ -166,6 +166,14 @@ __device__ __noinline__ uint64_t segments_of_nan(const T* row, const Share sh, i
 }
 
 // ------------------------------------------------------------------ logprobs
+// ln p of a logit x from its row's largest: (x - m) / tau - ln S.  Two finite
+// logits may be further apart than fp32 reaches, and their z not: the difference is
+// that of their halves, which is exact where x - m is (in this order, since x may
+// still be on its way: 64 x 128256 fp32 10.1 us, 10.2 by 0.5 x - 0.5 m).
+__device__ __forceinline__ float logprob_of(float x, float m, float inv, float ln_s) {
+  return fmaf(fmaf(0.5f, x, -0.5f * m), 2.0f * inv, -ln_s);
+}
+
 // A cluster takes a row, a CTA a share of it.  Each CTA sums its share and
 // finds its own list; they meet in the shared memory of the cluster's first
 // CTA, which joins them in order and writes.
@@ -347,8 +355,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
     auto write = [&](int place, uint64_t e, float m, float s, float ln_s) {
       const int64_t at = t * p.ld_top + place;
       if (p.top_index) p.top_index[at] = static_cast<int32_t>(rank_index(e));
-      // as far below the maximum as fp32 reaches
-      if (p.top_logprob) p.top_logprob[at] = s == 0.0f ? -INFINITY : fmaf(rank_value(e) - m, inv, -ln_s);
+      if (p.top_logprob) p.top_logprob[at] = s == 0.0f ? -INFINITY : logprob_of(rank_value(e), m, inv, ln_s);
     };
     if (tid == 0 && (n & 1)) top.entry[n] = 0;  // two are read at a time
     __syncthreads();
@@ -402,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logprobs_kernel(const Log
   }
   if (tid == 0) {
     const float log2s = log2f(r.s), lns = log2s * kRowLn2;  // -inf for a row of -inf
-    if (p.logprob) p.logprob[t] = !inside ? 0.0f : r.s == 0.0f ? -INFINITY : fmaf(own - r.m, inv, -lns);
+    if (p.logprob) p.logprob[t] = !inside ? 0.0f : r.s == 0.0f ? -INFINITY : logprob_of(own, r.m, inv, lns);
     if (p.lse) put_lse(r.m, lns, fmaf(r.m, inv, lns));
     if (kEntropy) p.entropy[t] = r.s == 0.0f ? 0.0f : (log2s - r.a / r.s) * kRowLn2;
   }

@@ -16,8 +16,8 @@ import numpy as np
 import pytest
 
 from oracle import vocab as vo
-from test_vocab_gpu import (HALF, TINY, close, f32, gpu, host, i32, logits_of, numbers, padding_untouched, rows_on_gpu,
-                            run_backward, special_rows, stored)
+from test_vocab_gpu import (HALF, TINY, check_logprobs, close, f32, gpu, host, i32, logits_of, numbers,
+                            padding_untouched, rows_on_gpu, run_backward, run_logprobs, special_rows, stored)
 
 pytestmark = pytest.mark.gpu
 
@@ -174,3 +174,27 @@ def test_in_a_graph(cuda_lib):
         both()
         torch.cuda.synchronize()
         assert all(np.array_equal(a, host(b)) for a, b in zip(replayed, (lse, lp, d)))
+
+
+@pytest.mark.parametrize("tau", [0.5, 1.0, 1.5, 3.0, 1e4])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_finite_logits_further_apart_than_fp32_reaches(cuda_lib, kind, tau):
+    """ln p is -inf only where it is beyond fp32 itself, in shares of a row (one
+    row), too; with a NaN or an infinity beside them it is NaN."""
+    low = special_rows(8, kind)[1][1, 0]
+    for T, V in ((40, 300), (1, 70001)):
+        x = stored(np.full((T, V), low), kind)
+        x[:, ::3], x[:, 7] = -low, -np.inf
+        x[:, 5] = 0.0
+        tokens = np.array([1, 0, 5, 7])[np.arange(T) % 4]
+        if T > 1:
+            x[8, 20], x[9, 20] = np.nan, np.inf
+            x[10] = np.where(np.arange(V) % 4 == 1, low, -np.inf)
+            x[11] = stored(np.where(np.arange(V) % 4 == 1, low, low / 2), kind)
+        got = run_logprobs(cuda_lib, x, kind, tokens, tau=tau, k=min(V, 128))
+        fine = ~(np.isnan(x) | (x == np.inf)).any(axis=1)
+        assert np.isnan(got["logprob"][~fine]).all() and np.isnan(got["top_logprob"][~fine]).all()
+        check_logprobs({n: v[fine] for n, v in got.items()}, x[fine], tokens[fine], tau=tau, k=min(V, 128))
+        # beyond fp32 at a temperature of 1, within at 3
+        one = np.nonzero(fine & (tokens == 1))[0][0]
+        assert (got["logprob"][one] == -np.inf) == (tau < 2)
